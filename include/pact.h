@@ -328,6 +328,98 @@ int pact_rmsnorm_bwd(const pact_nvfp4* yq, const uint16_t* gamma, const float* r
                      float* out_amax_opt, pact_stream_t stream);
 
 /*
+ * FP8 tensors: E4M3 values with one FP32 scale per block of 128, for projections held
+ * in 8 bits beside the NVFP4 ones.  The paper has no counterpart (its projections are
+ * NVFP4 throughout).
+ *   An activation or gradient X [rows, cols] has one scale per 128 values of a row:
+ *     q  E4M3 [rows, cols], contiguous;  s  FP32 [ceil(cols/128), rows]: the scales of
+ *     one block column are contiguous over the rows.
+ *   A weight [rows, cols] has one scale per 128 x 128 tile:
+ *     q  E4M3 [rows, cols], contiguous;  s  FP32 [ceil(rows/128), ceil(cols/128)].
+ * The last block of a row, and the last tile of a column, may be shorter.  Value of an
+ * element: e4m3(q) * s.  A block with largest magnitude amax is encoded with
+ *   t = max(amax, 448 * 2^-126);  s = RN(t / 448);  r = RN(448 / t);
+ *   q = e4m3_rne_satfinite(RN(x r))   (FP32 arithmetic; signed zeros are kept).
+ * The GEMM takes any scales, also ones that another program made.
+ * Rules for every call below: rows 1 .. 2^30; cols a multiple of 16, 16 .. 2^24; q
+ * 16-byte and s 4-byte aligned.  pact_fp8_scale_count and pact_fp8_weight_scale_count
+ * give the number of FP32 values in s.
+ */
+typedef struct pact_fp8 {
+  void* q;
+  float* s;
+  int64_t rows;
+  int64_t cols;
+} pact_fp8;
+size_t pact_fp8_scale_count(int64_t rows, int64_t cols);
+size_t pact_fp8_weight_scale_count(int64_t rows, int64_t cols);
+
+/*
+ * Quantise a BF16 activation or gradient x [M, K] (row stride ldx elements, ldx >= K,
+ * ldx % 8 == 0, 16-byte aligned) to FP8.  One pass, no workspace.
+ */
+int pact_quant_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, pact_fp8* out,
+                   pact_stream_t stream);
+
+/*
+ * Offline pack of the frozen weight W [N, K] (FP32, row-major, 16-byte aligned;
+ * Y = X W^T) into the FP8 forward layout [N, K] or backward layout [K, N] (the same
+ * codes and tile scales, transposed).  Rules: N and K multiples of 16.
+ */
+int pact_pack_weight_fp8_fwd(const float* W, int64_t N, int64_t K, pact_fp8* out_fwd,
+                             pact_stream_t stream);
+int pact_pack_weight_fp8_bwd(const float* W, int64_t N, int64_t K, pact_fp8* out_bwd,
+                             pact_stream_t stream);
+
+/*
+ * Frozen linear layer in FP8, any number of tokens from one up:
+ *   Y[m, n] = bf16( sum_b xq.s[b, m] w.s[n/128, b] sum_{k in block b} xq.q[m, k] w.q[n, k]
+ *                   [+ residual[m, n]] )
+ * with FP32 sums and one rounding.  Deterministic.
+ *   xq  FP8 activation [M, K];  w_fwd  FP8 weight [N, K];
+ *   residual_opt  BF16 [M, N] or NULL (may alias y);  y  BF16 [M, N].
+ * Input gradient: dX = dYq Wbwd^T [+ dX_prev], the same product over N:
+ *   dyq  FP8 gradient [M, N] (pact_quant_fp8);  w_bwd  FP8 weight [K, N];
+ *   dx_prev_opt  BF16 [M, K] or NULL (may alias dx, to add to it);  dx  BF16 [M, K].
+ * The weight is frozen and has no gradient.  y, dx and the addends 16-byte aligned.
+ */
+int pact_linear_fp8_fwd(const pact_fp8* xq, const pact_fp8* w_fwd, const uint16_t* residual_opt,
+                        uint16_t* y, pact_stream_t stream);
+int pact_linear_fp8_dgrad(const pact_fp8* dyq, const pact_fp8* w_bwd, const uint16_t* dx_prev_opt,
+                          uint16_t* dx, pact_stream_t stream);
+
+/*
+ * RMSNorm with the residual's addition, output in FP8:
+ *   h = bf16(x + residual)  (h = x without a residual);
+ *   rstd = 1 / sqrt(mean(h^2) + eps);  y = (h rstd) gamma  in FP32, quantised.
+ *   x BF16 [M, H];  residual_opt BF16 [M, H] and h_opt BF16 [M, H] out, both or neither
+ *   (h may alias x or residual);  gamma BF16 [H];  yq FP8 activation [M, H] out;
+ *   rstd FP32 [M] out.  x, residual, gamma and h 16-byte aligned.
+ * Rules: M 1 .. 2^30, H % 16 == 0, 16 <= H <= 16384, eps finite and >= 0.
+ * The result does not depend on the other rows of the call, but its sums may be taken
+ * in another order for another M.
+ */
+int pact_add_rmsnorm_quant_fp8(const uint16_t* x, const uint16_t* residual_opt,
+                               const uint16_t* gamma, int64_t M, int64_t H, float eps,
+                               uint16_t* h_opt, pact_fp8* yq, float* rstd, pact_stream_t stream);
+
+/*
+ * Its backward.  With n = h rstd and dn = dy gamma:
+ *   c = sum(dn n) / H;  dh = bf16(rstd (dn - n c) [+ dres]);  dgamma = sum over rows dy n.
+ * dh is the gradient of x and of the residual alike; dres is the gradient that reaches
+ * h by the residual stream.
+ *   h BF16 [M, H] (the forward's h, or x without a residual);  rstd FP32 [M];
+ *   dy, dres_opt, dh BF16 [M, H] (dh may alias dy or dres);  dgamma_opt FP32 [H] or NULL.
+ * Rules as for the forward.  ws: pact_add_rmsnorm_bwd_workspace_size() bytes when dgamma
+ * is asked for, else NULL.  Deterministic.
+ */
+size_t pact_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t H);
+int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd,
+                         const uint16_t* dy, const uint16_t* dres_opt, int64_t M, int64_t H,
+                         uint16_t* dh, float* dgamma_opt, void* ws, size_t ws_bytes,
+                         pact_stream_t stream);
+
+/*
  * The FP32 exp recipe used by pact_silu_mul_quant, exposed so that it can be
  * compared bit for bit with another implementation: Cody-Waite reduction
  * x = n ln2 + f (ln2 split in a 16-bit head and a tail), degree-7 Taylor

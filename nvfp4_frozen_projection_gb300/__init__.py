@@ -17,12 +17,15 @@ from dataclasses import dataclass
 import torch
 
 __all__ = [
-    "NVFP4", "PactError", "load_library", "library_path",
+    "NVFP4", "FP8", "FP8Weight", "PactError", "load_library", "library_path",
     "pact_quant_nvfp4", "pact_pack_weight_fwd", "pact_pack_weight_bwd",
     "pact_lora_linear_fwd", "pact_lora_linear_fwd_noalloc", "pact_lora_linear_dgrad",
     "pact_lora_linear_dgrad_q", "pact_lora_adapter_grad", "pact_rmsnorm_quant",
     "pact_silu_mul_quant", "pact_silu_mul_bwd", "pact_rmsnorm_bwd", "pact_test_pexp",
     "pact_pack_weight_fwd_gate_up", "pact_lora_linear_fwd_gate_up",
+    "pact_quant_fp8", "pact_pack_weight_fp8_fwd", "pact_pack_weight_fp8_bwd",
+    "pact_linear_fp8_fwd", "pact_linear_fp8_dgrad", "pact_add_rmsnorm_quant_fp8",
+    "pact_add_rmsnorm_bwd",
     "pact_test_wait_timeout", "pact_test_bounds_check", "pact_check_status",
     "pact_device_supported", "pact_launch_count", "pact_profile_next_gemm", "pact_version",
 ]
@@ -49,11 +52,17 @@ class _NVFP4Struct(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class _FP8Struct(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
 _LIB = None
 _LIB_LOCK = threading.Lock()
 
 _vp, _i64, _sz, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 _SP = ctypes.POINTER(_NVFP4Struct)
+_SP8 = ctypes.POINTER(_FP8Struct)
 _SIGNATURES = {
     "pact_nvfp4_codes_bytes": (_sz, [_i64, _i64]),
     "pact_nvfp4_sf_bytes": (_sz, [_i64, _i64]),
@@ -82,6 +91,16 @@ _SIGNATURES = {
     "pact_silu_mul_quant": (_int, [_vp, _i64, _i64, _vp, _SP, _SP, _SP, _vp, _sz, _vp]),
     "pact_silu_mul_bwd": (_int, [_SP, _SP, _vp, _vp, _vp, _vp]),
     "pact_rmsnorm_bwd": (_int, [_SP, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "pact_fp8_scale_count": (_sz, [_i64, _i64]),
+    "pact_fp8_weight_scale_count": (_sz, [_i64, _i64]),
+    "pact_quant_fp8": (_int, [_vp, _i64, _i64, _i64, _SP8, _vp]),
+    "pact_pack_weight_fp8_fwd": (_int, [_vp, _i64, _i64, _SP8, _vp]),
+    "pact_pack_weight_fp8_bwd": (_int, [_vp, _i64, _i64, _SP8, _vp]),
+    "pact_linear_fp8_fwd": (_int, [_SP8, _SP8, _vp, _vp, _vp]),
+    "pact_linear_fp8_dgrad": (_int, [_SP8, _SP8, _vp, _vp, _vp]),
+    "pact_add_rmsnorm_quant_fp8": (_int, [_vp, _vp, _vp, _i64, _i64, _f32, _vp, _SP8, _vp, _vp]),
+    "pact_add_rmsnorm_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "pact_add_rmsnorm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
     "pact_test_pexp": (_int, [_vp, _vp, _i64, _vp]),
     "pact_test_wait_timeout": (_int, [ctypes.c_uint32, _vp]),
     "pact_test_bounds_check": (_int, [_vp]),
@@ -161,6 +180,75 @@ class NVFP4:
     def struct(self) -> _NVFP4Struct:
         return _NVFP4Struct(self.codes.data_ptr(), self.sf.data_ptr(), self.g.data_ptr(),
                             self.rows, self.cols)
+
+
+# ------------------------------------------------------------------ FP8 tensors
+@dataclass
+class FP8:
+    """Device FP8 activation or gradient [rows, cols]: q float8_e4m3fn [rows, cols] and
+    s float32 [ceil(cols/128), rows], one scale per 128 values of a row."""
+    q: torch.Tensor
+    s: torch.Tensor
+
+    @property
+    def rows(self) -> int:
+        return self.q.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.q.shape[1]
+
+    @classmethod
+    def scale_shape(cls, rows: int, cols: int) -> tuple:
+        return (cols + 127) // 128, rows
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device=None):
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        return cls(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(cls.scale_shape(rows, cols), dtype=torch.float32, device=device))
+
+    def struct(self) -> _FP8Struct:
+        rows, cols = self.q.shape
+        return _FP8Struct(self.q.data_ptr(), self.s.data_ptr(), rows, cols)
+
+
+class FP8Weight(FP8):
+    """Device FP8 weight [rows, cols]: q float8_e4m3fn [rows, cols] and s float32
+    [ceil(rows/128), ceil(cols/128)], one scale per 128 x 128 tile."""
+
+    @classmethod
+    def scale_shape(cls, rows: int, cols: int) -> tuple:
+        return (rows + 127) // 128, (cols + 127) // 128
+
+
+def _need(t, dtype, shape, name, dev):
+    """t is a contiguous tensor of this dtype and shape on the current device dev."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _need_fp8(t, kind, name, dev, shape=None):
+    """t is an FP8 tensor of this kind (FP8 or FP8Weight), of this shape when given."""
+    if type(t) is not kind:
+        raise ValueError(f"{name} must be an {kind.__name__}, got {type(t).__name__}")
+    shape = shape or _need_2d(t.q, name + ".q")
+    _need(t.q, torch.float8_e4m3fn, shape, name + ".q", dev)
+    _need(t.s, torch.float32, kind.scale_shape(*shape), name + ".s", dev)
+
+
+def _need_2d(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    return tuple(t.shape)
 
 
 # ------------------------------------------------------------------ workspace
@@ -434,6 +522,156 @@ def pact_rmsnorm_bwd(yq: NVFP4, gamma: torch.Tensor, rstd: torch.Tensor, dy: tor
     _check(lib.pact_rmsnorm_bwd(ctypes.byref(s), _ptr(gamma), _ptr(rstd), _ptr(dy), _ptr(dres),
                                 _ptr(dx), _ptr(out_amax), _stream()))
     return dx
+
+
+# ------------------------------------------------------------------ FP8, blocks of 128
+def pact_quant_fp8(x: torch.Tensor, out: FP8 | None = None) -> FP8:
+    """Quantise BF16 x [M, K] (row stride may exceed K) to FP8."""
+    lib = load_library()
+    M, K = _need_2d(x, "x")
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"x must be torch.bfloat16, got {x.dtype}")
+    if x.stride(1) != 1:
+        raise ValueError("x must have unit column stride")
+    dev = torch.cuda.current_device()
+    if x.device.index != dev:
+        raise ValueError(f"x is on {x.device}, the current device is cuda:{dev}")
+    if out is None:
+        out = FP8.empty(M, K, x.device)
+    _need_fp8(out, FP8, "out", dev, (M, K))
+    s = out.struct()
+    # the stride of a single row says nothing: torch may report any number there
+    _check(lib.pact_quant_fp8(_ptr(x), M, K, x.stride(0) if M > 1 else _pad(K, 8),
+                              ctypes.byref(s), _stream()))
+    return out
+
+
+def _pack_fp8(W: torch.Tensor, backward: bool, out: FP8Weight | None) -> FP8Weight:
+    lib = load_library()
+    N, K = _need_2d(W, "W")
+    dev = torch.cuda.current_device()
+    _need(W, torch.float32, (N, K), "W", dev)
+    shape = (K, N) if backward else (N, K)
+    if out is None:
+        out = FP8Weight.empty(*shape, W.device)
+    _need_fp8(out, FP8Weight, "out", dev, shape)
+    s = out.struct()
+    fn = lib.pact_pack_weight_fp8_bwd if backward else lib.pact_pack_weight_fp8_fwd
+    _check(fn(_ptr(W), N, K, ctypes.byref(s), _stream()))
+    return out
+
+
+def pact_pack_weight_fp8_fwd(W: torch.Tensor, out: FP8Weight | None = None) -> FP8Weight:
+    """Pack the frozen FP32 weight W [N, K] into the FP8 forward layout [N, K]."""
+    return _pack_fp8(W, False, out)
+
+
+def pact_pack_weight_fp8_bwd(W: torch.Tensor, out: FP8Weight | None = None) -> FP8Weight:
+    """Pack the frozen FP32 weight W [N, K] into the FP8 backward layout [K, N]: the
+    forward layout's codes and tile scales, transposed."""
+    return _pack_fp8(W, True, out)
+
+
+def _linear_fp8(fn, x, xname, w, wname, add, addname, y, yname):
+    if not isinstance(x, FP8):
+        raise ValueError(f"{xname} must be an FP8, got {type(x).__name__}")
+    _need_2d(x.q, xname + ".q")
+    dev = torch.cuda.current_device()
+    _need_fp8(x, FP8, xname, dev)
+    _need_fp8(w, FP8Weight, wname, dev)
+    shape = (x.rows, w.rows)
+    if w.cols != x.cols:
+        raise ValueError(f"{xname} has {x.cols} columns, {wname} {w.cols}")
+    if y is None:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x.q.device)
+    _need(y, torch.bfloat16, shape, yname, dev)
+    if add is not None:
+        _need(add, torch.bfloat16, shape, addname, dev)
+    sx, sw = x.struct(), w.struct()
+    _check(fn(ctypes.byref(sx), ctypes.byref(sw), _ptr(add), _ptr(y), _stream()))
+    return y
+
+
+def pact_linear_fp8_fwd(xq: FP8, w_fwd: FP8Weight, residual: torch.Tensor | None = None,
+                        y: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = Xhat What^T [+ residual], BF16 [M, N]; any M from one token up.  residual may
+    be y itself."""
+    return _linear_fp8(load_library().pact_linear_fp8_fwd, xq, "xq", w_fwd, "w_fwd", residual,
+                       "residual", y, "y")
+
+
+def pact_linear_fp8_dgrad(dyq: FP8, w_bwd: FP8Weight, dx_prev: torch.Tensor | None = None,
+                          dx: torch.Tensor | None = None) -> torch.Tensor:
+    """dX = dYhat W [+ dX_prev], BF16 [M, K], on the backward layout.  dx_prev may be dx
+    itself, to add to it."""
+    return _linear_fp8(load_library().pact_linear_fp8_dgrad, dyq, "dyq", w_bwd, "w_bwd", dx_prev,
+                       "dx_prev", dx, "dx")
+
+
+def pact_add_rmsnorm_quant_fp8(x: torch.Tensor, residual: torch.Tensor | None,
+                               gamma: torch.Tensor, eps: float = 1e-5,
+                               h: torch.Tensor | None = None, out: FP8 | None = None,
+                               rstd: torch.Tensor | None = None):
+    """h = bf16(x + residual), RMSNorm of h to FP8.  Without a residual h is x itself.
+    h may be x or residual, to add in place.  Returns (h, yq, rstd)."""
+    lib = load_library()
+    M, H = _need_2d(x, "x")
+    dev = torch.cuda.current_device()
+    _need(x, torch.bfloat16, (M, H), "x", dev)
+    _need(gamma, torch.bfloat16, (H,), "gamma", dev)
+    if residual is not None:
+        _need(residual, torch.bfloat16, (M, H), "residual", dev)
+        if h is None:
+            h = torch.empty_like(x)
+        _need(h, torch.bfloat16, (M, H), "h", dev)
+    elif h is not None and h is not x:
+        raise ValueError("without a residual h is x itself: pass no other h")
+    if out is None:
+        out = FP8.empty(M, H, x.device)
+    _need_fp8(out, FP8, "out", dev, (M, H))
+    if rstd is None:
+        rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _need(rstd, torch.float32, (M,), "rstd", dev)
+    s = out.struct()
+    _check(lib.pact_add_rmsnorm_quant_fp8(_ptr(x), _ptr(residual), _ptr(gamma), M, H, float(eps),
+                                          _ptr(h) if residual is not None else None,
+                                          ctypes.byref(s), _ptr(rstd), _stream()))
+    return (x if residual is None else h), out, rstd
+
+
+def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
+                         dy: torch.Tensor, dres: torch.Tensor | None = None,
+                         dh: torch.Tensor | None = None,
+                         dgamma: torch.Tensor | bool | None = None):
+    """Backward of pact_add_rmsnorm_quant_fp8 from h and rstd: dh [+ dres], the gradient
+    of x and of the residual alike (dh may be dy or dres).  dgamma: an FP32 [H] tensor
+    to overwrite, True for a new one, None to leave it out.  Returns (dh, dgamma)."""
+    lib = load_library()
+    M, H = _need_2d(h, "h")
+    dev = torch.cuda.current_device()
+    _need(h, torch.bfloat16, (M, H), "h", dev)
+    _need(gamma, torch.bfloat16, (H,), "gamma", dev)
+    _need(rstd, torch.float32, (M,), "rstd", dev)
+    _need(dy, torch.bfloat16, (M, H), "dy", dev)
+    if dres is not None:
+        _need(dres, torch.bfloat16, (M, H), "dres", dev)
+    if dh is None:
+        dh = torch.empty_like(dy)
+    _need(dh, torch.bfloat16, (M, H), "dh", dev)
+    ws = None
+    if dgamma is False:
+        dgamma = None
+    if dgamma is not None:
+        if dgamma is True:
+            dgamma = torch.empty((H,), dtype=torch.float32, device=h.device)
+        _need(dgamma, torch.float32, (H,), "dgamma", dev)
+        # its own scratch in every call: a captured graph then keeps one of its own
+        ws = torch.empty((lib.pact_add_rmsnorm_bwd_workspace_size(M, H),), dtype=torch.uint8,
+                         device=h.device)
+    _check(lib.pact_add_rmsnorm_bwd(_ptr(h), _ptr(gamma), _ptr(rstd), _ptr(dy), _ptr(dres), M, H,
+                                    _ptr(dh), _ptr(dgamma), _ptr(ws),
+                                    0 if ws is None else ws.numel(), _stream()))
+    return dh, dgamma
 
 
 def pact_test_pexp(x: torch.Tensor) -> torch.Tensor:

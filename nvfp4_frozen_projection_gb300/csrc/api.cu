@@ -134,6 +134,27 @@ int check_nvfp4(const pact_nvfp4* t, const char* name, int64_t rows, int64_t col
   return PACT_OK;
 }
 
+int check_fp8(const pact_fp8* t, const char* name, int64_t rows, int64_t cols) {
+  if (!t) return fail(PACT_ERR_INVALID_ARG, "%s is null", name);
+  if (!t->q || !t->s) return fail(PACT_ERR_INVALID_ARG, "%s has a null field", name);
+  if (t->rows != rows || t->cols != cols)
+    return fail(PACT_ERR_SHAPE, "%s is [%lld, %lld], expected [%lld, %lld]", name,
+                (long long)t->rows, (long long)t->cols, (long long)rows, (long long)cols);
+  if (!aligned(t->q, 16) || !aligned(t->s, 4))
+    return fail(PACT_ERR_ALIGN, "%s q must be 16-byte and s 4-byte aligned", name);
+  return PACT_OK;
+}
+
+// Row counts up to 2^30 and widths up to 2^24, multiples of 16: row and column indices
+// and their sums with a tile's extent fit in 31 bits.
+constexpr int64_t kFp8MaxRows = (int64_t)1 << 30, kFp8MaxCols = (int64_t)1 << 24;
+
+int check_fp8_cols(int64_t c, const char* name) {
+  if (c < 16 || c % 16 || c > kFp8MaxCols)
+    return fail(PACT_ERR_SHAPE, "need %s a multiple of 16, 16 <= %s <= 2^24", name, name);
+  return PACT_OK;
+}
+
 // LoRA rank padded to 16, 32 or 64; the fused GEMM's LoRA operands are twice as
 // wide (a hi/lo BF16 pair of the down-projection output).
 int rp_for(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
@@ -639,6 +660,144 @@ int pact_rmsnorm_bwd(const pact_nvfp4* yq, const uint16_t* gamma, const float* r
                                      gamma, rstd, dy, dres_opt, M, H, dx,
                                      (unsigned*)out_amax_opt, d->sms, (cudaStream_t)stream);
   return e == cudaSuccess ? PACT_OK : cuda_fail(e, "rmsnorm bwd launch");
+}
+
+// ---------------------------------------------------------------- FP8, blocks of 128
+// Arguments are checked before the device is looked at.
+size_t pact_fp8_scale_count(int64_t rows, int64_t cols) {
+  return rows > 0 && cols > 0 ? (size_t)(rows * ((cols + 127) / 128)) : 0;
+}
+
+size_t pact_fp8_weight_scale_count(int64_t rows, int64_t cols) {
+  return rows > 0 && cols > 0 ? (size_t)(((rows + 127) / 128) * ((cols + 127) / 128)) : 0;
+}
+
+int pact_quant_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, pact_fp8* out,
+                   pact_stream_t stream) {
+  int rc;
+  if (M < 1 || M > kFp8MaxRows) return fail(PACT_ERR_SHAPE, "need 1 <= M <= 2^30");
+  if ((rc = check_fp8_cols(K, "K"))) return rc;
+  if (((M + 7) / 8) * ((K + 127) / 128) >= (int64_t)1 << 31)
+    return fail(PACT_ERR_SHAPE, "tensor too large: ceil(M / 8) * ceil(K / 128) must be < 2^31");
+  if (!x) return fail(PACT_ERR_INVALID_ARG, "x is null");
+  if (ldx < K || ldx % 8) return fail(PACT_ERR_SHAPE, "need ldx >= K and ldx %% 8 == 0");
+  if (!aligned(x, 16)) return fail(PACT_ERR_ALIGN, "x must be 16-byte aligned");
+  if ((rc = check_fp8(out, "out", M, K))) return rc;
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  cudaError_t e = launch_quant_fp8(x, M, K, ldx, (uint8_t*)out->q, out->s, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "fp8 quant launch");
+}
+
+static int pack_fp8(const float* W, int64_t N, int64_t K, pact_fp8* out, pact_stream_t stream,
+                    int backward) {
+  int rc;
+  if (!W) return fail(PACT_ERR_INVALID_ARG, "W is null");
+  if ((rc = check_fp8_cols(N, "N")) || (rc = check_fp8_cols(K, "K"))) return rc;
+  if (((N + 127) / 128) * ((K + 127) / 128) >= (int64_t)1 << 31)
+    return fail(PACT_ERR_SHAPE, "weight too large: ceil(N / 128) * ceil(K / 128) must be < 2^31");
+  if (!aligned(W, 16)) return fail(PACT_ERR_ALIGN, "W must be 16-byte aligned");
+  if ((rc = check_fp8(out, backward ? "out_bwd" : "out_fwd", backward ? K : N, backward ? N : K)))
+    return rc;
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  cudaError_t e = launch_pack_fp8(W, N, K, backward, (uint8_t*)out->q, out->s,
+                                  (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "fp8 pack launch");
+}
+
+int pact_pack_weight_fp8_fwd(const float* W, int64_t N, int64_t K, pact_fp8* out_fwd,
+                             pact_stream_t stream) {
+  return pack_fp8(W, N, K, out_fwd, stream, 0);
+}
+
+int pact_pack_weight_fp8_bwd(const float* W, int64_t N, int64_t K, pact_fp8* out_bwd,
+                             pact_stream_t stream) {
+  return pack_fp8(W, N, K, out_bwd, stream, 1);
+}
+
+static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, const char* wname,
+                      const uint16_t* add, const char* addname, uint16_t* out,
+                      const char* outname, pact_stream_t stream) {
+  int rc;
+  if (!x || !w) return fail(PACT_ERR_INVALID_ARG, "%s and %s are required", xname, wname);
+  const int64_t M = x->rows, K = x->cols, N = w->rows;
+  if (M < 1 || M > kFp8MaxRows) return fail(PACT_ERR_SHAPE, "need 1 <= rows <= 2^30");
+  if ((rc = check_fp8_cols(K, "the reduction width")) ||
+      (rc = check_fp8_cols(N, "the output width")))
+    return rc;
+  if ((rc = check_fp8(x, xname, M, K)) || (rc = check_fp8(w, wname, N, K))) return rc;
+  if (!out) return fail(PACT_ERR_INVALID_ARG, "%s is required", outname);
+  if (!aligned(out, 16) || (add && !aligned(add, 16)))
+    return fail(PACT_ERR_ALIGN, "%s and %s must be 16-byte aligned", outname, addname);
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  cudaError_t e = launch_fp8_few((const uint8_t*)x->q, x->s, (const uint8_t*)w->q, w->s, M, N, K,
+                                 add, out, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "fp8 linear launch");
+}
+
+int pact_linear_fp8_fwd(const pact_fp8* xq, const pact_fp8* w_fwd, const uint16_t* residual_opt,
+                        uint16_t* y, pact_stream_t stream) {
+  return linear_fp8(xq, "xq", w_fwd, "w_fwd", residual_opt, "residual", y, "y", stream);
+}
+
+int pact_linear_fp8_dgrad(const pact_fp8* dyq, const pact_fp8* w_bwd, const uint16_t* dx_prev_opt,
+                          uint16_t* dx, pact_stream_t stream) {
+  return linear_fp8(dyq, "dyq", w_bwd, "w_bwd", dx_prev_opt, "dx_prev", dx, "dx", stream);
+}
+
+static int check_norm_dims(int64_t M, int64_t H) {
+  if (M < 1 || M > kFp8MaxRows || H < 16 || H % 16 || H > 16384)
+    return fail(PACT_ERR_SHAPE, "need 1 <= M <= 2^30, H %% 16 == 0, 16 <= H <= 16384");
+  return PACT_OK;
+}
+
+int pact_add_rmsnorm_quant_fp8(const uint16_t* x, const uint16_t* residual_opt,
+                               const uint16_t* gamma, int64_t M, int64_t H, float eps,
+                               uint16_t* h_opt, pact_fp8* yq, float* rstd, pact_stream_t stream) {
+  int rc;
+  if (!residual_opt != !h_opt)
+    return fail(PACT_ERR_INVALID_ARG, "residual and h go together: both or neither");
+  if ((rc = check_norm_dims(M, H))) return rc;
+  if (!x || !gamma || !rstd) return fail(PACT_ERR_INVALID_ARG, "x, gamma and rstd are required");
+  if (!(eps >= 0.0f && eps <= 3.4028235e38f))
+    return fail(PACT_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!aligned(x, 16) || !aligned(gamma, 16) || !aligned(residual_opt, 16) ||
+      !aligned(h_opt, 16) || !aligned(rstd, 4))
+    return fail(PACT_ERR_ALIGN, "x, residual, gamma and h must be 16-byte aligned");
+  if ((rc = check_fp8(yq, "yq", M, H))) return rc;
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  cudaError_t e = launch_add_rmsnorm_fp8(x, residual_opt, gamma, M, H, eps, h_opt,
+                                         (uint8_t*)yq->q, yq->s, rstd, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "add rmsnorm launch");
+}
+
+size_t pact_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t H) {
+  if (M < 1 || M > kFp8MaxRows || H < 16 || H % 16 || H > 16384) return 0;
+  return align256((size_t)rmsnorm_bwd_partials(M, H) * (size_t)H * 4);
+}
+
+int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd,
+                         const uint16_t* dy, const uint16_t* dres_opt, int64_t M, int64_t H,
+                         uint16_t* dh, float* dgamma_opt, void* ws, size_t ws_bytes,
+                         pact_stream_t stream) {
+  int rc;
+  if ((rc = check_norm_dims(M, H))) return rc;
+  if (!h || !gamma || !rstd || !dy || !dh)
+    return fail(PACT_ERR_INVALID_ARG, "h, gamma, rstd, dy and dh are required");
+  if (!aligned(h, 16) || !aligned(gamma, 16) || !aligned(dy, 16) || !aligned(dh, 16) ||
+      !aligned(dres_opt, 16) || !aligned(rstd, 4) || !aligned(dgamma_opt, 4))
+    return fail(PACT_ERR_ALIGN, "h, gamma, dy, dres and dh must be 16-byte aligned");
+  if (dgamma_opt &&
+      (!ws || ws_bytes < pact_add_rmsnorm_bwd_workspace_size(M, H) || !aligned(ws, 256)))
+    return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  cudaError_t e = launch_add_rmsnorm_bwd(h, gamma, rstd, dy, dres_opt, M, H, dh, dgamma_opt,
+                                         (float*)ws, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "add rmsnorm bwd launch");
 }
 
 int pact_test_wait_timeout(uint32_t limit_us, pact_stream_t stream) {

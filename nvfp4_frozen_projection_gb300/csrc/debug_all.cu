@@ -8,3 +8,6 @@
 #include "lora.cu"
 #include "norm_act.cu"
 #include "noalloc.cu"
+#include "fp8_quant.cu"
+#include "fp8_norm.cu"
+#include "fp8_gemm.cu"

@@ -1,0 +1,307 @@
+// RMSNorm with the residual's addition: forward to FP8, and backward.
+//
+//   h = bf16(x + residual);  rstd = 1 / sqrt(mean(h^2) + eps);  y = (h rstd) gamma
+//   in FP32, quantised with one scale per 128 values (fp8.cuh).
+//   backward, with n = h rstd and dn = dy gamma:
+//     c = sum(dn n) / H;  dh = bf16(rstd (dn - n c) + dres);  dgamma = sum over rows dy n.
+//   x and the residual have the same gradient, dh.
+//
+// Both are bound by HBM: 4 bytes read and 3 written per value forward (2 and 1
+// without a residual), 6 read and 2 written backward.  A row is held in registers by
+// a group of 1 to 16 warps, so each input is read once: thread vectors of 8 values
+// (16 bytes), NV per thread, strided so that 16 neighbouring lanes hold one block of
+// 128 and a warp's access is 512 contiguous bytes.  The sums over a row run lane by
+// lane, then over the warp by a butterfly, then over the group's warps in order: the
+// same order on every call.
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace pact {
+
+struct RowPlan {
+  int nv;      // vectors of 8 per thread, 1..4
+  int wpr;     // warps per row, a power of two, 1..16
+  int groups;  // rows in flight per CTA
+  int threads;
+};
+
+// Fewest warps per row that keep a thread's share at four vectors: fewer warps means
+// fewer barriers.  With too few rows to fill the SMs a row is spread over more warps.
+static RowPlan row_plan(int64_t M, int64_t H) {
+  RowPlan p;
+  p.wpr = 1;
+  while (H > (int64_t)p.wpr * 1024) p.wpr *= 2;
+  while (p.wpr < 8 && H > (int64_t)p.wpr * 256 && M * p.wpr < 2048) p.wpr *= 2;
+  p.nv = (int)((H + p.wpr * 256 - 1) / (p.wpr * 256));
+  p.threads = p.wpr > 8 ? 32 * p.wpr : 256;
+  p.groups = p.threads / (32 * p.wpr);
+  return p;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Sum over the wpr warps of a row group; slot: 16 floats of this group (one of two
+// used in turn, so that a group's next sum does not overwrite values still read).
+__device__ __forceinline__ float group_sum(float v, int wpr, int wl, int group, float* slot) {
+  v = warp_sum(v);
+  if (wpr == 1) return v;
+  if ((threadIdx.x & 31) == 0) slot[wl] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * wpr) : "memory");
+  float t = slot[0];
+  for (int i = 1; i < wpr; ++i) t += slot[i];
+  return t;
+}
+
+template <int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    k_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, int64_t M,
+                      int64_t H, float eps, int wpr, uint16_t* h_out, uint8_t* q, float* s,
+                      float* rstd_out) {
+  __shared__ float slots[16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / wpr, wl = warp - group * wpr;
+  const int64_t row = (int64_t)blockIdx.x * ((THREADS / 32) / wpr) + group;
+  if (row >= M) return;  // a whole group
+  uint4 hv[NV];
+  const int64_t base = row * H;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+    hv[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < H) hv[i] = *reinterpret_cast<const uint4*>(x + base + c);
+  }
+  if (res) {
+    uint4 rv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+      rv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < H) rv[i] = *reinterpret_cast<const uint4*>(res + base + c);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float a[8], b[8];
+      bf16x8_to_f32(hv[i], a);
+      bf16x8_to_f32(rv[i], b);
+      hv[i] = make_uint4(pack_bf16x2(__fadd_rn(a[0], b[0]), __fadd_rn(a[1], b[1])),
+                         pack_bf16x2(__fadd_rn(a[2], b[2]), __fadd_rn(a[3], b[3])),
+                         pack_bf16x2(__fadd_rn(a[4], b[4]), __fadd_rn(a[5], b[5])),
+                         pack_bf16x2(__fadd_rn(a[6], b[6]), __fadd_rn(a[7], b[7])));
+      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+      if (c < H && PACT_IN(base + c + 8 <= M * H))
+        *reinterpret_cast<uint4*>(h_out + base + c) = hv[i];
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    PACT_NAN_BF16X2(hv[i].x);
+    PACT_NAN_BF16X2(hv[i].y);
+    PACT_NAN_BF16X2(hv[i].z);
+    PACT_NAN_BF16X2(hv[i].w);
+    float f[8];
+    bf16x8_to_f32(hv[i], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __fmaf_rn(f[e], f[e], ss);
+  }
+  ss = group_sum(ss, wpr, wl, group, slots + group * wpr);
+  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
+  if (wl == 0 && lane == 0) rstd_out[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+    uint4 gv = make_uint4(0u, 0u, 0u, 0u);
+    if (c < H) gv = *reinterpret_cast<const uint4*>(gamma + c);
+    float f[8], g[8], amax = 0.0f;
+    bf16x8_to_f32(hv[i], f);
+    bf16x8_to_f32(gv, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = __fmul_rn(__fmul_rn(f[e], rstd), g[e]);
+      amax = fmaxf(amax, fabsf(f[e]));
+    }
+    const Fp8Scale sc = fp8_scale(half_warp_max(amax));
+    if (c < H && PACT_IN(base + c + 8 <= M * H)) {
+      *reinterpret_cast<uint2*>(q + base + c) = e4m3x8(f, sc.r);
+      if ((lane & 15) == 0) s[(c >> 7) * M + row] = sc.s;
+    }
+  }
+}
+
+cudaError_t launch_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma,
+                                   int64_t M, int64_t H, float eps, uint16_t* h, uint8_t* q,
+                                   float* s, float* rstd, cudaStream_t stream) {
+  const RowPlan p = row_plan(M, H);
+  const unsigned grid = (unsigned)((M + p.groups - 1) / p.groups);
+  note_launch();
+#define PACT_NORM(NV, T) \
+  k_add_rmsnorm_fp8<NV, T><<<grid, T, 0, stream>>>(x, res, gamma, M, H, eps, p.wpr, h, q, s, rstd)
+  if (p.threads == 512) {
+    if (p.nv == 3) PACT_NORM(3, 512); else PACT_NORM(4, 512);
+  } else if (p.nv == 1) {
+    PACT_NORM(1, 256);
+  } else if (p.nv == 2) {
+    PACT_NORM(2, 256);
+  } else if (p.nv == 3) {
+    PACT_NORM(3, 256);
+  } else {
+    PACT_NORM(4, 256);
+  }
+#undef PACT_NORM
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- backward
+// A persistent grid: a thread owns the same columns in every row, so dgamma's partial
+// sums stay in its registers; each group writes one row of partial sums at the end,
+// and a second kernel adds them in a fixed order.
+constexpr int kBwdCtas = 304;
+
+static int bwd_ctas(int64_t M, const RowPlan& p) {
+  const int64_t n = (M + p.groups - 1) / p.groups;
+  return (int)(n < kBwdCtas ? n : kBwdCtas);
+}
+
+int64_t rmsnorm_bwd_partials(int64_t M, int64_t H) {
+  const RowPlan p = row_plan(M, H);
+  return (int64_t)bwd_ctas(M, p) * p.groups;
+}
+
+template <int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    k_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd_in,
+                      const uint16_t* dy, const uint16_t* dres, int64_t M, int64_t H, int wpr,
+                      uint16_t* dh, float* part) {
+  __shared__ float slots[2][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / wpr, wl = warp - group * wpr;
+  const int groups = (THREADS / 32) / wpr;
+  const float inv_h = __fdiv_rn(1.0f, (float)H);
+  float dg[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[i][e] = 0.0f;
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * groups + group; row < M;
+       row += (int64_t)gridDim.x * groups) {
+    const int64_t base = row * H;
+    uint4 hv[NV], dv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+      hv[i] = dv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < H) {
+        hv[i] = *reinterpret_cast<const uint4*>(h + base + c);
+        dv[i] = *reinterpret_cast<const uint4*>(dy + base + c);
+      }
+    }
+    const float rstd = rstd_in[row];
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+      uint4 gv = make_uint4(0u, 0u, 0u, 0u);
+      if (c < H) gv = *reinterpret_cast<const uint4*>(gamma + c);
+      float f[8], d[8], g[8];
+      bf16x8_to_f32(hv[i], f);
+      bf16x8_to_f32(dv[i], d);
+      bf16x8_to_f32(gv, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = __fmul_rn(f[e], rstd);
+        t = __fmaf_rn(__fmul_rn(d[e], g[e]), n, t);
+        dg[i][e] = __fmaf_rn(d[e], n, dg[i][e]);
+      }
+    }
+    t = group_sum(t, wpr, wl, group, slots[turn] + group * wpr);
+    turn ^= 1;
+    const float c0 = __fmul_rn(t, inv_h);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+      if (c >= H) continue;
+      const uint4 gv = *reinterpret_cast<const uint4*>(gamma + c);
+      uint4 rv = make_uint4(0u, 0u, 0u, 0u);
+      if (dres) rv = *reinterpret_cast<const uint4*>(dres + base + c);
+      float f[8], d[8], g[8], r[8];
+      bf16x8_to_f32(hv[i], f);
+      bf16x8_to_f32(dv[i], d);
+      bf16x8_to_f32(gv, g);
+      bf16x8_to_f32(rv, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = __fmul_rn(f[e], rstd);
+        f[e] = __fmaf_rn(rstd, __fmaf_rn(-n, c0, __fmul_rn(d[e], g[e])), r[e]);
+      }
+      const uint4 o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                 pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+      PACT_NAN_BF16X2(o.x);
+      PACT_NAN_BF16X2(o.y);
+      PACT_NAN_BF16X2(o.z);
+      PACT_NAN_BF16X2(o.w);
+      if (PACT_IN(base + c + 8 <= M * H)) *reinterpret_cast<uint4*>(dh + base + c) = o;
+    }
+  }
+  if (!part) return;
+  float* p = part + ((int64_t)blockIdx.x * groups + group) * H;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+    if (c >= H) continue;
+    *reinterpret_cast<float4*>(p + c) = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+    *reinterpret_cast<float4*>(p + c + 4) = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+  }
+}
+
+// dgamma[j] = sum over P rows of part, 16 row lanes per column, each in row order.
+__global__ void __launch_bounds__(512)
+    k_dgamma_reduce(const float* part, int P, int64_t H, float* dgamma) {
+  __shared__ float sum[16][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t j = (int64_t)blockIdx.x * 32 + tx;
+  float t = 0.0f;
+  if (j < H)
+    for (int p = ty; p < P; p += 16) t += part[(int64_t)p * H + j];
+  sum[ty][tx] = t;
+  __syncthreads();
+  if (ty == 0 && j < H) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t += sum[i][tx];
+    dgamma[j] = t;
+  }
+}
+
+cudaError_t launch_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd,
+                                   const uint16_t* dy, const uint16_t* dres, int64_t M, int64_t H,
+                                   uint16_t* dh, float* dgamma, float* part, cudaStream_t stream) {
+  const RowPlan p = row_plan(M, H);
+  const int grid = bwd_ctas(M, p);
+  float* pp = dgamma ? part : nullptr;
+  note_launch();
+#define PACT_NORM(NV, T) \
+  k_add_rmsnorm_bwd<NV, T><<<grid, T, 0, stream>>>(h, gamma, rstd, dy, dres, M, H, p.wpr, dh, pp)
+  if (p.threads == 512) {
+    if (p.nv == 3) PACT_NORM(3, 512); else PACT_NORM(4, 512);
+  } else if (p.nv == 1) {
+    PACT_NORM(1, 256);
+  } else if (p.nv == 2) {
+    PACT_NORM(2, 256);
+  } else if (p.nv == 3) {
+    PACT_NORM(3, 256);
+  } else {
+    PACT_NORM(4, 256);
+  }
+#undef PACT_NORM
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !dgamma) return e;
+  note_launch();
+  k_dgamma_reduce<<<(unsigned)((H + 31) / 32), 512, 0, stream>>>(part, grid * p.groups, H, dgamma);
+  return cudaGetLastError();
+}
+
+}  // namespace pact

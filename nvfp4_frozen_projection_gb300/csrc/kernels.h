@@ -134,6 +134,26 @@ cudaError_t launch_rmsnorm_bwd(const uint8_t* yc, const uint8_t* ysf, const floa
                                const uint16_t* gamma, const float* rstd, const uint16_t* dy,
                                const uint16_t* dres, int64_t M, int64_t H, uint16_t* dx,
                                unsigned* out_amax, int num_sms, cudaStream_t stream);
+
+// FP8 (fp8.cuh): activations q [M, K] with scales s [ceil(K/128), M], weights q [N, K]
+// with scales [ceil(N/128), ceil(K/128)].
+cudaError_t launch_quant_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q,
+                             float* s, cudaStream_t stream);
+cudaError_t launch_pack_fp8(const float* W, int64_t N, int64_t K, int backward, uint8_t* q,
+                            float* s, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma,
+                                   int64_t M, int64_t H, float eps, uint16_t* h, uint8_t* q,
+                                   float* s, float* rstd, cudaStream_t stream);
+// dgamma null: not computed and part unused; else part holds rmsnorm_bwd_partials(M, H)
+// rows of H FP32 partial sums.
+int64_t rmsnorm_bwd_partials(int64_t M, int64_t H);
+cudaError_t launch_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd,
+                                   const uint16_t* dy, const uint16_t* dres, int64_t M, int64_t H,
+                                   uint16_t* dh, float* dgamma, float* part, cudaStream_t stream);
+cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
+                           int64_t M, int64_t N, int64_t K, const uint16_t* add, uint16_t* out,
+                           cudaStream_t stream);
+
 cudaError_t launch_pexp(const float* x, float* y, int64_t n, cudaStream_t stream);
 
 }  // namespace pact

@@ -16,9 +16,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (NVFP4, pact_lora_linear_dgrad, pact_lora_linear_dgrad_q, pact_lora_linear_fwd,
+from . import (FP8, NVFP4, pact_linear_fp8_dgrad, pact_linear_fp8_fwd, pact_lora_linear_dgrad, pact_lora_linear_dgrad_q, pact_lora_linear_fwd,
                pact_lora_linear_fwd_gate_up, pact_pack_weight_bwd, pact_pack_weight_fwd_gate_up,
-               pact_lora_adapter_grad, pact_pack_weight_fwd, pact_quant_nvfp4, pact_rmsnorm_bwd,
+               pact_lora_adapter_grad, pact_pack_weight_fp8_bwd, pact_pack_weight_fp8_fwd,
+               pact_pack_weight_fwd, pact_quant_fp8, pact_quant_nvfp4, pact_rmsnorm_bwd,
                pact_rmsnorm_quant,
                pact_silu_mul_bwd, pact_silu_mul_quant)
 
@@ -60,6 +61,28 @@ class LoraLinear:
 
     def adapter_grad(self, xq: NVFP4, dy: torch.Tensor, dA=None, dB=None):
         return pact_lora_adapter_grad(xq, dy, self.A, self.B, self.scale, dA=dA, dB=dB)
+
+    def gemm_flops(self, m: int) -> float:
+        return 2.0 * m * self.d_in * self.d_out
+
+
+class Fp8Linear:
+    """Frozen weight W [d_out, d_in] held in FP8 (one scale per 128 x 128 tile), packed
+    once into the forward and backward layouts: for projections that are to keep eight
+    bits, and for decoding a few tokens at a time."""
+
+    def __init__(self, W: torch.Tensor):
+        self.d_out, self.d_in = W.shape
+        self.w_fwd = pact_pack_weight_fp8_fwd(W)
+        self.w_bwd = pact_pack_weight_fp8_bwd(W)
+
+    def forward(self, xq: FP8, y: torch.Tensor = None, residual=None):
+        return pact_linear_fp8_fwd(xq, self.w_fwd, residual=residual, y=y)
+
+    def dgrad(self, dy: torch.Tensor, dyq: FP8 = None, dx: torch.Tensor = None, dx_prev=None):
+        """Quantise dy (into dyq) and run the input gradient."""
+        return pact_linear_fp8_dgrad(pact_quant_fp8(dy, out=dyq), self.w_bwd, dx_prev=dx_prev,
+                                     dx=dx)
 
     def gemm_flops(self, m: int) -> float:
         return 2.0 * m * self.d_in * self.d_out
