@@ -732,8 +732,31 @@ static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, c
     return fail(PACT_ERR_ALIGN, "%s and %s must be 16-byte aligned", outname, addname);
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
-  cudaError_t e = launch_fp8_few((const uint8_t*)x->q, x->s, (const uint8_t*)w->q, w->s, M, N, K,
-                                 add, out, (cudaStream_t)stream);
+  cudaError_t e;
+  if (fp8_is_few(M, N, K)) {
+    e = launch_fp8_few((const uint8_t*)x->q, x->s, (const uint8_t*)w->q, w->s, M, N, K, add, out,
+                       (cudaStream_t)stream);
+  } else {
+    Fp8GemmLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    if ((rc = make_map(&L.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x->q, K, M, 128, 128,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        (rc = make_map(&L.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->q, K, N, 128, 128,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        (rc = make_map(&L.tmOut, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, N, M, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_64B)))
+      return rc;
+    L.p.sx = x->s;
+    L.p.sw = w->s;
+    L.p.add = add;
+    L.p.status = d->status;
+    L.p.M = (int)M;
+    L.p.N = (int)N;
+    L.p.nkb = (int)((K + 127) / 128);
+    L.K = K;
+    L.num_sms = d->sms;
+    e = launch_fp8_gemm(L, (cudaStream_t)stream);
+  }
   return e == cudaSuccess ? PACT_OK : cuda_fail(e, "fp8 linear launch");
 }
 

@@ -273,12 +273,6 @@ __device__ __forceinline__ void gate_up_stats(const uint32_t (&out)[NCH][16], in
   }
 }
 
-__device__ __forceinline__ void raise_error(volatile uint32_t* abort_flag, unsigned* status,
-                                            unsigned code) {
-  *abort_flag = 1u;
-  atomicOr(status, code);
-}
-
 // CM = CTAs per cluster along M: 1, or 2 for a pair.
 // PAIR (CM = 2): the two CTAs of a cluster compute the tiles (m, n) and (m + 1, n)
 // as one M = 256 pair MMA issued by the even CTA ("leader"): each CTA loads its A

@@ -150,6 +150,26 @@ int64_t rmsnorm_bwd_partials(int64_t M, int64_t H);
 cudaError_t launch_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd,
                                    const uint16_t* dy, const uint16_t* dres, int64_t M, int64_t H,
                                    uint16_t* dh, float* dgamma, float* part, cudaStream_t stream);
+struct Fp8GemmParams {
+  const float* sx;      // [nkb, M]
+  const float* sw;      // [ceil(N/128), nkb]
+  const uint16_t* add;  // BF16 [M, N] added before the cast, or null (may alias out)
+  unsigned* status;     // device status word
+  int M, N, nkb;        // out [M, N], nkb = ceil(K/128)
+  int num_m, num_n;     // tile grid
+  int band_mc;          // tile order, as in GemmParams
+};
+struct Fp8GemmLaunch {
+  // U8 maps over X [M, K] and W [N, K], boxes of 128 columns and 128 rows, 128-byte
+  // swizzle; the BF16 output [M, N], boxes of 32 x 32, 64-byte swizzle
+  CUtensorMap tmX, tmW, tmOut;
+  Fp8GemmParams p;
+  int64_t K;
+  int num_sms;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmLaunch& L, cudaStream_t stream);
+// Whether a product of this shape runs on launch_fp8_few.
+bool fp8_is_few(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
                            int64_t M, int64_t N, int64_t K, const uint16_t* add, uint16_t* out,
                            cudaStream_t stream);
