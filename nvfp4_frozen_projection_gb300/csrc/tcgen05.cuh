@@ -85,6 +85,11 @@ __device__ __forceinline__ void mbar_arrive_cta_relaxed(uint32_t bar, uint32_t c
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra)
                : "memory");
 }
+// The same at a shared::cluster address (cluster_addr).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t ra) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra)
+               : "memory");
+}
 
 // A 32-bit load from the shared memory of CTA `cta` of the cluster at this CTA-local
 // address (distributed shared memory).
@@ -107,6 +112,25 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
       : "r"(bar), "r"(parity), "r"(kWaitSuspendNs)
       : "memory");
   return ok != 0;
+}
+
+// Whether the phases of two barriers with these parities have completed, without
+// suspending the thread.  One question alone takes about 135 cycles (GB300); asked
+// together they overlap.  Bit 0: the first, bit 1: the second.
+__device__ __forceinline__ uint32_t mbar_test_two(uint32_t bar0, uint32_t par0, uint32_t bar1,
+                                                  uint32_t par1) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "selp.u32 t, 2, 0, q;\n\t"
+      "or.b32 %0, %0, t;\n\t}"
+      : "=&r"(r)
+      : "r"(bar0), "r"(par0), "r"(bar1), "r"(par1)
+      : "memory");
+  return r;
 }
 
 __device__ __forceinline__ uint64_t global_timer_ns() {
@@ -145,6 +169,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
+// Move registers between the warpgroups of a CTA: every warp of a warpgroup executes one
+// of these.  The shares of all warpgroups together must not exceed what the CTA was
+// launched with.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // A wait gave up: tell the CTA's other roles and record it in the device status word.
 __device__ __forceinline__ void raise_error(volatile uint32_t* abort_flag, unsigned* status,
                                             unsigned code) {
@@ -160,6 +196,24 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
+}
+
+// A load into this CTA's shared memory that signals a barrier of either CTA of its pair
+// (bar: a shared::cluster address, see cluster_addr).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0,
+                                                 int32_t c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+// The shared::cluster address of this CTA-local address in CTA `cta` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t cta) {
+  uint32_t ra;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(local), "r"(cta));
+  return ra;
 }
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -184,6 +238,30 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           "r"(dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// cp.async copies into shared memory; src_bytes = 0 writes zeros instead of reading.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // TMA store of a 2-D box from shared memory (bulk-group completion).
@@ -374,6 +452,24 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// tmem_ld_wait with the registers of two loads of 32 columns as operands, so that nothing
+// computed from them can be moved ahead of the wait.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t* v, uint32_t* w) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+        "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+        "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]),
+        "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]),
+        "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]),
+        "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]), "+r"(w[4]), "+r"(w[5]), "+r"(w[6]),
+        "+r"(w[7]), "+r"(w[8]), "+r"(w[9]), "+r"(w[10]), "+r"(w[11]), "+r"(w[12]), "+r"(w[13]),
+        "+r"(w[14]), "+r"(w[15]), "+r"(w[16]), "+r"(w[17]), "+r"(w[18]), "+r"(w[19]),
+        "+r"(w[20]), "+r"(w[21]), "+r"(w[22]), "+r"(w[23]), "+r"(w[24]), "+r"(w[25]),
+        "+r"(w[26]), "+r"(w[27]), "+r"(w[28]), "+r"(w[29]), "+r"(w[30]), "+r"(w[31])
+      :
+      : "memory");
 }
 
 // Store 8 / 16 / 32 consecutive 32-bit columns into this warp's 32 TMEM lanes.
