@@ -129,30 +129,36 @@ bool fp8_is_few(int64_t M, int64_t N, int64_t K) { return M <= 32; }
 // All 512 TMEM columns pass once per round of MMA, commit, the epilogue's wait, its
 // loads, its arrival and the issuer's wait, so a pair's 256 columns of a block are two
 // sub-blocks of 128 (64 rows of W from each CTA), freed one by one.
-//   warp 0     TMA producer: X and W tiles (128-byte rows, 128B swizzle) into the ring
-//              (in a pair, each CTA's copies signal the leader's barriers)
-//   warps 1-3  MMA issuers (in a pair, the leader's), warp 1 the TMEM allocator
-//   warps 4-11 epilogue: two warps per TMEM lane quarter, each half of the columns
-// The first warpgroup gives its registers to the epilogue (56 against 224 a thread): 128
-// sums and the slices in flight.
+//   warp 0      TMA producer: X and W tiles (128-byte rows, 128B swizzle) into the ring
+//               (in a pair, each CTA's copies signal the leader's barriers)
+//   warps 1-2   MMA issuers (in a pair, the leader's), warp 1 the TMEM allocator
+//   warp 3      the blocks' scales, up to 16 blocks ahead, into a ring of their own
+//   warps 4-11  epilogue: two warps per TMEM lane quarter, each half of the columns
+// The first warpgroup gives its registers to the epilogue, whose threads hold 128 sums
+// and the columns that land.
+//
+// 8192 x 4096 x 8192 takes 203 us (2.7 PFLOP/s, 0.73 of twice the measured BF16 rate).
+// The same kernel without the additions takes 193 us and with one barrier round for 16
+// blocks instead of one 153: what is left is that round.  Measured and not kept, all at
+// this size: 16 epilogue warps of 64 columns (232 us), loads carried over from one block to
+// the next (238, it spills), an issuer and a barrier for each sub-block with epilogue
+// warps that take both sub-blocks (238) or one each (230).
 template <bool PAIR>
 struct Fp8Cfg {
   static constexpr int STAGES = 6;
   static constexpr int CM = PAIR ? 2 : 1;
   static constexpr int BN = PAIR ? 256 : 128;
   static constexpr int NSUB = PAIR ? 2 : 1;  // sub-blocks of a block
-  static constexpr int CYC = PAIR ? 2 : 3;  // blocks whose accumulators fit in TMEM
+  static constexpr int CYC = 2;              // blocks with accumulators in TMEM
   static constexpr int NBUF = CYC * NSUB;    // buffers of 128 columns
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = 128 * 128;  // 128 rows of W in this CTA's shared memory
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STG_OFF = STAGES * STAGE_BYTES;
-  static constexpr int STG_BUF = 2048;  // 32 rows x 32 BF16, 64-byte swizzled rows
-  static constexpr int NSTG = 1;
-  // ring of the scales, one slot per block: sx for each epilogue thread, sw for each warp
-  static constexpr int SCL_OFF = STG_OFF + 8 * NSTG * STG_BUF;
-  static constexpr int SCL_SLOT = 256 * 4 + 8 * 4;
-  static constexpr int SCL_DEPTH = 16;
+  // ring of the scales, one slot per block: sx of 128 rows, sw of the warps' two halves;
+  // one barrier for each half of the ring
+  static constexpr int SCL_OFF = STAGES * STAGE_BYTES;
+  static constexpr int SCL_SLOT = 128 * 4 + 16;
+  static constexpr int SCL_DEPTH = 16, SCL_HALF = SCL_DEPTH / 2;
   static constexpr int BAR_OFF = SCL_OFF + SCL_DEPTH * SCL_SLOT;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;  // + barriers + alignment slack
   static constexpr int THREADS = 384;
@@ -160,12 +166,14 @@ struct Fp8Cfg {
   // shares of the first and of the two epilogue warpgroups
   static constexpr int LAUNCH_REGS = 168, LOW_REGS = 56, EPI_REGS = 224;
   static_assert(LOW_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "register shares");
+  static constexpr int EPI_WARPS = 8;
   static constexpr int EPI_COLS = BN / 2;  // columns of an epilogue warp, 64 of a sub-block
   // An issuer takes every CYC-th block, so the blocks of one accumulator all come from one
   // thread: another's could be two rounds ahead, where a barrier's parity looks the same.
   static constexpr int ISSUERS = CYC;
-  // barriers: full[S], empty[S], acc_full[CYC], acc_empty[NBUF], final
-  static constexpr int NBARS = 2 * STAGES + CYC + NBUF + 1;
+  // barriers: full[S], empty[S], acc_full[CYC], acc_empty[NBUF], scl_full[2],
+  // scl_empty[2], final
+  static constexpr int NBARS = 2 * STAGES + CYC + NBUF + 5;
   static_assert(BAR_OFF % 8 == 0 && NBARS * 8 <= 504 && SMEM_BYTES <= 232448, "shared memory");
   static_assert(STAGES % CYC == 0 && NBUF * 128 <= 512, "buffers repeat with the ring");
   static_assert(STAGES % ISSUERS == 0, "issuers' turns repeat with the ring");
@@ -181,7 +189,7 @@ constexpr uint64_t kFp8WaitNs = 2000000000ull;  // 2 s per pipeline wait
 template <bool PAIR>
 __global__ void __launch_bounds__(384, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-               const __grid_constant__ CUtensorMap tmOut, const Fp8GemmParams p) {
+               const Fp8GemmParams p) {
   using C = Fp8Cfg<PAIR>;
   constexpr int STAGES = C::STAGES, CM = C::CM, BN = C::BN, NSUB = C::NSUB, NBUF = C::NBUF;
   extern __shared__ uint8_t smem_raw[];
@@ -190,7 +198,8 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* smem = smem_raw + (base - raw);
   const uint32_t full0 = base + C::BAR_OFF, empty0 = full0 + 8 * STAGES;
   const uint32_t accf0 = empty0 + 8 * STAGES, acce0 = accf0 + 8 * C::CYC;
-  const uint32_t final_bar = acce0 + 8 * NBUF;
+  const uint32_t sclf0 = acce0 + 8 * NBUF, scle0 = sclf0 + 16;
+  const uint32_t final_bar = scle0 + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 504);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 508);
 
@@ -215,7 +224,11 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int b = 0; b < C::CYC; ++b) mbar_init(accf0 + 8 * b, 1);
     // one arrival per epilogue warp of each CTA
-    for (int b = 0; b < NBUF; ++b) mbar_init(acce0 + 8 * b, 8 * CM);
+    for (int b = 0; b < NBUF; ++b) mbar_init(acce0 + 8 * b, C::EPI_WARPS * CM);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sclf0 + 8 * i, 32);  // the lanes of the scale warp
+      mbar_init(scle0 + 8 * i, C::EPI_WARPS);
+    }
     mbar_init(final_bar, C::ISSUERS);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -223,7 +236,6 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmOut);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -363,10 +375,8 @@ __global__ void __launch_bounds__(384, 1)
       };
       if (warp == 1)
         issue(std::integral_constant<int, 0>());
-      else if (warp == 2)
+      else
         issue(std::integral_constant<int, 1>());
-      else if (C::ISSUERS > 2)
-        issue(std::integral_constant<int, 2>());
       if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
       // every MMA issued by these threads has completed once final_bar flips
       if constexpr (PAIR)
@@ -375,166 +385,143 @@ __global__ void __launch_bounds__(384, 1)
         mma_commit(final_bar);
       mbar_wait(final_bar, 0, kFp8WaitNs, nullptr);
     }
+    if (warp == 3) {
+      // ---------------------------------------------------------- scales
+      // Loads by the epilogue threads themselves, three blocks ahead, held them up for
+      // 30 % of the kernel's time (220 us against 155, 8192 x 4096 x 8192): they queue
+      // behind the tiles' copies.  A barrier for each block cost the epilogue's wait
+      // another 7 % (221 against 206 us), so there is one for eight blocks.
+      uint32_t slot = 0, phase = 0;
+      bool ok = true;
+      for (int u = unit0; u < nunits && ok; u += nclusters) {
+        int m0, n0;
+        unit_mn(u, m0, n0);
+        // columns past N have no scale of their own: their sums are not stored
+        const float* psw = p.sw + (int64_t)(min(n0 + (lane & 1) * C::EPI_COLS, p.N - 1) >> 7) * p.nkb;
+        const float* psx = p.sx + m0 + lane;
+        for (int kb = 0; kb < p.nkb; ++kb, psx += p.M, ++psw) {
+          const uint32_t half = slot / C::SCL_HALF;
+          if (slot % C::SCL_HALF == 0 &&
+              !mbar_wait(scle0 + 8 * half, phase ^ 1u, kFp8WaitNs, abort_flag)) {
+            raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_SF);
+            ok = false;
+            break;
+          }
+          const uint32_t at = base + C::SCL_OFF + slot * C::SCL_SLOT;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = m0 + lane + 32 * i < p.M;  // rows past M: zero
+            cp_async4(at + 4 * (lane + 32 * i), in ? psx + 32 * i : p.sx, in ? 4u : 0u);
+          }
+          if (lane < 2) cp_async4(at + 512 + 4 * lane, psw, 4u);
+          if (slot % C::SCL_HALF == C::SCL_HALF - 1) cp_async_mbar_arrive(sclf0 + 8 * half);
+          if (++slot == C::SCL_DEPTH) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (slot % C::SCL_HALF) cp_async_mbar_arrive(sclf0 + 8 * (slot / C::SCL_HALF));
+      cp_async_commit();
+      cp_async_wait<0>();
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     setmaxnreg_inc<C::EPI_REGS>();
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
-    const int ew = warp - 4;
-    const int c0 = (ew >> 2) * C::EPI_COLS;
-    const uint32_t stg = base + C::STG_OFF + (uint32_t)(ew * C::NSTG * C::STG_BUF);
-    const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((ew >> 2) * 64);
-    int cyc = 0;
-    uint32_t aphase = 0, nstore = 0;
+    const int q = warp & 3;            // TMEM lane quarter this warp may access
+    const int half = (warp - 4) >> 2;  // which half of the columns
+    const int c0 = half * C::EPI_COLS;
+    const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 64);
+    // blocks so far, from which the buffer, the ring slot and their parities follow (one
+    // register: the sums and slices leave few)
+    uint32_t blk = 0;
     bool ok = true;
     const uint32_t acce = PAIR ? cluster_addr(acce0, 0) : acce0;  // at the leader
-    // The scales of the blocks to come, copied into the ring 15 blocks ahead, across tiles
-    // too.  Loads into registers three blocks ahead held the epilogue up for 30 % of the
-    // kernel's time (220 us against 155 without, 8192 x 4096 x 8192): they queue behind
-    // the tiles' copies.
-    const uint32_t scl = base + C::SCL_OFF;
-    const uint32_t my_sx = 4u * (uint32_t)(threadIdx.x - 128), my_sw = 1024u + 4u * (uint32_t)ew;
-    int pu = unit0, pkb = 0;
-    uint32_t pslot = 0, psize = 0;
-    const float *psx = p.sx, *psw = p.sw;
-    auto fetch = [&]() {
-      if (pu < nunits) {
-        if (pkb == 0) {
-          int m0, n0;
-          unit_mn(pu, m0, n0);
-          const int m = m0 + q * 32 + lane;
-          psize = m < p.M ? 4u : 0u;  // rows past M: zero
-          psx = p.sx + (m < p.M ? m : 0);
-          // columns past N have no scale of their own: their sums are not stored
-          psw = p.sw + (int64_t)(min(n0 + c0, p.N - 1) >> 7) * p.nkb;
-        }
-        cp_async4(scl + pslot + my_sx, psx, psize);
-        cp_async4(scl + pslot + my_sw, psw, 4u);
-        if (++pkb == p.nkb) {
-          pkb = 0;
-          pu += nclusters;
-        } else {
-          psx += p.M;
-          ++psw;
-        }
+    static_assert(C::CYC == 2 && C::SCL_DEPTH == 16 && C::SCL_HALF == 8, "bits of blk");
+    auto buf = [&]() { return blk & 1u; };
+    // the next block's accumulators and, for every eighth, scales
+    auto wait_block = [&]() {
+      if ((blk & 7u) == 0 && !mbar_wait(sclf0 + (blk & 8u), (blk >> 4) & 1u, kFp8WaitNs, abort_flag))
+        return false;
+      return mbar_wait(accf0 + 8 * buf(), (blk >> 1) & 1u, kFp8WaitNs, abort_flag);
+    };
+    auto scale = [&]() {
+      const uint32_t at = base + C::SCL_OFF + (blk & 15u) * C::SCL_SLOT;
+      const float s = __fmul_rn(ld_shared_f32(at + 4u * (uint32_t)(q * 32 + lane)),
+                                ld_shared_f32(at + 512u + 4u * (uint32_t)half));
+      if ((blk & 7u) == 7u) {  // that half of the ring has been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scle0 + (blk & 8u));
       }
-      cp_async_commit();
-      pslot = pslot == (C::SCL_DEPTH - 1) * C::SCL_SLOT ? 0u : pslot + C::SCL_SLOT;
+      return s;
     };
-    uint32_t slot = 0;
-    float f_sx, f_sw;  // of the next block
-    auto next_scales = [&]() {
-      cp_async_wait<C::SCL_DEPTH - 2>();
-      f_sx = ld_shared_f32(scl + slot + my_sx);
-      f_sw = ld_shared_f32(scl + slot + my_sw);
-      slot = slot == (C::SCL_DEPTH - 1) * C::SCL_SLOT ? 0u : slot + C::SCL_SLOT;
-      fetch();  // into the slot read one block ago
-    };
-    for (int i = 0; i < C::SCL_DEPTH - 1; ++i) fetch();
-    next_scales();
     for (int u = unit0; u < nunits && ok; u += nclusters) {
       int m0, n0;
       unit_mn(u, m0, n0);
-      const int m = m0 + q * 32 + lane;
-      const bool row_ok = m < p.M;
-      const bool blk_live = m0 + q * 32 < p.M;
       float2 acc[C::EPI_COLS / 2];
 #pragma unroll
       for (int i = 0; i < C::EPI_COLS / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      for (int kb = 0; kb < p.nkb; ++kb) {
-        const float s = __fmul_rn(f_sx, f_sw);
-        const float2 s2 = make_float2(s, s);
-        if (!mbar_wait(accf0 + 8 * cyc, aphase, kFp8WaitNs, abort_flag)) {
-          raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        auto release = [&](int h) {  // buffer h of the block: its columns have landed
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR)
-              mbar_arrive_remote_relaxed(acce + 8 * (cyc * NSUB + h));
-            else
-              mbar_arrive(acce + 8 * (cyc * NSUB + h));
-          }
-        };
-        auto add = [&](int c, const uint32_t* v) {  // columns 32 c .. 32 c + 31
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[16 * c + i] = __ffma2_rn(
-                make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2,
-                acc[16 * c + i]);
-        };
-        const uint32_t tb = tq + (uint32_t)(cyc * NSUB * 128);
-        uint32_t v[32], w[32];
-        tmem_ld32(tb, v);
-        tmem_ld32(tb + 32, w);
-        tmem_ld_wait(v, w);
-        release(0);
-        if constexpr (NSUB == 2) {
-          // the second sub-block lands while the first is added
-          add(0, v);
-          tmem_ld32(tb + 128, v);
-          add(1, w);
-          tmem_ld32(tb + 160, w);
-          tmem_ld_wait(v, w);
-          release(1);
-        }
-        next_scales();
-        add(2 * NSUB - 2, v);
-        add(2 * NSUB - 1, w);
-        if (++cyc == C::CYC) {
-          cyc = 0;
-          aphase ^= 1u;
-        }
-      }
-      if (!ok) break;
-#pragma unroll
-      for (int ch = 0; ch < C::EPI_COLS / 32; ++ch) {
-        const int n = n0 + c0 + 32 * ch;
-        if (n >= p.N || !blk_live) continue;  // uniform across the warp
-        uint32_t o[16];
-        if (p.add && row_ok) {
-          const uint16_t* ap = p.add + (int64_t)m * p.N + n;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // N % 16 == 0: a vector of 8 columns lies inside or outside whole
-            uint4 a = make_uint4(0u, 0u, 0u, 0u);
-            if (n + 8 * k < p.N) a = *reinterpret_cast<const uint4*>(ap + 8 * k);
-            o[4 * k] = a.x;
-            o[4 * k + 1] = a.y;
-            o[4 * k + 2] = a.z;
-            o[4 * k + 3] = a.w;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[16 * ch + i] = __fadd2_rn(
-                acc[16 * ch + i], make_float2(__uint_as_float(o[i] << 16),
-                                              __uint_as_float(o[i] & 0xFFFF0000u)));
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = pack_bf16x2(acc[16 * ch + i].x, acc[16 * ch + i].y);
-        const uint32_t sb = stg + (nstore % C::NSTG) * C::STG_BUF;
-        if (nstore >= (uint32_t)C::NSTG && lane == 0) bulk_wait_read<C::NSTG - 1>();
-        __syncwarp();
-        uint8_t* row = smem + (sb - base) + 64 * lane;
-        const uint32_t sw = (uint32_t)(lane >> 1) & 3u;  // 64-byte swizzle of the store's map
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(row + 16 * (k ^ sw)) =
-              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        fence_proxy_async_smem();
+      auto release = [&](int h) {  // buffer h of the block: its columns have landed
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&tmOut, sb, n, m0 + q * 32);  // clips rows past M and columns past N
-          bulk_commit();
+          if constexpr (PAIR)
+            mbar_arrive_remote_relaxed(acce + 8 * (buf() * NSUB + h));
+          else
+            mbar_arrive(acce + 8 * (buf() * NSUB + h));
         }
-        ++nstore;
+      };
+      for (int kb = 0; kb < p.nkb; ++kb, ++blk) {
+        if (!(ok = wait_block())) break;
+        tc_fence_after();
+        const uint32_t tb = tq + buf() * (NSUB * 128);
+        uint32_t v[2][16];
+        tmem_ld16(tb, v[0]);
+        const float s = scale();
+#pragma unroll
+        for (int c = 0; c < C::EPI_COLS / 16; ++c) {
+          tmem_ld_wait16(v[c & 1]);
+          if (c + 1 < C::EPI_COLS / 16)  // the next slice lands while this one is added
+            tmem_ld16(tb + (c + 1) / 4 * 128 + (c + 1) % 4 * 16, v[(c + 1) & 1]);
+          if (c % 4 == 3) release(c / 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc[8 * c + i] =
+                __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]),
+                                       __uint_as_float(v[c & 1][2 * i + 1])),
+                           make_float2(s, s), acc[8 * c + i]);
+        }
+      }
+      if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
+      if (!ok) break;
+      // a lane stores its own row, 16 columns (whole sectors) at a time
+      const int64_t m = m0 + q * 32 + lane;
+      if (m >= p.M) continue;
+#pragma unroll
+      for (int c = 0; c < C::EPI_COLS / 16; ++c) {
+        const int n = n0 + c0 + 16 * c;
+        if (n >= p.N) break;  // N % 16 == 0: 16 columns lie inside or outside whole
+        const int64_t at = m * p.N + n;
+        if (p.add) {
+          const uint4 a[2] = {*reinterpret_cast<const uint4*>(p.add + at),
+                              *reinterpret_cast<const uint4*>(p.add + at + 8)};
+          const uint32_t* o = reinterpret_cast<const uint32_t*>(a);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc[8 * c + i] = __fadd2_rn(acc[8 * c + i],
+                                        make_float2(__uint_as_float(o[i] << 16),
+                                                    __uint_as_float(o[i] & 0xFFFF0000u)));
+        }
+        uint4 o[2];
+        uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ow[i] = pack_bf16x2(acc[8 * c + i].x, acc[8 * c + i].y);
+        if (PACT_IN(at + 16 <= (int64_t)p.M * p.N)) {
+          *reinterpret_cast<uint4*>(p.out + at) = o[0];
+          *reinterpret_cast<uint4*>(p.out + at + 8) = o[1];
+        }
       }
     }
-    cp_async_wait<0>();
-    if (lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -603,7 +590,7 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, cudaStream_t stream) {
     p.band_mc = b < 1 ? 1 : (b > num_mc ? num_mc : b);
   }
   note_launch();
-  return cudaLaunchKernelEx(&cfg, kern, L.tmX, L.tmW, L.tmOut, p);
+  return cudaLaunchKernelEx(&cfg, kern, L.tmX, L.tmW, p);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch& L, cudaStream_t stream) {
