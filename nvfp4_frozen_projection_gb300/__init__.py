@@ -222,8 +222,18 @@ class FP8Weight(FP8):
         return (rows + 127) // 128, (cols + 127) // 128
 
 
+# The FP8 calls also serve single tokens, where a launch takes 3 us: their checks and the
+# look-up of the stream are kept below that (torch.cuda.current_stream() alone takes 3).
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _need(t, dtype, shape, name, dev):
     """t is a contiguous tensor of this dtype and shape on the current device dev."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -232,15 +242,14 @@ def _need(t, dtype, shape, name, dev):
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device.index != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def _need_fp8(t, kind, name, dev, shape=None):
     """t is an FP8 tensor of this kind (FP8 or FP8Weight), of this shape when given."""
     if type(t) is not kind:
         raise ValueError(f"{name} must be an {kind.__name__}, got {type(t).__name__}")
-    shape = shape or _need_2d(t.q, name + ".q")
+    shape = tuple(shape or _need_2d(t.q, name + ".q"))
     _need(t.q, torch.float8_e4m3fn, shape, name + ".q", dev)
     _need(t.s, torch.float32, kind.scale_shape(*shape), name + ".s", dev)
 
@@ -248,7 +257,11 @@ def _need_fp8(t, kind, name, dev, shape=None):
 def _need_2d(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return tuple(t.shape)
+    return t.shape
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 # ------------------------------------------------------------------ workspace
@@ -527,7 +540,7 @@ def pact_rmsnorm_bwd(yq: NVFP4, gamma: torch.Tensor, rstd: torch.Tensor, dy: tor
 # ------------------------------------------------------------------ FP8, blocks of 128
 def pact_quant_fp8(x: torch.Tensor, out: FP8 | None = None) -> FP8:
     """Quantise BF16 x [M, K] (row stride may exceed K) to FP8."""
-    lib = load_library()
+    lib = _LIB or load_library()
     M, K = _need_2d(x, "x")
     if x.dtype != torch.bfloat16:
         raise ValueError(f"x must be torch.bfloat16, got {x.dtype}")
@@ -541,13 +554,13 @@ def pact_quant_fp8(x: torch.Tensor, out: FP8 | None = None) -> FP8:
     _need_fp8(out, FP8, "out", dev, (M, K))
     s = out.struct()
     # the stride of a single row says nothing: torch may report any number there
-    _check(lib.pact_quant_fp8(_ptr(x), M, K, x.stride(0) if M > 1 else _pad(K, 8),
-                              ctypes.byref(s), _stream()))
+    _check(lib.pact_quant_fp8(_addr(x), M, K, x.stride(0) if M > 1 else _pad(K, 8),
+                              ctypes.byref(s), _raw_stream(dev)))
     return out
 
 
 def _pack_fp8(W: torch.Tensor, backward: bool, out: FP8Weight | None) -> FP8Weight:
-    lib = load_library()
+    lib = _LIB or load_library()
     N, K = _need_2d(W, "W")
     dev = torch.cuda.current_device()
     _need(W, torch.float32, (N, K), "W", dev)
@@ -557,7 +570,7 @@ def _pack_fp8(W: torch.Tensor, backward: bool, out: FP8Weight | None) -> FP8Weig
     _need_fp8(out, FP8Weight, "out", dev, shape)
     s = out.struct()
     fn = lib.pact_pack_weight_fp8_bwd if backward else lib.pact_pack_weight_fp8_fwd
-    _check(fn(_ptr(W), N, K, ctypes.byref(s), _stream()))
+    _check(fn(_addr(W), N, K, ctypes.byref(s), _raw_stream(dev)))
     return out
 
 
@@ -588,7 +601,7 @@ def _linear_fp8(fn, x, xname, w, wname, add, addname, y, yname):
     if add is not None:
         _need(add, torch.bfloat16, shape, addname, dev)
     sx, sw = x.struct(), w.struct()
-    _check(fn(ctypes.byref(sx), ctypes.byref(sw), _ptr(add), _ptr(y), _stream()))
+    _check(fn(ctypes.byref(sx), ctypes.byref(sw), _addr(add), _addr(y), _raw_stream(dev)))
     return y
 
 
@@ -596,7 +609,7 @@ def pact_linear_fp8_fwd(xq: FP8, w_fwd: FP8Weight, residual: torch.Tensor | None
                         y: torch.Tensor | None = None) -> torch.Tensor:
     """Y = Xhat What^T [+ residual], BF16 [M, N]; any M from one token up.  residual may
     be y itself."""
-    return _linear_fp8(load_library().pact_linear_fp8_fwd, xq, "xq", w_fwd, "w_fwd", residual,
+    return _linear_fp8((_LIB or load_library()).pact_linear_fp8_fwd, xq, "xq", w_fwd, "w_fwd", residual,
                        "residual", y, "y")
 
 
@@ -604,7 +617,7 @@ def pact_linear_fp8_dgrad(dyq: FP8, w_bwd: FP8Weight, dx_prev: torch.Tensor | No
                           dx: torch.Tensor | None = None) -> torch.Tensor:
     """dX = dYhat W [+ dX_prev], BF16 [M, K], on the backward layout.  dx_prev may be dx
     itself, to add to it."""
-    return _linear_fp8(load_library().pact_linear_fp8_dgrad, dyq, "dyq", w_bwd, "w_bwd", dx_prev,
+    return _linear_fp8((_LIB or load_library()).pact_linear_fp8_dgrad, dyq, "dyq", w_bwd, "w_bwd", dx_prev,
                        "dx_prev", dx, "dx")
 
 
@@ -614,7 +627,7 @@ def pact_add_rmsnorm_quant_fp8(x: torch.Tensor, residual: torch.Tensor | None,
                                rstd: torch.Tensor | None = None):
     """h = bf16(x + residual), RMSNorm of h to FP8.  Without a residual h is x itself.
     h may be x or residual, to add in place.  Returns (h, yq, rstd)."""
-    lib = load_library()
+    lib = _LIB or load_library()
     M, H = _need_2d(x, "x")
     dev = torch.cuda.current_device()
     _need(x, torch.bfloat16, (M, H), "x", dev)
@@ -633,9 +646,9 @@ def pact_add_rmsnorm_quant_fp8(x: torch.Tensor, residual: torch.Tensor | None,
         rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
     _need(rstd, torch.float32, (M,), "rstd", dev)
     s = out.struct()
-    _check(lib.pact_add_rmsnorm_quant_fp8(_ptr(x), _ptr(residual), _ptr(gamma), M, H, float(eps),
-                                          _ptr(h) if residual is not None else None,
-                                          ctypes.byref(s), _ptr(rstd), _stream()))
+    _check(lib.pact_add_rmsnorm_quant_fp8(_addr(x), _addr(residual), _addr(gamma), M, H, float(eps),
+                                          _addr(h) if residual is not None else None,
+                                          ctypes.byref(s), _addr(rstd), _raw_stream(dev)))
     return (x if residual is None else h), out, rstd
 
 
@@ -646,7 +659,7 @@ def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tenso
     """Backward of pact_add_rmsnorm_quant_fp8 from h and rstd: dh [+ dres], the gradient
     of x and of the residual alike (dh may be dy or dres).  dgamma: an FP32 [H] tensor
     to overwrite, True for a new one, None to leave it out.  Returns (dh, dgamma)."""
-    lib = load_library()
+    lib = _LIB or load_library()
     M, H = _need_2d(h, "h")
     dev = torch.cuda.current_device()
     _need(h, torch.bfloat16, (M, H), "h", dev)
@@ -668,9 +681,9 @@ def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tenso
         # its own scratch in every call: a captured graph then keeps one of its own
         ws = torch.empty((lib.pact_add_rmsnorm_bwd_workspace_size(M, H),), dtype=torch.uint8,
                          device=h.device)
-    _check(lib.pact_add_rmsnorm_bwd(_ptr(h), _ptr(gamma), _ptr(rstd), _ptr(dy), _ptr(dres), M, H,
-                                    _ptr(dh), _ptr(dgamma), _ptr(ws),
-                                    0 if ws is None else ws.numel(), _stream()))
+    _check(lib.pact_add_rmsnorm_bwd(_addr(h), _addr(gamma), _addr(rstd), _addr(dy), _addr(dres), M, H,
+                                    _addr(dh), _addr(dgamma), _addr(ws),
+                                    0 if ws is None else ws.numel(), _raw_stream(dev)))
     return dh, dgamma
 
 
