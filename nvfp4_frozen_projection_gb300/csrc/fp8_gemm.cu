@@ -458,6 +458,13 @@ __global__ void __launch_bounds__(384, 1)
     for (int u = unit0; u < nunits && ok; u += nclusters) {
       int m0, n0;
       unit_mn(u, m0, n0);
+      const int64_t m = m0 + q * 32 + lane;
+      if (p.add && m < p.M) {  // the addend's row is in L2 when the sums are done
+#pragma unroll
+        for (int c = 0; c < C::EPI_COLS; c += 64)
+          if (n0 + c0 + c < p.N)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.add + m * p.N + n0 + c0 + c));
+      }
       float2 acc[C::EPI_COLS / 2];
 #pragma unroll
       for (int i = 0; i < C::EPI_COLS / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -494,31 +501,36 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
       if (!ok) break;
-      // a lane stores its own row, 16 columns (whole sectors) at a time
-      const int64_t m = m0 + q * 32 + lane;
+      // a lane stores its own row, whole sectors (16 columns) at a time; the addend comes
+      // 64 columns at a time
       if (m >= p.M) continue;
+      const int64_t at = m * p.N + n0 + c0;
+      const int live = min(p.N - n0 - c0, C::EPI_COLS);  // columns inside the output
 #pragma unroll
-      for (int c = 0; c < C::EPI_COLS / 16; ++c) {
-        const int n = n0 + c0 + 16 * c;
-        if (n >= p.N) break;  // N % 16 == 0: 16 columns lie inside or outside whole
-        const int64_t at = m * p.N + n;
+      for (int b = 0; b < C::EPI_COLS / 64; ++b) {
+        uint4 a[8];
         if (p.add) {
-          const uint4 a[2] = {*reinterpret_cast<const uint4*>(p.add + at),
-                              *reinterpret_cast<const uint4*>(p.add + at + 8)};
-          const uint32_t* o = reinterpret_cast<const uint32_t*>(a);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[8 * c + i] = __fadd2_rn(acc[8 * c + i],
-                                        make_float2(__uint_as_float(o[i] << 16),
-                                                    __uint_as_float(o[i] & 0xFFFF0000u)));
+          for (int k = 0; k < 8; ++k) {
+            a[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (64 * b + 8 * k < live)  // N % 16 == 0: eight columns lie inside or outside whole
+              a[k] = *reinterpret_cast<const uint4*>(p.add + at + 64 * b + 8 * k);
+          }
         }
-        uint4 o[2];
-        uint32_t* ow = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ow[i] = pack_bf16x2(acc[8 * c + i].x, acc[8 * c + i].y);
-        if (PACT_IN(at + 16 <= (int64_t)p.M * p.N)) {
-          *reinterpret_cast<uint4*>(p.out + at) = o[0];
-          *reinterpret_cast<uint4*>(p.out + at + 8) = o[1];
+        for (int k = 0; k < 8; ++k) {
+          float2* f = acc + 32 * b + 4 * k;
+          if (p.add) {
+            const uint32_t w[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              f[i] = __fadd2_rn(f[i], make_float2(__uint_as_float(w[i] << 16),
+                                                  __uint_as_float(w[i] & 0xFFFF0000u)));
+          }
+          if (64 * b + 8 * k < live && PACT_IN(at + 64 * b + 8 * k + 8 <= (int64_t)p.M * p.N))
+            *reinterpret_cast<uint4*>(p.out + at + 64 * b + 8 * k) =
+                make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                           pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
         }
       }
     }

@@ -156,23 +156,45 @@ cudaError_t launch_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const
 }
 
 // ---------------------------------------------------------------- backward
-// A persistent grid: a thread owns the same columns in every row, so dgamma's partial
-// sums stay in its registers; each group writes one row of partial sums at the end,
-// and a second kernel adds them in a fixed order.
-constexpr int kBwdCtas = 304;
+// A persistent grid: a thread owns the same columns in every row, so gamma and dgamma's
+// partial sums stay in its registers; each group writes one row of partial sums at the
+// end, and a second kernel adds them in a fixed order.  The next row's vectors are loaded
+// before this row is worked on: without that a row's three latencies (the loads, the sum
+// over the group, dres) add up (8192 x 4096: 110 us, 2.4 TB/s).
+// As row_plan, with at most two vectors a thread, since two rows are held at a time; above
+// 8192 columns four and one row.
+static RowPlan bwd_plan(int64_t M, int64_t H) {
+  RowPlan p;
+  p.wpr = 1;
+  const int64_t per_warp = H > 8192 ? 1024 : 512;
+  while (H > (int64_t)p.wpr * per_warp) p.wpr *= 2;
+  while (p.wpr < 8 && H > (int64_t)p.wpr * 256 && M * p.wpr < 2048) p.wpr *= 2;
+  p.nv = (int)((H + p.wpr * 256 - 1) / (p.wpr * 256));
+  p.threads = p.wpr > 8 ? 32 * p.wpr : 256;
+  p.groups = p.threads / (32 * p.wpr);
+  return p;
+}
 
 static int bwd_ctas(int64_t M, const RowPlan& p) {
   const int64_t n = (M + p.groups - 1) / p.groups;
-  return (int)(n < kBwdCtas ? n : kBwdCtas);
+  const int most = 152 * (p.threads > 256 ? 1 : (p.nv == 1 ? 3 : 2));  // resident at once
+  return (int)(n < most ? n : most);
 }
 
 int64_t rmsnorm_bwd_partials(int64_t M, int64_t H) {
-  const RowPlan p = row_plan(M, H);
+  const RowPlan p = bwd_plan(M, H);
   return (int64_t)bwd_ctas(M, p) * p.groups;
 }
 
-template <int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+template <int NV>
+struct BwdRow {
+  uint4 h[NV], dy[NV], dres[NV];
+  float rstd;
+};
+
+// AHEAD: the next row is loaded before this one is worked on.
+template <int NV, int THREADS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2))
     k_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd_in,
                       const uint16_t* dy, const uint16_t* dres, int64_t M, int64_t H, int wpr,
                       uint16_t* dh, float* part) {
@@ -181,62 +203,69 @@ __global__ void __launch_bounds__(THREADS)
   const int group = warp / wpr, wl = warp - group * wpr;
   const int groups = (THREADS / 32) / wpr;
   const float inv_h = __fdiv_rn(1.0f, (float)H);
+  const int c0 = (wl * 32 + lane) * 8, cstep = wpr * 256;  // vector i: column c0 + i cstep
+  uint4 gv[NV];
   float dg[NV][8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    gv[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c0 + i * cstep < H) gv[i] = *reinterpret_cast<const uint4*>(gamma + c0 + i * cstep);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[i][e] = 0.0f;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * groups + group; row < M;
-       row += (int64_t)gridDim.x * groups) {
-    const int64_t base = row * H;
-    uint4 hv[NV], dv[NV];
+  }
+  auto load = [&](int64_t row, BwdRow<NV>& r) {
+    r.rstd = rstd_in[row];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
-      hv[i] = dv[i] = make_uint4(0u, 0u, 0u, 0u);
+      r.h[i] = r.dy[i] = r.dres[i] = make_uint4(0u, 0u, 0u, 0u);
+      const int c = c0 + i * cstep;
       if (c < H) {
-        hv[i] = *reinterpret_cast<const uint4*>(h + base + c);
-        dv[i] = *reinterpret_cast<const uint4*>(dy + base + c);
+        r.h[i] = *reinterpret_cast<const uint4*>(h + row * H + c);
+        r.dy[i] = *reinterpret_cast<const uint4*>(dy + row * H + c);
+        if (dres) r.dres[i] = *reinterpret_cast<const uint4*>(dres + row * H + c);
       }
     }
-    const float rstd = rstd_in[row];
+  };
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  BwdRow<NV> cur;
+  if (row < M) load(row, cur);
+  for (; row < M; row += step) {
+    BwdRow<NV> next;
+    if constexpr (AHEAD) {
+      if (row + step < M) load(row + step, next);
+    }
     float t = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
-      uint4 gv = make_uint4(0u, 0u, 0u, 0u);
-      if (c < H) gv = *reinterpret_cast<const uint4*>(gamma + c);
       float f[8], d[8], g[8];
-      bf16x8_to_f32(hv[i], f);
-      bf16x8_to_f32(dv[i], d);
-      bf16x8_to_f32(gv, g);
+      bf16x8_to_f32(cur.h[i], f);
+      bf16x8_to_f32(cur.dy[i], d);
+      bf16x8_to_f32(gv[i], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float n = __fmul_rn(f[e], rstd);
+        const float n = __fmul_rn(f[e], cur.rstd);
         t = __fmaf_rn(__fmul_rn(d[e], g[e]), n, t);
         dg[i][e] = __fmaf_rn(d[e], n, dg[i][e]);
       }
     }
     t = group_sum(t, wpr, wl, group, slots[turn] + group * wpr);
     turn ^= 1;
-    const float c0 = __fmul_rn(t, inv_h);
+    const float c = __fmul_rn(t, inv_h);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
-      if (c >= H) continue;
-      const uint4 gv = *reinterpret_cast<const uint4*>(gamma + c);
-      uint4 rv = make_uint4(0u, 0u, 0u, 0u);
-      if (dres) rv = *reinterpret_cast<const uint4*>(dres + base + c);
+      const int col = c0 + i * cstep;
+      if (col >= H) continue;
       float f[8], d[8], g[8], r[8];
-      bf16x8_to_f32(hv[i], f);
-      bf16x8_to_f32(dv[i], d);
-      bf16x8_to_f32(gv, g);
-      bf16x8_to_f32(rv, r);
+      bf16x8_to_f32(cur.h[i], f);
+      bf16x8_to_f32(cur.dy[i], d);
+      bf16x8_to_f32(gv[i], g);
+      bf16x8_to_f32(cur.dres[i], r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float n = __fmul_rn(f[e], rstd);
-        f[e] = __fmaf_rn(rstd, __fmaf_rn(-n, c0, __fmul_rn(d[e], g[e])), r[e]);
+        const float n = __fmul_rn(f[e], cur.rstd);
+        f[e] = __fmaf_rn(cur.rstd, __fmaf_rn(-n, c, __fmul_rn(d[e], g[e])), r[e]);
       }
       const uint4 o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
@@ -244,34 +273,52 @@ __global__ void __launch_bounds__(THREADS)
       PACT_NAN_BF16X2(o.y);
       PACT_NAN_BF16X2(o.z);
       PACT_NAN_BF16X2(o.w);
-      if (PACT_IN(base + c + 8 <= M * H)) *reinterpret_cast<uint4*>(dh + base + c) = o;
+      if (PACT_IN(row * H + col + 8 <= M * H)) *reinterpret_cast<uint4*>(dh + row * H + col) = o;
     }
+    if constexpr (AHEAD)
+      cur = next;
+    else if (row + step < M)
+      load(row + step, cur);
   }
   if (!part) return;
   float* p = part + ((int64_t)blockIdx.x * groups + group) * H;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
+    const int c = c0 + i * cstep;
     if (c >= H) continue;
     *reinterpret_cast<float4*>(p + c) = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
     *reinterpret_cast<float4*>(p + c + 4) = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
   }
 }
 
-// dgamma[j] = sum over P rows of part, 16 row lanes per column, each in row order.
+// dgamma[j] = sum over the P rows of part: 8 columns (a sector) a CTA, 64 row lanes, each
+// in row order with eight loads in flight, then the lanes in order.
 __global__ void __launch_bounds__(512)
     k_dgamma_reduce(const float* part, int P, int64_t H, float* dgamma) {
-  __shared__ float sum[16][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t j = (int64_t)blockIdx.x * 32 + tx;
+  __shared__ float sum[64][9];
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+  const int64_t j = (int64_t)blockIdx.x * 8 + tx;  // H % 16 == 0
   float t = 0.0f;
-  if (j < H)
-    for (int p = ty; p < P; p += 16) t += part[(int64_t)p * H + j];
+  for (int p = ty; p < P; p += 8 * 64) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p + 64 * i < P ? part[(int64_t)(p + 64 * i) * H + j] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += v[i];
+  }
   sum[ty][tx] = t;
   __syncthreads();
-  if (ty == 0 && j < H) {
+  if (ty < 8) {
+    t = sum[8 * ty][tx];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) t += sum[i][tx];
+    for (int i = 1; i < 8; ++i) t += sum[8 * ty + i][tx];
+    sum[8 * ty][tx] = t;
+  }
+  __syncthreads();
+  if (ty == 0) {
+    t = sum[0][tx];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += sum[8 * i][tx];
     dgamma[j] = t;
   }
 }
@@ -279,28 +326,27 @@ __global__ void __launch_bounds__(512)
 cudaError_t launch_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd,
                                    const uint16_t* dy, const uint16_t* dres, int64_t M, int64_t H,
                                    uint16_t* dh, float* dgamma, float* part, cudaStream_t stream) {
-  const RowPlan p = row_plan(M, H);
+  const RowPlan p = bwd_plan(M, H);
   const int grid = bwd_ctas(M, p);
   float* pp = dgamma ? part : nullptr;
   note_launch();
-#define PACT_NORM(NV, T) \
-  k_add_rmsnorm_bwd<NV, T><<<grid, T, 0, stream>>>(h, gamma, rstd, dy, dres, M, H, p.wpr, dh, pp)
-  if (p.threads == 512) {
-    if (p.nv == 3) PACT_NORM(3, 512); else PACT_NORM(4, 512);
-  } else if (p.nv == 1) {
-    PACT_NORM(1, 256);
+#define PACT_NORM(NV, T, AHEAD)                                                              \
+  k_add_rmsnorm_bwd<NV, T, AHEAD>                                                            \
+      <<<grid, T, 0, stream>>>(h, gamma, rstd, dy, dres, M, H, p.wpr, dh, pp)
+  if (p.nv > 2) {
+    if (p.nv == 3) PACT_NORM(3, 512, false); else PACT_NORM(4, 512, false);
+  } else if (p.threads == 512) {
+    PACT_NORM(2, 512, true);
   } else if (p.nv == 2) {
-    PACT_NORM(2, 256);
-  } else if (p.nv == 3) {
-    PACT_NORM(3, 256);
+    PACT_NORM(2, 256, true);
   } else {
-    PACT_NORM(4, 256);
+    PACT_NORM(1, 256, true);
   }
 #undef PACT_NORM
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !dgamma) return e;
   note_launch();
-  k_dgamma_reduce<<<(unsigned)((H + 31) / 32), 512, 0, stream>>>(part, grid * p.groups, H, dgamma);
+  k_dgamma_reduce<<<(unsigned)(H / 8), 512, 0, stream>>>(part, grid * p.groups, H, dgamma);
   return cudaGetLastError();
 }
 
