@@ -742,8 +742,11 @@ static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, c
     if ((rc = make_map(&L.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x->q, K, M, 128, 128,
                        CU_TENSOR_MAP_SWIZZLE_128B)) ||
         (rc = make_map(&L.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->q, K, N, 128, 128,
-                       CU_TENSOR_MAP_SWIZZLE_128B)))
+                       CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        (rc = make_map(&L.tmOut, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, N, M, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_64B)))
       return rc;
+    L.p.add32 = add && aligned(add, 32);
     L.p.out = out;
     L.p.sx = x->s;
     L.p.sw = w->s;

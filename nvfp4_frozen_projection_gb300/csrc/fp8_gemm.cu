@@ -12,6 +12,7 @@
 #include "kernels.h"
 #include "tcgen05.cuh"
 
+#include <cstdlib>
 #include <type_traits>
 
 namespace pact {
@@ -159,7 +160,10 @@ struct Fp8Cfg {
   static constexpr int SCL_OFF = STAGES * STAGE_BYTES;
   static constexpr int SCL_SLOT = 128 * 4 + 16;
   static constexpr int SCL_DEPTH = 16, SCL_HALF = SCL_DEPTH / 2;
-  static constexpr int BAR_OFF = SCL_OFF + SCL_DEPTH * SCL_SLOT;
+  // output staging: per epilogue warp 32 rows x 32 BF16 columns, 64-byte swizzled rows
+  static constexpr int STG_OFF = (SCL_OFF + SCL_DEPTH * SCL_SLOT + 1023) / 1024 * 1024;
+  static constexpr int STG_BUF = 2048;
+  static constexpr int BAR_OFF = STG_OFF + 8 * STG_BUF;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;  // + barriers + alignment slack
   static constexpr int THREADS = 384;
   // registers a thread: at launch (65536 / 384 threads, a multiple of 8), and the
@@ -184,12 +188,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int n, int m) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+constexpr int kMaxSplit = 4;  // CTAs that share the blocks of one tile
 constexpr uint64_t kFp8WaitNs = 2000000000ull;  // 2 s per pipeline wait
 
-template <bool PAIR>
+template <bool PAIR, bool SPLIT, bool ADD>
 __global__ void __launch_bounds__(384, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-               const Fp8GemmParams p) {
+               const __grid_constant__ CUtensorMap tmOut, const Fp8GemmParams p) {
   using C = Fp8Cfg<PAIR>;
   constexpr int STAGES = C::STAGES, CM = C::CM, BN = C::BN, NSUB = C::NSUB, NBUF = C::NBUF;
   extern __shared__ uint8_t smem_raw[];
@@ -204,10 +209,16 @@ __global__ void __launch_bounds__(384, 1)
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 508);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(!(PAIR && SPLIT), "a cluster is a pair or shares the blocks of one tile");
   const uint32_t crank = PAIR ? cluster_ctarank() : 0u;
   const int num_mc = (p.num_m + CM - 1) / CM;
   const int nunits = num_mc * p.num_n;
-  const int unit0 = (int)blockIdx.x / CM, nclusters = (int)gridDim.x / CM;
+  const int csize = SPLIT ? p.split : CM;  // CTAs of a cluster
+  const int unit0 = (int)blockIdx.x / csize, nclusters = (int)gridDim.x / csize;
+  // the blocks of K that this CTA adds up
+  const uint32_t krank = SPLIT ? cluster_ctarank() : 0u;
+  const int kb0 = SPLIT ? (int)((int64_t)p.nkb * krank / p.split) : 0;
+  const int nk = (SPLIT ? (int)((int64_t)p.nkb * (krank + 1) / p.split) : p.nkb) - kb0;
   const int band = p.band_mc;
   auto unit_mn = [&](int u, int& m0, int& n0) {
     const int bi = u / (band * p.num_n), r = u - bi * band * p.num_n;
@@ -236,6 +247,7 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmOut);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(384, 1)
         int m0, n0;
         unit_mn(u, m0, n0);
         const int nb = n0 + (int)crank * 128;
-        for (int kb = 0; kb < p.nkb; ++kb) {
+        for (int kb = kb0; kb < kb0 + nk; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, kFp8WaitNs, abort_flag)) {
             ok = false;
             break;
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idesc = idesc_e4m3(128, 128 * CM);
       const uint64_t d0 = smem_desc(base, 16, 1024, 2);
       bool ok = true;
-      const int64_t blocks = (int64_t)my_units * p.nkb;
+      const int64_t blocks = (int64_t)my_units * nk;
       auto issue = [&](auto turn_c) {
         constexpr int turn = decltype(turn_c)::value;
         uint32_t pass = 0;
@@ -397,9 +409,10 @@ __global__ void __launch_bounds__(384, 1)
         int m0, n0;
         unit_mn(u, m0, n0);
         // columns past N have no scale of their own: their sums are not stored
-        const float* psw = p.sw + (int64_t)(min(n0 + (lane & 1) * C::EPI_COLS, p.N - 1) >> 7) * p.nkb;
-        const float* psx = p.sx + m0 + lane;
-        for (int kb = 0; kb < p.nkb; ++kb, psx += p.M, ++psw) {
+        const float* psw = p.sw + kb0 +
+                           (int64_t)(min(n0 + (lane & 1) * C::EPI_COLS, p.N - 1) >> 7) * p.nkb;
+        const float* psx = p.sx + (int64_t)kb0 * p.M + m0 + lane;
+        for (int kb = 0; kb < nk; ++kb, psx += p.M, ++psw) {
           const uint32_t half = slot / C::SCL_HALF;
           if (slot % C::SCL_HALF == 0 &&
               !mbar_wait(scle0 + 8 * half, phase ^ 1u, kFp8WaitNs, abort_flag)) {
@@ -424,6 +437,10 @@ __global__ void __launch_bounds__(384, 1)
       if (slot % C::SCL_HALF) cp_async_mbar_arrive(sclf0 + 8 * (slot / C::SCL_HALF));
       cp_async_commit();
       cp_async_wait<0>();
+    }
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_sync();  // the epilogue's partial sums
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -458,12 +475,14 @@ __global__ void __launch_bounds__(384, 1)
     for (int u = unit0; u < nunits && ok; u += nclusters) {
       int m0, n0;
       unit_mn(u, m0, n0);
-      const int64_t m = m0 + q * 32 + lane;
-      if (p.add && m < p.M) {  // the addend's row is in L2 when the sums are done
+      if constexpr (ADD) {  // the addend's rows are in L2 when the sums are done
+        const int64_t m = m0 + q * 32 + lane;
+        if (m < p.M) {
 #pragma unroll
-        for (int c = 0; c < C::EPI_COLS; c += 64)
-          if (n0 + c0 + c < p.N)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.add + m * p.N + n0 + c0 + c));
+          for (int c = 0; c < C::EPI_COLS; c += 64)
+            if (n0 + c0 + c < p.N)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(p.add + m * p.N + n0 + c0 + c));
+        }
       }
       float2 acc[C::EPI_COLS / 2];
 #pragma unroll
@@ -478,7 +497,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive(acce + 8 * (buf() * NSUB + h));
         }
       };
-      for (int kb = 0; kb < p.nkb; ++kb, ++blk) {
+      for (int kb = 0; kb < nk; ++kb, ++blk) {
         if (!(ok = wait_block())) break;
         tc_fence_after();
         const uint32_t tb = tq + buf() * (NSUB * 128);
@@ -501,36 +520,133 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
       if (!ok) break;
-      // a lane stores its own row, whole sectors (16 columns) at a time; the addend comes
-      // 64 columns at a time
-      if (m >= p.M) continue;
-      const int64_t at = m * p.N + n0 + c0;
+      if constexpr (SPLIT) {
+        // the one tile of this CTA: its partial sums go into the ring, which every copy and
+        // MMA is done with, as [128][128] FP32 with the 16-byte pieces of row r in the
+        // order piece ^ (r % 32), so that neither writing a row per lane nor reading along
+        // a row meets a bank twice
+        const int r = q * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < C::EPI_COLS / 4; ++i) {
+          const int piece = (c0 / 4 + i) ^ (r & 31);
+          *reinterpret_cast<float4*>(smem + r * 512 + piece * 16) =
+              make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+        }
+        break;
+      }
+      // 32 columns at a time through shared memory and out by TMA, which clips rows past M
+      // and columns past N.  (Stored by the lanes, a row each, an instruction touches 32
+      // rows: 2 us a tile on the load/store unit.)
+      if (m0 + q * 32 >= p.M) continue;
       const int live = min(p.N - n0 - c0, C::EPI_COLS);  // columns inside the output
+      // 64 columns of the addend, 32 bytes a load where its alignment allows; the next 64
+      // land while those before are stored
+      uint32_t a[32];
+      const int64_t m = m0 + q * 32 + lane;
+      auto load_add = [&](int b) {
 #pragma unroll
-      for (int b = 0; b < C::EPI_COLS / 64; ++b) {
-        uint4 a[8];
-        if (p.add) {
+        for (int k = 0; k < 4; ++k) {  // N % 16 == 0: 16 columns lie inside or outside whole
+          uint32_t* t = a + 8 * k;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            a[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (64 * b + 8 * k < live)  // N % 16 == 0: eight columns lie inside or outside whole
-              a[k] = *reinterpret_cast<const uint4*>(p.add + at + 64 * b + 8 * k);
+          for (int i = 0; i < 8; ++i) t[i] = 0u;
+          if (m >= p.M || 64 * b + 16 * k >= live) continue;
+          const uint16_t* at = p.add + m * p.N + n0 + c0 + 64 * b + 16 * k;
+          if (p.add32) {
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(t[0]), "=r"(t[1]), "=r"(t[2]), "=r"(t[3]), "=r"(t[4]), "=r"(t[5]),
+                           "=r"(t[6]), "=r"(t[7])
+                         : "l"(at)
+                         : "memory");
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4*>(at + 8 * i);
+              t[4 * i] = x.x;
+              t[4 * i + 1] = x.y;
+              t[4 * i + 2] = x.z;
+              t[4 * i + 3] = x.w;
+            }
           }
         }
+      };
+      if constexpr (ADD) load_add(0);
+      const uint32_t stg = base + C::STG_OFF + (uint32_t)((warp - 4) * C::STG_BUF);
+      uint8_t* row = smem + (stg - base) + 64 * lane;
+      const uint32_t sw = (uint32_t)(lane >> 1) & 3u;  // 64-byte swizzle of the store's map
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float2* f = acc + 32 * b + 4 * k;
-          if (p.add) {
-            const uint32_t w[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+      for (int b = 0; b < C::EPI_COLS / 64; ++b) {
+        if constexpr (ADD) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              f[i] = __fadd2_rn(f[i], make_float2(__uint_as_float(w[i] << 16),
-                                                  __uint_as_float(w[i] & 0xFFFF0000u)));
+          for (int i = 0; i < 32; ++i)
+            acc[32 * b + i] = __fadd2_rn(acc[32 * b + i],
+                                         make_float2(__uint_as_float(a[i] << 16),
+                                                     __uint_as_float(a[i] & 0xFFFF0000u)));
+          if (b + 1 < C::EPI_COLS / 64) load_add(b + 1);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (64 * b + 32 * j >= live) continue;  // uniform across the warp
+          const float2* f = acc + 32 * b + 16 * j;
+          if (lane == 0) bulk_wait_read<0>();  // the previous store has read the buffer
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(row + 16 * (k ^ sw)) = make_uint4(
+                pack_bf16x2(f[4 * k].x, f[4 * k].y), pack_bf16x2(f[4 * k + 1].x, f[4 * k + 1].y),
+                pack_bf16x2(f[4 * k + 2].x, f[4 * k + 2].y),
+                pack_bf16x2(f[4 * k + 3].x, f[4 * k + 3].y));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmOut, stg, n0 + c0 + 64 * b + 32 * j, m0 + q * 32);
+            bulk_commit();
           }
-          if (64 * b + 8 * k < live && PACT_IN(at + 64 * b + 8 * k + 8 <= (int64_t)p.M * p.N))
-            *reinterpret_cast<uint4*>(p.out + at + 64 * b + 8 * k) =
-                make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
-                           pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_sync();  // every CTA's partial sums are in its shared memory
+      // this CTA's rows of the tile: a warp takes a row of 128 columns, four a lane, and
+      // adds the CTAs' sums in their order
+      int m0, n0;
+      unit_mn(unit0, m0, n0);
+      const int r0 = 128 * (int)krank / p.split, r1 = 128 * (int)(krank + 1) / p.split;
+      const int n = n0 + 4 * lane;
+      for (int r = r0 + warp - 4; r < r1; r += 32) {  // four rows at a time
+        float4 v[4][kMaxSplit];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int rj = min(r + 8 * j, r1 - 1);
+          const uint32_t at = base + (uint32_t)(rj * 512 + ((lane ^ (rj & 31)) * 16));
+#pragma unroll
+          for (int c = 0; c < kMaxSplit; ++c)
+            v[j][c] = c < p.split ? ld_shared_cluster_v4f32(cluster_addr(at, (uint32_t)c))
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t m = m0 + r + 8 * j;
+          if (r + 8 * j >= r1 || m >= p.M || n >= p.N) continue;
+          float4 t = v[j][0];
+#pragma unroll
+          for (int c = 1; c < kMaxSplit; ++c) {
+            t.x += v[j][c].x;
+            t.y += v[j][c].y;
+            t.z += v[j][c].z;
+            t.w += v[j][c].w;
+          }
+          if (p.add) {
+            const uint2 a = *reinterpret_cast<const uint2*>(p.add + m * p.N + n);
+            t.x += __uint_as_float(a.x << 16);
+            t.y += __uint_as_float(a.x & 0xFFFF0000u);
+            t.z += __uint_as_float(a.y << 16);
+            t.w += __uint_as_float(a.y & 0xFFFF0000u);
+          }
+          if (PACT_IN(m * p.N + n + 4 <= (int64_t)p.M * p.N))
+            *reinterpret_cast<uint2*>(p.out + m * p.N + n) =
+                make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
         }
       }
     }
@@ -539,7 +655,8 @@ __global__ void __launch_bounds__(384, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // no CTA leaves while its peer may still signal it
+  // no CTA leaves while another may still signal it or read its sums
+  if constexpr (PAIR || SPLIT) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR)
@@ -549,10 +666,10 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-template <bool PAIR>
-static cudaError_t launch_tiles(const Fp8GemmLaunch& L, cudaStream_t stream) {
+template <bool PAIR, bool SPLIT, bool ADD>
+static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t stream) {
   using C = Fp8Cfg<PAIR>;
-  auto kern = k_fp8_gemm<PAIR>;
+  auto kern = k_fp8_gemm<PAIR, SPLIT, ADD>;
   static int max_clusters[64] = {};  // per device, once its attribute is set
   int dev = 0;
   cudaGetDevice(&dev);
@@ -560,7 +677,7 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C::CM;
+  attr[0].val.clusterDim.x = SPLIT ? split : C::CM;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(C::THREADS);
@@ -592,8 +709,9 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, cudaStream_t stream) {
   const int num_mc = (p.num_m + C::CM - 1) / C::CM;
   const int64_t units = (int64_t)num_mc * p.num_n;
   if (units >= (int64_t)1 << 30) return cudaErrorInvalidValue;
-  const int clusters = (int)(units < max_clusters[dev] ? units : max_clusters[dev]);
-  cfg.gridDim = dim3(clusters * C::CM);
+  const int clusters = SPLIT ? (int)units : (int)(units < max_clusters[dev] ? units : max_clusters[dev]);
+  cfg.gridDim = dim3(clusters * (SPLIT ? split : C::CM));
+  p.split = split;
   // tile order as in the NVFP4 GEMM: one band while X fits in L2 beside the tiles of W
   // in flight, else bands just wide enough to keep every cluster busy
   p.band_mc = num_mc;
@@ -602,12 +720,17 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, cudaStream_t stream) {
     p.band_mc = b < 1 ? 1 : (b > num_mc ? num_mc : b);
   }
   note_launch();
-  return cudaLaunchKernelEx(&cfg, kern, L.tmX, L.tmW, p);
+  return cudaLaunchKernelEx(&cfg, kern, L.tmX, L.tmW, L.tmOut, p);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch& L, cudaStream_t stream) {
-  if (L.p.M > 128 && L.p.N > 128) return launch_tiles<true>(L, stream);
-  return launch_tiles<false>(L, stream);
+  const int mode = getenv("FP8_MODE") ? atoi(getenv("FP8_MODE")) : 0;
+  if (mode >= 2 && mode <= 4) return launch_tiles<false, true, false>(L, mode, stream);
+  if (mode != 1 && L.p.M > 128 && L.p.N > 128)
+    return L.p.add ? launch_tiles<true, false, true>(L, 1, stream)
+                   : launch_tiles<true, false, false>(L, 1, stream);
+  return L.p.add ? launch_tiles<false, false, true>(L, 1, stream)
+                 : launch_tiles<false, false, false>(L, 1, stream);
 }
 
 }  // namespace pact

@@ -154,16 +154,18 @@ struct Fp8GemmParams {
   const float* sx;      // [nkb, M]
   const float* sw;      // [ceil(N/128), nkb]
   const uint16_t* add;  // BF16 [M, N] added before the cast, or null (may alias out)
+  int add32;            // add 32-byte aligned: fetched with 32-byte loads
   uint16_t* out;        // BF16 [M, N]
   unsigned* status;     // device status word
   int M, N, nkb;        // out [M, N], nkb = ceil(K/128)
   int num_m, num_n;     // tile grid
   int band_mc;          // tile order, as in GemmParams
+  int split;            // CTAs that share the blocks of one tile
 };
 struct Fp8GemmLaunch {
   // U8 maps over X [M, K] and W [N, K], boxes of 128 columns and 128 rows, 128-byte
-  // swizzle
-  CUtensorMap tmX, tmW;
+  // swizzle; the BF16 output [M, N], boxes of 32 x 32, 64-byte swizzle
+  CUtensorMap tmX, tmW, tmOut;
   Fp8GemmParams p;
   int64_t K;
   int num_sms;

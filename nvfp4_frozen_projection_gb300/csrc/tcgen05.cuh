@@ -101,6 +101,16 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t local, uint32_t 
   return v;
 }
 
+// A 16-byte load at a shared::cluster address (cluster_addr).
+__device__ __forceinline__ float4 ld_shared_cluster_v4f32(uint32_t ra) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(ra)
+               : "memory");
+  return v;
+}
+
 // try_wait with acquire at cluster scope: for barriers that other CTAs arrive on.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
