@@ -381,7 +381,8 @@ int pact_pack_weight_fp8_bwd(const float* W, int64_t N, int64_t K, pact_fp8* out
  * Input gradient: dX = dYq Wbwd^T [+ dX_prev], the same product over N:
  *   dyq  FP8 gradient [M, N] (pact_quant_fp8);  w_bwd  FP8 weight [K, N];
  *   dx_prev_opt  BF16 [M, K] or NULL (may alias dx, to add to it);  dx  BF16 [M, K].
- * The weight is frozen and has no gradient.  y, dx and the addends 16-byte aligned.
+ * The weight is frozen and has no gradient.  y, dx and the addends 16-byte aligned;
+ * ceil(rows / 128) * ceil(output width / 128) < 2^30.
  */
 int pact_linear_fp8_fwd(const pact_fp8* xq, const pact_fp8* w_fwd, const uint16_t* residual_opt,
                         uint16_t* y, pact_stream_t stream);

@@ -726,6 +726,8 @@ static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, c
   if ((rc = check_fp8_cols(K, "the reduction width")) ||
       (rc = check_fp8_cols(N, "the output width")))
     return rc;
+  if (((M + 127) / 128) * ((N + 127) / 128) >= (int64_t)1 << 30)
+    return fail(PACT_ERR_SHAPE, "output too large: ceil(M / 128) * ceil(N / 128) must be < 2^30");
   if ((rc = check_fp8(x, xname, M, K)) || (rc = check_fp8(w, wname, N, K))) return rc;
   if (!out) return fail(PACT_ERR_INVALID_ARG, "%s is required", outname);
   if (!aligned(out, 16) || (add && !aligned(add, 16)))
@@ -733,7 +735,7 @@ static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, c
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   cudaError_t e;
-  if (fp8_is_few(M, N, K)) {
+  if (fp8_is_few(M, N, K, d->sms)) {
     e = launch_fp8_few((const uint8_t*)x->q, x->s, (const uint8_t*)w->q, w->s, M, N, K, add, out,
                        (cudaStream_t)stream);
   } else {

@@ -12,14 +12,14 @@
 #include "kernels.h"
 #include "tcgen05.cuh"
 
-#include <cstdlib>
+#include <cmath>
 #include <type_traits>
 
 namespace pact {
 
 // ---------------------------------------------------------------- few tokens
-// A CTA computes 16 output columns (rows of W) for up to 8 NT tokens; its warps share
-// the blocks of K among them and add their sums through shared memory in warp order.
+// A CTA computes 16 output columns (rows of W) for up to 16 tokens; its warps share the
+// blocks of K among them and add their sums through shared memory in warp order.
 // The product is turned: W is the row operand (16 rows) and the tokens the column
 // operand (8 each), so that a single token wastes 7/8 of the tensor work but none of
 // the reads.  Within a block, lane 4 g + t holds the 16-byte pieces t and t + 4 of row
@@ -35,89 +35,162 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kFewWarps = 8;
-
+// One block of K as a warp holds it: 16 rows of W, 8 NT tokens, their scales.
 template <int NT>
-__global__ void __launch_bounds__(32 * kFewWarps)
+struct FewBlock {
+  uint4 a[2][2], b[NT][2];
+  float s0[NT], s1[NT], sw;
+};
+
+// WARPS share the blocks of K.  The next block's loads are in flight while this one is
+// multiplied.
+template <int NT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
     k_fp8_few(const uint8_t* __restrict__ x, const float* __restrict__ sx,
               const uint8_t* __restrict__ w, const float* __restrict__ sw, int64_t M, int64_t N,
               int64_t K, const uint16_t* add, uint16_t* out) {
-  __shared__ float sums[kFewWarps][16][8 * NT + 1];
+  __shared__ float sums[WARPS][16][8 * NT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (8 * NT);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int nkb = (int)((K + 127) / 128);
-  float acc[NT][4] = {};
-  for (int kb = warp; kb < nkb; kb += kFewWarps) {
-    const int64_t k0 = (int64_t)kb * 128 + 16 * t;
-    uint4 a[2][2], b[NT][2];
+  const uint8_t* wr = w + (n0 + g) * K + 16 * t;
+  const uint8_t* xr = x + (int64_t)g * K + 16 * t;
+  const float* swr = sw + (n0 >> 7) * nkb;
+  auto load = [&](int kb, FewBlock<NT>& f) {
+    const int64_t k0 = (int64_t)kb * 128;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int64_t k = k0 + 64 * c;
-      const bool ok = k < K;
+      const bool ok = k0 + 16 * t + 64 * c < K;  // K % 16 == 0: a piece lies in or out whole
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      a[0][c] = ok ? *reinterpret_cast<const uint4*>(w + (n0 + g) * K + k) : z;
-      a[1][c] = ok ? *reinterpret_cast<const uint4*>(w + (n0 + g + 8) * K + k) : z;
+      f.a[0][c] = ok ? ldg_stream(wr + k0 + 64 * c) : z;
+      f.a[1][c] = ok ? ldg_stream(wr + 8 * K + k0 + 64 * c) : z;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        b[j][c] = ok && m0 + 8 * j + g < M
-                      ? *reinterpret_cast<const uint4*>(x + (m0 + 8 * j + g) * K + k)
-                      : z;
+        f.b[j][c] = ok && 8 * j + g < M
+                        ? *reinterpret_cast<const uint4*>(xr + 8 * j * K + k0 + 64 * c)
+                        : z;
     }
-    const float s = sw[(n0 >> 7) * nkb + kb];
+    f.sw = swr[kb];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {  // the tokens of d[0] and d[2], d[1] and d[3]
+      const int64_t m = 8 * j + 2 * t;
+      f.s0[j] = m < M ? sx[(int64_t)kb * M + m] : 0.0f;
+      f.s1[j] = m + 1 < M ? sx[(int64_t)kb * M + m + 1] : 0.0f;
+    }
+  };
+  float acc[NT][4] = {};
+  FewBlock<NT> cur, next;
+  if (warp < nkb) load(warp, cur);
+  for (int kb = warp; kb < nkb; kb += WARPS) {
+    if (kb + WARPS < nkb) load(kb + WARPS, next);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float d[4] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        mma_e4m3(d, a[0][c].x, a[1][c].x, a[0][c].y, a[1][c].y, b[j][c].x, b[j][c].y);
-        mma_e4m3(d, a[0][c].z, a[1][c].z, a[0][c].w, a[1][c].w, b[j][c].z, b[j][c].w);
+        mma_e4m3(d, cur.a[0][c].x, cur.a[1][c].x, cur.a[0][c].y, cur.a[1][c].y, cur.b[j][c].x,
+                 cur.b[j][c].y);
+        mma_e4m3(d, cur.a[0][c].z, cur.a[1][c].z, cur.a[0][c].w, cur.a[1][c].w, cur.b[j][c].z,
+                 cur.b[j][c].w);
       }
-      const int64_t m = m0 + 8 * j + 2 * t;  // the token of d[0] and d[2]; d[1], d[3]: m + 1
-      const float s0 = m < M ? __fmul_rn(sx[(int64_t)kb * M + m], s) : 0.0f;
-      const float s1 = m + 1 < M ? __fmul_rn(sx[(int64_t)kb * M + m + 1], s) : 0.0f;
+      const float s0 = __fmul_rn(cur.s0[j], cur.sw), s1 = __fmul_rn(cur.s1[j], cur.sw);
       acc[j][0] = __fmaf_rn(d[0], s0, acc[j][0]);
       acc[j][1] = __fmaf_rn(d[1], s1, acc[j][1]);
       acc[j][2] = __fmaf_rn(d[2], s0, acc[j][2]);
       acc[j][3] = __fmaf_rn(d[3], s1, acc[j][3]);
     }
+    cur = next;
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[warp][g + 8 * (i >> 1)][8 * j + 2 * t + (i & 1)] = acc[j][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * 8 * NT; i += 32 * kFewWarps) {
-    const int n = i & 15, m = i >> 4;
-    if (m0 + m >= M) break;
-    float v = sums[0][n][m];
+  if (threadIdx.x < 16 * 8 * NT) {
+    const int n = threadIdx.x & 15, m = threadIdx.x >> 4;
+    if (m < M) {
+      float v = sums[0][n][m];
 #pragma unroll
-    for (int k = 1; k < kFewWarps; ++k) v += sums[k][n][m];
-    const int64_t at = (m0 + m) * N + n0 + n;
-    if (add) v += __uint_as_float((uint32_t)add[at] << 16);
-    if (PACT_IN(at < M * N)) out[at] = (uint16_t)(pack_bf16x2(v, v) & 0xFFFFu);
+      for (int k = 1; k < WARPS; ++k) v += sums[k][n][m];
+      const int64_t at = m * N + n0 + n;
+      if (add) v += __uint_as_float((uint32_t)add[at] << 16);
+      if (PACT_IN(at < M * N)) out[at] = (uint16_t)(pack_bf16x2(v, v) & 0xFFFFu);
+    }
   }
 }
 
-template <int NT>
+template <int NT, int WARPS>
 static cudaError_t launch_few(const uint8_t* x, const float* sx, const uint8_t* w,
                               const float* sw, int64_t M, int64_t N, int64_t K,
                               const uint16_t* add, uint16_t* out, cudaStream_t stream) {
-  const dim3 grid((unsigned)(N / 16), (unsigned)((M + 8 * NT - 1) / (8 * NT)));
   note_launch();
-  k_fp8_few<NT><<<grid, 32 * kFewWarps, 0, stream>>>(x, sx, w, sw, M, N, K, add, out);
+  k_fp8_few<NT, WARPS>
+      <<<(unsigned)(N / 16), 32 * WARPS, 0, stream>>>(x, sx, w, sw, M, N, K, add, out);
   return cudaGetLastError();
 }
 
 cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
                            int64_t M, int64_t N, int64_t K, const uint16_t* add, uint16_t* out,
                            cudaStream_t stream) {
-  if (M <= 8) return launch_few<1>(x, sx, w, sw, M, N, K, add, out, stream);
-  if (M <= 16) return launch_few<2>(x, sx, w, sw, M, N, K, add, out, stream);
-  return launch_few<4>(x, sx, w, sw, M, N, K, add, out, stream);
+  // 16 warps where a CTA has an SM to itself: 1 x 2048 x 8192 4.5 us against 5.5 with
+  // eight; 1 x 8192 x 2048 6.5 against 5.2
+  if (N <= 16 * 152)
+    return M <= 8 ? launch_few<1, 16>(x, sx, w, sw, M, N, K, add, out, stream)
+                  : launch_few<2, 16>(x, sx, w, sw, M, N, K, add, out, stream);
+  return M <= 8 ? launch_few<1, 8>(x, sx, w, sw, M, N, K, add, out, stream)
+                : launch_few<2, 8>(x, sx, w, sw, M, N, K, add, out, stream);
 }
 
+// ---------------------------------------------------------------- which kernel
+// The estimated time (us) of each way to run a product decides.  The constants are fitted
+// to GB300 measurements of M 1 .. 8192, N 512 .. 16384, K 1024 .. 16384 (launch included;
+// b = blocks of 128 along K):
+//   few     2.2 + N K / 4.3e6            16 x 4096 x 4096 5.7 us; 8 x 16384 x 16384 55
+//   tiles   2.7 + waves (1.2 + 0.27 b)   64 x 2048 x 2048 8.3; 128 x 4096 x 8192 21.4;
+//                                        8192 x 4096 x 8192 263
+//   shared  6.3 + 0.29 b / CTAs          128 x 4096 x 8192 12.5; 512 x 1024 x 16384 15.8
+//   pairs   5.0 + waves (1.5 + 0.41 b)   256 x 4096 x 8192 31.4; 2048 x 2048 x 2048 12.9;
+//                                        8192 x 4096 x 8192 196
+// and none but `few` under 3 + N K / 5.6e6, the weight's way out of HBM.  Sharing a tile's
+// blocks among a cluster's CTAs helps where there are few tiles; clusters of three or four
+// with this much shared memory fill 128 SMs, pairs all of them.
+enum Fp8Way { kFew, kTiles, kShared, kPairs };
+struct Fp8Plan {
+  Fp8Way way;
+  int split;
+};
+static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
+  Fp8Plan p = {kFew, 1};
+  if (M <= 8) return p;  // the tensor cores' rows would be empty
+  const double b = (double)((K + 127) / 128);
+  const double tiles = (double)((M + 127) / 128) * (double)((N + 127) / 128);
+  double best = 2.7 + std::ceil(tiles / sms) * (1.2 + 0.27 * b);
+  p.way = kTiles;
+  for (int s = 2; s <= 4; ++s) {
+    const double t = 6.3 + 0.29 * std::ceil(b / s);
+    if (tiles * s <= (s == 2 ? sms : sms * 128 / 152) && b >= 2 * s && t < best) {
+      best = t;
+      p.way = kShared;
+      p.split = s;
+    }
+  }
+  if (M > 128 && N > 128) {
+    const double pairs = (double)((M + 255) / 256) * (double)((N + 255) / 256);
+    const double t = 5.0 + std::ceil(pairs / (sms / 2)) * (1.5 + 0.41 * b);
+    if (t < best) {
+      best = t;
+      p.way = kPairs;
+      p.split = 1;
+    }
+  }
+  const double weight = (double)N * (double)K;
+  if (M <= 16 && 2.2 + weight / 4.3e6 < std::fmax(best, 3.0 + weight / 5.6e6)) p.way = kFew;
+  return p;
+}
 
-bool fp8_is_few(int64_t M, int64_t N, int64_t K) { return M <= 32; }
+bool fp8_is_few(int64_t M, int64_t N, int64_t K, int sms) {
+  return fp8_plan(M, N, K, sms).way == kFew;
+}
 
 // ---------------------------------------------------------------- many tokens
 // A persistent CTA per SM (128 x 128 tiles), or CTA pair (cluster of two along M,
@@ -707,8 +780,7 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
   p.num_m = (p.M + 127) / 128;
   p.num_n = (p.N + C::BN - 1) / C::BN;
   const int num_mc = (p.num_m + C::CM - 1) / C::CM;
-  const int64_t units = (int64_t)num_mc * p.num_n;
-  if (units >= (int64_t)1 << 30) return cudaErrorInvalidValue;
+  const int64_t units = (int64_t)num_mc * p.num_n;  // < 2^30, checked by the caller
   const int clusters = SPLIT ? (int)units : (int)(units < max_clusters[dev] ? units : max_clusters[dev]);
   cfg.gridDim = dim3(clusters * (SPLIT ? split : C::CM));
   p.split = split;
@@ -724,9 +796,9 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch& L, cudaStream_t stream) {
-  const int mode = getenv("FP8_MODE") ? atoi(getenv("FP8_MODE")) : 0;
-  if (mode >= 2 && mode <= 4) return launch_tiles<false, true, false>(L, mode, stream);
-  if (mode != 1 && L.p.M > 128 && L.p.N > 128)
+  const Fp8Plan plan = fp8_plan(L.p.M, L.p.N, L.K, L.num_sms);
+  if (plan.way == kShared) return launch_tiles<false, true, false>(L, plan.split, stream);
+  if (plan.way == kPairs)
     return L.p.add ? launch_tiles<true, false, true>(L, 1, stream)
                    : launch_tiles<true, false, false>(L, 1, stream);
   return L.p.add ? launch_tiles<false, false, true>(L, 1, stream)

@@ -72,6 +72,7 @@ def test_linear_refusals(lib, name):
     assert f(f8(4, 64), f8(32, 80), None, P, None) == SHAPE
     assert f(f8(4, 72), f8(32, 72), None, P, None) == SHAPE
     assert f(f8(4, 64), f8(24, 64), None, P, None) == SHAPE
+    assert f(f8(2**30, 64), f8(2**17, 64), None, P, None) == SHAPE  # too many tiles
     assert f(f8(4, 64, q=0), f8(32, 64), None, P, None) == INVALID
     assert f(f8(4, 64), f8(32, 64, s=0), None, P, None) == INVALID
     assert f(f8(4, 64, q=P + 8), f8(32, 64), None, P, None) == ALIGN
