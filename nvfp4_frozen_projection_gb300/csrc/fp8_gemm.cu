@@ -223,7 +223,7 @@ struct Fp8Cfg {
   static constexpr int CM = PAIR ? 2 : 1;
   static constexpr int BN = PAIR ? 256 : 128;
   static constexpr int NSUB = PAIR ? 2 : 1;  // sub-blocks of a block
-  static constexpr int CYC = 2;              // blocks with accumulators in TMEM
+  static constexpr int CYC = PAIR ? 2 : 4;   // blocks with accumulators in TMEM
   static constexpr int NBUF = CYC * NSUB;    // buffers of 128 columns
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = 128 * 128;  // 128 rows of W in this CTA's shared memory
@@ -245,15 +245,17 @@ struct Fp8Cfg {
   static_assert(LOW_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "register shares");
   static constexpr int EPI_WARPS = 8;
   static constexpr int EPI_COLS = BN / 2;  // columns of an epilogue warp, 64 of a sub-block
-  // An issuer takes every CYC-th block, so the blocks of one accumulator all come from one
-  // thread: another's could be two rounds ahead, where a barrier's parity looks the same.
-  static constexpr int ISSUERS = CYC;
+  // Two issuers take the blocks in turn.  An accumulator's blocks all come from one of
+  // them, and before it asks for a buffer it has been given the one two blocks earlier:
+  // no thread is ever two rounds ahead, where a barrier's parity looks the same.
+  static constexpr int ISSUERS = 2;
+  static constexpr int ROUND = PAIR ? 6 : 12;  // blocks until ring and buffers repeat together
   // barriers: full[S], empty[S], acc_full[CYC], acc_empty[NBUF], scl_full[2],
   // scl_empty[2], final
   static constexpr int NBARS = 2 * STAGES + CYC + NBUF + 5;
   static_assert(BAR_OFF % 8 == 0 && NBARS * 8 <= 504 && SMEM_BYTES <= 232448, "shared memory");
-  static_assert(STAGES % CYC == 0 && NBUF * 128 <= 512, "buffers repeat with the ring");
-  static_assert(STAGES % ISSUERS == 0, "issuers' turns repeat with the ring");
+  static_assert(ROUND % STAGES == 0 && ROUND % CYC == 0 && CYC % ISSUERS == 0, "turns");
+  static_assert(NBUF * 128 <= 512, "TMEM columns");
 };
 
 __host__ __device__ constexpr uint32_t idesc_e4m3(int n, int m) {
@@ -418,15 +420,16 @@ __global__ void __launch_bounds__(384, 1)
       auto issue = [&](auto turn_c) {
         constexpr int turn = decltype(turn_c)::value;
         uint32_t pass = 0;
-        for (int64_t first = 0; first < blocks && ok; first += STAGES, ++pass) {
+        for (int64_t first = 0; first < blocks && ok; first += C::ROUND, ++pass) {
 #pragma unroll
-          for (int s = turn; s < STAGES; s += C::ISSUERS) {
-            if (first + s >= blocks) break;
-            const int cyc = s % C::CYC;
-            const uint32_t uses = pass * (STAGES / C::CYC) + s / C::CYC;
-            const uint32_t seen = mbar_test_two(full0 + 8 * s, pass & 1u,
+          for (int i = turn; i < C::ROUND; i += C::ISSUERS) {
+            if (first + i >= blocks) break;
+            const int s = i % STAGES, cyc = i % C::CYC;
+            const uint32_t fills = pass * (C::ROUND / STAGES) + i / STAGES;
+            const uint32_t uses = pass * (C::ROUND / C::CYC) + i / C::CYC;
+            const uint32_t seen = mbar_test_two(full0 + 8 * s, fills & 1u,
                                                 acce0 + 8 * (cyc * NSUB), (uses & 1u) ^ 1u);
-            if (!(seen & 1u) && !wait_x(full0 + 8 * s, pass & 1u)) {
+            if (!(seen & 1u) && !wait_x(full0 + 8 * s, fills & 1u)) {
               ok = false;
               break;
             }
@@ -527,13 +530,13 @@ __global__ void __launch_bounds__(384, 1)
     uint32_t blk = 0;
     bool ok = true;
     const uint32_t acce = PAIR ? cluster_addr(acce0, 0) : acce0;  // at the leader
-    static_assert(C::CYC == 2 && C::SCL_DEPTH == 16 && C::SCL_HALF == 8, "bits of blk");
-    auto buf = [&]() { return blk & 1u; };
+    static_assert((C::CYC & (C::CYC - 1)) == 0 && C::SCL_DEPTH == 16 && C::SCL_HALF == 8, "bits");
+    auto buf = [&]() { return blk & (uint32_t)(C::CYC - 1); };
     // the next block's accumulators and, for every eighth, scales
     auto wait_block = [&]() {
       if ((blk & 7u) == 0 && !mbar_wait(sclf0 + (blk & 8u), (blk >> 4) & 1u, kFp8WaitNs, abort_flag))
         return false;
-      return mbar_wait(accf0 + 8 * buf(), (blk >> 1) & 1u, kFp8WaitNs, abort_flag);
+      return mbar_wait(accf0 + 8 * buf(), (blk / C::CYC) & 1u, kFp8WaitNs, abort_flag);
     };
     auto scale = [&]() {
       const uint32_t at = base + C::SCL_OFF + (blk & 15u) * C::SCL_SLOT;
