@@ -22,6 +22,11 @@ Cases (M = tokens; the other sizes are the Llama-3B layer's):
   rmsnorm-bwd         RMSNorm backward of a [M, 3072] NVFP4 output, with a residual gradient
   silu-bwd            SiLU-multiply backward from [M, 8192] NVFP4 gate/up copies
   pack-weight         forward and backward NVFP4 packs of the gate|up weight [2 x 8192, 3072]
+  fp8-linear          FP8 product Y = X W^T, 8192 -> 4096
+  fp8-linear-res      the same with a residual
+  fp8-quant           FP8 quantisation of a BF16 [M, 8192] tensor
+  fp8-norm            RMSNorm with the residual's addition -> FP8, [M, 4096]
+  fp8-norm-bwd        its backward, with a residual gradient and dgamma
 
 The default M (4096) keeps the inputs of the SiLU, GEMM and weight-pack cases above
 the 129 MB L2 and every case's device memory under 1 GB, the size a full ncu capture
@@ -35,7 +40,8 @@ import argparse
 
 import torch
 
-from . import (pact_check_status, pact_lora_adapter_grad, pact_lora_linear_dgrad,
+from . import (pact_add_rmsnorm_bwd, pact_add_rmsnorm_quant_fp8, pact_check_status,
+               pact_linear_fp8_fwd, pact_pack_weight_fp8_fwd, pact_quant_fp8, pact_lora_adapter_grad, pact_lora_linear_dgrad,
                pact_lora_linear_dgrad_q, pact_lora_linear_fwd_gate_up,
                pact_pack_weight_fwd_gate_up,
                pact_lora_linear_fwd, pact_pack_weight_bwd, pact_pack_weight_fwd,
@@ -95,6 +101,27 @@ def run(case: str, m: int, reps: int) -> None:
         dB = torch.empty(r, n_out, dtype=torch.float32, device=dev)
         for _ in range(reps):
             pact_lora_adapter_grad(xq, dy, A, B, 2.0, dA=dA, dB=dB)
+    elif case in ("fp8-linear", "fp8-linear-res"):
+        w = pact_pack_weight_fp8_fwd(torch.randn(4096, INTER, device=dev, generator=gen) * 0.02)
+        xq = pact_quant_fp8(torch.randn(m, INTER, device=dev, generator=gen).bfloat16())
+        y = torch.empty(m, 4096, dtype=torch.bfloat16, device=dev)
+        res = torch.zeros_like(y) if case == "fp8-linear-res" else None
+        for _ in range(reps):
+            pact_linear_fp8_fwd(xq, w, residual=res, y=y)
+    elif case == "fp8-quant":
+        x = torch.randn(m, INTER, device=dev, generator=gen).bfloat16()
+        q = pact_quant_fp8(x)
+        for _ in range(reps):
+            pact_quant_fp8(x, out=q)
+    elif case in ("fp8-norm", "fp8-norm-bwd"):
+        x, res, dy = (torch.randn(m, 4096, device=dev, generator=gen).bfloat16() for _ in range(3))
+        gamma = torch.ones(4096, dtype=torch.bfloat16, device=dev)
+        h, yq, rstd = pact_add_rmsnorm_quant_fp8(x, res, gamma)
+        for _ in range(reps):
+            if case == "fp8-norm":
+                pact_add_rmsnorm_quant_fp8(x, res, gamma, h=h, out=yq, rstd=rstd)
+            else:
+                pact_add_rmsnorm_bwd(h, gamma, rstd, dy, dres=res, dh=x, dgamma=True)
     elif case == "quant":
         x = torch.randn(m, HIDDEN, device=dev, generator=gen).bfloat16()
         q = pact_quant_nvfp4(x)
