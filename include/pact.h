@@ -412,7 +412,8 @@ int pact_add_rmsnorm_quant_fp8(const uint16_t* x, const uint16_t* residual_opt,
  *   h BF16 [M, H] (the forward's h, or x without a residual);  rstd FP32 [M];
  *   dy, dres_opt, dh BF16 [M, H] (dh may alias dy or dres);  dgamma_opt FP32 [H] or NULL.
  * Rules as for the forward.  ws: pact_add_rmsnorm_bwd_workspace_size() bytes when dgamma
- * is asked for, else NULL.  Deterministic.
+ * is asked for; NULL without dgamma or where that size is 0 (small tensors).
+ * Deterministic.
  */
 size_t pact_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t H);
 int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd,

@@ -679,8 +679,9 @@ def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tenso
             dgamma = torch.empty((H,), dtype=torch.float32, device=h.device)
         _need(dgamma, torch.float32, (H,), "dgamma", dev)
         # its own scratch in every call: a captured graph then keeps one of its own
-        ws = torch.empty((lib.pact_add_rmsnorm_bwd_workspace_size(M, H),), dtype=torch.uint8,
-                         device=h.device)
+        size = lib.pact_add_rmsnorm_bwd_workspace_size(M, H)
+        if size:
+            ws = torch.empty((size,), dtype=torch.uint8, device=h.device)
     _check(lib.pact_add_rmsnorm_bwd(_addr(h), _addr(gamma), _addr(rstd), _addr(dy), _addr(dres), M, H,
                                     _addr(dh), _addr(dgamma), _addr(ws),
                                     0 if ws is None else ws.numel(), _raw_stream(dev)))

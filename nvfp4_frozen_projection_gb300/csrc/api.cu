@@ -817,8 +817,8 @@ int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* 
   if (!aligned(h, 16) || !aligned(gamma, 16) || !aligned(dy, 16) || !aligned(dh, 16) ||
       !aligned(dres_opt, 16) || !aligned(rstd, 4) || !aligned(dgamma_opt, 4))
     return fail(PACT_ERR_ALIGN, "h, gamma, dy, dres and dh must be 16-byte aligned");
-  if (dgamma_opt &&
-      (!ws || ws_bytes < pact_add_rmsnorm_bwd_workspace_size(M, H) || !aligned(ws, 256)))
+  const size_t need = dgamma_opt ? pact_add_rmsnorm_bwd_workspace_size(M, H) : 0;
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 256)))
     return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;

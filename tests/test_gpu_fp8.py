@@ -9,8 +9,9 @@ at most 2^-8 of the value):
               40 u.  The FP8 output, given that rstd, bit for bit.
   dh          2^-8 of the value, and u times: 4 |rstd dn| (products and sum),
               8 |rstd n c|, and 64 |rstd n| mean |dn n| for the sum c, chains as above.
-  dgamma      u (rows added in one chain + 80) sum |dy n|: rows of one group, then at
-              most 305 / 16 partial sums of each group, 16 lanes.
+  dgamma      u (rows / 304 + 80) sum |dy n|: the rows of one of 304 groups in a chain,
+              then up to 2432 partial sums, 64 lanes of 38 and 16 joins; or, up to 4096
+              rows, 128 lanes of 32 and 11 joins.
   product     2^-8 of the value, and 2^-23 (128 + blocks + 8) sum |x w|: FP32 additions
               of a block in any order, truncated or rounded, then one fused step for
               each block, the scales' product, and the join.
@@ -206,7 +207,7 @@ def test_add_rmsnorm_in_place(into):
     assert torch.equal(yq.q.view(torch.uint8), yq2.q.view(torch.uint8))
 
 
-@pytest.mark.parametrize("m,h", NORM_SHAPES + [(3000, 1040)])
+@pytest.mark.parametrize("m,h", NORM_SHAPES + [(3000, 1040), (5000, 528), (4097, 64), (1500, 8192)])
 @pytest.mark.parametrize("with_res", [True, False])
 def test_add_rmsnorm_bwd(m, h, with_res):
     rng = np.random.default_rng(m * 5 + h)
@@ -233,10 +234,11 @@ def test_add_rmsnorm_bwd(m, h, with_res):
     assert none is None and torch.equal(again, dh)
 
 
-def test_add_rmsnorm_bwd_in_place():
+@pytest.mark.parametrize("m,h", [(40, 1040), (5000, 528), (30, 8192)])
+def test_add_rmsnorm_bwd_in_place(m, h):
     rng = np.random.default_rng(8)
-    hh, dy, dres = bf16(rng, (40, 1040)), bf16(rng, (40, 1040)), bf16(rng, (40, 1040))
-    gamma = bf16(rng, (1040,))
+    hh, dy, dres = (bf16(rng, (m, h)) for _ in range(3))
+    gamma = bf16(rng, (h,))
     _, _, rstd = pk.pact_add_rmsnorm_quant_fp8(hh, None, gamma)
     want, dg = pk.pact_add_rmsnorm_bwd(hh, gamma, rstd, dy, dres=dres, dgamma=True)
     for name in ("dy", "dres"):
