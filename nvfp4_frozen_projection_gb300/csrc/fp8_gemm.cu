@@ -158,9 +158,10 @@ enum Fp8Way { kFew, kTiles, kShared, kPairs };
 struct Fp8Plan {
   Fp8Way way;
   int split;
+  int64_t whole;  // pairs: the tiles before a last wave of halves, 0 without one
 };
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
-  Fp8Plan p = {kFew, 1};
+  Fp8Plan p = {kFew, 1, 0};
   if (M <= 8) return p;  // the tensor cores' rows would be empty
   const double b = (double)((K + 127) / 128);
   const double tiles = (double)((M + 127) / 128) * (double)((N + 127) / 128);
@@ -176,11 +177,17 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
   }
   if (M > 128 && N > 128) {
     const double pairs = (double)((M + 255) / 256) * (double)((N + 255) / 256);
-    const double t = 5.0 + std::ceil(pairs / (sms / 2)) * (1.5 + 0.41 * b);
+    // tiles left over for at most half the pairs go as halves, in a launch of their own
+    // (5 us), where that beats a wave of whole ones: 8192 x 2048 x 16384
+    const double wave = 1.5 + 0.41 * b, full = std::floor(pairs / (sms / 2));
+    const double left = pairs - full * (sms / 2);
+    const bool halves = full > 0 && left > 0 && 2 * left <= sms / 2 && 5.0 + 0.65 * wave < wave;
+    const double t = 5.0 + full * wave + (left == 0 ? 0.0 : (halves ? 5.0 + 0.65 * wave : wave));
     if (t < best) {
       best = t;
       p.way = kPairs;
       p.split = 1;
+      p.whole = halves ? (int64_t)(full * (sms / 2)) : 0;
     }
   }
   const double weight = (double)N * (double)K;
@@ -266,7 +273,10 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int n, int m) {
 constexpr int kMaxSplit = 4;  // CTAs that share the blocks of one tile
 constexpr uint64_t kFp8WaitNs = 2000000000ull;  // 2 s per pipeline wait
 
-template <bool PAIR, bool SPLIT, bool ADD>
+// PART: the units are halves (128 columns) of a pair's tiles, for the tiles that do not
+// fill a last wave.  Every block still goes round both sub-blocks' buffers, the second
+// unused.
+template <bool PAIR, bool SPLIT, bool ADD, bool PART>
 __global__ void __launch_bounds__(384, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                const __grid_constant__ CUtensorMap tmOut, const Fp8GemmParams p) {
@@ -285,9 +295,10 @@ __global__ void __launch_bounds__(384, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(!(PAIR && SPLIT), "a cluster is a pair or shares the blocks of one tile");
+  static_assert(PAIR || !PART, "halves of a pair's tile");
   const uint32_t crank = PAIR ? cluster_ctarank() : 0u;
   const int num_mc = (p.num_m + CM - 1) / CM;
-  const int nunits = num_mc * p.num_n;
+  const int nunits = p.units;
   const int csize = SPLIT ? p.split : CM;  // CTAs of a cluster
   const int unit0 = (int)blockIdx.x / csize, nclusters = (int)gridDim.x / csize;
   // the blocks of K that this CTA adds up
@@ -295,12 +306,14 @@ __global__ void __launch_bounds__(384, 1)
   const int kb0 = SPLIT ? (int)((int64_t)p.nkb * krank / p.split) : 0;
   const int nk = (SPLIT ? (int)((int64_t)p.nkb * (krank + 1) / p.split) : p.nkb) - kb0;
   const int band = p.band_mc;
+  // the first row and column of unit u
   auto unit_mn = [&](int u, int& m0, int& n0) {
-    const int bi = u / (band * p.num_n), r = u - bi * band * p.num_n;
+    const int t = p.first + (PART ? u >> 1 : u);
+    const int bi = t / (band * p.num_n), r = t - bi * band * p.num_n;
     const int mc0 = bi * band, bm = min(band, num_mc - mc0);
     const int n = r / bm;
     m0 = ((mc0 + (r - n * bm)) * CM + (int)crank) * 128;
-    n0 = n * BN;
+    n0 = n * BN + (PART ? 128 * (u & 1) : 0);
   };
 
   if (threadIdx.x == 0) {
@@ -349,7 +362,8 @@ __global__ void __launch_bounds__(384, 1)
       for (int u = unit0; u < nunits && ok; u += nclusters) {
         int m0, n0;
         unit_mn(u, m0, n0);
-        const int nb = n0 + (int)crank * 128;
+        // of half a tile each CTA uses 64 rows of W, the first of the box
+        const int nb = n0 + (int)crank * (PART ? 64 : 128);
         for (int kb = kb0; kb < kb0 + nk; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, kFp8WaitNs, abort_flag)) {
             ok = false;
@@ -443,6 +457,7 @@ __global__ void __launch_bounds__(384, 1)
                 ok = false;
                 break;
               }
+              if (PART && h == 1) continue;
               tc_fence_after();
               // sub-block h of a pair takes rows 64 h .. 64 h + 63 of each CTA's tile of W
               const uint64_t db = da + ((C::A_BYTES + h * 64 * 128) >> 4);
@@ -486,7 +501,7 @@ __global__ void __launch_bounds__(384, 1)
         unit_mn(u, m0, n0);
         // columns past N have no scale of their own: their sums are not stored
         const float* psw = p.sw + kb0 +
-                           (int64_t)(min(n0 + (lane & 1) * C::EPI_COLS, p.N - 1) >> 7) * p.nkb;
+                           (int64_t)(min(n0 + (PART ? 0 : (lane & 1) * C::EPI_COLS), p.N - 1) >> 7) * p.nkb;
         const float* psx = p.sx + (int64_t)kb0 * p.M + m0 + lane;
         for (int kb = 0; kb < nk; ++kb, psx += p.M, ++psw) {
           const uint32_t half = slot / C::SCL_HALF;
@@ -523,7 +538,8 @@ __global__ void __launch_bounds__(384, 1)
     setmaxnreg_inc<C::EPI_REGS>();
     const int q = warp & 3;            // TMEM lane quarter this warp may access
     const int half = (warp - 4) >> 2;  // which half of the columns
-    const int c0 = half * C::EPI_COLS;
+    constexpr int COLS = PART ? 64 : C::EPI_COLS;  // of this warp
+    const int c0 = half * COLS;
     const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 64);
     // blocks so far, from which the buffer, the ring slot and their parities follow (one
     // register: the sums and slices leave few)
@@ -555,14 +571,14 @@ __global__ void __launch_bounds__(384, 1)
         const int64_t m = m0 + q * 32 + lane;
         if (m < p.M) {
 #pragma unroll
-          for (int c = 0; c < C::EPI_COLS; c += 64)
+          for (int c = 0; c < COLS; c += 64)
             if (n0 + c0 + c < p.N)
               asm volatile("prefetch.global.L2 [%0];" ::"l"(p.add + m * p.N + n0 + c0 + c));
         }
       }
-      float2 acc[C::EPI_COLS / 2];
+      float2 acc[COLS / 2];
 #pragma unroll
-      for (int i = 0; i < C::EPI_COLS / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < COLS / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
       auto release = [&](int h) {  // buffer h of the block: its columns have landed
         tc_fence_before();
         __syncwarp();
@@ -581,9 +597,9 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld16(tb, v[0]);
         const float s = scale();
 #pragma unroll
-        for (int c = 0; c < C::EPI_COLS / 16; ++c) {
+        for (int c = 0; c < COLS / 16; ++c) {
           tmem_ld_wait16(v[c & 1]);
-          if (c + 1 < C::EPI_COLS / 16)  // the next slice lands while this one is added
+          if (c + 1 < COLS / 16)  // the next slice lands while this one is added
             tmem_ld16(tb + (c + 1) / 4 * 128 + (c + 1) % 4 * 16, v[(c + 1) & 1]);
           if (c % 4 == 3) release(c / 4);
 #pragma unroll
@@ -593,6 +609,7 @@ __global__ void __launch_bounds__(384, 1)
                                        __uint_as_float(v[c & 1][2 * i + 1])),
                            make_float2(s, s), acc[8 * c + i]);
         }
+        if constexpr (PART) release(1);  // not written
       }
       if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
       if (!ok) break;
@@ -614,7 +631,7 @@ __global__ void __launch_bounds__(384, 1)
       // and columns past N.  (Stored by the lanes, a row each, an instruction touches 32
       // rows: 2 us a tile on the load/store unit.)
       if (m0 + q * 32 >= p.M) continue;
-      const int live = min(p.N - n0 - c0, C::EPI_COLS);  // columns inside the output
+      const int live = min(p.N - n0 - c0, COLS);  // columns inside the output
       // 64 columns of the addend, 32 bytes a load where its alignment allows; the next 64
       // land while those before are stored
       uint32_t a[32];
@@ -650,14 +667,14 @@ __global__ void __launch_bounds__(384, 1)
       uint8_t* row = smem + (stg - base) + 64 * lane;
       const uint32_t sw = (uint32_t)(lane >> 1) & 3u;  // 64-byte swizzle of the store's map
 #pragma unroll
-      for (int b = 0; b < C::EPI_COLS / 64; ++b) {
+      for (int b = 0; b < COLS / 64; ++b) {
         if constexpr (ADD) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             acc[32 * b + i] = __fadd2_rn(acc[32 * b + i],
                                          make_float2(__uint_as_float(a[i] << 16),
                                                      __uint_as_float(a[i] & 0xFFFF0000u)));
-          if (b + 1 < C::EPI_COLS / 64) load_add(b + 1);
+          if (b + 1 < COLS / 64) load_add(b + 1);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -742,10 +759,12 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-template <bool PAIR, bool SPLIT, bool ADD>
-static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t stream) {
+// The tiles from `first` on, `count` of them (0: to the last).
+template <bool PAIR, bool SPLIT, bool ADD, bool PART = false>
+static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t stream,
+                                int64_t first = 0, int64_t count = 0) {
   using C = Fp8Cfg<PAIR>;
-  auto kern = k_fp8_gemm<PAIR, SPLIT, ADD>;
+  auto kern = k_fp8_gemm<PAIR, SPLIT, ADD, PART>;
   static int max_clusters[64] = {};  // per device, once its attribute is set
   int dev = 0;
   cudaGetDevice(&dev);
@@ -783,15 +802,18 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
   p.num_m = (p.M + 127) / 128;
   p.num_n = (p.N + C::BN - 1) / C::BN;
   const int num_mc = (p.num_m + C::CM - 1) / C::CM;
-  const int64_t units = (int64_t)num_mc * p.num_n;  // < 2^30, checked by the caller
-  const int clusters = SPLIT ? (int)units : (int)(units < max_clusters[dev] ? units : max_clusters[dev]);
+  const int64_t tiles = (int64_t)num_mc * p.num_n;  // < 2^30, checked by the caller
+  p.first = (int)first;
+  p.units = (int)((count ? count : tiles - first) * (PART ? 2 : 1));
+  const int clusters = SPLIT || p.units < max_clusters[dev] ? p.units : max_clusters[dev];
   cfg.gridDim = dim3(clusters * (SPLIT ? split : C::CM));
   p.split = split;
   // tile order as in the NVFP4 GEMM: one band while X fits in L2 beside the tiles of W
   // in flight, else bands just wide enough to keep every cluster busy
   p.band_mc = num_mc;
   if ((double)p.num_m * 128.0 * (double)L.K > 32.0 * 1024 * 1024) {
-    const int b = (clusters + p.num_n - 1) / p.num_n;
+    // the same for every launch over these tiles, whose order it sets
+    const int b = (max_clusters[dev] + p.num_n - 1) / p.num_n;
     p.band_mc = b < 1 ? 1 : (b > num_mc ? num_mc : b);
   }
   note_launch();
@@ -801,9 +823,13 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch& L, cudaStream_t stream) {
   const Fp8Plan plan = fp8_plan(L.p.M, L.p.N, L.K, L.num_sms);
   if (plan.way == kShared) return launch_tiles<false, true, false>(L, plan.split, stream);
-  if (plan.way == kPairs)
-    return L.p.add ? launch_tiles<true, false, true>(L, 1, stream)
-                   : launch_tiles<true, false, false>(L, 1, stream);
+  if (plan.way == kPairs) {
+    const cudaError_t e = L.p.add ? launch_tiles<true, false, true>(L, 1, stream, 0, plan.whole)
+                                  : launch_tiles<true, false, false>(L, 1, stream, 0, plan.whole);
+    if (e != cudaSuccess || !plan.whole) return e;
+    return L.p.add ? launch_tiles<true, false, true, true>(L, 1, stream, plan.whole)
+                   : launch_tiles<true, false, false, true>(L, 1, stream, plan.whole);
+  }
   return L.p.add ? launch_tiles<false, false, true>(L, 1, stream)
                  : launch_tiles<false, false, false>(L, 1, stream);
 }

@@ -161,6 +161,7 @@ struct Fp8GemmParams {
   int num_m, num_n;     // tile grid
   int band_mc;          // tile order, as in GemmParams
   int split;            // CTAs that share the blocks of one tile
+  int first, units;     // the launch's first tile, and its tiles (or halves)
 };
 struct Fp8GemmLaunch {
   // U8 maps over X [M, K] and W [N, K], boxes of 128 columns and 128 rows, 128-byte

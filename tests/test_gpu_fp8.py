@@ -294,6 +294,31 @@ def test_linear_fwd(m, n, k, with_add):
     assert torch.equal(again, y)  # the same bits on every call
 
 
+@pytest.mark.parametrize("m,n,k", [(4500, 2544, 4112), (8200, 2048, 4240), (5000, 4112, 2064)])
+@pytest.mark.parametrize("with_add", [False, True])
+def test_linear_many_tiles(m, n, k, with_add):
+    """Several waves of tiles, the last of them ragged, against a 64-bit product on the GPU
+    with the bound of the other products."""
+    rng = np.random.default_rng(m + n)
+    g = torch.Generator(device="cuda").manual_seed(m)
+    xq = pk.pact_quant_fp8(torch.randn(m, k, device="cuda", generator=g).bfloat16())
+    w = random_weight(rng, n, k)
+    add = bf16(rng, (m, n)) if with_add else None
+    gy = Guarded((m, n), torch.bfloat16)
+    y = pk.pact_linear_fp8_fwd(xq, w, residual=add, y=gy.t)
+    pk.pact_check_status()
+    gy.check()
+    a = xq.q.double() * xq.s.double().t().repeat_interleave(128, 1)[:, :k]
+    sw = w.s.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    b = w.q.double() * sw
+    want, mag = a @ b.t(), a.abs() @ b.abs().t()
+    if add is not None:
+        want, mag = want + add.double(), mag + add.double().abs()
+    tol = 2.0 ** -8 * want.abs() + 2.0 ** -23 * (136 + ref.blocks_of(k)) * mag
+    assert bool(((y.double() - want).abs() <= tol * (1 + 2.0 ** -8)).all())
+    assert torch.equal(pk.pact_linear_fp8_fwd(xq, w, residual=add), y)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 2048, 1024), (12, 528, 4112), (24, 1040, 272), (64, 2048, 2064),
                                    (333, 2064, 1040), (640, 1024, 512), (2100, 4080, 528)])
 def test_linear_exact_sums(m, n, k):
