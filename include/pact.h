@@ -340,7 +340,10 @@ int pact_rmsnorm_bwd(const pact_nvfp4* yq, const uint16_t* gamma, const float* r
  * element: e4m3(q) * s.  A block with largest magnitude amax is encoded with
  *   t = max(amax, 448 * 2^-126);  s = RN(t / 448);  r = RN(448 / t);
  *   q = e4m3_rne_satfinite(RN(x r))   (FP32 arithmetic; signed zeros are kept).
- * The GEMM takes any scales, also ones that another program made.
+ * The GEMM takes any scales, also ones that another program made, as long as the products
+ * of an activation's and a weight's scales are normal FP32 numbers or zero.
+ * A NaN or an infinity becomes a NaN code: of an activation, that row of a product is NaN
+ * and no other row is touched.
  * Rules for every call below: rows 1 .. 2^30; cols a multiple of 16, 16 .. 2^24; q
  * 16-byte and s 4-byte aligned.  pact_fp8_scale_count and pact_fp8_weight_scale_count
  * give the number of FP32 values in s.
@@ -410,7 +413,7 @@ int pact_add_rmsnorm_quant_fp8(const uint16_t* x, const uint16_t* residual_opt,
  * dh is the gradient of x and of the residual alike; dres is the gradient that reaches
  * h by the residual stream.
  *   h BF16 [M, H] (the forward's h, or x without a residual);  rstd FP32 [M];
- *   dy, dres_opt, dh BF16 [M, H] (dh may alias dy or dres);  dgamma_opt FP32 [H] or NULL.
+ *   dy, dres_opt, dh BF16 [M, H] (dh may be dy, dres or h);  dgamma_opt FP32 [H] or NULL.
  * Rules as for the forward.  ws: pact_add_rmsnorm_bwd_workspace_size() bytes when dgamma
  * is asked for; NULL without dgamma or where that size is 0 (small tensors).
  * Deterministic.

@@ -657,7 +657,7 @@ def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tenso
                          dh: torch.Tensor | None = None,
                          dgamma: torch.Tensor | bool | None = None):
     """Backward of pact_add_rmsnorm_quant_fp8 from h and rstd: dh [+ dres], the gradient
-    of x and of the residual alike (dh may be dy or dres).  dgamma: an FP32 [H] tensor
+    of x and of the residual alike (dh may be dy, dres or h).  dgamma: an FP32 [H] tensor
     to overwrite, True for a new one, None to leave it out.  Returns (dh, dgamma)."""
     lib = _LIB or load_library()
     M, H = _need_2d(h, "h")

@@ -178,7 +178,8 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
   if (M > 128 && N > 128) {
     const double pairs = (double)((M + 255) / 256) * (double)((N + 255) / 256);
     // tiles left over for at most half the pairs go as halves, in a launch of their own
-    // (5 us), where that beats a wave of whole ones: 8192 x 2048 x 16384
+    // (5 us), where that beats a wave of whole ones: 8192 x 2048 x 16384 took 225 us with
+    // a wave of 28 tiles and takes 209 with 56 halves
     const double wave = 1.5 + 0.41 * b, full = std::floor(pairs / (sms / 2));
     const double left = pairs - full * (sms / 2);
     const bool halves = full > 0 && left > 0 && 2 * left <= sms / 2 && 5.0 + 0.65 * wave < wave;
@@ -218,9 +219,9 @@ bool fp8_is_few(int64_t M, int64_t N, int64_t K, int sms) {
 // The first warpgroup gives its registers to the epilogue, whose threads hold 128 sums
 // and the columns that land.
 //
-// 8192 x 4096 x 8192 takes 203 us (2.7 PFLOP/s, 0.73 of twice the measured BF16 rate).
-// The same kernel without the additions takes 193 us and with one barrier round for 16
-// blocks instead of one 153: what is left is that round.  Measured and not kept, all at
+// 8192 x 4096 x 8192 takes 197 us (2.8 PFLOP/s, 0.75 of twice the measured BF16 rate).
+// When it took 203, it took 193 without the additions and 153 with one barrier round for
+// 16 blocks instead of one: what is left is that round.  Measured and not kept, all at
 // this size: 16 epilogue warps of 64 columns (232 us), loads carried over from one block to
 // the next (238, it spills), an issuer and a barrier for each sub-block with epilogue
 // warps that take both sub-blocks (238) or one each (230).
@@ -501,7 +502,8 @@ __global__ void __launch_bounds__(384, 1)
         unit_mn(u, m0, n0);
         // columns past N have no scale of their own: their sums are not stored
         const float* psw = p.sw + kb0 +
-                           (int64_t)(min(n0 + (PART ? 0 : (lane & 1) * C::EPI_COLS), p.N - 1) >> 7) * p.nkb;
+                           (int64_t)(min(n0 + (PART ? 0 : (lane & 1) * C::EPI_COLS), p.N - 1) >> 7) *
+                               p.nkb;
         const float* psx = p.sx + (int64_t)kb0 * p.M + m0 + lane;
         for (int kb = 0; kb < nk; ++kb, psx += p.M, ++psw) {
           const uint32_t half = slot / C::SCL_HALF;
@@ -812,8 +814,8 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
   // in flight, else bands just wide enough to keep every cluster busy
   p.band_mc = num_mc;
   if ((double)p.num_m * 128.0 * (double)L.K > 32.0 * 1024 * 1024) {
-    // the same for every launch over these tiles, whose order it sets
-    const int b = (max_clusters[dev] + p.num_n - 1) / p.num_n;
+    // from the device's size, so that every launch over these tiles has the same order
+    const int b = (L.num_sms / C::CM + p.num_n - 1) / p.num_n;
     p.band_mc = b < 1 ? 1 : (b > num_mc ? num_mc : b);
   }
   note_launch();

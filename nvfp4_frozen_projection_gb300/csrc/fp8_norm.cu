@@ -392,9 +392,9 @@ cudaError_t launch_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, con
   const RowPlan p = bwd_plan(M, H);
   const int grid = bwd_ctas(M, p);
   const bool small = dgamma && bwd_in_one(M, H);
-  // in the same launch unless dh overwrites the dy that the columns read, or the rows take
-  // larger CTAs
-  const bool one = small && p.threads == 256 && dh != dy;
+  // in the same launch unless dh overwrites what the columns read, or the rows take larger
+  // CTAs
+  const bool one = small && p.threads == 256 && dh != dy && dh != h;
   const int cols = (int)(H / 16);
   float* pp = dgamma && !small ? part : nullptr;
   if (small && !one) {

@@ -16,7 +16,8 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (FP8, NVFP4, pact_linear_fp8_dgrad, pact_linear_fp8_fwd, pact_lora_linear_dgrad, pact_lora_linear_dgrad_q, pact_lora_linear_fwd,
+from . import (FP8, NVFP4, pact_linear_fp8_dgrad, pact_linear_fp8_fwd, pact_lora_linear_dgrad,
+               pact_lora_linear_dgrad_q, pact_lora_linear_fwd,
                pact_lora_linear_fwd_gate_up, pact_pack_weight_bwd, pact_pack_weight_fwd_gate_up,
                pact_lora_adapter_grad, pact_pack_weight_fp8_bwd, pact_pack_weight_fp8_fwd,
                pact_pack_weight_fwd, pact_quant_fp8, pact_quant_nvfp4, pact_rmsnorm_bwd,

@@ -393,6 +393,37 @@ def test_rows_do_not_depend_on_the_batch(m):
     assert not bool(torch.isfinite(y[m // 2]).any())
 
 
+@pytest.mark.parametrize("m,n,k", [(5, 528, 1040), (40, 528, 1040), (700, 528, 4112)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_nan_and_infinity_stay_in_their_row(m, n, k, bad):
+    rng = np.random.default_rng(m)
+    x, w = activation(rng, m, k), random_weight(rng, n, k)
+    gamma = bf16(rng, (k,), 0.1) + 1
+    quant, norm = pk.pact_quant_fp8(x), pk.pact_add_rmsnorm_quant_fp8(x, None, gamma)[1]
+    y, yn = pk.pact_linear_fp8_fwd(quant, w), pk.pact_linear_fp8_fwd(norm, w)
+    row = m // 2
+    x[row, k - 3] = bad
+    keep = torch.arange(m, device="cuda") != row
+    for before, made in ((y, pk.pact_quant_fp8(x)),
+                         (yn, pk.pact_add_rmsnorm_quant_fp8(x, None, gamma)[1])):
+        assert bool(torch.isnan(made.q[row, k - 3].float()))
+        after = pk.pact_linear_fp8_fwd(made, w)
+        assert torch.equal(after[keep], before[keep])
+        assert bool(torch.isnan(after[row]).all())
+
+
+@pytest.mark.parametrize("m,h", [(300, 1040), (2, 16384), (3, 64), (5000, 1040), (600, 16384)])
+def test_add_rmsnorm_bwd_over_h(m, h):
+    """dh written over h gives what it gives elsewhere."""
+    rng = np.random.default_rng(m + h)
+    hh, dy, gamma = bf16(rng, (m, h)), bf16(rng, (m, h)), bf16(rng, (h,))
+    rstd = pk.pact_add_rmsnorm_quant_fp8(hh, None, gamma)[2]
+    dh, dg = pk.pact_add_rmsnorm_bwd(hh, gamma, rstd, dy, dgamma=True)
+    got, dg2 = pk.pact_add_rmsnorm_bwd(hh, gamma, rstd, dy, dh=hh, dgamma=True)
+    assert got is hh and torch.equal(got, dh)
+    assert torch.equal(dg2, dg)
+
+
 def test_product_offsets_past_32_bits():
     """An input and an output of more than 2^32 values: the rows at the end are those
     of a small call on them."""
