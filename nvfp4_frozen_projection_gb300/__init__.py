@@ -208,10 +208,6 @@ class FP8:
         return cls(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
                    torch.empty(cls.scale_shape(rows, cols), dtype=torch.float32, device=device))
 
-    def struct(self) -> _FP8Struct:
-        rows, cols = self.q.shape
-        return _FP8Struct(self.q.data_ptr(), self.s.data_ptr(), rows, cols)
-
 
 class FP8Weight(FP8):
     """Device FP8 weight [rows, cols]: q float8_e4m3fn [rows, cols] and s float32
@@ -245,19 +241,24 @@ def _need(t, dtype, shape, name, dev):
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _need_fp8(t, kind, name, dev, shape=None):
-    """t is an FP8 tensor of this kind (FP8 or FP8Weight), of this shape when given."""
-    if type(t) is not kind:
-        raise ValueError(f"{name} must be an {kind.__name__}, got {type(t).__name__}")
-    shape = tuple(shape or _need_2d(t.q, name + ".q"))
-    _need(t.q, torch.float8_e4m3fn, shape, name + ".q", dev)
-    _need(t.s, torch.float32, kind.scale_shape(*shape), name + ".s", dev)
-
-
 def _need_2d(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     return t.shape
+
+
+def _need_fp8(t, kind, name, dev=None, shape=None) -> _FP8Struct:
+    """t is an FP8 tensor of this kind (FP8 or FP8Weight) on the current device (dev, when
+    it is known already), of this shape when given; its struct for the call."""
+    if type(t) is not kind:
+        raise ValueError(f"{name} must be an {kind.__name__}, got {type(t).__name__}")
+    q, s = t.q, t.s
+    rows, cols = shape = tuple(shape or _need_2d(q, name + ".q"))
+    if dev is None:
+        dev = torch.cuda.current_device()
+    _need(q, torch.float8_e4m3fn, shape, name + ".q", dev)
+    _need(s, torch.float32, kind.scale_shape(rows, cols), name + ".s", dev)
+    return _FP8Struct(q.data_ptr(), s.data_ptr(), rows, cols)
 
 
 def _addr(t):
@@ -551,8 +552,7 @@ def pact_quant_fp8(x: torch.Tensor, out: FP8 | None = None) -> FP8:
         raise ValueError(f"x is on {x.device}, the current device is cuda:{dev}")
     if out is None:
         out = FP8.empty(M, K, x.device)
-    _need_fp8(out, FP8, "out", dev, (M, K))
-    s = out.struct()
+    s = _need_fp8(out, FP8, "out", dev, (M, K))
     # the stride of a single row says nothing: torch may report any number there
     _check(lib.pact_quant_fp8(_addr(x), M, K, x.stride(0) if M > 1 else _pad(K, 8),
                               ctypes.byref(s), _raw_stream(dev)))
@@ -567,8 +567,7 @@ def _pack_fp8(W: torch.Tensor, backward: bool, out: FP8Weight | None) -> FP8Weig
     shape = (K, N) if backward else (N, K)
     if out is None:
         out = FP8Weight.empty(*shape, W.device)
-    _need_fp8(out, FP8Weight, "out", dev, shape)
-    s = out.struct()
+    s = _need_fp8(out, FP8Weight, "out", dev, shape)
     fn = lib.pact_pack_weight_fp8_bwd if backward else lib.pact_pack_weight_fp8_fwd
     _check(fn(_addr(W), N, K, ctypes.byref(s), _raw_stream(dev)))
     return out
@@ -586,21 +585,17 @@ def pact_pack_weight_fp8_bwd(W: torch.Tensor, out: FP8Weight | None = None) -> F
 
 
 def _linear_fp8(fn, x, xname, w, wname, add, addname, y, yname):
-    if not isinstance(x, FP8):
-        raise ValueError(f"{xname} must be an FP8, got {type(x).__name__}")
-    _need_2d(x.q, xname + ".q")
-    dev = torch.cuda.current_device()
-    _need_fp8(x, FP8, xname, dev)
-    _need_fp8(w, FP8Weight, wname, dev)
-    shape = (x.rows, w.rows)
-    if w.cols != x.cols:
-        raise ValueError(f"{xname} has {x.cols} columns, {wname} {w.cols}")
+    sx = _need_fp8(x, FP8, xname)
+    dev = x.q.get_device()
+    sw = _need_fp8(w, FP8Weight, wname, dev)
+    shape = (sx.rows, sw.rows)
+    if sw.cols != sx.cols:
+        raise ValueError(f"{xname} has {sx.cols} columns, {wname} {sw.cols}")
     if y is None:
         y = torch.empty(shape, dtype=torch.bfloat16, device=x.q.device)
     _need(y, torch.bfloat16, shape, yname, dev)
     if add is not None:
         _need(add, torch.bfloat16, shape, addname, dev)
-    sx, sw = x.struct(), w.struct()
     _check(fn(ctypes.byref(sx), ctypes.byref(sw), _addr(add), _addr(y), _raw_stream(dev)))
     return y
 
@@ -641,11 +636,10 @@ def pact_add_rmsnorm_quant_fp8(x: torch.Tensor, residual: torch.Tensor | None,
         raise ValueError("without a residual h is x itself: pass no other h")
     if out is None:
         out = FP8.empty(M, H, x.device)
-    _need_fp8(out, FP8, "out", dev, (M, H))
+    s = _need_fp8(out, FP8, "out", dev, (M, H))
     if rstd is None:
         rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
     _need(rstd, torch.float32, (M,), "rstd", dev)
-    s = out.struct()
     _check(lib.pact_add_rmsnorm_quant_fp8(_addr(x), _addr(residual), _addr(gamma), M, H, float(eps),
                                           _addr(h) if residual is not None else None,
                                           ctypes.byref(s), _addr(rstd), _raw_stream(dev)))
