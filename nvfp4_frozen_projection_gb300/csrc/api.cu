@@ -737,7 +737,7 @@ static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, c
   cudaError_t e;
   if (fp8_is_few(M, N, K, d->sms)) {
     e = launch_fp8_few((const uint8_t*)x->q, x->s, (const uint8_t*)w->q, w->s, M, N, K, add, out,
-                       (cudaStream_t)stream);
+                       d->sms, (cudaStream_t)stream);
   } else {
     Fp8GemmLaunch L;
     std::memset(&L, 0, sizeof(L));

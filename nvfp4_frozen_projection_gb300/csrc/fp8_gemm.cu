@@ -18,8 +18,10 @@
 namespace pact {
 
 // ---------------------------------------------------------------- few tokens
-// A CTA computes 16 output columns (rows of W) for up to 16 tokens; its warps share the
-// blocks of K among them and add their sums through shared memory in warp order.
+// A CTA computes 16 output columns (rows of W) for 8 or 16 tokens; its warps share the
+// blocks of K among them and add their sums through shared memory in warp order.  Further
+// tokens are other CTAs' (blockIdx.y), which read the weight out of L2: 32 x 2048 x 2048
+// 4.0 us, against 6.0 with 32 tokens a CTA and 7.8 on tcgen05.
 // The product is turned: W is the row operand (16 rows) and the tokens the column
 // operand (8 each), so that a single token wastes 7/8 of the tensor work but none of
 // the reads.  Within a block, lane 4 g + t holds the 16-byte pieces t and t + 4 of row
@@ -54,7 +56,8 @@ __global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int nkb = (int)((K + 127) / 128);
   const uint8_t* wr = w + (n0 + g) * K + 16 * t;
-  const uint8_t* xr = x + (int64_t)g * K + 16 * t;
+  const int64_t m0 = (int64_t)blockIdx.y * 8 * NT;
+  const uint8_t* xr = x + (m0 + g) * K + 16 * t;
   const float* swr = sw + (n0 >> 7) * nkb;
   auto load = [&](int kb, FewBlock<NT>& f) {
     const int64_t k0 = (int64_t)kb * 128;
@@ -66,14 +69,14 @@ __global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
       f.a[1][c] = ok ? ldg_stream(wr + 8 * K + k0 + 64 * c) : z;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        f.b[j][c] = ok && 8 * j + g < M
+        f.b[j][c] = ok && m0 + 8 * j + g < M
                         ? *reinterpret_cast<const uint4*>(xr + 8 * j * K + k0 + 64 * c)
                         : z;
     }
     f.sw = swr[kb];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {  // the tokens of d[0] and d[2], d[1] and d[3]
-      const int64_t m = 8 * j + 2 * t;
+      const int64_t m = m0 + 8 * j + 2 * t;
       f.s0[j] = m < M ? sx[(int64_t)kb * M + m] : 0.0f;
       f.s1[j] = m + 1 < M ? sx[(int64_t)kb * M + m + 1] : 0.0f;
     }
@@ -106,16 +109,15 @@ __global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[warp][g + 8 * (i >> 1)][8 * j + 2 * t + (i & 1)] = acc[j][i];
   __syncthreads();
-  if (threadIdx.x < 16 * 8 * NT) {
-    const int n = threadIdx.x & 15, m = threadIdx.x >> 4;
-    if (m < M) {
-      float v = sums[0][n][m];
+  for (int i = threadIdx.x; i < 16 * 8 * NT; i += 32 * WARPS) {
+    const int n = i & 15, m = i >> 4;
+    if (m0 + m >= M) break;
+    float v = sums[0][n][m];
 #pragma unroll
-      for (int k = 1; k < WARPS; ++k) v += sums[k][n][m];
-      const int64_t at = m * N + n0 + n;
-      if (add) v += __uint_as_float((uint32_t)add[at] << 16);
-      if (PACT_IN(at < M * N)) out[at] = (uint16_t)(pack_bf16x2(v, v) & 0xFFFFu);
-    }
+    for (int k = 1; k < WARPS; ++k) v += sums[k][n][m];
+    const int64_t at = (m0 + m) * N + n0 + n;
+    if (add) v += __uint_as_float((uint32_t)add[at] << 16);
+    if (PACT_IN(at < M * N)) out[at] = (uint16_t)(pack_bf16x2(v, v) & 0xFFFFu);
   }
 }
 
@@ -125,16 +127,20 @@ static cudaError_t launch_few(const uint8_t* x, const float* sx, const uint8_t* 
                               const uint16_t* add, uint16_t* out, cudaStream_t stream) {
   note_launch();
   k_fp8_few<NT, WARPS>
-      <<<(unsigned)(N / 16), 32 * WARPS, 0, stream>>>(x, sx, w, sw, M, N, K, add, out);
+      <<<dim3((unsigned)(N / 16), (unsigned)((M + 8 * NT - 1) / (8 * NT))), 32 * WARPS, 0, stream>>>(
+          x, sx, w, sw, M, N, K, add, out);
   return cudaGetLastError();
 }
 
+// CTAs of 16 warps, where each has an SM to itself: 1 x 2048 x 8192 4.5 us against 5.5 with
+// eight, 32 x 1024 x 8192 5.4 against 5.8; 1 x 8192 x 2048 6.5 against 5.2,
+// 32 x 2048 x 2048 5.4 against 4.0.
+static bool few_wide(int64_t M, int64_t N, int sms) { return (N / 16) * ((M + 15) / 16) <= sms; }
+
 cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
                            int64_t M, int64_t N, int64_t K, const uint16_t* add, uint16_t* out,
-                           cudaStream_t stream) {
-  // 16 warps where a CTA has an SM to itself: 1 x 2048 x 8192 4.5 us against 5.5 with
-  // eight; 1 x 8192 x 2048 6.5 against 5.2
-  if (N <= 16 * 152)
+                           int sms, cudaStream_t stream) {
+  if (few_wide(M, N, sms))
     return M <= 8 ? launch_few<1, 16>(x, sx, w, sw, M, N, K, add, out, stream)
                   : launch_few<2, 16>(x, sx, w, sw, M, N, K, add, out, stream);
   return M <= 8 ? launch_few<1, 8>(x, sx, w, sw, M, N, K, add, out, stream)
@@ -145,8 +151,10 @@ cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, 
 // The estimated time (us) of each way to run a product decides.  The constants are fitted
 // to GB300 measurements of M 1 .. 8192, N 512 .. 16384, K 1024 .. 16384 (launch included;
 // b = blocks of 128 along K):
-//   few     2.2 + N K / 4.3e6            16 x 4096 x 4096 5.7 us; 8 x 16384 x 16384 55
-//   tiles   2.7 + waves (1.2 + 0.27 b)   64 x 2048 x 2048 8.3; 128 x 4096 x 8192 21.4;
+//   few     2.2 + the longer of N K / 4.3e6 and waves (0.5 + 0.9 blocks of a warp)
+//                                        16 x 4096 x 4096 5.7 us; 8 x 16384 x 16384 55;
+//                                        24 x 2048 x 2048 3.8; 256 x 512 x 512 3.8
+//   tiles   2.7 + waves (1.2 + 0.27 b)   512 x 2048 x 512 5.0; 128 x 4096 x 8192 21.4;
 //                                        8192 x 4096 x 8192 263
 //   shared  6.3 + 0.29 b / CTAs          128 x 4096 x 8192 12.5; 512 x 1024 x 16384 15.8
 //   pairs   5.0 + waves (1.5 + 0.41 b)   256 x 4096 x 8192 31.4; 2048 x 2048 x 2048 12.9;
@@ -192,7 +200,13 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
     }
   }
   const double weight = (double)N * (double)K;
-  if (M <= 16 && 2.2 + weight / 4.3e6 < std::fmax(best, 3.0 + weight / 5.6e6)) p.way = kFew;
+  const bool wide = few_wide(M, N, sms);
+  const double ctas = (double)(N / 16) * (double)((M + 15) / 16);
+  const double waves = std::fmax(1.0, ctas / (wide ? sms : 2 * sms));
+  const double few =
+      2.2 + std::fmax(weight / 4.3e6, waves * (0.5 + 0.9 * std::ceil(b / (wide ? 16 : 8))));
+  // up to 1024 tokens, beyond which nothing was measured (and the grid would grow too high)
+  if (M <= 1024 && few < std::fmax(best, 3.0 + weight / 5.6e6)) p.way = kFew;
   return p;
 }
 

@@ -174,10 +174,9 @@ struct Fp8GemmLaunch {
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch& L, cudaStream_t stream);
 // Whether a product of this shape runs on launch_fp8_few.
 bool fp8_is_few(int64_t M, int64_t N, int64_t K, int sms);
-// M <= 16.
 cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
                            int64_t M, int64_t N, int64_t K, const uint16_t* add, uint16_t* out,
-                           cudaStream_t stream);
+                           int sms, cudaStream_t stream);
 
 cudaError_t launch_pexp(const float* x, float* y, int64_t n, cudaStream_t stream);
 

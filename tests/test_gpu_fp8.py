@@ -276,7 +276,9 @@ PRODUCTS = [(1, 16, 16), (1, 2048, 2048), (2, 1040, 144), (7, 128, 8192), (8, 27
             (33, 1040, 1040), (64, 2048, 2048), (65, 144, 2064), (127, 1024, 1024),
             (128, 512, 4096), (129, 2064, 656), (200, 1040, 272), (256, 256, 128), (257, 2048, 640),
             (300, 16, 16), (333, 1040, 2064), (512, 4096, 1040), (1000, 1296, 2048),
-            (2050, 528, 1168), (2100, 4080, 1040), (2305, 4096, 144)]
+            (2050, 528, 1168), (2100, 4080, 1040), (2305, 4096, 144),
+            # CTAs of a cluster that share a tile: four, three, two; many CTAs of few tokens
+            (100, 4096, 2192), (120, 4880, 2064), (500, 2048, 4112), (700, 128, 528)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
@@ -320,7 +322,7 @@ def test_linear_many_tiles(m, n, k, with_add):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 2048, 1024), (12, 528, 4112), (24, 1040, 272), (64, 2048, 2064),
-                                   (333, 2064, 1040), (640, 1024, 512), (2100, 4080, 528)])
+                                   (64, 4096, 2064), (333, 2064, 1040), (640, 1024, 512), (2100, 4080, 528)])
 def test_linear_exact_sums(m, n, k):
     """Small whole numbers: every partial sum is exact, so the result is too."""
     rng = np.random.default_rng(k)
