@@ -741,7 +741,8 @@ static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, c
   } else {
     Fp8GemmLaunch L;
     std::memset(&L, 0, sizeof(L));
-    if ((rc = make_map(&L.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x->q, K, M, 128, 128,
+    L.p.box_m = M < 128 ? (int)(M + 7) / 8 * 8 : 128;
+    if ((rc = make_map(&L.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x->q, K, M, 128, L.p.box_m,
                        CU_TENSOR_MAP_SWIZZLE_128B)) ||
         (rc = make_map(&L.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->q, K, N, 128, 128,
                        CU_TENSOR_MAP_SWIZZLE_128B)) ||

@@ -132,19 +132,24 @@ static cudaError_t launch_few(const uint8_t* x, const float* sx, const uint8_t* 
   return cudaGetLastError();
 }
 
-// CTAs of 16 warps, where each has an SM to itself: 1 x 2048 x 8192 4.5 us against 5.5 with
-// eight, 32 x 1024 x 8192 5.4 against 5.8; 1 x 8192 x 2048 6.5 against 5.2,
-// 32 x 2048 x 2048 5.4 against 4.0.
-static bool few_wide(int64_t M, int64_t N, int sms) { return (N / 16) * ((M + 15) / 16) <= sms; }
+// Warps a CTA: 16 where each CTA has an SM to itself, 8 where two of those share one, else
+// 4: 1 x 2048 x 8192 4.5 us with 16 and 5.5 with 8; 32 x 2048 x 2048 5.4, 4.1 with 8, 4.8
+// with 4; 64 x 2048 x 2048 6.7 with 8, 5.7 with 4, 7.7 with 2.
+static int few_warps(int64_t M, int64_t N, int sms) {
+  const int64_t ctas = (N / 16) * ((M + 15) / 16);
+  return ctas <= sms ? 16 : (ctas <= 2 * sms ? 8 : 4);
+}
 
 cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
                            int64_t M, int64_t N, int64_t K, const uint16_t* add, uint16_t* out,
                            int sms, cudaStream_t stream) {
-  if (few_wide(M, N, sms))
-    return M <= 8 ? launch_few<1, 16>(x, sx, w, sw, M, N, K, add, out, stream)
-                  : launch_few<2, 16>(x, sx, w, sw, M, N, K, add, out, stream);
-  return M <= 8 ? launch_few<1, 8>(x, sx, w, sw, M, N, K, add, out, stream)
-                : launch_few<2, 8>(x, sx, w, sw, M, N, K, add, out, stream);
+  const int warps = few_warps(M, N, sms);
+#define PACT_FEW(NT)                                                                       \
+  (warps == 16  ? launch_few<NT, 16>(x, sx, w, sw, M, N, K, add, out, stream)              \
+   : warps == 8 ? launch_few<NT, 8>(x, sx, w, sw, M, N, K, add, out, stream)               \
+                : launch_few<NT, 4>(x, sx, w, sw, M, N, K, add, out, stream))
+  return M <= 8 ? PACT_FEW(1) : PACT_FEW(2);
+#undef PACT_FEW
 }
 
 // ---------------------------------------------------------------- which kernel
@@ -200,11 +205,11 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
     }
   }
   const double weight = (double)N * (double)K;
-  const bool wide = few_wide(M, N, sms);
+  const int warps = few_warps(M, N, sms);
   const double ctas = (double)(N / 16) * (double)((M + 15) / 16);
-  const double waves = std::fmax(1.0, ctas / (wide ? sms : 2 * sms));
+  const double waves = std::fmax(1.0, ctas * warps / (16.0 * sms));
   const double few =
-      2.2 + std::fmax(weight / 4.3e6, waves * (0.5 + 0.9 * std::ceil(b / (wide ? 16 : 8))));
+      2.2 + std::fmax(weight / 4.3e6, waves * (0.5 + 0.9 * std::ceil(b / warps)));
   // up to 1024 tokens, beyond which nothing was measured (and the grid would grow too high)
   if (M <= 1024 && few < std::fmax(best, 3.0 + weight / 5.6e6)) p.way = kFew;
   return p;
@@ -384,11 +389,14 @@ __global__ void __launch_bounds__(384, 1)
             ok = false;
             break;
           }
-          // whole boxes arrive: zeros past K and past the last row.  The leader's barrier
+          // whole boxes arrive: zeros past K and past the last row.  (With fewer than 128
+          // rows in all, X's boxes are no higher than those: boxes mostly past M are slow,
+          // 24 x 16384 x 2048 11.6 us against 9.0.  The rows above hold whatever the
+          // memory held, and reach only sums that are not stored.)  The leader's barrier
           // counts the bytes of both CTAs; the peer's may come before the leader expects
           // them, and the phase still waits for the leader's own arrival.
           const uint32_t sb = base + stage * C::STAGE_BYTES;
-          if (!PAIR || crank == 0) mbar_expect_tx(full0 + 8 * stage, CM * C::STAGE_BYTES);
+          if (!PAIR || crank == 0) mbar_expect_tx(full0 + 8 * stage, CM * (p.box_m * 128 + C::B_BYTES));
           if constexpr (PAIR) {
             const uint32_t fb = lead_full0 + 8 * stage;
             tma_load_2d_pair(sb, &tmX, kb * 128, m0, fb);

@@ -158,14 +158,15 @@ struct Fp8GemmParams {
   uint16_t* out;        // BF16 [M, N]
   unsigned* status;     // device status word
   int M, N, nkb;        // out [M, N], nkb = ceil(K/128)
+  int box_m;            // rows of a box of X: 128, or M rounded up to 8 where that is fewer
   int num_m, num_n;     // tile grid
   int band_mc;          // tile order, as in GemmParams
   int split;            // CTAs that share the blocks of one tile
   int first, units;     // the launch's first tile, and its tiles (or halves)
 };
 struct Fp8GemmLaunch {
-  // U8 maps over X [M, K] and W [N, K], boxes of 128 columns and 128 rows, 128-byte
-  // swizzle; the BF16 output [M, N], boxes of 32 x 32, 64-byte swizzle
+  // U8 maps over X [M, K] and W [N, K], boxes of 128 columns and box_m or 128 rows,
+  // 128-byte swizzle; the BF16 output [M, N], boxes of 32 x 32, 64-byte swizzle
   CUtensorMap tmX, tmW, tmOut;
   Fp8GemmParams p;
   int64_t K;
