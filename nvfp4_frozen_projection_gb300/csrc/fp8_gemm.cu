@@ -243,7 +243,8 @@ bool fp8_is_few(int64_t M, int64_t N, int64_t K, int sms) {
 // 16 blocks instead of one: what is left is that round.  Measured and not kept, all at
 // this size: 16 epilogue warps of 64 columns (232 us), loads carried over from one block to
 // the next (238, it spills), an issuer and a barrier for each sub-block with epilogue
-// warps that take both sub-blocks (238) or one each (230).
+// warps that take both sub-blocks (238) or one each (230), the same with the two issuers
+// (205; its boxes of 64 rows of W alone cost 24 x 16384 x 2048 a microsecond).
 template <bool PAIR>
 struct Fp8Cfg {
   static constexpr int STAGES = 6;
@@ -382,7 +383,8 @@ __global__ void __launch_bounds__(384, 1)
       for (int u = unit0; u < nunits && ok; u += nclusters) {
         int m0, n0;
         unit_mn(u, m0, n0);
-        // of half a tile each CTA uses 64 rows of W, the first of the box
+        // of half a tile each CTA uses 64 rows of W, the first of the box (a box of those
+        // alone gained nothing)
         const int nb = n0 + (int)crank * (PART ? 64 : 128);
         for (int kb = kb0; kb < kb0 + nk; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, kFp8WaitNs, abort_flag)) {
@@ -396,7 +398,8 @@ __global__ void __launch_bounds__(384, 1)
           // counts the bytes of both CTAs; the peer's may come before the leader expects
           // them, and the phase still waits for the leader's own arrival.
           const uint32_t sb = base + stage * C::STAGE_BYTES;
-          if (!PAIR || crank == 0) mbar_expect_tx(full0 + 8 * stage, CM * (p.box_m * 128 + C::B_BYTES));
+          if (!PAIR || crank == 0)
+            mbar_expect_tx(full0 + 8 * stage, CM * (p.box_m * 128 + C::B_BYTES));
           if constexpr (PAIR) {
             const uint32_t fb = lead_full0 + 8 * stage;
             tma_load_2d_pair(sb, &tmX, kb * 128, m0, fb);
