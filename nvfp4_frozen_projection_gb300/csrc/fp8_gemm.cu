@@ -238,13 +238,14 @@ bool fp8_is_few(int64_t M, int64_t N, int64_t K, int sms) {
 // The first warpgroup gives its registers to the epilogue, whose threads hold 128 sums
 // and the columns that land.
 //
-// 8192 x 4096 x 8192 takes 197 us (2.8 PFLOP/s, 0.75 of twice the measured BF16 rate).
+// 8192 x 4096 x 8192 takes 196 to 200 us (2.8 PFLOP/s, 0.75 of twice the measured BF16 rate).
 // When it took 203, it took 193 without the additions and 153 with one barrier round for
 // 16 blocks instead of one: what is left is that round.  Measured and not kept, all at
 // this size: 16 epilogue warps of 64 columns (232 us), loads carried over from one block to
 // the next (238, it spills), an issuer and a barrier for each sub-block with epilogue
-// warps that take both sub-blocks (238) or one each (230), the same with the two issuers
-// (205; its boxes of 64 rows of W alone cost 24 x 16384 x 2048 a microsecond).
+// warps that take both sub-blocks (238) or one each (230), the same with two issuers
+// (205), slices of 32 columns (200, no difference).  Runs differ by 5 % with where the
+// tensors lie in memory.
 template <bool PAIR>
 struct Fp8Cfg {
   static constexpr int STAGES = 6;
