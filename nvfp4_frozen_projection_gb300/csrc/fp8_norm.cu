@@ -15,6 +15,7 @@
 // same order on every call.
 #include "fp8.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 
 namespace pact {
 
@@ -163,8 +164,10 @@ cudaError_t launch_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* res, const
 // end, and a second kernel adds them in a fixed order.  The next row's vectors are loaded
 // before this row is worked on: without that a row's three latencies (the loads, the sum
 // over the group, dres) add up (8192 x 4096: 110 us, 2.4 TB/s).
-// As row_plan, with at most two vectors a thread, since two rows are held at a time; above
-// 8192 columns four and one row.
+// As row_plan, with at most two vectors a thread, since two rows are held at a time.  Above
+// 8192 columns three or four, and the next row waits in shared memory (12288 columns, 2048
+// rows: 42.6 us, 49.9 without the next row; up to 8192 columns that is slower, 4096 x 8192
+// 58.9 us against 50.1).
 static RowPlan bwd_plan(int64_t M, int64_t H) {
   RowPlan p;
   p.wpr = 1;
@@ -247,14 +250,20 @@ __device__ __forceinline__ void dgamma_columns(const uint16_t* h, const uint16_t
   }
 }
 
-// AHEAD: the next row is loaded before this one is worked on.  dgamma, when not null, is
-// made by the CTAs from row_ctas on (H / 16 of them, 256 threads).
-template <int NV, int THREADS, bool AHEAD>
+// dgamma, when not null, is made by the CTAs from row_ctas on (H / 16 of them, 256
+// threads).
+template <int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2))
     k_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* rstd_in,
                       const uint16_t* dy, const uint16_t* dres, int64_t M, int64_t H, int wpr,
                       int row_ctas, uint16_t* dh, float* part, float* dgamma) {
   __shared__ float slots[2][16];
+  // more than two vectors a thread: dgamma's partial sums and the next row in shared
+  // memory, gamma in L1
+  constexpr bool WIDE = NV > 2;
+  extern __shared__ float4 wide_smem[];
+  float4(*dg_wide)[THREADS] = reinterpret_cast<float4(*)[THREADS]>(wide_smem);
+  uint4(*ahead)[THREADS] = reinterpret_cast<uint4(*)[THREADS]>(wide_smem + 2 * NV * THREADS);
   if constexpr (THREADS == 256) {
     __shared__ float sums[8][16];
     if ((int)blockIdx.x >= row_ctas) {
@@ -267,15 +276,24 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
   const int groups = (THREADS / 32) / wpr;
   const float inv_h = __fdiv_rn(1.0f, (float)H);
   const int c0 = (wl * 32 + lane) * 8, cstep = wpr * 256;  // vector i: column c0 + i cstep
-  uint4 gv[NV];
-  float dg[NV][8];
+  uint4 gv[WIDE ? 1 : NV];
+  float dg[WIDE ? 1 : NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    gv[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c0 + i * cstep < H) gv[i] = *reinterpret_cast<const uint4*>(gamma + c0 + i * cstep);
+    if constexpr (WIDE) {
+      dg_wide[2 * i][threadIdx.x] = dg_wide[2 * i + 1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+      gv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c0 + i * cstep < H) gv[i] = *reinterpret_cast<const uint4*>(gamma + c0 + i * cstep);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg[i][e] = 0.0f;
+      for (int e = 0; e < 8; ++e) dg[i][e] = 0.0f;
+    }
   }
+  auto gamma_of = [&](int i) {
+    if constexpr (!WIDE) return gv[i];
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    return c0 + i * cstep < H ? *reinterpret_cast<const uint4*>(gamma + c0 + i * cstep) : z;
+  };
   auto load = [&](int64_t row, BwdRow<NV>& r) {
     r.rstd = rstd_in[row];
 #pragma unroll
@@ -289,15 +307,46 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
       }
     }
   };
+  // WIDE: the next row on its way into shared memory, each thread's vectors in slots of
+  // its own
+  float rstd_next = 0.0f;
+  auto fetch = [&](int64_t row) {
+    rstd_next = rstd_in[row];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * cstep;
+      const uint32_t n = c < H ? 16u : 0u;  // none: zeros
+      const int64_t at = c < H ? row * H + c : 0;
+      cp_async16(smem_addr(&ahead[3 * i][threadIdx.x]), h + at, n);
+      cp_async16(smem_addr(&ahead[3 * i + 1][threadIdx.x]), dy + at, n);
+      cp_async16(smem_addr(&ahead[3 * i + 2][threadIdx.x]), dres ? dres + at : dy, dres ? n : 0u);
+    }
+    cp_async_commit();
+  };
   int turn = 0;
   const int64_t step = (int64_t)row_ctas * groups;
   int64_t row = (int64_t)blockIdx.x * groups + group;
-  BwdRow<NV> cur;
-  if (row < M) load(row, cur);
+  BwdRow<NV> cur, next;
+  if (row < M) {
+    if constexpr (WIDE)
+      fetch(row);
+    else
+      load(row, cur);
+  }
   for (; row < M; row += step) {
-    BwdRow<NV> next;
-    if constexpr (AHEAD) {
-      if (row + step < M) load(row + step, next);
+    if constexpr (WIDE) {
+      cp_async_wait<0>();
+      cur.rstd = rstd_next;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        cur.h[i] = ahead[3 * i][threadIdx.x];
+        cur.dy[i] = ahead[3 * i + 1][threadIdx.x];
+        cur.dres[i] = ahead[3 * i + 2][threadIdx.x];
+      }
+      __syncwarp();  // the slots have been read
+      if (row + step < M) fetch(row + step);
+    } else if (row + step < M) {
+      load(row + step, next);
     }
     float t = 0.0f;
 #pragma unroll
@@ -305,12 +354,26 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
       float f[8], d[8], g[8];
       bf16x8_to_f32(cur.h[i], f);
       bf16x8_to_f32(cur.dy[i], d);
-      bf16x8_to_f32(gv[i], g);
+      bf16x8_to_f32(gamma_of(i), g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float n = __fmul_rn(f[e], cur.rstd);
         t = __fmaf_rn(__fmul_rn(d[e], g[e]), n, t);
-        dg[i][e] = __fmaf_rn(d[e], n, dg[i][e]);
+        if constexpr (WIDE)
+          f[e] = n;
+        else
+          dg[i][e] = __fmaf_rn(d[e], n, dg[i][e]);
+      }
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float4 a = dg_wide[2 * i + k][threadIdx.x];
+          a.x = __fmaf_rn(d[4 * k], f[4 * k], a.x);
+          a.y = __fmaf_rn(d[4 * k + 1], f[4 * k + 1], a.y);
+          a.z = __fmaf_rn(d[4 * k + 2], f[4 * k + 2], a.z);
+          a.w = __fmaf_rn(d[4 * k + 3], f[4 * k + 3], a.w);
+          dg_wide[2 * i + k][threadIdx.x] = a;
+        }
       }
     }
     t = group_sum(t, wpr, wl, group, slots[turn] + group * wpr);
@@ -323,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
       float f[8], d[8], g[8], r[8];
       bf16x8_to_f32(cur.h[i], f);
       bf16x8_to_f32(cur.dy[i], d);
-      bf16x8_to_f32(gv[i], g);
+      bf16x8_to_f32(gamma_of(i), g);
       bf16x8_to_f32(cur.dres[i], r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -338,10 +401,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
       PACT_NAN_BF16X2(o.w);
       if (PACT_IN(row * H + col + 8 <= M * H)) *reinterpret_cast<uint4*>(dh + row * H + col) = o;
     }
-    if constexpr (AHEAD)
-      cur = next;
-    else if (row + step < M)
-      load(row + step, cur);
+    if constexpr (!WIDE) cur = next;
   }
   if (!part) return;
   float* p = part + ((int64_t)blockIdx.x * groups + group) * H;
@@ -349,8 +409,13 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
   for (int i = 0; i < NV; ++i) {
     const int c = c0 + i * cstep;
     if (c >= H) continue;
-    *reinterpret_cast<float4*>(p + c) = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-    *reinterpret_cast<float4*>(p + c + 4) = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+    if constexpr (WIDE) {
+      *reinterpret_cast<float4*>(p + c) = dg_wide[2 * i][threadIdx.x];
+      *reinterpret_cast<float4*>(p + c + 4) = dg_wide[2 * i + 1][threadIdx.x];
+    } else {
+      *reinterpret_cast<float4*>(p + c) = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+      *reinterpret_cast<float4*>(p + c + 4) = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+    }
   }
 }
 
@@ -399,25 +464,34 @@ cudaError_t launch_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, con
   float* pp = dgamma && !small ? part : nullptr;
   if (small && !one) {
     note_launch();
-    k_add_rmsnorm_bwd<1, 256, true><<<cols, 256, 0, stream>>>(h, gamma, rstd, dy, nullptr, M, H, 1,
+    k_add_rmsnorm_bwd<1, 256><<<cols, 256, 0, stream>>>(h, gamma, rstd, dy, nullptr, M, H, 1,
                                                               0, nullptr, nullptr, dgamma);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   note_launch();
-#define PACT_NORM(NV, T, AHEAD)                                                              \
-  k_add_rmsnorm_bwd<NV, T, AHEAD>                                                            \
-      <<<grid + (one ? cols : 0), T, 0, stream>>>(h, gamma, rstd, dy, dres, M, H, p.wpr, grid, \
-                                                  dh, pp, one ? dgamma : nullptr)
-  if (p.nv > 2) {
-    if (p.nv == 3) PACT_NORM(3, 512, false); else PACT_NORM(4, 512, false);
-  } else if (p.threads == 512) {
-    PACT_NORM(2, 512, true);
-  } else if (p.nv == 2) {
-    PACT_NORM(2, 256, true);
-  } else {
-    PACT_NORM(1, 256, true);
+  // five vectors of 16 bytes for each of a thread's: two of sums, three of the next row
+  const size_t smem = p.nv > 2 ? (size_t)p.nv * 5 * 16 * p.threads : 0;
+  if (smem) {
+    cudaError_t e = cudaFuncSetAttribute(
+        p.nv == 4 ? k_add_rmsnorm_bwd<4, 512> : k_add_rmsnorm_bwd<3, 512>,
+        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
   }
+#define PACT_NORM(NV, T)                                                                     \
+  k_add_rmsnorm_bwd<NV, T>                                                                   \
+      <<<grid + (one ? cols : 0), T, smem, stream>>>(h, gamma, rstd, dy, dres, M, H, p.wpr, grid, \
+                                                     dh, pp, one ? dgamma : nullptr)
+  if (p.nv == 4)
+    PACT_NORM(4, 512);
+  else if (p.nv == 3)
+    PACT_NORM(3, 512);
+  else if (p.threads == 512)
+    PACT_NORM(2, 512);
+  else if (p.nv == 2)
+    PACT_NORM(2, 256);
+  else
+    PACT_NORM(1, 256);
 #undef PACT_NORM
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !dgamma || small) return e;
