@@ -207,7 +207,8 @@ def test_add_rmsnorm_in_place(into):
     assert torch.equal(yq.q.view(torch.uint8), yq2.q.view(torch.uint8))
 
 
-@pytest.mark.parametrize("m,h", NORM_SHAPES + [(3000, 1040), (5000, 528), (4097, 64), (1500, 8192)])
+@pytest.mark.parametrize("m,h", NORM_SHAPES + [(3000, 1040), (5000, 528), (4097, 64), (1500, 8192),
+                                            (700, 10000), (320, 16384), (400, 8208)])
 @pytest.mark.parametrize("with_res", [True, False])
 def test_add_rmsnorm_bwd(m, h, with_res):
     rng = np.random.default_rng(m * 5 + h)
@@ -234,7 +235,7 @@ def test_add_rmsnorm_bwd(m, h, with_res):
     assert none is None and torch.equal(again, dh)
 
 
-@pytest.mark.parametrize("m,h", [(40, 1040), (5000, 528), (30, 8192)])
+@pytest.mark.parametrize("m,h", [(40, 1040), (5000, 528), (30, 8192), (500, 12304)])
 def test_add_rmsnorm_bwd_in_place(m, h):
     rng = np.random.default_rng(8)
     hh, dy, dres = (bf16(rng, (m, h)) for _ in range(3))
