@@ -346,7 +346,8 @@ int pact_rmsnorm_bwd(const pact_nvfp4* yq, const uint16_t* gamma, const float* r
  * and no other row is touched.
  * Rules for every call below: rows 1 .. 2^30; cols a multiple of 16, 16 .. 2^24; q
  * 16-byte and s 4-byte aligned.  pact_fp8_scale_count and pact_fp8_weight_scale_count
- * give the number of FP32 values in s.
+ * give the number of FP32 values in s.  A tensor that may be another one is that one
+ * whole or shares no memory with it.
  */
 typedef struct pact_fp8 {
   void* q;
@@ -380,10 +381,10 @@ int pact_pack_weight_fp8_bwd(const float* W, int64_t N, int64_t K, pact_fp8* out
  *                   [+ residual[m, n]] )
  * with FP32 sums and one rounding.  Deterministic.
  *   xq  FP8 activation [M, K];  w_fwd  FP8 weight [N, K];
- *   residual_opt  BF16 [M, N] or NULL (may alias y);  y  BF16 [M, N].
+ *   residual_opt  BF16 [M, N] or NULL (may be y);  y  BF16 [M, N].
  * Input gradient: dX = dYq Wbwd^T [+ dX_prev], the same product over N:
  *   dyq  FP8 gradient [M, N] (pact_quant_fp8);  w_bwd  FP8 weight [K, N];
- *   dx_prev_opt  BF16 [M, K] or NULL (may alias dx, to add to it);  dx  BF16 [M, K].
+ *   dx_prev_opt  BF16 [M, K] or NULL (may be dx, to add to it);  dx  BF16 [M, K].
  * The weight is frozen and has no gradient.  y, dx and the addends 16-byte aligned;
  * ceil(rows / 128) * ceil(output width / 128) < 2^30.
  */
@@ -397,7 +398,7 @@ int pact_linear_fp8_dgrad(const pact_fp8* dyq, const pact_fp8* w_bwd, const uint
  *   h = bf16(x + residual)  (h = x without a residual);
  *   rstd = 1 / sqrt(mean(h^2) + eps);  y = (h rstd) gamma  in FP32, quantised.
  *   x BF16 [M, H];  residual_opt BF16 [M, H] and h_opt BF16 [M, H] out, both or neither
- *   (h may alias x or residual);  gamma BF16 [H];  yq FP8 activation [M, H] out;
+ *   (h may be x or residual);  gamma BF16 [H];  yq FP8 activation [M, H] out;
  *   rstd FP32 [M] out.  x, residual, gamma and h 16-byte aligned.
  * Rules: M 1 .. 2^30, H % 16 == 0, 16 <= H <= 16384, eps finite and >= 0.
  * The result does not depend on the other rows of the call, but its sums may be taken

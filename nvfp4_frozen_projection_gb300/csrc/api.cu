@@ -155,6 +155,13 @@ int check_fp8_cols(int64_t c, const char* name) {
   return PACT_OK;
 }
 
+// Whether two tensors of so many bytes share memory without being the same: an in-place
+// call reads each value before its own thread overwrites it, and no other.
+bool partly_same(const void* a, const void* b, int64_t bytes) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x != y && (x < y ? y - x : x - y) < (uintptr_t)bytes;
+}
+
 // LoRA rank padded to 16, 32 or 64; the fused GEMM's LoRA operands are twice as
 // wide (a hi/lo BF16 pair of the down-projection output).
 int rp_for(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
@@ -732,6 +739,8 @@ static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, c
   if (!out) return fail(PACT_ERR_INVALID_ARG, "%s is required", outname);
   if (!aligned(out, 16) || (add && !aligned(add, 16)))
     return fail(PACT_ERR_ALIGN, "%s and %s must be 16-byte aligned", outname, addname);
+  if (partly_same(add, out, 2 * M * N))
+    return fail(PACT_ERR_INVALID_ARG, "%s overlaps %s in part", addname, outname);
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   cudaError_t e;
@@ -795,6 +804,8 @@ int pact_add_rmsnorm_quant_fp8(const uint16_t* x, const uint16_t* residual_opt,
       !aligned(h_opt, 16) || !aligned(rstd, 4))
     return fail(PACT_ERR_ALIGN, "x, residual, gamma and h must be 16-byte aligned");
   if ((rc = check_fp8(yq, "yq", M, H))) return rc;
+  if (partly_same(h_opt, x, 2 * M * H) || partly_same(h_opt, residual_opt, 2 * M * H))
+    return fail(PACT_ERR_INVALID_ARG, "h overlaps x or residual in part");
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   cudaError_t e = launch_add_rmsnorm_fp8(x, residual_opt, gamma, M, H, eps, h_opt,
@@ -821,6 +832,9 @@ int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* 
   const size_t need = dgamma_opt ? pact_add_rmsnorm_bwd_workspace_size(M, H) : 0;
   if (need && (!ws || ws_bytes < need || !aligned(ws, 256)))
     return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
+  if (partly_same(dh, h, 2 * M * H) || partly_same(dh, dy, 2 * M * H) ||
+      partly_same(dh, dres_opt, 2 * M * H))
+    return fail(PACT_ERR_INVALID_ARG, "dh overlaps h, dy or dres in part");
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   cudaError_t e = launch_add_rmsnorm_bwd(h, gamma, rstd, dy, dres_opt, M, H, dh, dgamma_opt,

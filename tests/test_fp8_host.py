@@ -78,6 +78,8 @@ def test_linear_refusals(lib, name):
     assert f(f8(4, 64, q=P + 8), f8(32, 64), None, P, None) == ALIGN
     assert f(f8(4, 64), f8(32, 64), P + 2, P, None) == ALIGN
     assert f(f8(4, 64), f8(32, 64), None, P + 8, None) == ALIGN
+    for add in (P + 16, P - 16, P + 2 * 4 * 32 - 16):  # in part the output's memory
+        assert f(f8(4, 64), f8(32, 64), add, P, None) == INVALID
 
 
 def test_norm_refusals(lib):
@@ -103,6 +105,8 @@ def test_norm_refusals(lib):
         assert call(**{k: P + 8}) == ALIGN
     assert call(rstd=P + 2) == ALIGN
     assert call(out=f8(4, 80)) == SHAPE
+    for k in ("x", "res", "h"):
+        assert call(**{k: P + 2 * 4 * 64 - 16}) == INVALID
 
 
 def test_norm_bwd_refusals(lib):
@@ -125,6 +129,8 @@ def test_norm_bwd_refusals(lib):
         assert call(**{k: P + 8}) == ALIGN
     assert call(dg=P + 2) == ALIGN
     assert call(n=ok["n"] - 1) == INVALID and call(ws=P + 128) == INVALID
+    for k in ("h", "dy", "dres"):
+        assert call(**{k: P + 16}) == INVALID
     assert size(0, 64) == 0 and size(4, 40) == 0 and size(4, 16400) == 0
     assert size(M, 64) % 256 == 0 and size(M, 64) >= 64 * 4
     assert size(4, 64) == 0  # a small tensor needs none
