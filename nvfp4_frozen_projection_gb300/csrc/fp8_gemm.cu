@@ -12,6 +12,7 @@
 #include "kernels.h"
 #include "tcgen05.cuh"
 
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -793,7 +794,7 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
                                 int64_t first = 0, int64_t count = 0) {
   using C = Fp8Cfg<PAIR>;
   auto kern = k_fp8_gemm<PAIR, SPLIT, ADD, PART>;
-  static int max_clusters[64] = {};  // per device, once its attribute is set
+  static std::atomic<int> max_clusters[64];  // per device, once its attribute is set
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64) return cudaErrorInvalidDevice;
@@ -808,7 +809,8 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (max_clusters[dev] == 0) {
+  int resident = max_clusters[dev].load(std::memory_order_acquire);
+  if (resident == 0) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -824,7 +826,8 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
       if (e != cudaSuccess) return e;
       if (n < 1) return cudaErrorInvalidConfiguration;
     }
-    max_clusters[dev] = n;
+    resident = n;
+    max_clusters[dev].store(n, std::memory_order_release);
   }
   Fp8GemmParams p = L.p;
   p.num_m = (p.M + 127) / 128;
@@ -833,7 +836,7 @@ static cudaError_t launch_tiles(const Fp8GemmLaunch& L, int split, cudaStream_t 
   const int64_t tiles = (int64_t)num_mc * p.num_n;  // < 2^30, checked by the caller
   p.first = (int)first;
   p.units = (int)((count ? count : tiles - first) * (PART ? 2 : 1));
-  const int clusters = SPLIT || p.units < max_clusters[dev] ? p.units : max_clusters[dev];
+  const int clusters = SPLIT || p.units < resident ? p.units : resident;
   cfg.gridDim = dim3(clusters * (SPLIT ? split : C::CM));
   p.split = split;
   // tile order as in the NVFP4 GEMM: one band while X fits in L2 beside the tiles of W
