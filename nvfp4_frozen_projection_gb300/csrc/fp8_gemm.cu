@@ -158,7 +158,8 @@ cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, 
 // to GB300 measurements of M 1 .. 8192, N 512 .. 16384, K 1024 .. 16384 (launch included;
 // b = blocks of 128 along K):
 //   few     2.2 + the longer of N K / 4.3e6 and waves (0.5 + 0.9 blocks of a warp)
-//                                        16 x 4096 x 4096 5.7 us; 8 x 16384 x 16384 55;
+//                                        16 x 4096 x 4096 5.7 us; 8 x 16384 x 16384 63
+//                                        (tiles 49); 8 x 8192 x 4096 9.6 (shared 11.3);
 //                                        24 x 2048 x 2048 3.8; 256 x 512 x 512 3.8
 //   tiles   2.7 + waves (1.2 + 0.27 b)   512 x 2048 x 512 5.0; 128 x 4096 x 8192 21.4;
 //                                        8192 x 4096 x 8192 263
@@ -176,7 +177,6 @@ struct Fp8Plan {
 };
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
   Fp8Plan p = {kFew, 1, 0};
-  if (M <= 8) return p;  // the tensor cores' rows would be empty
   const double b = (double)((K + 127) / 128);
   const double tiles = (double)((M + 127) / 128) * (double)((N + 127) / 128);
   double best = 2.7 + std::ceil(tiles / sms) * (1.2 + 0.27 * b);

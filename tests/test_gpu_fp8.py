@@ -279,7 +279,7 @@ PRODUCTS = [(1, 16, 16), (1, 2048, 2048), (2, 1040, 144), (7, 128, 8192), (8, 27
             (300, 16, 16), (333, 1040, 2064), (512, 4096, 1040), (1000, 1296, 2048),
             (2050, 528, 1168), (2100, 4080, 1040), (2305, 4096, 144),
             # CTAs of a cluster that share a tile: four, three, two; many CTAs of few tokens
-            (100, 4096, 2192), (120, 4880, 2064), (500, 2048, 4112), (700, 128, 528)]
+            (3, 16384, 2064), (100, 4096, 2192), (120, 4880, 2064), (500, 2048, 4112), (700, 128, 528)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
