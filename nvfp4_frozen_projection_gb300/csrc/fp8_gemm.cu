@@ -27,8 +27,10 @@ namespace pact {
 // operand (8 each), so that a single token wastes 7/8 of the tensor work but none of
 // the reads.  Within a block, lane 4 g + t holds the 16-byte pieces t and t + 4 of row
 // g: the order of k inside the contraction is free as long as both operands use the
-// same one, so the fragments come straight from global memory, 64 contiguous bytes of
-// a row per access.
+// same one, so a fragment is a 16-byte read.
+// The weight's way out of HBM bounds it: 1 x 8192 x 8192 takes 14.1 us (4.8 TB/s) with
+// 192 KB an SM on their way into shared memory; with the next block's fragments on their way
+// into registers it took 17.6.
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -38,42 +40,62 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One block of K as a warp holds it: 16 rows of W, 8 NT tokens, their scales.
+// A block's scales, of a lane's tokens and of the weight.
 template <int NT>
-struct FewBlock {
-  uint4 a[2][2], b[NT][2];
+struct FewScales {
   float s0[NT], s1[NT], sw;
 };
 
-// WARPS share the blocks of K.  The next block's loads are in flight while this one is
+// WARPS share the blocks of K.  Each has a ring in shared memory, filled by asynchronous
+// copies, whose stages hold a block's 16 rows of W and 8 NT rows of X, 128 bytes each; row
+// r's 16-byte piece p lies at p ^ 4 (r % 2), so that a quarter warp's reads, four pieces of
+// two rows, meet no bank twice.  The next block's scales are loaded while this one is
 // multiplied.
+template <int NT>
+struct FewCfg {
+  static constexpr int DEPTH = NT == 1 ? 4 : 3;
+  static constexpr int STAGE = 2048 + NT * 1024;
+};
+
 template <int NT, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
     k_fp8_few(const uint8_t* __restrict__ x, const float* __restrict__ sx,
               const uint8_t* __restrict__ w, const float* __restrict__ sw, int64_t M, int64_t N,
               int64_t K, const uint16_t* add, uint16_t* out) {
   __shared__ float sums[WARPS][16][8 * NT + 1];
+  extern __shared__ uint4 few_ring[];
+  constexpr int DEPTH = FewCfg<NT>::DEPTH, STAGE = FewCfg<NT>::STAGE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int nkb = (int)((K + 127) / 128);
-  const uint8_t* wr = w + (n0 + g) * K + 16 * t;
   const int64_t m0 = (int64_t)blockIdx.y * 8 * NT;
-  const uint8_t* xr = x + (m0 + g) * K + 16 * t;
   const float* swr = sw + (n0 >> 7) * nkb;
-  auto load = [&](int kb, FewBlock<NT>& f) {
-    const int64_t k0 = (int64_t)kb * 128;
+  const uint32_t ring = smem_addr(few_ring) + (uint32_t)warp * (DEPTH * STAGE);
+  // lane l copies piece l % 8 of the rows l / 8 + 4 i
+  const int cr = lane >> 3, cp = lane & 7;
+  const uint8_t* wc = w + (n0 + cr) * K + 16 * cp;
+  const uint8_t* xc = x + (m0 + cr) * K + 16 * cp;
+  const uint32_t cdst = ring + (uint32_t)(cr * 128 + ((cp ^ ((cr & 1) << 2)) << 4));
+  auto fetch = [&](int kb, int stage) {
+    if (kb < nkb) {
+      const bool ok = (int64_t)kb * 128 + 16 * cp < K;  // K % 16 == 0: a piece is in or out
+      const int64_t k0 = (int64_t)kb * 128;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const bool ok = k0 + 16 * t + 64 * c < K;  // K % 16 == 0: a piece lies in or out whole
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      f.a[0][c] = ok ? ldg_stream(wr + k0 + 64 * c) : z;
-      f.a[1][c] = ok ? ldg_stream(wr + 8 * K + k0 + 64 * c) : z;
+      for (int i = 0; i < 4; ++i)
+        cp_async16(cdst + (uint32_t)(stage * STAGE + i * 512), ok ? wc + k0 + i * 4 * K : w,
+                   ok ? 16u : 0u);
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        f.b[j][c] = ok && m0 + 8 * j + g < M
-                        ? *reinterpret_cast<const uint4*>(xr + 8 * j * K + k0 + 64 * c)
-                        : z;
+      for (int i = 0; i < 2 * NT; ++i) {  // zeros past K and past the last token
+        const bool in = ok && m0 + cr + 4 * i < M;
+        cp_async16(cdst + (uint32_t)(stage * STAGE + 2048 + i * 512),
+                   in ? xc + k0 + i * 4 * K : x, in ? 16u : 0u);
+      }
     }
+    cp_async_commit();
+  };
+  // rows g and g + 8, pieces t and t + 4
+  const uint32_t rsrc = ring + (uint32_t)(g * 128), sw0 = (uint32_t)((t ^ ((g & 1) << 2)) << 4);
+  auto load = [&](int kb, FewScales<NT>& f) {
     f.sw = swr[kb];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {  // the tokens of d[0] and d[2], d[1] and d[3]
@@ -83,19 +105,31 @@ __global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 24 : 16) / WARPS)
     }
   };
   float acc[NT][4] = {};
-  FewBlock<NT> cur, next;
+  FewScales<NT> cur, next;
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) fetch(warp + i * WARPS, i);
   if (warp < nkb) load(warp, cur);
+  int stage = 0;
   for (int kb = warp; kb < nkb; kb += WARPS) {
+    __syncwarp();  // the block before has been read out of the stage that is filled now
+    fetch(kb + (DEPTH - 1) * WARPS, stage == 0 ? DEPTH - 1 : stage - 1);
     if (kb + WARPS < nkb) load(kb + WARPS, next);
+    cp_async_wait<DEPTH - 1>();
+    __syncwarp();  // every lane's copies of this block have landed
+    uint4 a[2 + NT][2];  // two groups of eight rows of W, then the tokens
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 2 + NT; ++i)
+        a[i][c] = ld_shared_v4(rsrc + (uint32_t)(stage * STAGE + i * 1024) + (sw0 ^ (64u * c)));
+    if (++stage == DEPTH) stage = 0;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float d[4] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        mma_e4m3(d, cur.a[0][c].x, cur.a[1][c].x, cur.a[0][c].y, cur.a[1][c].y, cur.b[j][c].x,
-                 cur.b[j][c].y);
-        mma_e4m3(d, cur.a[0][c].z, cur.a[1][c].z, cur.a[0][c].w, cur.a[1][c].w, cur.b[j][c].z,
-                 cur.b[j][c].w);
+        mma_e4m3(d, a[0][c].x, a[1][c].x, a[0][c].y, a[1][c].y, a[2 + j][c].x, a[2 + j][c].y);
+        mma_e4m3(d, a[0][c].z, a[1][c].z, a[0][c].w, a[1][c].w, a[2 + j][c].z, a[2 + j][c].w);
       }
       const float s0 = __fmul_rn(cur.s0[j], cur.sw), s1 = __fmul_rn(cur.s1[j], cur.sw);
       acc[j][0] = __fmaf_rn(d[0], s0, acc[j][0]);
@@ -126,16 +160,26 @@ template <int NT, int WARPS>
 static cudaError_t launch_few(const uint8_t* x, const float* sx, const uint8_t* w,
                               const float* sw, int64_t M, int64_t N, int64_t K,
                               const uint16_t* add, uint16_t* out, cudaStream_t stream) {
+  constexpr int ring = WARPS * FewCfg<NT>::DEPTH * FewCfg<NT>::STAGE;
+  static std::atomic<uint64_t> attribute_set;  // a bit per device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!(attribute_set.load(std::memory_order_acquire) >> dev & 1)) {
+    cudaError_t e = cudaFuncSetAttribute(k_fp8_few<NT, WARPS>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    if (e != cudaSuccess) return e;
+    attribute_set.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+  }
   note_launch();
-  k_fp8_few<NT, WARPS>
-      <<<dim3((unsigned)(N / 16), (unsigned)((M + 8 * NT - 1) / (8 * NT))), 32 * WARPS, 0, stream>>>(
-          x, sx, w, sw, M, N, K, add, out);
+  k_fp8_few<NT, WARPS><<<dim3((unsigned)(N / 16), (unsigned)((M + 8 * NT - 1) / (8 * NT))),
+                         32 * WARPS, ring, stream>>>(x, sx, w, sw, M, N, K, add, out);
   return cudaGetLastError();
 }
 
 // Warps a CTA: 16 where each CTA has an SM to itself, 8 where two of those share one, else
-// 4: 1 x 2048 x 8192 4.5 us with 16 and 5.5 with 8; 32 x 2048 x 2048 5.4, 4.1 with 8, 4.8
-// with 4; 64 x 2048 x 2048 6.7 with 8, 5.7 with 4, 7.7 with 2.
+// 4 (us with 16, 8, 4): 1 x 2048 x 8192 4.5, 4.9, 6.0; 1 x 4096 x 4096 5.2, 4.4, 4.6;
+// 1 x 8192 x 8192 18.9, 15.7, 14.1; 64 x 2048 x 2048 8.8, 6.2, 5.7.
 static int few_warps(int64_t M, int64_t N, int sms) {
   const int64_t ctas = (N / 16) * ((M + 15) / 16);
   return ctas <= sms ? 16 : (ctas <= 2 * sms ? 8 : 4);
@@ -157,10 +201,12 @@ cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, 
 // The estimated time (us) of each way to run a product decides.  The constants are fitted
 // to GB300 measurements of M 1 .. 8192, N 512 .. 16384, K 1024 .. 16384 (launch included;
 // b = blocks of 128 along K):
-//   few     2.2 + the longer of N K / 4.3e6 and waves (0.5 + 0.9 blocks of a warp)
-//                                        16 x 4096 x 4096 5.7 us; 8 x 16384 x 16384 63
-//                                        (tiles 49); 8 x 8192 x 4096 9.6 (shared 11.3);
-//                                        24 x 2048 x 2048 3.8; 256 x 512 x 512 3.8
+//   few     2.2 + the longer of N K / r and waves (0.5 + c blocks of a warp), r = 5.4e6 and
+//           c = 0.65 up to 8 tokens, else 4.3e6 and 0.9
+//                                        1 x 8192 x 8192 14.1 us (tiles, shared 17.1);
+//                                        1 x 16384 x 16384 45.8 (47.2), 8 tokens 48.8 (47.2);
+//                                        16 x 4096 x 4096 5.8; 24 x 2048 x 2048 4.0;
+//                                        256 x 512 x 512 3.1
 //   tiles   2.7 + waves (1.2 + 0.27 b)   512 x 2048 x 512 5.0; 128 x 4096 x 8192 21.4;
 //                                        8192 x 4096 x 8192 263
 //   shared  6.3 + 0.29 b / CTAs          128 x 4096 x 8192 12.5; 512 x 1024 x 16384 15.8
@@ -209,8 +255,9 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
   const int warps = few_warps(M, N, sms);
   const double ctas = (double)(N / 16) * (double)((M + 15) / 16);
   const double waves = std::fmax(1.0, ctas * warps / (16.0 * sms));
+  const double rate = M <= 8 ? 5.4e6 : 4.3e6, block = M <= 8 ? 0.65 : 0.9;
   const double few =
-      2.2 + std::fmax(weight / 4.3e6, waves * (0.5 + 0.9 * std::ceil(b / warps)));
+      2.2 + std::fmax(weight / rate, waves * (0.5 + block * std::ceil(b / warps)));
   // up to 1024 tokens, beyond which nothing was measured (and the grid would grow too high)
   if (M <= 1024 && few < std::fmax(best, 3.0 + weight / 5.6e6)) p.way = kFew;
   return p;
