@@ -376,6 +376,16 @@ __global__ void __launch_bounds__(384, 1)
   const int kb0 = SPLIT ? (int)((int64_t)p.nkb * krank / p.split) : 0;
   const int nk = (SPLIT ? (int)((int64_t)p.nkb * (krank + 1) / p.split) : p.nkb) - kb0;
   const int band = p.band_mc;
+  // A wait on a barrier that is signalled from outside this CTA in a pair: the copies, the
+  // MMAs' commits and the accumulators' releases.  The releases are relaxed: what they
+  // order are TMEM reads, which tcgen05.wait::ld and the tcgen05 fences on both sides keep
+  // in place.
+  auto wait_x_for = [&](uint32_t bar, uint32_t par, uint64_t ns, const volatile uint32_t* flag) {
+    return PAIR ? mbar_wait_cluster(bar, par, ns, flag) : mbar_wait(bar, par, ns, flag);
+  };
+  auto wait_x = [&](uint32_t bar, uint32_t par) {
+    return wait_x_for(bar, par, kFp8WaitNs, abort_flag);
+  };
   // the first row and column of unit u
   auto unit_mn = [&](int u, int& m0, int& n0) {
     const int t = p.first + (PART ? u >> 1 : u);
@@ -436,7 +446,7 @@ __global__ void __launch_bounds__(384, 1)
         // alone gained nothing)
         const int nb = n0 + (int)crank * (PART ? 64 : 128);
         for (int kb = kb0; kb < kb0 + nk; ++kb) {
-          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, kFp8WaitNs, abort_flag)) {
+          if (!wait_x(empty0 + 8 * stage, phase ^ 1u)) {
             ok = false;
             break;
           }
@@ -477,13 +487,13 @@ __global__ void __launch_bounds__(384, 1)
         } else {
           for (int s = 0; s < STAGES; ++s)
             if (pend & (1u << s))
-              mbar_wait(full0 + 8 * s, (pend_par >> s) & 1u, 10000000ull, nullptr);
+              wait_x_for(full0 + 8 * s, (pend_par >> s) & 1u, 10000000ull, nullptr);
         }
       } else if constexpr (PAIR) {
         // the leader's commits arrive on this CTA's empty barriers: wait for the last
         // STAGES of them before the CTA may exit
         for (int i = 0; i < STAGES; ++i) {
-          mbar_wait(empty0 + 8 * stage, phase ^ 1u, kFp8WaitNs, abort_flag);
+          wait_x(empty0 + 8 * stage, phase ^ 1u);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -499,9 +509,6 @@ __global__ void __launch_bounds__(384, 1)
       // the ring is unrolled, so that a stage's and a buffer's addresses are the base and
       // a constant.
       const int my_units = unit0 < nunits ? (nunits - unit0 + nclusters - 1) / nclusters : 0;
-      auto wait_x = [&](uint32_t bar, uint32_t par) {
-        return mbar_wait(bar, par, kFp8WaitNs, abort_flag);
-      };
       constexpr uint32_t idesc = idesc_e4m3(128, 128 * CM);
       const uint64_t d0 = smem_desc(base, 16, 1024, 2);
       bool ok = true;
@@ -516,8 +523,8 @@ __global__ void __launch_bounds__(384, 1)
             const int s = i % STAGES, cyc = i % C::CYC;
             const uint32_t fills = pass * (C::ROUND / STAGES) + i / STAGES;
             const uint32_t uses = pass * (C::ROUND / C::CYC) + i / C::CYC;
-            const uint32_t seen = mbar_test_two(full0 + 8 * s, fills & 1u,
-                                                acce0 + 8 * (cyc * NSUB), (uses & 1u) ^ 1u);
+            const uint32_t seen = mbar_test_two<PAIR>(full0 + 8 * s, fills & 1u,
+                                                      acce0 + 8 * (cyc * NSUB), (uses & 1u) ^ 1u);
             if (!(seen & 1u) && !wait_x(full0 + 8 * s, fills & 1u)) {
               ok = false;
               break;
@@ -628,7 +635,7 @@ __global__ void __launch_bounds__(384, 1)
     auto wait_block = [&]() {
       if ((blk & 7u) == 0 && !mbar_wait(sclf0 + (blk & 8u), (blk >> 4) & 1u, kFp8WaitNs, abort_flag))
         return false;
-      return mbar_wait(accf0 + 8 * buf(), (blk / C::CYC) & 1u, kFp8WaitNs, abort_flag);
+      return wait_x(accf0 + 8 * buf(), (blk / C::CYC) & 1u);
     };
     auto scale = [&]() {
       const uint32_t at = base + C::SCL_OFF + (blk & 15u) * C::SCL_SLOT;

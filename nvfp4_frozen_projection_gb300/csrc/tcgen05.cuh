@@ -126,20 +126,34 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 
 // Whether the phases of two barriers with these parities have completed, without
 // suspending the thread.  One question alone takes about 135 cycles (GB300); asked
-// together they overlap.  Bit 0: the first, bit 1: the second.
+// together they overlap.  Bit 0: the first, bit 1: the second.  CLUSTER: for barriers
+// that other CTAs of the cluster arrive on.
+template <bool CLUSTER>
 __device__ __forceinline__ uint32_t mbar_test_two(uint32_t bar0, uint32_t par0, uint32_t bar1,
                                                   uint32_t par1) {
   uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t"
-      "selp.u32 t, 2, 0, q;\n\t"
-      "or.b32 %0, %0, t;\n\t}"
-      : "=&r"(r)
-      : "r"(bar0), "r"(par0), "r"(bar1), "r"(par1)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%3], %4;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "selp.u32 t, 2, 0, q;\n\t"
+        "or.b32 %0, %0, t;\n\t}"
+        : "=&r"(r)
+        : "r"(bar0), "r"(par0), "r"(bar1), "r"(par1)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "selp.u32 t, 2, 0, q;\n\t"
+        "or.b32 %0, %0, t;\n\t}"
+        : "=&r"(r)
+        : "r"(bar0), "r"(par0), "r"(bar1), "r"(par1)
+        : "memory");
   return r;
 }
 

@@ -1,0 +1,42 @@
+"""Orderings inside the FP8 product's kernel that no result shows: read from its source."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "nvfp4_frozen_projection_gb300", "csrc")
+
+
+def _code(name):
+    src = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", src, flags=re.S))
+
+
+def _calls(src, name):
+    """The first argument and the template arguments of each call of `name`."""
+    return [(m.group(2).strip(), m.group(1)) for m in
+            re.finditer(r"\b%s(<\w+>)?\(([^,()]*)" % name, src)]
+
+
+@pytest.mark.parametrize("barrier", ["full0", "empty0", "accf0", "acce0"])
+def test_waits_on_barriers_of_a_pair_have_cluster_scope(barrier):
+    """In a pair the other CTA's copies, commits and releases arrive on these barriers, so
+    every wait on them is wait_x, wait_x_for or mbar_test_two<PAIR>: cluster scope there,
+    CTA scope in a kernel without a pair."""
+    src = _code("fp8_gemm.cu")
+    src = src[src.index("k_fp8_gemm("):]
+    waits = [c for c, _ in _calls(src, "wait_x") + _calls(src, "wait_x_for")]
+    tests = _calls(src, "mbar_test_two")
+    assert any(c.startswith(barrier) for c in waits)
+    assert not [c for c, _ in _calls(src, "mbar_wait") if c.startswith(barrier)]
+    assert tests and all(t == "<PAIR>" for _, t in tests)
+    assert re.search(r"return PAIR \? mbar_wait_cluster\(bar, par, ns, flag\)", src)
+
+
+def test_cluster_waits_acquire_at_cluster_scope():
+    src = _code("tcgen05.cuh")
+    for name, n in (("mbar_try_wait_cluster", 1), ("mbar_test_two", 2)):
+        body = src[src.index(" %s(" % name):]
+        body = body[:body.index("\n}")]
+        assert len(re.findall(r"mbarrier\.(?:try|test)_wait\.parity\.acquire\.cluster", body)) == n
