@@ -32,7 +32,8 @@
  *     The release build does not look; a NaN or an infinity there gives
  *     unspecified output values (codes, scales and per-tensor scales included),
  *     but every call still stays within its buffers and ends: no value steers an
- *     address or a loop bound.
+ *     address or a loop bound.  The FP8 calls take a NaN or an infinity and say what
+ *     becomes of it; the debug build records none there.
  */
 #ifndef PACT_H
 #define PACT_H
@@ -343,7 +344,8 @@ int pact_rmsnorm_bwd(const pact_nvfp4* yq, const uint16_t* gamma, const float* r
  * The GEMM takes any scales, also ones that another program made, as long as the products
  * of an activation's and a weight's scales are normal FP32 numbers or zero.
  * A NaN or an infinity becomes a NaN code: of an activation, that row of a product is NaN
- * and no other row is touched.
+ * and no other row is touched.  One in the norm's backward dy leaves no finite value in its
+ * row of dh and in its column of dgamma, and touches nothing else.
  * Rules for every call below: rows 1 .. 2^30; cols a multiple of 16, 16 .. 2^24; q
  * 16-byte and s 4-byte aligned.  pact_fp8_scale_count and pact_fp8_weight_scale_count
  * give the number of FP32 values in s.  A tensor that may be another one is that one

@@ -507,12 +507,17 @@ __device__ __forceinline__ uint32_t e2m1x2_scaled_bf16x2(uint32_t byte, __half2 
 }
 
 // max |bf16| over 8 packed values, as FP32 bits (non-negative, so unsigned order).
-__device__ __forceinline__ uint32_t absmax_bf16x8_bits(const uint4& v) {
-  PACT_NAN_BF16X2(v.x), PACT_NAN_BF16X2(v.y), PACT_NAN_BF16X2(v.z), PACT_NAN_BF16X2(v.w);
+// A NaN counts as larger than infinity.
+__device__ __forceinline__ uint32_t absmax_bf16x8_bits_any(const uint4& v) {
   uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
   uint32_t hi = m >> 16, lo = m & 0xFFFFu;
   return (hi > lo ? hi : lo) << 16;
+}
+// The same for finite inputs: the debug build records a NaN.
+__device__ __forceinline__ uint32_t absmax_bf16x8_bits(const uint4& v) {
+  PACT_NAN_BF16X2(v.x), PACT_NAN_BF16X2(v.y), PACT_NAN_BF16X2(v.z), PACT_NAN_BF16X2(v.w);
+  return absmax_bf16x8_bits_any(v);
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {

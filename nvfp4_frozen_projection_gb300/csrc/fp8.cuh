@@ -8,6 +8,8 @@
 // its own (its values are zeros).  The product with r instead of a division by s is
 // part of the definition: one instruction per value, and the two differ only where a
 // quotient lies within 2^-23 of a rounding border of E4M3, whose steps are 2^-4.
+// A NaN or an infinity is taken as it is (its code is a NaN), so the FP8 kernels have none
+// of the debug build's checks for NaN.
 #pragma once
 
 #include "common.cuh"

@@ -102,10 +102,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2)
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    PACT_NAN_BF16X2(hv[i].x);
-    PACT_NAN_BF16X2(hv[i].y);
-    PACT_NAN_BF16X2(hv[i].z);
-    PACT_NAN_BF16X2(hv[i].w);
     float f[8];
     bf16x8_to_f32(hv[i], f);
 #pragma unroll
@@ -395,10 +391,6 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
       }
       const uint4 o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-      PACT_NAN_BF16X2(o.x);
-      PACT_NAN_BF16X2(o.y);
-      PACT_NAN_BF16X2(o.z);
-      PACT_NAN_BF16X2(o.w);
       if (PACT_IN(row * H + col + 8 <= M * H)) *reinterpret_cast<uint4*>(dh + row * H + col) = o;
     }
     if constexpr (!WIDE) cur = next;

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256, 6)
   uint32_t pk[kQRows / 4];
 #pragma unroll
   for (int i = 0; i < kQRows / 4; ++i) {
-    pk[i] = (absmax_bf16x8_bits(v[2 * i]) >> 16) | absmax_bf16x8_bits(v[2 * i + 1]);
+    pk[i] = (absmax_bf16x8_bits_any(v[2 * i]) >> 16) | absmax_bf16x8_bits_any(v[2 * i + 1]);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
       pk[i] = __vmaxu2(pk[i], __shfl_xor_sync(0xFFFFFFFFu, pk[i], o));
@@ -84,10 +84,6 @@ __global__ void __launch_bounds__(256)
   for (int i = warp; i < 128; i += 8)
     if (n0 + i < N && col_ok) {
       const float4 w = *reinterpret_cast<const float4*>(W + (n0 + i) * K + k0 + 4 * lane);
-      PACT_NAN_F32(w.x);
-      PACT_NAN_F32(w.y);
-      PACT_NAN_F32(w.z);
-      PACT_NAN_F32(w.w);
       amax = fmaxf(amax, fmaxf(fmaxf(fabsf(w.x), fabsf(w.y)), fmaxf(fabsf(w.z), fabsf(w.w))));
     }
 #pragma unroll

@@ -10,7 +10,8 @@
 //     corrupting memory;
 //   - NaN in the values a quantisation, statistic or output amax reads
 //     (PACT_NAN_*): inputs are finite by contract, and a NaN records PACT_DEV_NAN
-//     while the values are used as they are.
+//     while the values are used as they are.  The FP8 calls take a NaN, and have none
+//     of these.
 #pragma once
 
 #include <stdint.h>
