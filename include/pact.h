@@ -470,6 +470,18 @@ int pact_test_wait_timeout(uint32_t limit_us, pact_stream_t stream);
  */
 int pact_test_bounds_check(pact_stream_t stream);
 
+/*
+ * How pact_linear_fp8_fwd and pact_linear_fp8_dgrad run a product of `rows` rows, output
+ * width N and reduction width K on a device of `sms` SMs (host arithmetic only, for tests):
+ *   plan[0]  0: few tokens, warp-level MMAs; 1: a CTA per 128 x 128 tile; 2: a cluster per
+ *            tile, its CTAs sharing the reduction; 3: CTA pairs, 256 x 256 tiles
+ *   plan[1]  way 0: warps a CTA; way 2: CTAs a tile; else 1
+ *   plan[2]  way 3: the tiles of the whole waves, before a last wave of half tiles; 0
+ *            without one
+ * The sizes obey the product's rules.
+ */
+int pact_test_fp8_plan(int64_t rows, int64_t N, int64_t K, int sms, int64_t plan[3]);
+
 /* Synchronises the stream, then returns and clears the device status word:
  * PACT_OK, PACT_ERR_TIMEOUT or PACT_ERR_DEVICE_STATUS.  For tests and debugging. */
 int pact_check_status(pact_stream_t stream);

@@ -26,7 +26,7 @@ __all__ = [
     "pact_quant_fp8", "pact_pack_weight_fp8_fwd", "pact_pack_weight_fp8_bwd",
     "pact_linear_fp8_fwd", "pact_linear_fp8_dgrad", "pact_add_rmsnorm_quant_fp8",
     "pact_add_rmsnorm_bwd",
-    "pact_test_wait_timeout", "pact_test_bounds_check", "pact_check_status",
+    "pact_test_fp8_plan", "pact_test_wait_timeout", "pact_test_bounds_check", "pact_check_status",
     "pact_device_supported", "pact_launch_count", "pact_profile_next_gemm", "pact_version",
 ]
 
@@ -101,6 +101,7 @@ _SIGNATURES = {
     "pact_add_rmsnorm_quant_fp8": (_int, [_vp, _vp, _vp, _i64, _i64, _f32, _vp, _SP8, _vp, _vp]),
     "pact_add_rmsnorm_bwd_workspace_size": (_sz, [_i64, _i64]),
     "pact_add_rmsnorm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "pact_test_fp8_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_i64)]),
     "pact_test_pexp": (_int, [_vp, _vp, _i64, _vp]),
     "pact_test_wait_timeout": (_int, [ctypes.c_uint32, _vp]),
     "pact_test_bounds_check": (_int, [_vp]),
@@ -680,6 +681,14 @@ def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tenso
                                     _addr(dh), _addr(dgamma), _addr(ws),
                                     0 if ws is None else ws.numel(), _raw_stream(dev)))
     return dh, dgamma
+
+
+def pact_test_fp8_plan(rows: int, n: int, k: int, sms: int = 152) -> tuple:
+    """How the FP8 product runs these sizes on a device of so many SMs: (way, CTAs or warps,
+    tiles before a last wave of halves).  Host arithmetic only."""
+    plan = (_i64 * 3)()
+    _check((_LIB or load_library()).pact_test_fp8_plan(rows, n, k, sms, plan))
+    return ("few", "tiles", "shared", "pairs")[plan[0]], plan[1], plan[2]
 
 
 def pact_test_pexp(x: torch.Tensor) -> torch.Tensor:

@@ -723,19 +723,27 @@ int pact_pack_weight_fp8_bwd(const float* W, int64_t N, int64_t K, pact_fp8* out
   return pack_fp8(W, N, K, out_bwd, stream, 1);
 }
 
-static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, const char* wname,
-                      const uint16_t* add, const char* addname, uint16_t* out,
-                      const char* outname, pact_stream_t stream) {
+// The rules on a product's sizes.
+static int check_fp8_product(int64_t M, int64_t N, int64_t K) {
   int rc;
-  if (!x || !w) return fail(PACT_ERR_INVALID_ARG, "%s and %s are required", xname, wname);
-  const int64_t M = x->rows, K = x->cols, N = w->rows;
   if (M < 1 || M > kFp8MaxRows) return fail(PACT_ERR_SHAPE, "need 1 <= rows <= 2^30");
   if ((rc = check_fp8_cols(K, "the reduction width")) ||
       (rc = check_fp8_cols(N, "the output width")))
     return rc;
   if (((M + 127) / 128) * ((N + 127) / 128) >= (int64_t)1 << 30)
     return fail(PACT_ERR_SHAPE, "output too large: ceil(M / 128) * ceil(N / 128) must be < 2^30");
-  if ((rc = check_fp8(x, xname, M, K)) || (rc = check_fp8(w, wname, N, K))) return rc;
+  return PACT_OK;
+}
+
+static int linear_fp8(const pact_fp8* x, const char* xname, const pact_fp8* w, const char* wname,
+                      const uint16_t* add, const char* addname, uint16_t* out,
+                      const char* outname, pact_stream_t stream) {
+  int rc;
+  if (!x || !w) return fail(PACT_ERR_INVALID_ARG, "%s and %s are required", xname, wname);
+  const int64_t M = x->rows, K = x->cols, N = w->rows;
+  if ((rc = check_fp8_product(M, N, K)) || (rc = check_fp8(x, xname, M, K)) ||
+      (rc = check_fp8(w, wname, N, K)))
+    return rc;
   if (!out) return fail(PACT_ERR_INVALID_ARG, "%s is required", outname);
   if (!aligned(out, 16) || (add && !aligned(add, 16)))
     return fail(PACT_ERR_ALIGN, "%s and %s must be 16-byte aligned", outname, addname);
@@ -840,6 +848,14 @@ int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* 
   cudaError_t e = launch_add_rmsnorm_bwd(h, gamma, rstd, dy, dres_opt, M, H, dh, dgamma_opt,
                                          (float*)ws, (cudaStream_t)stream);
   return e == cudaSuccess ? PACT_OK : cuda_fail(e, "add rmsnorm bwd launch");
+}
+
+int pact_test_fp8_plan(int64_t rows, int64_t N, int64_t K, int sms, int64_t plan[3]) {
+  const int rc = check_fp8_product(rows, N, K);
+  if (rc) return rc;
+  if (sms < 2 || !plan) return fail(PACT_ERR_INVALID_ARG, "need two SMs or more, and plan");
+  fp8_plan_of(rows, N, K, sms, plan);
+  return PACT_OK;
 }
 
 int pact_test_wait_timeout(uint32_t limit_us, pact_stream_t stream) {

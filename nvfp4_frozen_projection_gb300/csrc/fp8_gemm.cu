@@ -263,6 +263,13 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
   return p;
 }
 
+void fp8_plan_of(int64_t M, int64_t N, int64_t K, int sms, int64_t plan[3]) {
+  const Fp8Plan p = fp8_plan(M, N, K, sms);
+  plan[0] = p.way;
+  plan[1] = p.way == kFew ? few_warps(M, N, sms) : (p.way == kShared ? p.split : 1);
+  plan[2] = p.way == kPairs ? p.whole : 0;
+}
+
 bool fp8_is_few(int64_t M, int64_t N, int64_t K, int sms) {
   return fp8_plan(M, N, K, sms).way == kFew;
 }

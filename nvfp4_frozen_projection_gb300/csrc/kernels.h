@@ -173,6 +173,8 @@ struct Fp8GemmLaunch {
   int num_sms;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch& L, cudaStream_t stream);
+// What pact_test_fp8_plan gives.
+void fp8_plan_of(int64_t M, int64_t N, int64_t K, int sms, int64_t plan[3]);
 // Whether a product of this shape runs on launch_fp8_few.
 bool fp8_is_few(int64_t M, int64_t N, int64_t K, int sms);
 cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
