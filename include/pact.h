@@ -341,8 +341,11 @@ int pact_rmsnorm_bwd(const pact_nvfp4* yq, const uint16_t* gamma, const float* r
  * element: e4m3(q) * s.  A block with largest magnitude amax is encoded with
  *   t = max(amax, 448 * 2^-126);  s = RN(t / 448);  r = RN(448 / t);
  *   q = e4m3_rne_satfinite(RN(x r))   (FP32 arithmetic; signed zeros are kept).
- * The GEMM takes any scales, also ones that another program made, as long as the products
- * of an activation's and a weight's scales are normal FP32 numbers or zero.
+ * The GEMM takes any finite scales, also ones that another program made, as long as no
+ * product of an activation's and a weight's scale overflows FP32.  It rounds that product to
+ * FP32 first.  One below 2^-126 is a multiple of 2^-149 then, which adds up to 2^-150 times
+ * the sum of the block's |xq.q w.q| to an output's error; a block of zero codes, whose scale
+ * is 2^-126, still gives zero.
  * A NaN or an infinity becomes a NaN code: of an activation, that row of a product is NaN
  * and no other row is touched.  One in the norm's backward dy leaves no finite value in its
  * row of dh and in its column of dgamma, and touches nothing else.

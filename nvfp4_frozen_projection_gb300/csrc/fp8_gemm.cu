@@ -6,8 +6,10 @@
 // X [M, K] and W [N, K] are E4M3 (K contiguous), sx FP32 [ceil(K/128), M], sw FP32
 // [ceil(N/128), ceil(K/128)].  A block's products are summed on the tensor cores in
 // FP32; each block's sum is then multiplied by its two scales and added in FP32
-// registers, so scales are any FP32 numbers, not powers of two only.  The input
-// gradient is the same product on the weight's backward layout.
+// registers, so scales need not be powers of two.  The two scales are multiplied first, in
+// FP32: a product below 2^-126 (block maxima near 2^-117 against ordinary weights) has
+// fewer than 24 bits.  The input gradient is the same product on the weight's backward
+// layout.
 #include "fp8.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
