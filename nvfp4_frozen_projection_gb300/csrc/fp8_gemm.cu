@@ -30,9 +30,10 @@ namespace pact {
 // the reads.  Within a block, lane 4 g + t holds the 16-byte pieces t and t + 4 of row
 // g: the order of k inside the contraction is free as long as both operands use the
 // same one, so a fragment is a 16-byte read.
-// The weight's way out of HBM bounds it: 1 x 8192 x 8192 takes 14.1 us (4.8 TB/s) with
-// 192 KB an SM on their way into shared memory; with the next block's fragments on their way
-// into registers it took 17.6.
+// The weight's way out of HBM bounds it: 1 x 8192 x 8192 takes 13.9 us (4.8 TB/s) with up
+// to 128 KB of the weight an SM on their way into shared memory; with the next block's
+// fragments on their way into registers it took 17.6.  A weight that stays in L2 from one
+// call to the next is faster (1 x 8192 x 8192 11.3, 1 x 4096 x 8192 6.5 against 8.8).
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -201,22 +202,31 @@ cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, 
 
 // ---------------------------------------------------------------- which kernel
 // The estimated time (us) of each way to run a product decides.  The constants are fitted
-// to GB300 measurements of M 1 .. 8192, N 512 .. 16384, K 1024 .. 16384 (launch included;
-// b = blocks of 128 along K):
-//   few     2.2 + the longer of N K / r and waves (0.5 + c blocks of a warp), r = 5.4e6 and
-//           c = 0.65 up to 8 tokens, else 4.3e6 and 0.9
-//                                        1 x 8192 x 8192 14.1 us (tiles, shared 17.1);
-//                                        1 x 16384 x 16384 45.8 (47.2), 8 tokens 48.8 (47.2);
-//                                        16 x 4096 x 4096 5.8; 24 x 2048 x 2048 4.0;
+// to GB300 measurements of M 1 .. 8192, N 512 .. 131072, K 512 .. 28672 (launch included;
+// b = blocks of 128 along K); smaller products follow the same formulas.
+//   few     up to 8 tokens 2.2 + the whole waves of resident CTAs + the last one.  A wave
+//           that fills `full` of the places takes the longer of its bytes of W at 6.2e6 a us
+//           and 0.5 + (0.3 + 0.4 full + 0.012 (M - 1)) blocks of a warp.
+//           More tokens: 2.2 + the longer of N K / 4.3e6 and waves (0.5 + 0.9 blocks of a
+//           warp)                        16 x 4096 x 4096 5.8 us; 24 x 2048 x 2048 4.0;
 //                                        256 x 512 x 512 3.1
 //   tiles   2.7 + waves (1.2 + 0.27 b)   512 x 2048 x 512 5.0; 128 x 4096 x 8192 21.4;
 //                                        8192 x 4096 x 8192 263
 //   shared  6.3 + 0.29 b / CTAs          128 x 4096 x 8192 12.5; 512 x 1024 x 16384 15.8
 //   pairs   5.0 + waves (1.5 + 0.41 b)   256 x 4096 x 8192 31.4; 2048 x 2048 x 2048 12.9;
 //                                        8192 x 4096 x 8192 196
-// and none but `few` under 3 + N K / 5.6e6, the weight's way out of HBM.  Sharing a tile's
-// blocks among a cluster's CTAs helps where there are few tiles; clusters of three or four
-// with this much shared memory fill 128 SMs, pairs all of them.
+// and none but `few` under the weight's way out of HBM: 4.5 + N K / 6.2e6 up to 8 tokens,
+// 3 + N K / 5.6e6 beyond.  Sharing a tile's blocks among a cluster's CTAs helps where there
+// are few tiles; clusters of three or four with this much shared memory fill 128 of 152 SMs,
+// pairs all of them.
+// Up to 8 tokens, with weights that come out of HBM (us; few, the best other way; the one
+// taken first):
+//   1 x  8192 x  8192  few 13.9, shared 17.3     1 x 28672 x  8192  few 37.9, tiles 45.0
+//   1 x  8192 x 16384  few 24.8, shared 27.6     1 x 16384 x 16384  few 46.4, tiles 48.8
+//   1 x 14336 x 14336  tiles 37.6, few 39.3      8 x 12288 x 12288  tiles 30.9, few 37.1
+//   1 x  5120 x 13824  few 17.2, shared 18.7     8 x 10240 x  8192  tiles 20.6, few 22.8
+// Of 32 weights at 1, 2, 5 and 8 tokens the estimate takes the slower way for six products,
+// which then take 2 to 6 % longer (2 x 5120 x 13824: shared 18.7, few 17.7).
 enum Fp8Way { kFew, kTiles, kShared, kPairs };
 struct Fp8Plan {
   Fp8Way way;
@@ -256,12 +266,23 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sms) {
   const double weight = (double)N * (double)K;
   const int warps = few_warps(M, N, sms);
   const double ctas = (double)(N / 16) * (double)((M + 15) / 16);
-  const double waves = std::fmax(1.0, ctas * warps / (16.0 * sms));
-  const double rate = M <= 8 ? 5.4e6 : 4.3e6, block = M <= 8 ? 0.65 : 0.9;
-  const double few =
-      2.2 + std::fmax(weight / rate, waves * (0.5 + block * std::ceil(b / warps)));
+  const double slots = 16.0 * sms / warps;  // resident CTAs
+  const double rounds = std::ceil(b / warps);
+  double few, floor;
+  if (M <= 8) {
+    auto wave = [&](double full) {
+      return std::fmax(full * slots * 16.0 * (double)K / 6.2e6,
+                       0.5 + (0.3 + 0.4 * full + 0.012 * (double)(M - 1)) * rounds);
+    };
+    const double whole = std::ceil(ctas / slots) - 1.0;
+    few = 2.2 + whole * wave(1.0) + wave(ctas / slots - whole);
+    floor = 4.5 + weight / 6.2e6;
+  } else {
+    few = 2.2 + std::fmax(weight / 4.3e6, std::fmax(1.0, ctas / slots) * (0.5 + 0.9 * rounds));
+    floor = 3.0 + weight / 5.6e6;
+  }
   // up to 1024 tokens, beyond which nothing was measured (and the grid would grow too high)
-  if (M <= 1024 && few < std::fmax(best, 3.0 + weight / 5.6e6)) p.way = kFew;
+  if (M <= 1024 && few < std::fmax(best, floor)) p.way = kFew;
   return p;
 }
 

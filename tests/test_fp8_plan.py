@@ -37,3 +37,23 @@ def test_plan_of_the_largest_sizes(rows, n, k):
     tiles = -(-rows // 256) * -(-n // 256)
     assert way != "pairs" or 0 <= whole < tiles
     assert way != "shared" or 2 <= share <= 4
+
+
+# Products of few tokens whose ways differ by 4 % or more on a GB300, weights out of HBM (us):
+# the way that is faster, and both times.
+MEASURED = [
+    (1, 8192, 8192, "few", 13.9, 17.3), (1, 8192, 16384, "few", 24.8, 27.6),
+    (1, 16384, 16384, "few", 46.4, 48.8), (1, 28672, 8192, "few", 37.9, 45.0),
+    (1, 14336, 14336, "tiles", 37.6, 39.3), (1, 14336, 4096, "few", 12.9, 14.2),
+    (1, 32000, 4096, "few", 24.2, 25.9), (1, 5120, 13824, "few", 17.2, 18.7),
+    (1, 10240, 5120, "few", 13.6, 14.7), (1, 131072, 512, "tiles", 16.4, 20.2),
+    (8, 28672, 8192, "few", 39.5, 44.8), (8, 8192, 16384, "few", 25.8, 27.9),
+    (8, 12288, 12288, "tiles", 30.9, 37.1), (8, 14336, 14336, "tiles", 37.8, 43.1),
+    (8, 10240, 8192, "tiles", 20.6, 22.8), (8, 10240, 5120, "tiles", 14.7, 15.5),
+    (8, 5120, 13824, "shared", 18.7, 20.0), (8, 8192, 8192, "few", 14.0, 17.4),
+]
+
+
+@pytest.mark.parametrize("rows,n,k,way,us,other", MEASURED)
+def test_the_faster_way_is_taken_for_few_tokens(rows, n, k, way, us, other):
+    assert us < other and pk.pact_test_fp8_plan(rows, n, k)[0] == way
