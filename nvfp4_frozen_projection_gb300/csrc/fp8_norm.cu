@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 2)
   }
   ss = group_sum(ss, wpr, wl, group, slots + group * wpr);
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
-  if (wl == 0 && lane == 0) rstd_out[row] = rstd;
+  if (wl == 0 && lane == 0 && PACT_IN(row < M)) rstd_out[row] = rstd;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t c = (int64_t)((i * wpr + wl) * 32 + lane) * 8;
@@ -242,7 +242,7 @@ __device__ __forceinline__ void dgamma_columns(const uint16_t* h, const uint16_t
     float t = sums[0][threadIdx.x];
 #pragma unroll
     for (int w = 1; w < 8; ++w) t += sums[w][threadIdx.x];
-    dgamma[c0 + threadIdx.x] = t;
+    if (PACT_IN(c0 + threadIdx.x < H)) dgamma[c0 + threadIdx.x] = t;
   }
 }
 
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : (NV == 1 ? 3 : 2)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = c0 + i * cstep;
-    if (c >= H) continue;
+    if (c >= H || !PACT_IN((int)blockIdx.x < row_ctas && c + 8 <= H)) continue;
     if constexpr (WIDE) {
       *reinterpret_cast<float4*>(p + c) = dg_wide[2 * i][threadIdx.x];
       *reinterpret_cast<float4*>(p + c + 4) = dg_wide[2 * i + 1][threadIdx.x];
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(512)
     t = sum[0][tx];
 #pragma unroll
     for (int i = 1; i < 8; ++i) t += sum[8 * i][tx];
-    dgamma[j] = t;
+    if (PACT_IN(j < H)) dgamma[j] = t;
   }
 }
 

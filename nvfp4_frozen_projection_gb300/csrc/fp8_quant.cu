@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(256, 6)
     if (col_ok && m < M && PACT_IN(m * K + c + 8 <= M * K))
       *reinterpret_cast<uint2*>(q + m * K + c) = e4m3x8(xf, r);
   }
-  if (lane < kQRows && m0 + lane < M) s[(int64_t)kb * M + m0 + lane] = mine.s;
+  if (lane < kQRows && m0 + lane < M && PACT_IN((int64_t)kb * 128 < K))
+    s[(int64_t)kb * M + m0 + lane] = mine.s;
 }
 
 cudaError_t launch_quant_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q,
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 1; i < 8; ++i) amax = fmaxf(amax, red[i]);
   const Fp8Scale f = fp8_scale(amax);
-  if (threadIdx.x == 0)
+  if (threadIdx.x == 0 && PACT_IN(nb < nnb && kb < nkb))
     s[backward ? (int64_t)kb * nnb + nb : (int64_t)nb * nkb + kb] = f.s;
   for (int i = warp; i < 128; i += 8) {
     if (n0 + i >= N || !col_ok) continue;

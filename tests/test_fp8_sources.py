@@ -1,4 +1,5 @@
-"""Orderings inside the FP8 product's kernel that no result shows: read from its source."""
+"""What no result of the FP8 kernels shows, read from their source: the scope of waits in a
+pair, and the debug build's checks."""
 import os
 import re
 
@@ -40,3 +41,16 @@ def test_cluster_waits_acquire_at_cluster_scope():
         body = src[src.index(" %s(" % name):]
         body = body[:body.index("\n}")]
         assert len(re.findall(r"mbarrier\.(?:try|test)_wait\.parity\.acquire\.cluster", body)) == n
+
+
+@pytest.mark.parametrize("name", ["fp8_quant.cu", "fp8_norm.cu", "fp8_gemm.cu"])
+def test_stores_to_global_memory_are_checked_in_the_debug_build(name):
+    """Each store at an address computed by hand is under PACT_IN, in its own statement or
+    the lines just before it."""
+    lines = [ln for ln in _code(name).split("\n") if ln.strip()]
+    store = re.compile(r"(\*reinterpret_cast<\w+\*>\((q|h_out|dh|p|p\.out|out) \+.*|"
+                       r"\b(s|rstd_out|dgamma|out)\[.*\]) =[^=]?")
+    found = [i for i, ln in enumerate(lines) if store.search(ln)]
+    assert found
+    for i in found:
+        assert any("PACT_IN(" in ln for ln in lines[max(0, i - 7):i + 1]), lines[i]
