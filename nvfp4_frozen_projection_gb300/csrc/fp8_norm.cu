@@ -176,6 +176,8 @@ static RowPlan bwd_plan(int64_t M, int64_t H) {
   return p;
 }
 
+// The grid is that of a GB300 on any device, so that the size of the workspace and the order
+// of dgamma's sums follow from the sizes alone.
 static int bwd_ctas(int64_t M, const RowPlan& p) {
   const int64_t n = (M + p.groups - 1) / p.groups;
   const int most = 152 * (p.threads > 256 ? 1 : (p.nv == 1 ? 3 : 2));  // resident at once

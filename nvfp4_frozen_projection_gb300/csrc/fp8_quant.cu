@@ -70,7 +70,9 @@ cudaError_t launch_quant_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ld
 // One CTA per 128 x 128 tile of W [N, K]: amax, then the codes of the forward layout
 // [N, K] (scales [ceil(N/128), ceil(K/128)]) or of the backward layout [K, N] (codes
 // and scales transposed).  Offline: the backward layout goes through shared memory so
-// that its stores are coalesced, and that is all the tuning it gets.
+// that its stores are coalesced, and that is all the tuning it gets.  W is read twice, the
+// second time out of L1 or L2: 8192 x 16384 takes 145 us forward and 167 backward, against
+// 99 for one read and one write out of HBM.
 __global__ void __launch_bounds__(256)
     k_pack_fp8(const float* __restrict__ W, int64_t N, int64_t K, int backward,
                uint8_t* __restrict__ q, float* __restrict__ s) {
