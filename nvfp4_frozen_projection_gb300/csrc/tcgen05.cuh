@@ -111,23 +111,36 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4f32(uint32_t ra) {
   return v;
 }
 
-// try_wait with acquire at cluster scope: for barriers that other CTAs arrive on.
+// try_wait with acquire at cluster scope: for barriers that other CTAs arrive on.  TMEM:
+// relaxed, for barriers that order nothing but TMEM accesses, which the
+// tcgen05.fence::after_thread_sync behind the wait keeps in place.
+template <bool TMEM = false>
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kWaitSuspendNs)
-      : "memory");
+  if constexpr (TMEM)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kWaitSuspendNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kWaitSuspendNs)
+        : "memory");
   return ok != 0;
 }
 
 // Whether the phases of two barriers with these parities have completed, without
 // suspending the thread.  One question alone takes about 135 cycles (GB300); asked
 // together they overlap.  Bit 0: the first, bit 1: the second.  CLUSTER: for barriers
-// that other CTAs of the cluster arrive on.
+// that other CTAs of the cluster arrive on, the second one ordering TMEM accesses alone
+// (relaxed, as in mbar_try_wait_cluster<true>).
 template <bool CLUSTER>
 __device__ __forceinline__ uint32_t mbar_test_two(uint32_t bar0, uint32_t par0, uint32_t bar1,
                                                   uint32_t par1) {
@@ -136,7 +149,7 @@ __device__ __forceinline__ uint32_t mbar_test_two(uint32_t bar0, uint32_t par0, 
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
         "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%3], %4;\n\t"
+        "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 q, [%3], %4;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t"
         "selp.u32 t, 2, 0, q;\n\t"
         "or.b32 %0, %0, t;\n\t}"
@@ -179,13 +192,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   }
 }
 
-// mbar_wait for a barrier that other CTAs of the cluster arrive on.
+// mbar_wait for a barrier that other CTAs of the cluster arrive on (TMEM: as in
+// mbar_try_wait_cluster).
+template <bool TMEM = false>
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                                   const volatile uint32_t* abort) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait_cluster<TMEM>(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait_cluster<TMEM>(bar, parity)) return true;
     if ((i & 255u) == 0u) {
       if (abort != nullptr && *abort) return false;
       if (global_timer_ns() - t0 > limit_ns) return false;

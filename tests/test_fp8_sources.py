@@ -23,24 +23,34 @@ def _calls(src, name):
 @pytest.mark.parametrize("barrier", ["full0", "empty0", "accf0", "acce0"])
 def test_waits_on_barriers_of_a_pair_have_cluster_scope(barrier):
     """In a pair the other CTA's copies, commits and releases arrive on these barriers, so
-    every wait on them is wait_x, wait_x_for or mbar_test_two<PAIR>: cluster scope there,
-    CTA scope in a kernel without a pair."""
+    every wait on them is wait_x, wait_x_for, wait_tmem or mbar_test_two<PAIR>: cluster scope
+    there, CTA scope in a kernel without a pair.  Those of accumulators are relaxed, and a
+    tcgen05 fence follows each."""
     src = _code("fp8_gemm.cu")
     src = src[src.index("k_fp8_gemm("):]
-    waits = [c for c, _ in _calls(src, "wait_x") + _calls(src, "wait_x_for")]
+    tmem = barrier in ("accf0", "acce0")
+    waits = [c for c, _ in (_calls(src, "wait_tmem") if tmem else
+                            _calls(src, "wait_x") + _calls(src, "wait_x_for"))]
     tests = _calls(src, "mbar_test_two")
     assert any(c.startswith(barrier) for c in waits)
     assert not [c for c, _ in _calls(src, "mbar_wait") if c.startswith(barrier)]
     assert tests and all(t == "<PAIR>" for _, t in tests)
     assert re.search(r"return PAIR \? mbar_wait_cluster\(bar, par, ns, flag\)", src)
+    assert re.search(r"return PAIR \? mbar_wait_cluster<true>\(bar, par, kFp8WaitNs", src)
+    # the fence: before the next MMA, and before the next TMEM load
+    for wait, use in (("!wait_tmem(acce0", "mma_f8<PAIR>("), ("if (!(ok = wait_block()))", "tmem_ld16(")):
+        after = src[src.index(wait):]
+        assert "tc_fence_after();" in after[:after.index(use)]
 
 
 def test_cluster_waits_acquire_at_cluster_scope():
     src = _code("tcgen05.cuh")
-    for name, n in (("mbar_try_wait_cluster", 1), ("mbar_test_two", 2)):
+    for name in ("mbar_try_wait_cluster", "mbar_test_two"):
         body = src[src.index(" %s(" % name):]
         body = body[:body.index("\n}")]
-        assert len(re.findall(r"mbarrier\.(?:try|test)_wait\.parity\.acquire\.cluster", body)) == n
+        for order in ("acquire", "relaxed"):
+            wait = r"mbarrier\.(?:try|test)_wait\.parity\.%s\.cluster" % order
+            assert len(re.findall(wait, body)) == 1
 
 
 @pytest.mark.parametrize("name", ["fp8_quant.cu", "fp8_norm.cu", "fp8_gemm.cu"])
