@@ -62,14 +62,14 @@ PROJS = ("q", "k", "v", "o", "gate_up", "down")
 # of the sources and build script that kernel was compiled from when it was taken.
 # The roofline reports it only while those files are unchanged, else null.
 GU_FWD_TRAFFIC = {
-    "bytes": 45200000 + 217360000,
+    "bytes": 45250000 + 217630000,
     "tokens": 8192,
     "sources": ("nvfp4_frozen_projection_gb300/csrc/gemm.cu",
                 "nvfp4_frozen_projection_gb300/csrc/tcgen05.cuh",
                 "nvfp4_frozen_projection_gb300/csrc/common.cuh",
                 "nvfp4_frozen_projection_gb300/csrc/kernels.h",
                 "nvfp4_frozen_projection_gb300/build.py"),
-    "sha256": "9d908fffe7582e3d969e7c96ec9f2c430c4a3d295504d82d6e514bc9b07d900d",
+    "sha256": "51044d2b577f59fe9ff2f480675c7c1f1ebff35f21047e057fed28fded861b8e",
 }
 INPUTS = ("x", "attn", "dy", "dq", "dk", "dv")
 
