@@ -431,6 +431,133 @@ int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* 
                          pact_stream_t stream);
 
 /*
+ * What a decoder layer has between its q, k and v projections and its o projection, and
+ * what an optimizer does with the adapters' gradients.  The paper names these parts of the
+ * layer and gives no design of them.
+ *
+ * A tensor of heads: BF16, value (t, h, d) at p[t ld + h D + d], for rows tokens and heads
+ * heads of D values; ld > heads D where the heads are columns of a wider matrix.
+ * Rules for every call below: rows 1 .. 2^30; D % 16 == 0; p 16-byte aligned; ld % 8 == 0,
+ * heads D <= ld <= 2^30; 1 <= heads <= 2^16.
+ */
+typedef struct pact_heads {
+  uint16_t* p;
+  int64_t rows;
+  int64_t heads;
+  int64_t ld;
+} pact_heads;
+
+/*
+ * The table of a rotary position embedding: turns[i] = inv_freq[i] / (2 pi) of a turn, as a
+ * fraction of 2^64, for n frequencies in radians per position (FP64, device; any sign).
+ * 1 <= n <= 256.
+ */
+int pact_rope_turns(const double* inv_freq, int64_t n, int64_t* turns, pact_stream_t stream);
+
+/*
+ * RMSNorm of every head of the queries and keys, and the rotary position embedding, in one
+ * pass.  For a head x of a token at position pos:
+ *   z = x / sqrt(mean(x^2) + eps) * gamma  (z = x without gammas);
+ *   pair i turns by the angle pos inv_freq[i]: a' = a cos - b sin, b' = b cos + a sin,
+ *   (a, b) = (z[i], z[i + rot/2]), or with interleaved != 0 (z[2i], z[2i + 1]);
+ *   columns from rot on stay as they are.
+ * FP32 arithmetic, one rounding at the end; the angle is exact before its rounding to FP32.
+ *   q, k, q_out, k_out  heads [T, hq, D] and [T, hk, D]; an output may be its own input;
+ *   positions  INT32 [T], any value;  turns  [rot/2] (pact_rope_turns);
+ *   gamma_q_opt, gamma_k_opt  BF16 [D], both or neither, 16-byte aligned.
+ * Rules: D <= 256; rot % 16 == 0, 16 <= rot <= D; eps finite and >= 0.
+ */
+int pact_qk_norm_rope(const pact_heads* q, const pact_heads* k, int64_t D, int64_t rot,
+                      const int32_t* positions, const int64_t* turns, int interleaved,
+                      const uint16_t* gamma_q_opt, const uint16_t* gamma_k_opt, float eps,
+                      pact_heads* q_out, pact_heads* k_out, pact_stream_t stream);
+
+/*
+ * Its backward: g = the gradient turned back, n = x / sqrt(mean(x^2) + eps), dn = g gamma;
+ *   dx = (dn - n mean(dn n)) / sqrt(mean(x^2) + eps)   (dx = g without gammas);
+ *   dgamma = sum over tokens and heads g n.
+ *   dyq, dyk  the gradients of q_out and k_out;  q_opt, k_opt  the forward's inputs, needed
+ *   with gammas and unused without;  dq, dk  outputs, each may be dyq or dyk, or q or k;
+ *   dgamma_q_opt, dgamma_k_opt  FP32 [D], both or neither (with gammas only), overwritten.
+ * ws: pact_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned, when dgamma is asked
+ * for.  Deterministic.  Other rules as for the forward.
+ */
+size_t pact_qk_norm_rope_bwd_workspace_size(int64_t T, int64_t heads_q, int64_t heads_k, int64_t D);
+int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pact_heads* q_opt,
+                          const pact_heads* k_opt, int64_t D, int64_t rot,
+                          const int32_t* positions, const int64_t* turns, int interleaved,
+                          const uint16_t* gamma_q_opt, const uint16_t* gamma_k_opt, float eps,
+                          pact_heads* dq, pact_heads* dk, float* dgamma_q_opt,
+                          float* dgamma_k_opt, void* ws, size_t ws_bytes, pact_stream_t stream);
+
+/*
+ * Attention over packed sequences.  Rows cu_q[b] .. cu_q[b+1]-1 of q are the queries of
+ * sequence b (lq of them), rows cu_k[b] .. cu_k[b+1]-1 of k and v its keys (lk); query head
+ * h reads key head h / (hq / hk).  With causal != 0 query i sees the keys j <= i + lk - lq:
+ * the last query stands at the last key.
+ *   o = softmax(scale q k^T) v over the keys seen;  lse = log(sum exp(scale q k^T)), natural.
+ * A query that sees no key gets o = 0 and lse = -inf.  FP32 sums; the probabilities are
+ * rounded to BF16 for their product with v.
+ *   q, o  heads [Tq, hq, D];  k, v  heads [Tk, hk, D];  lse  FP32 [hq, Tq];
+ *   cu_q, cu_k  INT32 [nseq + 1], ascending, on the device.  Rows of o and lse that belong
+ *   to no sequence are left as they were.  Values of cu outside [0, T] are taken as the
+ *   nearest of these, a length below zero as zero: no value leads outside the tensors, and
+ *   sequences that overlap give unspecified values in their shared rows.
+ *   A NaN or an infinity stays within its sequence and its key head.
+ * Rules: D <= 128; hq % hk == 0; 1 <= nseq <= 2^20; scale finite and > 0.
+ */
+int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_heads* v, int64_t D,
+                       const int32_t* cu_q, const int32_t* cu_k, int64_t nseq, int causal,
+                       float scale, pact_heads* o, float* lse, pact_stream_t stream);
+
+/*
+ * Its backward, which recomputes the probabilities P = exp(scale q k^T - lse):
+ *   delta = sum_d do o;  dv = P^T do;  dS = P (do v^T - delta);
+ *   dq = scale dS k;  dk = scale dS^T q, dk and dv summed over the query heads of a key head.
+ * P and dS are rounded to BF16 for their products.  Deterministic: no atomics.
+ *   d_o (the gradient of o), o, dq  as q;  dk, dv  as k;  lse  the forward's.
+ * Rows of dq, dk and dv that belong to no sequence are left as they were; a key that no
+ * query sees gets zeros.  ws: pact_attention_bwd_workspace_size() bytes, 256-byte aligned.
+ */
+size_t pact_attention_bwd_workspace_size(int64_t Tq, int64_t heads_q);
+int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_heads* k,
+                       const pact_heads* v, const pact_heads* o, const float* lse, int64_t D,
+                       const int32_t* cu_q, const int32_t* cu_k, int64_t nseq, int causal,
+                       float scale, pact_heads* dq, pact_heads* dk, pact_heads* dv, void* ws,
+                       size_t ws_bytes, pact_stream_t stream);
+
+/*
+ * The norm of many FP32 tensors together (the adapters' gradients of all layers), and
+ * clipping by it:
+ *   norm = sqrt(sum over all values g^2);  coef = min(1, max_norm / (norm + 1e-6));
+ *   out = g coef.
+ * The tensors are listed in device memory: data [count] pointers (4-byte aligned), numel
+ * [count] values each, first [count] the tensor's first chunk: the sum of pact_grad_chunks()
+ * over the tensors before it; chunks is the sum over all.  The lists are read when the call
+ * runs, and no value of them may lead outside the tensors.
+ * out: a list of pointers like data (may be data itself: clipping in place; a tensor that
+ * needs no clipping is not written then), each a whole tensor of its own.  norm FP32 [1].
+ * Squares are summed in FP32 over 16 values and in FP64 beyond, without overflow or
+ * underflow for any finite values.  A NaN, or an infinity with a finite max_norm, makes the
+ * norm NaN or infinite, and the coefficient NaN or zero.  Deterministic.
+ * Rules: count 1 .. 2^20; chunks 0 .. 2^40; max_norm >= 0 (infinity: no clipping).
+ * ws: pact_grad_norm_workspace_size() bytes, 256-byte aligned.
+ */
+typedef struct pact_tensor_list {
+  float* const* data;
+  const int64_t* numel;
+  const int64_t* first;
+  int64_t count;
+  int64_t chunks;
+} pact_tensor_list;
+int64_t pact_grad_chunks(int64_t numel);
+size_t pact_grad_norm_workspace_size(void);
+int pact_grad_norm(const pact_tensor_list* grads, float* norm, void* ws, size_t ws_bytes,
+                   pact_stream_t stream);
+int pact_clip_grad_norm(const pact_tensor_list* grads, float* const* out, double max_norm,
+                        float* norm, void* ws, size_t ws_bytes, pact_stream_t stream);
+
+/*
  * The FP32 exp recipe used by pact_silu_mul_quant, exposed so that it can be
  * compared bit for bit with another implementation: Cody-Waite reduction
  * x = n ln2 + f (ln2 split in a 16-bit head and a tail), degree-7 Taylor

@@ -26,6 +26,8 @@ __all__ = [
     "pact_quant_fp8", "pact_pack_weight_fp8_fwd", "pact_pack_weight_fp8_bwd",
     "pact_linear_fp8_fwd", "pact_linear_fp8_dgrad", "pact_add_rmsnorm_quant_fp8",
     "pact_add_rmsnorm_bwd",
+    "GradList", "pact_rope_turns", "pact_qk_norm_rope", "pact_qk_norm_rope_bwd",
+    "pact_attention_fwd", "pact_attention_bwd", "pact_grad_norm", "pact_clip_grad_norm",
     "pact_test_fp8_plan", "pact_test_wait_timeout", "pact_test_bounds_check", "pact_check_status",
     "pact_device_supported", "pact_launch_count", "pact_profile_next_gemm", "pact_version",
 ]
@@ -57,12 +59,24 @@ class _FP8Struct(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class _HeadsStruct(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("rows", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("ld", ctypes.c_int64)]
+
+
+class _ListStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("chunks", ctypes.c_int64)]
+
+
 _LIB = None
 _LIB_LOCK = threading.Lock()
 
 _vp, _i64, _sz, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 _SP = ctypes.POINTER(_NVFP4Struct)
 _SP8 = ctypes.POINTER(_FP8Struct)
+_SPH = ctypes.POINTER(_HeadsStruct)
+_SPL = ctypes.POINTER(_ListStruct)
 _SIGNATURES = {
     "pact_nvfp4_codes_bytes": (_sz, [_i64, _i64]),
     "pact_nvfp4_sf_bytes": (_sz, [_i64, _i64]),
@@ -101,6 +115,20 @@ _SIGNATURES = {
     "pact_add_rmsnorm_quant_fp8": (_int, [_vp, _vp, _vp, _i64, _i64, _f32, _vp, _SP8, _vp, _vp]),
     "pact_add_rmsnorm_bwd_workspace_size": (_sz, [_i64, _i64]),
     "pact_add_rmsnorm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "pact_rope_turns": (_int, [_vp, _i64, _vp, _vp]),
+    "pact_qk_norm_rope": (_int, [_SPH, _SPH, _i64, _i64, _vp, _vp, _int, _vp, _vp, _f32, _SPH, _SPH,
+                                 _vp]),
+    "pact_qk_norm_rope_bwd_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "pact_qk_norm_rope_bwd": (_int, [_SPH, _SPH, _SPH, _SPH, _i64, _i64, _vp, _vp, _int, _vp, _vp,
+                                     _f32, _SPH, _SPH, _vp, _vp, _vp, _sz, _vp]),
+    "pact_attention_fwd": (_int, [_SPH, _SPH, _SPH, _i64, _vp, _vp, _i64, _int, _f32, _SPH, _vp, _vp]),
+    "pact_attention_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "pact_attention_bwd": (_int, [_SPH, _SPH, _SPH, _SPH, _SPH, _vp, _i64, _vp, _vp, _i64, _int, _f32,
+                                  _SPH, _SPH, _SPH, _vp, _sz, _vp]),
+    "pact_grad_chunks": (_i64, [_i64]),
+    "pact_grad_norm_workspace_size": (_sz, []),
+    "pact_grad_norm": (_int, [_SPL, _vp, _vp, _sz, _vp]),
+    "pact_clip_grad_norm": (_int, [_SPL, _vp, ctypes.c_double, _vp, _vp, _sz, _vp]),
     "pact_test_fp8_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_i64)]),
     "pact_test_pexp": (_int, [_vp, _vp, _i64, _vp]),
     "pact_test_wait_timeout": (_int, [ctypes.c_uint32, _vp]),
@@ -681,6 +709,259 @@ def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tenso
                                     _addr(dh), _addr(dgamma), _addr(ws),
                                     0 if ws is None else ws.numel(), _raw_stream(dev)))
     return dh, dgamma
+
+
+# ------------------------------------------------------------------ heads and attention
+def _need_heads(t, name, dev, like=None) -> _HeadsStruct:
+    """t is a BF16 tensor of heads [T, heads, D] on the current device, of this shape when
+    given, whose tokens lie ld values apart and whose heads are contiguous; its struct."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D CUDA tensor [tokens, heads, D]")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    rows, heads, d = shape = t.shape
+    if like is not None and shape != like:
+        raise ValueError(f"{name} must have shape {list(like)}, got {list(shape)}")
+    ld, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+        raise ValueError(f"the heads of {name} must be contiguous")
+    # the stride of a single row says nothing: torch may report any number there
+    return _HeadsStruct(t.data_ptr(), rows, heads, ld if rows > 1 else heads * d)
+
+
+def pact_rope_turns(inv_freq: torch.Tensor, turns: torch.Tensor | None = None) -> torch.Tensor:
+    """The table of a rotary embedding (int64 [n], fractions of a turn) from its frequencies
+    in radians per position, float64 [n]."""
+    lib = _LIB or load_library()
+    n = inv_freq.shape[0] if isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1 else 0
+    dev = torch.cuda.current_device()
+    _need(inv_freq, torch.float64, (n,), "inv_freq", dev)
+    if turns is None:
+        turns = torch.empty((n,), dtype=torch.int64, device=inv_freq.device)
+    _need(turns, torch.int64, (n,), "turns", dev)
+    _check(lib.pact_rope_turns(_addr(inv_freq), n, _addr(turns), _raw_stream(dev)))
+    return turns
+
+
+def _need_rope(positions, turns, gamma_q, gamma_k, T, D, dev):
+    _need(positions, torch.int32, (T,), "positions", dev)
+    n = turns.shape[0] if isinstance(turns, torch.Tensor) and turns.dim() == 1 else 0
+    _need(turns, torch.int64, (n,), "turns", dev)
+    if gamma_q is not None:
+        _need(gamma_q, torch.bfloat16, (D,), "gamma_q", dev)
+    if gamma_k is not None:
+        _need(gamma_k, torch.bfloat16, (D,), "gamma_k", dev)
+    return 2 * n
+
+
+def pact_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
+                      turns: torch.Tensor, gamma_q: torch.Tensor | None = None,
+                      gamma_k: torch.Tensor | None = None, eps: float = 1e-5,
+                      interleaved: bool = False, q_out: torch.Tensor | None = None,
+                      k_out: torch.Tensor | None = None):
+    """RMSNorm of every head (with gammas) and the rotary embedding of the first
+    2 len(turns) columns, for q [T, hq, D] and k [T, hk, D].  An output may be its own
+    input.  Returns (q_out, k_out)."""
+    lib = _LIB or load_library()
+    dev = torch.cuda.current_device()
+    sq, sk = _need_heads(q, "q", dev), _need_heads(k, "k", dev)
+    T, _, D = q.shape
+    if k.shape[2] != D:
+        raise ValueError(f"q has heads of {D}, k of {k.shape[2]}")
+    rot = _need_rope(positions, turns, gamma_q, gamma_k, T, D, dev)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    so, sp = _need_heads(q_out, "q_out", dev, q.shape), _need_heads(k_out, "k_out", dev, k.shape)
+    _check(lib.pact_qk_norm_rope(sq, sk, D, rot, _addr(positions), _addr(turns),
+                                 int(bool(interleaved)), _addr(gamma_q), _addr(gamma_k), float(eps),
+                                 so, sp, _raw_stream(dev)))
+    return q_out, k_out
+
+
+def pact_qk_norm_rope_bwd(dyq: torch.Tensor, dyk: torch.Tensor, positions: torch.Tensor,
+                          turns: torch.Tensor, q: torch.Tensor | None = None,
+                          k: torch.Tensor | None = None, gamma_q: torch.Tensor | None = None,
+                          gamma_k: torch.Tensor | None = None, eps: float = 1e-5,
+                          interleaved: bool = False, dq: torch.Tensor | None = None,
+                          dk: torch.Tensor | None = None,
+                          dgamma_q: torch.Tensor | bool | None = None,
+                          dgamma_k: torch.Tensor | bool | None = None):
+    """Backward of pact_qk_norm_rope; q and k are its inputs, needed with gammas.  dq may
+    be dyq or q, dk dyk or k.  dgamma_q, dgamma_k: FP32 [D] tensors to overwrite, True for
+    new ones, None to leave both out.  Returns (dq, dk, dgamma_q, dgamma_k)."""
+    lib = _LIB or load_library()
+    dev = torch.cuda.current_device()
+    sq, sk = _need_heads(dyq, "dyq", dev), _need_heads(dyk, "dyk", dev)
+    T, hq, D = dyq.shape
+    if dyk.shape[2] != D:
+        raise ValueError(f"dyq has heads of {D}, dyk of {dyk.shape[2]}")
+    rot = _need_rope(positions, turns, gamma_q, gamma_k, T, D, dev)
+    xq = _need_heads(q, "q", dev, dyq.shape) if q is not None else None
+    xk = _need_heads(k, "k", dev, dyk.shape) if k is not None else None
+    if dq is None:
+        dq = torch.empty(dyq.shape, dtype=torch.bfloat16, device=dyq.device)
+    if dk is None:
+        dk = torch.empty(dyk.shape, dtype=torch.bfloat16, device=dyq.device)
+    so, sp = _need_heads(dq, "dq", dev, dyq.shape), _need_heads(dk, "dk", dev, dyk.shape)
+    grads = []
+    for g, name in ((dgamma_q, "dgamma_q"), (dgamma_k, "dgamma_k")):
+        if g is True:
+            g = torch.empty((D,), dtype=torch.float32, device=dyq.device)
+        elif g is False:
+            g = None
+        if g is not None:
+            _need(g, torch.float32, (D,), name, dev)
+        grads.append(g)
+    ws = None
+    if grads[0] is not None:
+        # its own scratch in every call: a captured graph then keeps one of its own
+        ws = torch.empty((lib.pact_qk_norm_rope_bwd_workspace_size(T, hq, dyk.shape[1], D),),
+                         dtype=torch.uint8, device=dyq.device)
+    _check(lib.pact_qk_norm_rope_bwd(sq, sk, xq, xk, D, rot, _addr(positions), _addr(turns),
+                                     int(bool(interleaved)), _addr(gamma_q), _addr(gamma_k),
+                                     float(eps), so, sp, _addr(grads[0]), _addr(grads[1]), _addr(ws),
+                                     0 if ws is None else ws.numel(), _raw_stream(dev)))
+    return dq, dk, grads[0], grads[1]
+
+
+def _need_attention(q, k, v, cu_q, cu_k, scale, dev):
+    sq, sk = _need_heads(q, "q", dev), _need_heads(k, "k", dev)
+    sv = _need_heads(v, "v", dev, k.shape)
+    D = q.shape[2]
+    if k.shape[2] != D:
+        raise ValueError(f"q has heads of {D}, k of {k.shape[2]}")
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("cu_q must be a 1-D tensor of at least two offsets")
+    _need(cu_q, torch.int32, cu_q.shape, "cu_q", dev)
+    _need(cu_k, torch.int32, cu_q.shape, "cu_k", dev)
+    return sq, sk, sv, D, cu_q.shape[0] - 1, float(D ** -0.5 if scale is None else scale)
+
+
+def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                       cu_k: torch.Tensor, causal: bool = True, scale: float | None = None,
+                       o: torch.Tensor | None = None, lse: torch.Tensor | None = None):
+    """Attention over packed sequences: q [Tq, hq, D], k and v [Tk, hk, D], sequence b at
+    rows cu_q[b]:cu_q[b + 1] and cu_k[b]:cu_k[b + 1] (int32, on the device).  scale is
+    1 / sqrt(D) by default.  Returns (o [Tq, hq, D], lse FP32 [hq, Tq]); rows of no
+    sequence are left as they were."""
+    lib = _LIB or load_library()
+    dev = torch.cuda.current_device()
+    sq, sk, sv, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
+    if o is None:
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    so = _need_heads(o, "o", dev, q.shape)
+    if lse is None:
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    _need(lse, torch.float32, (q.shape[1], q.shape[0]), "lse", dev)
+    _check(lib.pact_attention_fwd(sq, sk, sv, D, _addr(cu_q), _addr(cu_k), n, int(bool(causal)),
+                                  scale, so, _addr(lse), _raw_stream(dev)))
+    return o, lse
+
+
+def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       o: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                       causal: bool = True, scale: float | None = None,
+                       dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                       dv: torch.Tensor | None = None):
+    """Backward of pact_attention_fwd from its inputs, its o and lse and the gradient do of
+    o.  Returns (dq, dk, dv); rows of no sequence are left as they were."""
+    lib = _LIB or load_library()
+    dev = torch.cuda.current_device()
+    sq, sk, sv, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
+    sdo, so = _need_heads(do, "do", dev, q.shape), _need_heads(o, "o", dev, q.shape)
+    _need(lse, torch.float32, (q.shape[1], q.shape[0]), "lse", dev)
+    dq, dk, dv = (torch.empty(x.shape, dtype=torch.bfloat16, device=q.device) if g is None else g
+                  for g, x in ((dq, q), (dk, k), (dv, v)))
+    outs = [_need_heads(g, name, dev, x.shape)
+            for g, x, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"))]
+    # its own scratch in every call: a captured graph then keeps one of its own
+    ws = torch.empty((lib.pact_attention_bwd_workspace_size(q.shape[0], q.shape[1]),),
+                     dtype=torch.uint8, device=q.device)
+    _check(lib.pact_attention_bwd(sdo, sq, sk, sv, so, _addr(lse), D, _addr(cu_q), _addr(cu_k), n,
+                                  int(bool(causal)), scale, *outs, _addr(ws), ws.numel(),
+                                  _raw_stream(dev)))
+    return dq, dk, dv
+
+
+# ------------------------------------------------------------------ gradient norm
+class GradList:
+    """FP32 tensors whose norm is taken together, listed in device memory once; they keep
+    their addresses while the list is in use.  Contiguous, all on the current device, no two
+    sharing memory."""
+
+    def __init__(self, tensors):
+        lib = _LIB or load_library()
+        self.tensors = tuple(tensors)
+        if not self.tensors:
+            raise ValueError("a gradient list needs at least one tensor")
+        self.device = dev = torch.cuda.current_device()
+        for i, t in enumerate(self.tensors):
+            _need(t, torch.float32, tuple(t.shape) if isinstance(t, torch.Tensor) else (),
+                  f"tensor {i}", dev)
+        self.numels = tuple(t.numel() for t in self.tensors)
+        spans = sorted((t.data_ptr(), t.numel()) for t in self.tensors if t.numel())
+        if any(a + 4 * n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+            raise ValueError("the tensors of a gradient list must not share memory")
+        first, at = [], 0
+        for n in self.numels:
+            first.append(at)
+            at += lib.pact_grad_chunks(n)
+        self.chunks = at
+        self._table = torch.tensor([[t.data_ptr() for t in self.tensors], list(self.numels), first],
+                                   dtype=torch.int64).to(f"cuda:{dev}")
+        step = 8 * len(self.tensors)
+        self.data = self._table.data_ptr()
+        self._struct = _ListStruct(self.data, self.data + step, self.data + 2 * step,
+                                   len(self.tensors), at)
+
+
+def _need_list(g, name, dev):
+    if not isinstance(g, GradList):
+        raise ValueError(f"{name} must be a GradList, got {type(g).__name__}")
+    if g.device != dev:
+        raise ValueError(f"{name} is on cuda:{g.device}, the current device is cuda:{dev}")
+
+
+def _grad_scratch(norm, dev, lib):
+    if norm is None:
+        norm = torch.empty((1,), dtype=torch.float32, device=f"cuda:{dev}")
+    _need(norm, torch.float32, (1,), "norm", dev)
+    # its own scratch in every call: a captured graph then keeps one of its own
+    return norm, torch.empty((lib.pact_grad_norm_workspace_size(),), dtype=torch.uint8,
+                             device=norm.device)
+
+
+def pact_grad_norm(grads: GradList, norm: torch.Tensor | None = None) -> torch.Tensor:
+    """The square root of the sum of all values' squares, FP32 [1]."""
+    lib = _LIB or load_library()
+    dev = torch.cuda.current_device()
+    _need_list(grads, "grads", dev)
+    norm, ws = _grad_scratch(norm, dev, lib)
+    _check(lib.pact_grad_norm(grads._struct, _addr(norm), _addr(ws), ws.numel(), _raw_stream(dev)))
+    return norm
+
+
+def pact_clip_grad_norm(grads: GradList, max_norm: float, norm: torch.Tensor | None = None,
+                        out: GradList | None = None) -> torch.Tensor:
+    """Scale every value by min(1, max_norm / (norm + 1e-6)), in place or into `out` (a list
+    of the same sizes).  Returns the norm before clipping, FP32 [1]."""
+    lib = _LIB or load_library()
+    dev = torch.cuda.current_device()
+    _need_list(grads, "grads", dev)
+    if out is None:
+        out = grads
+    elif out is not grads:
+        _need_list(out, "out", dev)
+        if out.numels != grads.numels:
+            raise ValueError("out must list tensors of the same sizes as grads")
+    norm, ws = _grad_scratch(norm, dev, lib)
+    _check(lib.pact_clip_grad_norm(grads._struct, out.data, float(max_norm), _addr(norm), _addr(ws),
+                                   ws.numel(), _raw_stream(dev)))
+    return norm
 
 
 def pact_test_fp8_plan(rows: int, n: int, k: int, sms: int = 152) -> tuple:

@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libpact.so")
 # the debug build: every source as one unit (debug_all.cu), stores bounds-checked
 DEBUG_LIB = os.path.join(HERE, "libpact_debug.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "lora.cu", "norm_act.cu", "noalloc.cu",
-           "fp8_quant.cu", "fp8_norm.cu", "fp8_gemm.cu"]
+           "fp8_quant.cu", "fp8_norm.cu", "fp8_gemm.cu", "rope.cu", "attention_fwd.cu",
+           "attention_bwd.cu", "grad_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-Xptxas", "-v", "-Wno-deprecated-gpu-targets"]

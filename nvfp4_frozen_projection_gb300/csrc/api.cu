@@ -114,6 +114,23 @@ int pact::make_map(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const
   return PACT_OK;
 }
 
+// 3-D tiled map over BF16 heads [rows, heads, D], value (t, h, d) at t ld + h D + d; boxes of
+// 64 columns x box_heads x box_rows, 128-byte swizzle.
+static int make_heads_map(CUtensorMap* m, const pact_heads* t, int64_t D, uint32_t box_heads,
+                          uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(PACT_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)t->heads, (cuuint64_t)t->rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)t->ld * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t->p, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PACT_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return PACT_OK;
+}
+
 namespace {
 
 // ---------------------------------------------------------------- validation helpers
@@ -160,6 +177,33 @@ int check_fp8_cols(int64_t c, const char* name) {
 bool partly_same(const void* a, const void* b, int64_t bytes) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return a && b && x != y && (x < y ? y - x : x - y) < (uintptr_t)bytes;
+}
+
+int check_heads(const pact_heads* t, const char* name, int64_t rows, int64_t heads, int64_t D) {
+  if (!t || !t->p) return fail(PACT_ERR_INVALID_ARG, "%s is required", name);
+  if (t->rows < 1 || t->rows > kFp8MaxRows || t->heads < 1 || t->heads > 65536)
+    return fail(PACT_ERR_SHAPE, "%s: need 1 <= rows <= 2^30 and 1 <= heads <= 2^16", name);
+  if (t->rows != rows || t->heads != heads)
+    return fail(PACT_ERR_SHAPE, "%s has %lld rows of %lld heads, expected %lld of %lld", name,
+                (long long)t->rows, (long long)t->heads, (long long)rows, (long long)heads);
+  if (t->ld % 8 || t->ld < heads * D || t->ld > (int64_t)1 << 30)
+    return fail(PACT_ERR_SHAPE, "%s: need ld %% 8 == 0 and heads * D <= ld <= 2^30", name);
+  if (!aligned(t->p, 16)) return fail(PACT_ERR_ALIGN, "%s must be 16-byte aligned", name);
+  return PACT_OK;
+}
+
+// Whether two tensors of heads share memory without being the same one: columns of one
+// matrix that do not meet share none.
+bool heads_clash(const pact_heads* a, const pact_heads* b, int64_t D) {
+  const uintptr_t x = (uintptr_t)a->p, y = (uintptr_t)b->p;
+  if (x == y) return a->ld != b->ld || a->heads != b->heads;
+  const pact_heads *lo = x < y ? a : b, *hi = x < y ? b : a;
+  const uint64_t gap = (uint64_t)((uintptr_t)hi->p - (uintptr_t)lo->p) / 2;
+  const uint64_t wl = (uint64_t)(lo->heads * D), wh = (uint64_t)(hi->heads * D);
+  if (gap >= (uint64_t)((lo->rows - 1) * lo->ld) + wl) return false;
+  if (lo->ld != hi->ld) return true;
+  const uint64_t off = gap % (uint64_t)lo->ld;
+  return off < wl || off + wh > (uint64_t)lo->ld;
 }
 
 // LoRA rank padded to 16, 32 or 64; the fused GEMM's LoRA operands are twice as
@@ -848,6 +892,291 @@ int pact_add_rmsnorm_bwd(const uint16_t* h, const uint16_t* gamma, const float* 
   cudaError_t e = launch_add_rmsnorm_bwd(h, gamma, rstd, dy, dres_opt, M, H, dh, dgamma_opt,
                                          (float*)ws, (cudaStream_t)stream);
   return e == cudaSuccess ? PACT_OK : cuda_fail(e, "add rmsnorm bwd launch");
+}
+
+// ---------------------------------------------------------------- heads and attention
+int pact_rope_turns(const double* inv_freq, int64_t n, int64_t* turns, pact_stream_t stream) {
+  if (!inv_freq || !turns) return fail(PACT_ERR_INVALID_ARG, "inv_freq and turns are required");
+  if (n < 1 || n > 256) return fail(PACT_ERR_SHAPE, "need 1 <= n <= 256 frequencies");
+  if (!aligned(inv_freq, 8) || !aligned(turns, 8))
+    return fail(PACT_ERR_ALIGN, "inv_freq and turns must be 8-byte aligned");
+  DeviceInfo* d;
+  int rc = device_info(&d);
+  if (rc) return rc;
+  cudaError_t e = launch_rope_turns(inv_freq, (int)n, turns, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "rope turns launch");
+}
+
+// The rules that the rotation's two directions share; fills p but for the tensors' pointers.
+static int check_rope(const pact_heads* q, const char* qname, const pact_heads* k,
+                      const char* kname, int64_t D, int64_t rot, const int32_t* positions,
+                      const int64_t* turns, const uint16_t* gq, const uint16_t* gk, float eps,
+                      RopeParams* p) {
+  int rc;
+  if (D < 16 || D > 256 || D % 16)
+    return fail(PACT_ERR_SHAPE, "need D %% 16 == 0 and 16 <= D <= 256");
+  if (rot < 16 || rot > D || rot % 16)
+    return fail(PACT_ERR_SHAPE, "need rot %% 16 == 0 and 16 <= rot <= D");
+  if (!q || !k) return fail(PACT_ERR_INVALID_ARG, "%s and %s are required", qname, kname);
+  if ((rc = check_heads(q, qname, q->rows, q->heads, D)) ||
+      (rc = check_heads(k, kname, q->rows, k->heads, D)))
+    return rc;
+  if (!positions || !turns) return fail(PACT_ERR_INVALID_ARG, "positions and turns are required");
+  if (!gq != !gk)
+    return fail(PACT_ERR_INVALID_ARG, "gamma_q and gamma_k go together: both or neither");
+  if (!(eps >= 0.0f && eps <= 3.4028235e38f))
+    return fail(PACT_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!aligned(positions, 4) || !aligned(turns, 8) || !aligned(gq, 16) || !aligned(gk, 16))
+    return fail(PACT_ERR_ALIGN,
+                "positions must be 4-byte, turns 8-byte and the gammas 16-byte aligned");
+  std::memset(p, 0, sizeof(*p));
+  p->q = q->p;
+  p->k = k->p;
+  p->ldq = q->ld;
+  p->ldk = k->ld;
+  p->gamma_q = gq;
+  p->gamma_k = gk;
+  p->positions = positions;
+  p->turns = turns;
+  p->T = q->rows;
+  p->hq = (int)q->heads;
+  p->hk = (int)k->heads;
+  p->D = (int)D;
+  p->rot = (int)rot;
+  p->eps = eps;
+  return PACT_OK;
+}
+
+int pact_qk_norm_rope(const pact_heads* q, const pact_heads* k, int64_t D, int64_t rot,
+                      const int32_t* positions, const int64_t* turns, int interleaved,
+                      const uint16_t* gamma_q_opt, const uint16_t* gamma_k_opt, float eps,
+                      pact_heads* q_out, pact_heads* k_out, pact_stream_t stream) {
+  RopeParams p;
+  int rc;
+  if ((rc = check_rope(q, "q", k, "k", D, rot, positions, turns, gamma_q_opt, gamma_k_opt, eps,
+                       &p)) ||
+      (rc = check_heads(q_out, "q_out", q->rows, q->heads, D)) ||
+      (rc = check_heads(k_out, "k_out", k->rows, k->heads, D)))
+    return rc;
+  if (heads_clash(q_out, q, D) || heads_clash(k_out, k, D))
+    return fail(PACT_ERR_INVALID_ARG, "q_out overlaps q, or k_out k, in part");
+  p.q_out = q_out->p;
+  p.k_out = k_out->p;
+  p.ldqo = q_out->ld;
+  p.ldko = k_out->ld;
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  cudaError_t e = launch_qk_norm_rope(p, interleaved != 0, d->sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "qk norm rope launch");
+}
+
+size_t pact_qk_norm_rope_bwd_workspace_size(int64_t T, int64_t heads_q, int64_t heads_k,
+                                            int64_t D) {
+  if (T < 1 || T > kFp8MaxRows || heads_q < 1 || heads_q > 65536 || heads_k < 1 ||
+      heads_k > 65536 || D < 16 || D > 256 || D % 16)
+    return 0;
+  return align256((size_t)rope_bwd_blocks(T, (int)(heads_q + heads_k), (int)D, kRopeSms) * 8 *
+                  (size_t)D);
+}
+
+int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pact_heads* q_opt,
+                          const pact_heads* k_opt, int64_t D, int64_t rot,
+                          const int32_t* positions, const int64_t* turns, int interleaved,
+                          const uint16_t* gamma_q_opt, const uint16_t* gamma_k_opt, float eps,
+                          pact_heads* dq, pact_heads* dk, float* dgamma_q_opt,
+                          float* dgamma_k_opt, void* ws, size_t ws_bytes, pact_stream_t stream) {
+  RopeParams p;
+  int rc;
+  if ((rc = check_rope(dyq, "dyq", dyk, "dyk", D, rot, positions, turns, gamma_q_opt, gamma_k_opt,
+                       eps, &p)) ||
+      (rc = check_heads(dq, "dq", dyq->rows, dyq->heads, D)) ||
+      (rc = check_heads(dk, "dk", dyk->rows, dyk->heads, D)))
+    return rc;
+  if (heads_clash(dq, dyq, D) || heads_clash(dk, dyk, D))
+    return fail(PACT_ERR_INVALID_ARG, "dq overlaps dyq, or dk dyk, in part");
+  if (gamma_q_opt) {
+    if ((rc = check_heads(q_opt, "q", dyq->rows, dyq->heads, D)) ||
+        (rc = check_heads(k_opt, "k", dyk->rows, dyk->heads, D)))
+      return rc;
+    if (heads_clash(dq, q_opt, D) || heads_clash(dk, k_opt, D))
+      return fail(PACT_ERR_INVALID_ARG, "dq overlaps q, or dk k, in part");
+    p.xq = q_opt->p;
+    p.xk = k_opt->p;
+    p.ldxq = q_opt->ld;
+    p.ldxk = k_opt->ld;
+  }
+  if (!dgamma_q_opt != !dgamma_k_opt)
+    return fail(PACT_ERR_INVALID_ARG, "dgamma_q and dgamma_k go together: both or neither");
+  if (dgamma_q_opt && !gamma_q_opt)
+    return fail(PACT_ERR_INVALID_ARG, "dgamma needs gamma_q and gamma_k");
+  if (!aligned(dgamma_q_opt, 4) || !aligned(dgamma_k_opt, 4))
+    return fail(PACT_ERR_ALIGN, "dgamma_q and dgamma_k must be 4-byte aligned");
+  if (dgamma_q_opt) {
+    const size_t need = pact_qk_norm_rope_bwd_workspace_size(p.T, p.hq, p.hk, D);
+    if (!ws || ws_bytes < need || !aligned(ws, 256))
+      return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
+  }
+  p.q_out = dq->p;
+  p.k_out = dk->p;
+  p.ldqo = dq->ld;
+  p.ldko = dk->ld;
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  cudaError_t e = launch_qk_norm_rope_bwd(p, interleaved != 0, dgamma_q_opt, dgamma_k_opt,
+                                          (float*)ws, kRopeSms, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "qk norm rope bwd launch");
+}
+
+// The rules that attention's two directions share, on q, k, v and the sequences.
+static int check_attention(const pact_heads* q, const pact_heads* k, const pact_heads* v,
+                           int64_t D, const int32_t* cu_q, const int32_t* cu_k, int64_t nseq,
+                           int causal, float scale, AttnParams* p) {
+  int rc;
+  if (D < 16 || D > 128 || D % 16)
+    return fail(PACT_ERR_SHAPE, "need D %% 16 == 0 and 16 <= D <= 128");
+  if (!q || !k) return fail(PACT_ERR_INVALID_ARG, "q and k are required");
+  if ((rc = check_heads(q, "q", q->rows, q->heads, D)) ||
+      (rc = check_heads(k, "k", k->rows, k->heads, D)) ||
+      (rc = check_heads(v, "v", k->rows, k->heads, D)))
+    return rc;
+  if (q->heads % k->heads) return fail(PACT_ERR_SHAPE, "need hq %% hk == 0");
+  if (!cu_q || !cu_k) return fail(PACT_ERR_INVALID_ARG, "cu_q and cu_k are required");
+  if (nseq < 1 || nseq > (int64_t)1 << 20) return fail(PACT_ERR_SHAPE, "need 1 <= nseq <= 2^20");
+  if (!aligned(cu_q, 4) || !aligned(cu_k, 4))
+    return fail(PACT_ERR_ALIGN, "cu_q and cu_k must be 4-byte aligned");
+  if (!(scale > 0.0f && scale <= 3.4028235e38f))
+    return fail(PACT_ERR_INVALID_ARG, "scale must be finite and positive");
+  std::memset(p, 0, sizeof(*p));
+  p->cu_q = cu_q;
+  p->cu_k = cu_k;
+  p->nseq = (int)nseq;
+  p->tq = (int)q->rows;
+  p->tk = (int)k->rows;
+  p->hq = (int)q->heads;
+  p->hk = (int)k->heads;
+  p->group = p->hq / p->hk;
+  p->D = (int)D;
+  for (p->gp = p->group < 128 ? p->group : 128; p->group % p->gp; --p->gp) {
+  }
+  p->tpt = 128 / p->gp;
+  p->gp_mul = (uint32_t)((65536 + p->gp - 1) / p->gp);
+  p->subs = p->group / p->gp;
+  p->units_h = p->hk * p->subs;
+  p->scale = scale;
+  p->c = scale * 1.4426950408889634f;
+  p->causal = causal != 0;
+  return PACT_OK;
+}
+
+int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_heads* v, int64_t D,
+                       const int32_t* cu_q, const int32_t* cu_k, int64_t nseq, int causal,
+                       float scale, pact_heads* o, float* lse, pact_stream_t stream) {
+  AttnFwdLaunch L;
+  int rc;
+  if ((rc = check_attention(q, k, v, D, cu_q, cu_k, nseq, causal, scale, &L.p)) ||
+      (rc = check_heads(o, "o", q->rows, q->heads, D)))
+    return rc;
+  if (!lse) return fail(PACT_ERR_INVALID_ARG, "lse is required");
+  if (!aligned(lse, 4)) return fail(PACT_ERR_ALIGN, "lse must be 4-byte aligned");
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  if ((rc = make_heads_map(&L.tmQ, q, D, L.p.gp, L.p.tpt)) ||
+      (rc = make_heads_map(&L.tmK, k, D, 1, 128)) || (rc = make_heads_map(&L.tmV, v, D, 1, 128)))
+    return rc;
+  L.p.o = o->p;
+  L.p.ldo = o->ld;
+  L.p.lse = lse;
+  L.p.status = d->status;
+  L.num_sms = d->sms;
+  cudaError_t e = launch_attn_fwd(L, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "attention launch");
+}
+
+size_t pact_attention_bwd_workspace_size(int64_t Tq, int64_t heads_q) {
+  if (Tq < 1 || Tq > kFp8MaxRows || heads_q < 1 || heads_q > 65536) return 0;
+  return align256((size_t)Tq * (size_t)heads_q * 4);
+}
+
+int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_heads* k,
+                       const pact_heads* v, const pact_heads* o, const float* lse, int64_t D,
+                       const int32_t* cu_q, const int32_t* cu_k, int64_t nseq, int causal,
+                       float scale, pact_heads* dq, pact_heads* dk, pact_heads* dv, void* ws,
+                       size_t ws_bytes, pact_stream_t stream) {
+  AttnBwdLaunch L;
+  int rc;
+  if ((rc = check_attention(q, k, v, D, cu_q, cu_k, nseq, causal, scale, &L.p)) ||
+      (rc = check_heads(d_o, "d_o", q->rows, q->heads, D)) ||
+      (rc = check_heads(o, "o", q->rows, q->heads, D)) ||
+      (rc = check_heads(dq, "dq", q->rows, q->heads, D)) ||
+      (rc = check_heads(dk, "dk", k->rows, k->heads, D)) ||
+      (rc = check_heads(dv, "dv", k->rows, k->heads, D)))
+    return rc;
+  if (!lse) return fail(PACT_ERR_INVALID_ARG, "lse is required");
+  if (!aligned(lse, 4)) return fail(PACT_ERR_ALIGN, "lse must be 4-byte aligned");
+  if (!ws || ws_bytes < pact_attention_bwd_workspace_size(q->rows, q->heads) || !aligned(ws, 256))
+    return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
+  DeviceInfo* d;
+  if ((rc = device_info(&d))) return rc;
+  if ((rc = make_heads_map(&L.tmQ, q, D, L.p.gp, L.p.tpt)) ||
+      (rc = make_heads_map(&L.tmdO, d_o, D, L.p.gp, L.p.tpt)) ||
+      (rc = make_heads_map(&L.tmK, k, D, 1, 128)) || (rc = make_heads_map(&L.tmV, v, D, 1, 128)))
+    return rc;
+  L.p.lse_in = lse;
+  L.p.o_in = o->p;
+  L.p.ldoi = o->ld;
+  L.p.dout = d_o->p;
+  L.p.lddo = d_o->ld;
+  L.p.delta = (float*)ws;
+  L.p.dq = dq->p;
+  L.p.dk = dk->p;
+  L.p.dv = dv->p;
+  L.p.lddq = dq->ld;
+  L.p.lddk = dk->ld;
+  L.p.lddv = dv->ld;
+  L.p.status = d->status;
+  L.num_sms = d->sms;
+  cudaError_t e = launch_attn_bwd(L, (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "attention bwd launch");
+}
+
+int64_t pact_grad_chunks(int64_t numel) {
+  return numel < 1 ? 0 : (numel + kGradChunk - 1) / kGradChunk;
+}
+
+// the blocks' sums: 4 an SM of the GPU that the library is for, whatever the device has
+constexpr int kGradSms = 152;
+size_t pact_grad_norm_workspace_size(void) { return align256(4 * kGradSms * sizeof(double)); }
+
+static int grad_norm(const pact_tensor_list* g, float* const* out, bool clip, double max_norm,
+                     float* norm, void* ws, size_t ws_bytes, pact_stream_t stream) {
+  if (!g || !g->data || !g->numel || !g->first || !norm || (clip && !out))
+    return fail(PACT_ERR_INVALID_ARG, "the lists and norm are required");
+  if (g->count < 1 || g->count > (int64_t)1 << 20 || g->chunks < 0 ||
+      g->chunks > (int64_t)1 << 40)
+    return fail(PACT_ERR_SHAPE, "need 1 <= count <= 2^20 and 0 <= chunks <= 2^40");
+  if (!aligned(g->data, 8) || !aligned(g->numel, 8) || !aligned(g->first, 8) ||
+      !aligned(out, 8) || !aligned(norm, 4))
+    return fail(PACT_ERR_ALIGN, "the lists must be 8-byte and norm 4-byte aligned");
+  if (!(max_norm >= 0.0)) return fail(PACT_ERR_INVALID_ARG, "max_norm must not be negative or NaN");
+  if (!ws || ws_bytes < pact_grad_norm_workspace_size() || !aligned(ws, 256))
+    return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
+  DeviceInfo* d;
+  int rc = device_info(&d);
+  if (rc) return rc;
+  GradTable t = {g->data, g->numel, g->first, g->count, g->chunks};
+  cudaError_t e = launch_grad_norm(t, clip ? out : nullptr, max_norm, norm, (double*)ws, kGradSms,
+                                   (cudaStream_t)stream);
+  return e == cudaSuccess ? PACT_OK : cuda_fail(e, "grad norm launch");
+}
+
+int pact_grad_norm(const pact_tensor_list* grads, float* norm, void* ws, size_t ws_bytes,
+                   pact_stream_t stream) {
+  return grad_norm(grads, nullptr, false, 0.0, norm, ws, ws_bytes, stream);
+}
+
+int pact_clip_grad_norm(const pact_tensor_list* grads, float* const* out, double max_norm,
+                        float* norm, void* ws, size_t ws_bytes, pact_stream_t stream) {
+  return grad_norm(grads, out, true, max_norm, norm, ws, ws_bytes, stream);
 }
 
 int pact_test_fp8_plan(int64_t rows, int64_t N, int64_t K, int sms, int64_t plan[3]) {

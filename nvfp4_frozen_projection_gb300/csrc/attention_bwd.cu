@@ -1,0 +1,868 @@
+// Attention over packed sequences, backward.  The probabilities are computed again from the
+// forward's lse, P = exp(scale S - lse):
+//   delta = sum_d do o;  dP = do v^T;  dS = P (dP - delta);
+//   dq = scale dS k;  dk = scale dS^T q;  dv = P^T do, the last two summed over the query
+//   heads that share a key head.
+//
+// Three launches.  delta is a pass over do and o (HBM).  dq and dk|dv are kernels of their
+// own, each with its sums in TMEM from the first tile to the last: seven products a tile in
+// place of the five of one kernel, whose dq would have to be added up in memory over all key
+// tiles, in an order that changes from run to run.  A CTA has one tile of 128 rows; one
+// thread issues the products, two warpgroups hold a row a thread and half its columns each.
+//
+//   dq:     rows are queries.  TMEM: S twice (0, 128), dP (256, dS over it), dq (384).
+//           Order: S of the next keys; dS ready: dq += dS k, then dP of the next keys.
+//   dk|dv:  rows are keys, columns the (token, head) rows of a query tile.  TMEM: S^T (0, P^T
+//           over it), dP^T (128, dS^T over it), dv (256), dk (384).
+//           Order: P ready: dv += P^T do, S^T of the next queries; dS ready: dk += dS^T q,
+//           dP^T of the next queries.
+// So the tensor cores have work while exponentials are taken, and MMAs of one thread run in
+// order, which is what lets the next S or dP overwrite the P or dS before it.  P and dS are
+// rounded to BF16 for their products; everything else is FP32.
+#include "attention.cuh"
+
+namespace pact {
+
+// A warpgroup's half of the columns of a 128-column tile, 64 of them, becomes 32 columns of
+// BF16 pairs at its own first column (0 or 64): neither half lies over what the other reads.
+__device__ __forceinline__ uint32_t half_step(int k) { return (k >> 2) * 64 + (k & 3) * 8; }
+
+// ------------------------------------------------------------------ delta
+template <int SEG>
+__global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
+  const int lane = threadIdx.x & 31, sl = lane & (SEG - 1);
+  const int64_t row = (int64_t)blockIdx.x * (256 / SEG) + threadIdx.x / SEG;
+  const int64_t rows = (int64_t)p.tq * p.hq;
+  const bool live = row < rows && sl * 8 < p.D;
+  const int64_t t = live ? row / p.hq : 0;
+  const int h = live ? (int)(row - t * p.hq) : 0;
+  float sum = 0.0f;
+  if (live) {
+    float a[8], b[8];
+    bf16x8_to_f32(*reinterpret_cast<const uint4*>(p.dout + t * p.lddo + (int64_t)h * p.D + sl * 8), a);
+    bf16x8_to_f32(*reinterpret_cast<const uint4*>(p.o_in + t * p.ldoi + (int64_t)h * p.D + sl * 8), b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = __fmaf_rn(a[e], b[e], sum);
+  }
+#pragma unroll
+  for (int o = SEG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (live && sl == 0 && PACT_IN(t < p.tq && h < p.hq)) p.delta[(int64_t)h * p.tq + t] = sum;
+}
+
+// ------------------------------------------------------------------ a ring of tiles
+// The copying warp's side of a ring of shared-memory tiles.  `valid` rows of a tile belong to
+// the sequence; a tile with fewer than `rows` has the others zeroed before the MMAs see it.
+template <int BOXES, int STAGES>
+struct TileRing {
+  static constexpr uint32_t TILE = BOXES * kBox;
+  uint32_t tiles;  // shared address of the ring
+  uint8_t* mem;
+  uint32_t full, empty, tail;
+  volatile uint32_t* abort_flag;
+  int stage = 0;
+  uint32_t phase = 0, tails = 0, pend = 0, pend_par = 0;
+
+  __device__ __forceinline__ bool load(const CUtensorMap* tm, int head, int row, int rows,
+                                       int valid, int lane) {
+    if (!mbar_wait(empty + 8 * stage, phase ^ 1u, kAttnWaitNs, abort_flag)) return false;
+    const bool whole = valid >= rows;
+    const uint32_t dst = tiles + stage * TILE, bar = whole ? full + 8 * stage : tail;
+    if (lane == 0) {
+      mbar_expect_tx(bar, (uint32_t)rows * 128 * BOXES);
+#pragma unroll
+      for (int b = 0; b < BOXES; ++b) tma_load_3d(dst + b * kBox, tm, b * 64, head, row, bar);
+    }
+    __syncwarp();
+    if (whole) {
+      pend |= 1u << stage;
+      pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+    } else {
+      if (!mbar_wait(tail, tails & 1u, kAttnWaitNs, nullptr)) return false;
+      ++tails;
+      zero_rows(mem + stage * TILE, BOXES, valid, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * stage);
+    }
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    return true;
+  }
+  // copies in flight land before the CTA can exit
+  __device__ __forceinline__ void drain() {
+    for (int s = 0; s < STAGES; ++s)
+      if (pend & (1u << s)) mbar_wait(full + 8 * s, (pend_par >> s) & 1u, 10000000ull, nullptr);
+  }
+};
+
+template <int DP>
+struct BwdCfg {
+  static constexpr int BOXES = DP / 64;
+  static constexpr uint32_t TILE = BOXES * kBox;
+  static constexpr int STAGES = DP == 64 ? 8 : 5;
+  // two tiles that stay for a unit, the ring, and (dk|dv) two buffers of 128 -lse and delta
+  static constexpr uint32_t RING_OFF = 2 * TILE, STAT_OFF = RING_OFF + STAGES * TILE;
+  static constexpr uint32_t BAR_OFF = STAT_OFF + 2048;
+  // 12 barriers and 4 of the statistics, the ring's; behind them the TMEM slot and the abort flag
+  static constexpr uint32_t SLOT_OFF = BAR_OFF + 128 + 16 * STAGES, SMEM = SLOT_OFF + 16;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct BwdBars {
+  uint32_t fix_full[2], fix_empty[2];  // the two tiles of a unit
+  uint32_t s_full[2], dp_full, p_full, ds_full, acc_full, tail, final_bar;
+  uint32_t stat_full, stat_empty;  // [2] each
+  uint32_t full, empty;            // the ring
+};
+__device__ __forceinline__ BwdBars bwd_bars(uint32_t b, int stages) {
+  BwdBars r;
+  r.fix_full[0] = b;
+  r.fix_full[1] = b + 8;
+  r.fix_empty[0] = b + 16;
+  r.fix_empty[1] = b + 24;
+  r.s_full[0] = b + 32;
+  r.s_full[1] = b + 40;
+  r.dp_full = b + 48;
+  r.p_full = b + 56;
+  r.ds_full = b + 64;
+  r.acc_full = b + 72;
+  r.tail = b + 80;
+  r.final_bar = b + 88;
+  r.stat_full = b + 96;
+  r.stat_empty = b + 112;
+  r.full = b + 128;
+  r.empty = r.full + 8 * stages;
+  return r;
+}
+
+// ------------------------------------------------------------------ dq
+template <int DP>
+__global__ void __launch_bounds__(384, 1)
+    k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+              const AttnParams p) {
+  using C = BwdCfg<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_addr(smem);
+  if (base & 1023u) {  // the swizzle needs it, and the budget leaves no room to round up
+    if (threadIdx.x == 0) atomicOr(p.status, (unsigned)PACT_DEV_BOUNDS);
+    return;
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::SLOT_OFF + 4);
+  const BwdBars B = bwd_bars(base + C::BAR_OFF, C::STAGES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B.fix_full[i], 1);
+      mbar_init(B.fix_empty[i], 1);
+      mbar_init(B.s_full[i], 1);
+    }
+    mbar_init(B.dp_full, 1);
+    mbar_init(B.ds_full, 8);  // the computing warps
+    mbar_init(B.acc_full, 1);
+    mbar_init(B.tail, 1);
+    mbar_init(B.final_bar, 1);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(B.full + 8 * s, 1);
+      mbar_init(B.empty + 8 * s, 1);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  SeqFinder finder = seq_finder(p, p.tpt, false);
+  Seq s;
+  int tok0, nk, kvh, h0;
+  auto next_unit = [&](int64_t u) {
+    const int64_t t = u / p.units_h;
+    const int hu = (int)(u - t * p.units_h);
+    if (!finder.find(t, s)) return false;
+    kvh = hu / p.subs;
+    h0 = kvh * p.group + (hu - kvh * p.subs) * p.gp;
+    tok0 = (p.causal ? s.tiles - 1 - s.tile : s.tile) * p.tpt;  // the longest first
+    int kend = s.lk;
+    if (p.causal) kend = SeqFinder::clampi(min(tok0 + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
+    nk = (kend + 127) / 128;
+    return true;
+  };
+
+  if (warp >= 8) {
+    setmaxnreg_dec<72>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ copies
+      TileRing<C::BOXES, C::STAGES> ring;
+      ring.tiles = base + C::RING_OFF;
+      ring.mem = smem + C::RING_OFF;
+      ring.full = B.full;
+      ring.empty = B.empty;
+      ring.tail = B.tail;
+      ring.abort_flag = abort_flag;
+      uint32_t uses = 0;
+      bool ok = true;
+      auto load_fix = [&](int i, const CUtensorMap* tm) {
+        if (!mbar_wait(B.fix_empty[i], (uses & 1u) ^ 1u, kAttnWaitNs, abort_flag)) return false;
+        if (lane == 0) {
+          mbar_expect_tx(B.fix_full[i], (uint32_t)(p.tpt * p.gp) * 128 * C::BOXES);
+#pragma unroll
+          for (int b = 0; b < C::BOXES; ++b)
+            tma_load_3d(base + i * C::TILE + b * kBox, tm, b * 64, h0, s.q0 + tok0, B.fix_full[i]);
+        }
+        __syncwarp();
+        return true;
+      };
+      uint32_t fixed = 0;
+      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+        if (nk == 0) continue;
+        for (int j = 0; j < nk && ok; ++j) {
+          const int row = s.k0 + j * 128, valid = s.lk - j * 128;
+          if (j == 0) {
+            ok = load_fix(0, &tmQ);
+            if (ok) fixed = 1;
+          }
+          ok = ok && ring.load(&tmK, kvh, row, 128, valid, lane);
+          if (j == 0) {
+            ok = ok && load_fix(1, &tmdO);
+            if (ok) fixed = 2;
+          }
+          ok = ok && ring.load(&tmV, kvh, row, 128, valid, lane);
+        }
+        if (ok) {
+          ++uses;
+          fixed = 0;
+        }
+      }
+      if (!ok) {
+        if (lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_TMA);
+        ring.drain();
+        for (uint32_t i = 0; i < fixed; ++i) mbar_wait(B.fix_full[i], uses & 1u, 10000000ull, nullptr);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMAs
+      int stage = 0;  // of K of the current tile; V follows it
+      uint32_t phase = 0, uses = 0, tiles = 0;
+      bool ok = true;
+      const uint32_t idesc_s = attn_idesc(128, false), idesc_d = attn_idesc(p.D, true);
+      const int ksteps = p.D / 16;
+      auto ahead = [&](int& st, uint32_t& ph, int by) {
+        st += by;
+        if (st >= C::STAGES) {
+          st -= C::STAGES;
+          ph ^= 1u;
+        }
+      };
+      auto wait_tile = [&](int st, uint32_t ph) {
+        return mbar_wait(B.full + 8 * st, ph, kAttnWaitNs, abort_flag);
+      };
+      // 128 x 128 product of a fixed tile and a ring tile over the head's columns
+      auto mma_rows = [&](uint32_t d, int fix, int st) {
+        const uint64_t da = desc_k(base + fix * C::TILE);
+        const uint64_t db = desc_k(base + C::RING_OFF + st * C::TILE);
+        for (int k = 0; k < ksteps; ++k)
+          mma_bf16(tmem + d, step_k(da, k), step_k(db, k), idesc_s, k > 0);
+      };
+      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+        if (nk == 0) continue;
+        ok = mbar_wait(B.fix_full[0], uses & 1u, kAttnWaitNs, abort_flag) && wait_tile(stage, phase);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          mma_rows((tiles & 1u) * 128, 0, stage);
+          mma_commit(B.s_full[tiles & 1u]);
+          if (nk == 1) mma_commit(B.fix_empty[0]);
+        }
+        __syncwarp();
+        int vst = stage;
+        uint32_t vph = phase;
+        ahead(vst, vph, 1);
+        ok = mbar_wait(B.fix_full[1], uses & 1u, kAttnWaitNs, abort_flag) && wait_tile(vst, vph);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          mma_rows(256, 1, vst);
+          mma_commit(B.dp_full);
+          mma_commit(B.empty + 8 * vst);
+          if (nk == 1) mma_commit(B.fix_empty[1]);
+        }
+        __syncwarp();
+        for (int j = 0; j < nk; ++j, ++tiles) {
+          const bool more = j + 1 < nk;
+          int kst = stage, nvst;
+          uint32_t kph = phase, nvph;
+          ahead(kst, kph, 2);
+          nvst = kst;
+          nvph = kph;
+          ahead(nvst, nvph, 1);
+          if (more) {
+            if (!(ok = wait_tile(kst, kph))) break;
+            tc_fence_after();
+            if (lane == 0) {
+              mma_rows(((tiles + 1) & 1u) * 128, 0, kst);
+              mma_commit(B.s_full[(tiles + 1) & 1u]);
+              if (j + 2 == nk) mma_commit(B.fix_empty[0]);
+            }
+            __syncwarp();
+          }
+          if (!(ok = mbar_wait(B.ds_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t d = desc_n(base + C::RING_OFF + stage * C::TILE);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_ta(tmem + 384, tmem + 256 + half_step(k), step_n(d, k), idesc_d,
+                          (j > 0 || k > 0) ? 1u : 0u);
+            mma_commit(B.empty + 8 * stage);
+            if (!more) mma_commit(B.acc_full);
+          }
+          __syncwarp();
+          if (more) {
+            if (!(ok = wait_tile(nvst, nvph))) break;
+            tc_fence_after();
+            if (lane == 0) {
+              mma_rows(256, 1, nvst);
+              mma_commit(B.dp_full);
+              mma_commit(B.empty + 8 * nvst);
+              if (j + 2 == nk) mma_commit(B.fix_empty[1]);
+            }
+            __syncwarp();
+          }
+          ahead(stage, phase, 2);
+        }
+        ++uses;
+      }
+      if (lane == 0) {
+        if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
+        mma_commit(B.final_bar);
+        mbar_wait(B.final_bar, 0, kAttnWaitNs, nullptr);
+      }
+      __syncwarp();
+    }
+  } else {
+    // -------------------------------------------------------------- a row and 64 columns a thread
+    setmaxnreg_inc<216>();
+    const int half = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float c = p.c;
+    uint32_t tiles = 0, uses = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      const int rt = row_token(p, row), tok = tok0 + rt;
+      const bool live = tok < s.lq && row < p.tpt * p.gp;
+      const int lim = p.causal ? min(s.lk, tok + 1 + s.lk - s.lq) : s.lk;
+      const int lim_all = p.causal ? min(s.lk, tok0 + 1 + s.lk - s.lq) : s.lk;
+      float nlse = 0.0f, delta = 0.0f;
+      if (live && nk > 0) {
+        const int64_t at = (int64_t)(h0 + row - rt * p.gp) * p.tq + s.q0 + tok;
+        nlse = -p.lse_in[at] * kLog2e;
+        delta = p.delta[at];
+      }
+      for (int j = 0; j < nk; ++j, ++tiles) {
+        if (!(ok = mbar_wait(B.s_full[tiles & 1u], (tiles >> 1) & 1u, kAttnWaitNs, abort_flag))) break;
+        tc_fence_after();
+        uint32_t v[64];
+        const uint32_t ts = tl + (tiles & 1u) * 128 + half * 64;
+        tmem_ld32(ts, v);
+        tmem_ld32(ts + 32, v + 32);
+        tmem_ld_wait32(v);
+        tmem_ld_wait32(v + 32);
+        float pr[64];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float2 x = __ffma2_rn(
+              make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+              make_float2(c, c), make_float2(nlse, nlse));
+          pr[2 * e] = ex2_ftz(x.x);
+          pr[2 * e + 1] = ex2_ftz(x.y);
+        }
+        if ((j + 1) * 128 > lim_all) {
+          const int x = lim - j * 128 - half * 64;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) pr[e] = e < x ? pr[e] : 0.0f;
+        }
+        if (!(ok = mbar_wait(B.dp_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t td = tl + 256 + half * 64;
+        tmem_ld32(td, v);
+        tmem_ld32(td + 32, v + 32);
+        tmem_ld_wait32(v);
+        tmem_ld_wait32(v + 32);
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          w[e] = pack_bf16x2(pr[2 * e] * (__uint_as_float(v[2 * e]) - delta),
+                             pr[2 * e + 1] * (__uint_as_float(v[2 * e + 1]) - delta));
+        tmem_st32(td, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.ds_full);
+      }
+      if (!ok) break;
+      if (nk > 0) {
+        if (!(ok = mbar_wait(B.acc_full, uses & 1u, kAttnWaitNs, abort_flag))) break;
+        ++uses;
+        tc_fence_after();
+      }
+      const int b = half * 64, cols = p.D - b;
+      if (cols <= 0) continue;
+      uint32_t w[32];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t o[16];
+        const bool have = nk > 0 && h * 16 < cols;
+        if (have) {
+          tmem_ld16(tl + 384 + b + 16 * h, o);
+          tmem_ld_wait16(o);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[8 * h + e] = have && lim > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * p.scale,
+                                                       __uint_as_float(o[2 * e + 1]) * p.scale)
+                                         : 0u;
+      }
+      store_rows64(w, lane, min(cols, 64), [&](int r) -> uint16_t* {
+        const int rr = quarter * 32 + r;
+        const int t = row_token(p, rr), tt = tok0 + t;
+        if (tt >= s.lq || rr >= p.tpt * p.gp || !PACT_IN(s.q0 + tt < p.tq)) return nullptr;
+        return p.dq + (int64_t)(s.q0 + tt) * p.lddq + (int64_t)(h0 + rr - t * p.gp) * p.D + b;
+      });
+    }
+    if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dk and dv
+template <int DP>
+__global__ void __launch_bounds__(384, 1)
+    k_attn_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const AttnParams p) {
+  using C = BwdCfg<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_addr(smem);
+  if (base & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.status, (unsigned)PACT_DEV_BOUNDS);
+    return;
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::SLOT_OFF + 4);
+  const BwdBars B = bwd_bars(base + C::BAR_OFF, C::STAGES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(B.fix_full[0], 1);
+    mbar_init(B.fix_empty[0], 1);
+    mbar_init(B.s_full[0], 1);
+    mbar_init(B.dp_full, 1);
+    mbar_init(B.p_full, 8);  // the computing warps
+    mbar_init(B.ds_full, 8);
+    mbar_init(B.acc_full, 1);
+    mbar_init(B.tail, 1);
+    mbar_init(B.final_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B.stat_full + 8 * i, 1);
+      mbar_init(B.stat_empty + 8 * i, 8);
+    }
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(B.full + 8 * s, 1);
+      mbar_init(B.empty + 8 * s, 1);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == 9) {
+    // rows that no copy writes (gp that does not divide 128) are zeros for good
+    for (int st = 0; st < C::STAGES; ++st)
+      zero_rows(smem + C::RING_OFF + st * C::TILE, C::BOXES, p.tpt * p.gp, lane);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  SeqFinder finder = seq_finder(p, 128, true);
+  Seq s;
+  int key0, kvh, qt0, nqt, n;  // first key; first query tile and how many; times the subgroups
+  auto next_unit = [&](int64_t u) {
+    const int64_t t = u / p.hk;
+    kvh = (int)(u - t * p.hk);
+    if (!finder.find(t, s)) return false;
+    key0 = s.tile * 128;
+    qt0 = 0;
+    if (p.causal) qt0 = SeqFinder::clampi(key0 - (s.lk - s.lq), 0, s.lq) / p.tpt;
+    nqt = (s.lq + p.tpt - 1) / p.tpt - qt0;
+    n = nqt * p.subs;
+    return true;
+  };
+  // iteration i of a unit: its first query head, and its tile's first token
+  auto tile_of = [&](int i, int& h0, int& tok0) {
+    const int sub = p.subs == 1 ? 0 : i / nqt;
+    h0 = kvh * p.group + sub * p.gp;
+    tok0 = (qt0 + i - sub * nqt) * p.tpt;
+  };
+
+  if (warp >= 8) {
+    setmaxnreg_dec<72>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ copies
+      TileRing<C::BOXES, C::STAGES> ring;
+      ring.tiles = base + C::RING_OFF;
+      ring.mem = smem + C::RING_OFF;
+      ring.full = B.full;
+      ring.empty = B.empty;
+      ring.tail = B.tail;
+      ring.abort_flag = abort_flag;
+      uint32_t uses = 0;
+      bool ok = true, fixed = false;
+      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+        if (n == 0) continue;
+        if (!(ok = mbar_wait(B.fix_empty[0], (uses & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
+        if (lane == 0) {
+          mbar_expect_tx(B.fix_full[0], 2 * C::TILE);
+#pragma unroll
+          for (int b = 0; b < C::BOXES; ++b) {
+            tma_load_3d(base + b * kBox, &tmK, b * 64, kvh, s.k0 + key0, B.fix_full[0]);
+            tma_load_3d(base + C::TILE + b * kBox, &tmV, b * 64, kvh, s.k0 + key0, B.fix_full[0]);
+          }
+        }
+        __syncwarp();
+        fixed = true;
+        for (int i = 0; i < n && ok; ++i) {
+          int h0, tok0;
+          tile_of(i, h0, tok0);
+          const int rows = p.tpt * p.gp, valid = min(p.tpt, s.lq - tok0) * p.gp;
+          ok = ring.load(&tmQ, h0, s.q0 + tok0, rows, valid, lane);
+          ok = ok && ring.load(&tmdO, h0, s.q0 + tok0, rows, valid, lane);
+        }
+        if (ok) {
+          ++uses;
+          fixed = false;
+        }
+      }
+      if (!ok) {
+        if (lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_TMA);
+        ring.drain();
+        if (fixed) mbar_wait(B.fix_full[0], uses & 1u, 10000000ull, nullptr);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMAs
+      int stage = 0;  // of Q of the current tile; dO follows it
+      uint32_t phase = 0, uses = 0, tiles = 0;
+      bool ok = true;
+      const uint32_t idesc_s = attn_idesc(128, false), idesc_d = attn_idesc(p.D, true);
+      const int ksteps = p.D / 16;
+      auto ahead = [&](int& st, uint32_t& ph, int by) {
+        st += by;
+        if (st >= C::STAGES) {
+          st -= C::STAGES;
+          ph ^= 1u;
+        }
+      };
+      auto wait_tile = [&](int st, uint32_t ph) {
+        return mbar_wait(B.full + 8 * st, ph, kAttnWaitNs, abort_flag);
+      };
+      auto mma_rows = [&](uint32_t d, int fix, int st) {
+        const uint64_t da = desc_k(base + fix * C::TILE);
+        const uint64_t db = desc_k(base + C::RING_OFF + st * C::TILE);
+        for (int k = 0; k < ksteps; ++k)
+          mma_bf16(tmem + d, step_k(da, k), step_k(db, k), idesc_s, k > 0);
+      };
+      // sum += (P or dS at column `a`)^T times a ring tile's rows
+      auto mma_sum = [&](uint32_t d, uint32_t a, int st, bool first) {
+        const uint64_t db = desc_n(base + C::RING_OFF + st * C::TILE);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_ta(tmem + d, tmem + a + half_step(k), step_n(db, k), idesc_d,
+                      (!first || k > 0) ? 1u : 0u);
+      };
+      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+        if (n == 0) continue;
+        int ost = stage;
+        uint32_t oph = phase;
+        ahead(ost, oph, 1);
+        ok = mbar_wait(B.fix_full[0], uses & 1u, kAttnWaitNs, abort_flag) && wait_tile(stage, phase);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          mma_rows(0, 0, stage);
+          mma_commit(B.s_full[0]);
+        }
+        __syncwarp();
+        if (!(ok = wait_tile(ost, oph))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          mma_rows(128, 1, ost);
+          mma_commit(B.dp_full);
+          if (n == 1) mma_commit(B.fix_empty[0]);
+        }
+        __syncwarp();
+        for (int i = 0; i < n; ++i, ++tiles) {
+          const bool more = i + 1 < n;
+          int nq = stage, no;
+          uint32_t nqp = phase, nop;
+          ost = stage;
+          oph = phase;
+          ahead(ost, oph, 1);
+          ahead(nq, nqp, 2);
+          no = nq;
+          nop = nqp;
+          ahead(no, nop, 1);
+          if (!(ok = mbar_wait(B.p_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            mma_sum(256, 0, ost, i == 0);
+            mma_commit(B.empty + 8 * ost);
+          }
+          __syncwarp();
+          if (more) {
+            if (!(ok = wait_tile(nq, nqp))) break;
+            tc_fence_after();
+            if (lane == 0) {
+              mma_rows(0, 0, nq);
+              mma_commit(B.s_full[0]);
+            }
+            __syncwarp();
+          }
+          if (!(ok = mbar_wait(B.ds_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            mma_sum(384, 128, stage, i == 0);
+            mma_commit(B.empty + 8 * stage);
+            if (!more) mma_commit(B.acc_full);
+          }
+          __syncwarp();
+          if (more) {
+            if (!(ok = wait_tile(no, nop))) break;
+            tc_fence_after();
+            if (lane == 0) {
+              mma_rows(128, 1, no);
+              mma_commit(B.dp_full);
+              if (i + 2 == n) mma_commit(B.fix_empty[0]);
+            }
+            __syncwarp();
+          }
+          ahead(stage, phase, 2);
+        }
+        ++uses;
+      }
+      if (lane == 0) {
+        if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
+        mma_commit(B.final_bar);
+        mbar_wait(B.final_bar, 0, kAttnWaitNs, nullptr);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ------------------------------------------------------------ -lse and delta of the columns
+      uint32_t tiles = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+        for (int i = 0; i < n; ++i, ++tiles) {
+          int h0, tok0;
+          tile_of(i, h0, tok0);
+          const uint32_t buf = tiles & 1u;
+          float nl[4], de[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int x = k * 32 + lane, rt = row_token(p, x), tok = tok0 + rt;
+            nl[k] = -INFINITY;  // rows of no query: P = 0
+            de[k] = 0.0f;
+            if (x < p.tpt * p.gp && tok < s.lq) {
+              const int64_t at = (int64_t)(h0 + x - rt * p.gp) * p.tq + s.q0 + tok;
+              nl[k] = -p.lse_in[at] * kLog2e;
+              de[k] = p.delta[at];
+            }
+          }
+          if (!(ok = mbar_wait(B.stat_empty + 8 * buf, ((tiles >> 1) & 1u) ^ 1u, kAttnWaitNs,
+                               abort_flag)))
+            break;
+          float* st = reinterpret_cast<float*>(smem + C::STAT_OFF + buf * 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            st[k * 32 + lane] = nl[k];
+            st[128 + k * 32 + lane] = de[k];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(B.stat_full + 8 * buf);
+        }
+      }
+      if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_SF);
+    }
+  } else {
+    // -------------------------------------------------------------- a key and 64 columns a thread
+    setmaxnreg_inc<216>();
+    const int half = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
+    const float c = p.c;
+    uint32_t tiles = 0, uses = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      const int key = key0 + row;
+      for (int i = 0; i < n; ++i, ++tiles) {
+        int h0, tok0;
+        tile_of(i, h0, tok0);
+        const uint32_t buf = tiles & 1u;
+        const float* st = reinterpret_cast<const float*>(smem + C::STAT_OFF + buf * 1024) + half * 64;
+        if (!(ok = mbar_wait(B.stat_full + 8 * buf, (tiles >> 1) & 1u, kAttnWaitNs, abort_flag) &&
+                   mbar_wait(B.s_full[0], tiles & 1u, kAttnWaitNs, abort_flag)))
+          break;
+        tc_fence_after();
+        uint32_t v[64];
+        tmem_ld32(tl, v);
+        tmem_ld32(tl + 32, v + 32);
+        tmem_ld_wait32(v);
+        tmem_ld_wait32(v + 32);
+        float pr[64];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 nl = *reinterpret_cast<const float4*>(st + 4 * e);
+          const float2 a = __ffma2_rn(
+              make_float2(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])),
+              make_float2(c, c), make_float2(nl.x, nl.y));
+          const float2 b = __ffma2_rn(
+              make_float2(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])),
+              make_float2(c, c), make_float2(nl.z, nl.w));
+          pr[4 * e] = ex2_ftz(a.x);
+          pr[4 * e + 1] = ex2_ftz(a.y);
+          pr[4 * e + 2] = ex2_ftz(b.x);
+          pr[4 * e + 3] = ex2_ftz(b.y);
+        }
+        if (p.causal && key0 + 127 - (s.lk - s.lq) > tok0) {
+          // the first column whose token sees this key
+          const int64_t x0 = (int64_t)(key - (s.lk - s.lq) - tok0) * p.gp - half * 64;
+          const int x = (int)(x0 > 64 ? 64 : (x0 < 0 ? 0 : x0));
+#pragma unroll
+          for (int e = 0; e < 64; ++e) pr[e] = e >= x ? pr[e] : 0.0f;
+        }
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) w[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
+        tmem_st32(tl, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.p_full);
+
+        if (!(ok = mbar_wait(B.dp_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
+        tc_fence_after();
+        tmem_ld32(tl + 128, v);
+        tmem_ld32(tl + 160, v + 32);
+        tmem_ld_wait32(v);
+        tmem_ld_wait32(v + 32);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 de = *reinterpret_cast<const float4*>(st + 128 + 4 * e);
+          w[2 * e] = pack_bf16x2(pr[4 * e] * (__uint_as_float(v[4 * e]) - de.x),
+                                 pr[4 * e + 1] * (__uint_as_float(v[4 * e + 1]) - de.y));
+          w[2 * e + 1] = pack_bf16x2(pr[4 * e + 2] * (__uint_as_float(v[4 * e + 2]) - de.z),
+                                     pr[4 * e + 3] * (__uint_as_float(v[4 * e + 3]) - de.w));
+        }
+        tmem_st32(tl + 128, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(B.ds_full);
+          mbar_arrive(B.stat_empty + 8 * buf);
+        }
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!(ok = mbar_wait(B.acc_full, uses & 1u, kAttnWaitNs, abort_flag))) break;
+        ++uses;
+        tc_fence_after();
+      }
+      // one warpgroup stores dv, the other dk
+      const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (half ? 384 : 256);
+      uint16_t* out = half ? p.dk : p.dv;
+      const int64_t ld = half ? p.lddk : p.lddv;
+      const float f = half ? p.scale : 1.0f;
+      for (int b = 0; b < p.D; b += 64) {
+        const int cols = min(64, p.D - b);
+        uint32_t w[32];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t o[16];
+          const bool have = n > 0 && h * 16 < cols;
+          if (have) {
+            tmem_ld16(ta + b + 16 * h, o);
+            tmem_ld_wait16(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[8 * h + e] = have ? pack_bf16x2(__uint_as_float(o[2 * e]) * f,
+                                              __uint_as_float(o[2 * e + 1]) * f)
+                                : 0u;
+        }
+        store_rows64(w, lane, cols, [&](int r) -> uint16_t* {
+          const int k = key0 + quarter * 32 + r;
+          if (k >= s.lk || !PACT_IN(s.k0 + k < p.tk)) return nullptr;
+          return out + (int64_t)(s.k0 + k) * ld + (int64_t)kvh * p.D + b;
+        });
+      }
+    }
+    if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DP>
+static cudaError_t launch_bwd(const AttnBwdLaunch& L, unsigned gq, unsigned gk, cudaStream_t st) {
+  constexpr uint32_t sm = BwdCfg<DP>::SMEM;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(k_attn_dq<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)) ||
+      (e = cudaFuncSetAttribute(k_attn_dkdv<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)))
+    return e;
+  note_launch();
+  k_attn_dq<DP><<<gq, 384, sm, st>>>(L.tmQ, L.tmdO, L.tmK, L.tmV, L.p);
+  if ((e = cudaGetLastError())) return e;
+  note_launch();
+  k_attn_dkdv<DP><<<gk, 384, sm, st>>>(L.tmQ, L.tmdO, L.tmK, L.tmV, L.p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_bwd(const AttnBwdLaunch& L, cudaStream_t st) {
+  const AttnParams& p = L.p;
+  const int64_t rows = (int64_t)p.tq * p.hq;
+  note_launch();
+  if (p.D <= 64)
+    k_attn_delta<8><<<(unsigned)((rows + 31) / 32), 256, 0, st>>>(p);
+  else
+    k_attn_delta<16><<<(unsigned)((rows + 15) / 16), 256, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // at most: whole tiles of all rows, and a ragged one for each sequence
+  const int64_t uq = ((int64_t)p.tq / p.tpt + p.nseq) * p.units_h;
+  const int64_t uk = ((int64_t)p.tk / 128 + p.nseq) * p.hk;
+  const unsigned gq = (unsigned)(uq < L.num_sms ? uq : L.num_sms);
+  const unsigned gk = (unsigned)(uk < L.num_sms ? uk : L.num_sms);
+  return p.D <= 64 ? launch_bwd<64>(L, gq, gk, st) : launch_bwd<128>(L, gq, gk, st);
+}
+
+}  // namespace pact

@@ -1,0 +1,418 @@
+// Attention over packed sequences, forward:
+//   S = q k^T;  P = softmax(scale S) over the visible keys;  o = P v;
+//   lse = log(sum of exp(scale S)).
+// With causal, query i of a sequence's lq sees key j of its lk when j <= i + lk - lq.
+//
+// One pass over the keys with the running maximum and sum of the softmax.  A CTA has two
+// tiles of 128 query rows (attention.cuh) against tiles of 128 keys, and a warpgroup for each,
+// a row a thread; while one softmax runs, the tensor cores work for the other tile:
+//   S_i  128 TMEM columns, P_i (BF16) over the first half of them, O_i behind both S.
+// One thread issues P_0 V, S_0 of the next keys, P_1 V, S_1 of the next keys, in turn;
+// MMAs of one thread run in order, so S_i may be issued behind the P_i V that reads P_i out
+// of the same columns.  Keys and values pass through one ring of shared memory.
+//
+// The running maximum m of a row moves only when a new one is above it by more than 2^8 in
+// the exponentials' scale: the sums stay far from FP32's range, and the rescaling of O in
+// TMEM that a moved m needs is rare.  P is rounded to BF16 for its product (its sum is of
+// the FP32 values); sums, maxima and O are FP32.
+#include "attention.cuh"
+
+namespace pact {
+
+template <int DP>
+struct FwdCfg {
+  static constexpr int BOXES = DP / 64;
+  static constexpr uint32_t TILE = BOXES * kBox;
+  static constexpr int STAGES = DP == 64 ? 8 : 5;
+  static constexpr uint32_t Q_OFF = 0, KV_OFF = 2 * TILE;
+  static constexpr uint32_t BAR_OFF = KV_OFF + STAGES * TILE;
+  static constexpr uint32_t SMEM = BAR_OFF + 512 + 1024;
+  // q_full[2] q_empty[2] s_full[2] p_full[2] o_done[2] tail final kv_full[ST] kv_empty[ST]
+  static constexpr int NBARS = 12 + 2 * STAGES;
+  static_assert(SMEM <= 232448 && NBARS * 8 <= 504, "shared memory");
+};
+
+template <int DP>
+__global__ void __launch_bounds__(384, 1)
+    k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+  using C = FwdCfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const uint32_t bars = base + C::BAR_OFF;
+  const uint32_t q_full = bars, q_empty = bars + 16, s_full = bars + 32, p_full = bars + 48,
+                 o_done = bars + 64, tail_bar = bars + 80, final_bar = bars + 88,
+                 kv_full = bars + 96, kv_empty = kv_full + 8 * C::STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 504);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 508);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);  // the warps of a tile
+      mbar_init(o_done + 8 * i, 1);
+    }
+    mbar_init(tail_bar, 1);
+    mbar_init(final_bar, 1);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(kv_full + 8 * s, 1);
+      mbar_init(kv_empty + 8 * s, 1);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int tpu = 2 * p.tpt;  // tokens of a unit
+  SeqFinder finder = seq_finder(p, tpu, false);
+  Seq s;
+  // the unit's tiles: first token, and tiles of keys that they see
+  int tok0[2], nk[2], kvh, h0;
+  auto next_unit = [&](int64_t u) {
+    const int64_t t = u / p.units_h;
+    const int hu = (int)(u - t * p.units_h);
+    if (!finder.find(t, s)) return false;
+    kvh = hu / p.subs;
+    h0 = kvh * p.group + (hu - kvh * p.subs) * p.gp;
+    const int tile = p.causal ? s.tiles - 1 - s.tile : s.tile;  // the longest first
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      tok0[i] = tile * tpu + i * p.tpt;
+      int kend = 0;
+      if (tok0[i] < s.lq) {
+        kend = s.lk;
+        if (p.causal)
+          kend = SeqFinder::clampi(min(tok0[i] + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
+      }
+      nk[i] = (kend + 127) / 128;
+    }
+    return true;
+  };
+
+  if (warp >= 8) {
+    setmaxnreg_dec<72>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ copies
+      int stage = 0;
+      uint32_t phase = 0, q_uses[2] = {0, 0}, tails = 0;
+      uint32_t pend = 0, pend_par = 0;
+      bool ok = true;
+      auto load_kv = [&](const CUtensorMap* tm, int row, int valid) {
+        if (!mbar_wait(kv_empty + 8 * stage, phase ^ 1u, kAttnWaitNs, abort_flag)) return false;
+        const uint32_t dst = base + C::KV_OFF + stage * C::TILE, full = kv_full + 8 * stage;
+        if (valid >= 128) {
+          if (lane == 0) {
+            mbar_expect_tx(full, C::TILE);
+#pragma unroll
+            for (int b = 0; b < C::BOXES; ++b)
+              tma_load_3d(dst + b * kBox, tm, b * 64, kvh, row, full);
+          }
+          pend |= 1u << stage;
+          pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+        } else {  // rows behind the sequence become zeros before the MMAs see the tile
+          if (lane == 0) {
+            mbar_expect_tx(tail_bar, C::TILE);
+#pragma unroll
+            for (int b = 0; b < C::BOXES; ++b)
+              tma_load_3d(dst + b * kBox, tm, b * 64, kvh, row, tail_bar);
+          }
+          __syncwarp();
+          if (!mbar_wait(tail_bar, tails & 1u, kAttnWaitNs, nullptr)) return false;
+          ++tails;
+          zero_rows(smem + C::KV_OFF + stage * C::TILE, C::BOXES, valid, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return true;
+      };
+      auto load_q = [&](int i) {
+        if (!mbar_wait(q_empty + 8 * i, (q_uses[i] & 1u) ^ 1u, kAttnWaitNs, abort_flag)) return false;
+        ++q_uses[i];
+        if (lane == 0) {
+          const uint32_t rows = (uint32_t)(p.tpt * p.gp), full = q_full + 8 * i;
+          mbar_expect_tx(full, rows * 128 * C::BOXES);
+#pragma unroll
+          for (int b = 0; b < C::BOXES; ++b)
+            tma_load_3d(base + C::Q_OFF + i * C::TILE + b * kBox, &tmQ, b * 64, h0, s.q0 + tok0[i],
+                        full);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+        const int n = max(nk[0], nk[1]);
+        for (int j = 0; j < n && ok; ++j) {
+          if (j == 0 && nk[0] > 0) ok = load_q(0);
+          ok = ok && load_kv(&tmK, s.k0 + j * 128, 128);
+          if (j == 0 && nk[1] > 0) ok = ok && load_q(1);
+          ok = ok && load_kv(&tmV, s.k0 + j * 128, s.lk - j * 128);
+        }
+      }
+      if (!ok) {
+        if (lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_TMA);
+        // copies in flight land before the CTA can exit
+        for (int st = 0; st < C::STAGES; ++st)
+          if (pend & (1u << st))
+            mbar_wait(kv_full + 8 * st, (pend_par >> st) & 1u, 10000000ull, nullptr);
+        for (int i = 0; i < 2; ++i)
+          if (q_uses[i]) mbar_wait(q_full + 8 * i, (q_uses[i] & 1u) ^ 1u, 10000000ull, nullptr);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMAs
+      int stage = 0;
+      uint32_t phase = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+      bool ok = true;
+      const uint32_t idesc_s = attn_idesc(128, false), idesc_o = attn_idesc(p.D, true);
+      const int ksteps = p.D / 16;
+      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+        const int n = max(nk[0], nk[1]);
+        // step j: the values of tile j - 1 (the stage that is being used), the keys of j
+        int v_stage = 0;
+        for (int j = 0; j <= n && ok; ++j) {
+          if (n == 0) break;
+          bool v_seen = false, k_seen = false;
+          uint32_t v_phase = phase;
+          int k_stage = stage;
+          uint32_t k_phase = phase;
+          if (j > 0) {
+            v_stage = stage;
+            v_phase = phase;
+            k_stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+            k_phase = stage + 1 == C::STAGES ? phase ^ 1u : phase;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (j > 0 && j - 1 < nk[i]) {
+              if (!v_seen) ok = ok && mbar_wait(kv_full + 8 * v_stage, v_phase, kAttnWaitNs, abort_flag);
+              v_seen = true;
+              ok = ok && mbar_wait(p_full + 8 * i, p_uses[i] & 1u, kAttnWaitNs, abort_flag);
+              ++p_uses[i];
+              if (!ok) break;
+              tc_fence_after();
+              if (lane == 0) {
+                const uint64_t d = desc_n(base + C::KV_OFF + v_stage * C::TILE);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  mma_bf16_ta(tmem + 256 + i * 128, tmem + i * 128 + k * 8, step_n(d, k), idesc_o,
+                              (j > 1 || k > 0) ? 1u : 0u);
+                mma_commit(o_done + 8 * i);
+              }
+              __syncwarp();
+            }
+            if (j < nk[i]) {
+              if (!k_seen) ok = ok && mbar_wait(kv_full + 8 * k_stage, k_phase, kAttnWaitNs, abort_flag);
+              k_seen = true;
+              if (j == 0) {
+                ok = ok && mbar_wait(q_full + 8 * i, q_uses[i] & 1u, kAttnWaitNs, abort_flag);
+                ++q_uses[i];
+              }
+              if (!ok) break;
+              tc_fence_after();
+              if (lane == 0) {
+                const uint64_t da = desc_k(base + C::Q_OFF + i * C::TILE);
+                const uint64_t db = desc_k(base + C::KV_OFF + k_stage * C::TILE);
+                for (int k = 0; k < ksteps; ++k)
+                  mma_bf16(tmem + i * 128, step_k(da, k), step_k(db, k), idesc_s, k > 0);
+                mma_commit(s_full + 8 * i);
+                if (j == nk[i] - 1) mma_commit(q_empty + 8 * i);
+              }
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            if (j > 0) mma_commit(kv_empty + 8 * v_stage);
+            if (j < n) mma_commit(kv_empty + 8 * k_stage);
+          }
+          __syncwarp();
+          // the stage after the last one used: V of tile j follows K of tile j
+          stage = j < n ? k_stage : v_stage;
+          phase = j < n ? k_phase : v_phase;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (lane == 0) {
+        if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
+        mma_commit(final_bar);  // every MMA and commit of this thread has completed then
+        mbar_wait(final_bar, 0, kAttnWaitNs, nullptr);
+      }
+      __syncwarp();
+    }
+  } else {
+    // -------------------------------------------------------------- softmax, a row a thread
+    setmaxnreg_inc<216>();
+    const int i = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * 128;
+    const float c = p.c;
+    uint32_t uses = 0;  // S tiles so far
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      const int n = nk[i];
+      const int tok = tok0[i] + row_token(p, row);
+      // keys that this row sees, and that every row of the tile sees
+      const int lim = p.causal ? min(s.lk, tok + 1 + s.lk - s.lq) : s.lk;
+      const int lim_all = p.causal ? min(s.lk, tok0[i] + 1 + s.lk - s.lq) : s.lk;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < n; ++j, ++uses) {
+        if (!(ok = mbar_wait(s_full + 8 * i, uses & 1u, kAttnWaitNs, abort_flag))) break;
+        tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, v + 32 * b);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld_wait32(v + 32 * b);
+        if ((j + 1) * 128 > lim_all) {
+          const int x = lim - j * 128;
+#pragma unroll
+          for (int e = 0; e < 128; ++e) v[e] = e < x ? v[e] : 0xFF800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          m = top;
+        } else {
+          const bool move = (top - m) * c > 8.0f;
+          if (__any_sync(0xFFFFFFFFu, move)) {
+            const float m2 = move ? top : m;
+            const float f = move ? ex2_ftz((m - m2) * c) : 1.0f;
+            l *= f;
+            m = m2;
+            // O holds the products so far once the last P V has completed
+            if (!(ok = mbar_wait(o_done + 8 * i, (uses - 1u) & 1u, kAttnWaitNs, abort_flag))) break;
+            tc_fence_after();
+            for (int b = 0; b < p.D; b += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + b, o);
+              tmem_ld_wait16(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(to + b, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float mc = m == -INFINITY ? 0.0f : -m * c;
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(v[64 * b + 2 * e]),
+                                              __uint_as_float(v[64 * b + 2 * e + 1])),
+                                  make_float2(c, c), make_float2(mc, mc));
+            x.x = ex2_ftz(x.x);
+            x.y = ex2_ftz(x.y);
+            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+            w[e] = pack_bf16x2(x.x, x.y);
+          }
+          tmem_st32(ts + 32 * b, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * i);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- o and lse
+      if (tok0[i] >= s.lq) continue;
+      const bool live = tok < s.lq && row < p.tpt * p.gp;
+      float inv = 0.0f;
+      if (n > 0) {
+        if (!(ok = mbar_wait(o_done + 8 * i, (uses - 1u) & 1u, kAttnWaitNs, abort_flag))) break;
+        tc_fence_after();
+        inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // a NaN stays one
+      }
+      const bool empty = n == 0 || lim <= 0;
+      for (int b = 0; b < p.D; b += 64) {
+        uint32_t w[32];
+        const int cols = min(64, p.D - b);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t o[16];
+          if (n > 0 && h * 16 < cols) {
+            tmem_ld16(to + b + 16 * h, o);
+            tmem_ld_wait16(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[8 * h + e] = (empty || h * 16 >= cols)
+                               ? 0u
+                               : pack_bf16x2(__uint_as_float(o[2 * e]) * inv,
+                                             __uint_as_float(o[2 * e + 1]) * inv);
+        }
+        store_rows64(w, lane, cols, [&](int r) -> uint16_t* {
+          const int rr = quarter * 32 + r;
+          const int t = row_token(p, rr), tt = tok0[i] + t;
+          if (tt >= s.lq || rr >= p.tpt * p.gp || !PACT_IN(s.q0 + tt < p.tq)) return nullptr;
+          return p.o + (int64_t)(s.q0 + tt) * p.ldo + (int64_t)(h0 + rr - t * p.gp) * p.D + b;
+        });
+      }
+      if (live && PACT_IN(s.q0 + tok < p.tq)) {
+        const int h = h0 + row - row_token(p, row) * p.gp;
+        p.lse[(int64_t)h * p.tq + s.q0 + tok] =
+            empty ? -INFINITY : (m * c + log2f(l)) * kLn2;
+      }
+    }
+    if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+cudaError_t launch_attn_fwd(const AttnFwdLaunch& L, cudaStream_t st) {
+  const AttnParams& p = L.p;
+  const int64_t tpu = 2 * p.tpt;
+  // at most: whole tiles of all tokens, and a ragged one for each sequence
+  const int64_t units = ((int64_t)p.tq / tpu + p.nseq) * p.units_h;
+  const unsigned grid = (unsigned)(units < L.num_sms ? units : L.num_sms);
+  cudaError_t e;
+  note_launch();
+  if (p.D <= 64) {
+    constexpr uint32_t sm = FwdCfg<64>::SMEM;
+    if ((e = cudaFuncSetAttribute(k_attn_fwd<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)))
+      return e;
+    k_attn_fwd<64><<<grid, 384, sm, st>>>(L.tmQ, L.tmK, L.tmV, p);
+  } else {
+    constexpr uint32_t sm = FwdCfg<128>::SMEM;
+    if ((e = cudaFuncSetAttribute(k_attn_fwd<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)))
+      return e;
+    k_attn_fwd<128><<<grid, 384, sm, st>>>(L.tmQ, L.tmK, L.tmV, p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace pact

@@ -11,3 +11,7 @@
 #include "fp8_quant.cu"
 #include "fp8_norm.cu"
 #include "fp8_gemm.cu"
+#include "rope.cu"
+#include "attention_fwd.cu"
+#include "attention_bwd.cu"
+#include "grad_norm.cu"

@@ -181,6 +181,80 @@ cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, 
                            int64_t M, int64_t N, int64_t K, const uint16_t* add, uint16_t* out,
                            int sms, cudaStream_t stream);
 
+// Norms of queries and keys with the rotary embedding (rope.cu).  Token t's heads of a
+// tensor begin ld values behind those of token t - 1.
+struct RopeParams {
+  const uint16_t *q, *k;    // inputs; backward: the gradients of the outputs
+  const uint16_t *xq, *xk;  // backward with norms: the forward's inputs
+  uint16_t *q_out, *k_out;  // outputs; backward: dq and dk
+  int64_t ldq, ldk, ldxq, ldxk, ldqo, ldko;
+  const uint16_t *gamma_q, *gamma_k;  // [D], or null: no norms
+  const int32_t* positions;           // [T]
+  const int64_t* turns;               // [rot / 2]
+  int64_t T;
+  int hq, hk, D, rot;
+  float eps;
+};
+cudaError_t launch_rope_turns(const double* inv_freq, int n, int64_t* turns, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(const RopeParams& p, int pairs, int num_sms, cudaStream_t stream);
+// dgamma null: not computed and part unused; else part holds rope_bwd_blocks rows of 2 D FP32.
+constexpr int kRopeSms = 152;  // blocks are sized for these, whatever the device has
+int64_t rope_bwd_blocks(int64_t T, int heads, int D, int num_sms);
+cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, int pairs, float* dgq, float* dgk,
+                                    float* part, int num_sms, cudaStream_t stream);
+
+// Gradient norm and clipping (grad_norm.cu): tensor i has numel[i] values at data[i], its
+// first chunk of kGradChunk values is first[i] of `chunks`.  All on the device.
+constexpr int kGradChunk = 4096;
+struct GradTable {
+  float* const* data;
+  const int64_t* numel;
+  const int64_t* first;
+  int64_t count, chunks;
+};
+int64_t grad_norm_blocks(int64_t chunks, int num_sms);
+cudaError_t launch_grad_norm(const GradTable& t, float* const* out, double max_norm, float* norm,
+                             double* part, int num_sms, cudaStream_t stream);
+
+// Attention over packed sequences (attention.cuh).
+struct AttnParams {
+  const int *cu_q, *cu_k;  // [nseq + 1]
+  int nseq, tq, tk;
+  int hq, hk, group, D;  // group = hq / hk
+  int gp, tpt;           // heads and tokens of a query tile
+  uint32_t gp_mul;       // ceil(2^16 / gp)
+  int subs;              // query tiles of a key head's group: group / gp
+  int units_h;           // units of one token range
+  float scale, c;        // c = scale log2 e
+  int causal;
+  const float* lse_in;
+  float* lse;  // [hq, tq]
+  uint16_t* o;
+  int64_t ldo;
+  // backward
+  const uint16_t* o_in;
+  const uint16_t* dout;
+  int64_t ldoi, lddo;
+  float* delta;  // [hq, tq]
+  uint16_t *dq, *dk, *dv;
+  int64_t lddq, lddk, lddv;
+  unsigned* status;
+};
+struct AttnFwdLaunch {
+  // BF16 [T, heads, D], boxes of 64 columns, 128-byte swizzle: Q gp heads x tpt tokens, K and
+  // V one head x 128 tokens
+  CUtensorMap tmQ, tmK, tmV;
+  AttnParams p;
+  int num_sms;
+};
+cudaError_t launch_attn_fwd(const AttnFwdLaunch& L, cudaStream_t stream);
+struct AttnBwdLaunch {
+  CUtensorMap tmQ, tmdO, tmK, tmV;
+  AttnParams p;
+  int num_sms;
+};
+cudaError_t launch_attn_bwd(const AttnBwdLaunch& L, cudaStream_t stream);
+
 cudaError_t launch_pexp(const float* x, float* y, int64_t n, cudaStream_t stream);
 
 }  // namespace pact
