@@ -43,6 +43,33 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// The warp's number, known to be the same in all of its lanes.
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
+}
+
+// Whether this lane is the one of its warp that issues copies and MMAs.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// A place in a ring of shared-memory tiles and the parity of its turn.
+struct RingPos {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance(int stages, int by = 1) {
+    stage += by;
+    if (stage >= stages) {
+      stage -= stages;
+      phase ^= 1u;
+    }
+  }
+};
+
 // Wait for a tcgen05.ld of 32 columns, whose registers are operands so that nothing
 // computed from them moves ahead of the wait.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t* v) {

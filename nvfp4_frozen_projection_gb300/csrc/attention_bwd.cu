@@ -7,15 +7,16 @@
 // Three launches.  delta is a pass over do and o (HBM).  dq and dk|dv are kernels of their
 // own, each with its sums in TMEM from the first tile to the last: seven products a tile in
 // place of the five of one kernel, whose dq would have to be added up in memory over all key
-// tiles, in an order that changes from run to run.  A CTA has one tile of 128 rows; one
-// thread issues the products, two warpgroups hold a row a thread and half its columns each.
+// tiles, in an order that changes from run to run.  A CTA has one tile of 128 rows; two
+// threads issue the products, two warpgroups hold a row a thread and half its columns each.
 //
 //   dq:     rows are queries.  TMEM: S twice (0, 128), dP (256, dS over it), dq (384).
-//           Order: S of the next keys; dS ready: dq += dS k, then dP of the next keys.
+//           One thread issues S as its buffers are read, the other, once dS is there,
+//           dq += dS k and dP of the next keys.
 //   dk|dv:  rows are keys, columns the (token, head) rows of a query tile.  TMEM: S^T (0, P^T
 //           over it), dP^T (128, dS^T over it), dv (256), dk (384).
-//           Order: P ready: dv += P^T do, S^T of the next queries; dS ready: dk += dS^T q,
-//           dP^T of the next queries.
+//           One thread issues, once P is there, dv += P^T do and S^T of the next queries,
+//           the other, once dS is there, dk += dS^T q and dP^T of the next queries.
 // So the tensor cores have work while exponentials are taken, and MMAs of one thread run in
 // order, which is what lets the next S or dP overwrite the P or dS before it.  P and dS are
 // rounded to BF16 for their products; everything else is FP32.
@@ -105,34 +106,35 @@ struct BwdCfg {
   // two tiles that stay for a unit, the ring, and (dk|dv) two buffers of 128 -lse and delta
   static constexpr uint32_t RING_OFF = 2 * TILE, STAT_OFF = RING_OFF + STAGES * TILE;
   static constexpr uint32_t BAR_OFF = STAT_OFF + 2048;
-  // 12 barriers and 4 of the statistics, the ring's; behind them the TMEM slot and the abort flag
-  static constexpr uint32_t SLOT_OFF = BAR_OFF + 128 + 16 * STAGES, SMEM = SLOT_OFF + 16;
+  // 17 barriers and the ring's; behind them the TMEM slot and the abort flag
+  static constexpr uint32_t SLOT_OFF = BAR_OFF + 136 + 16 * STAGES, SMEM = SLOT_OFF + 16;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
+// Shared addresses of the barriers; those with a number in brackets lie 8 bytes apart.
 struct BwdBars {
-  uint32_t fix_full[2], fix_empty[2];  // the two tiles of a unit
-  uint32_t s_full[2], dp_full, p_full, ds_full, acc_full, tail, final_bar;
-  uint32_t stat_full, stat_empty;  // [2] each
+  uint32_t fix_full, fix_empty;  // [2] the two tiles of a unit
+  uint32_t s_full;               // [2]
+  uint32_t dp_full, p_full, ds_full, acc_full, tail;
+  uint32_t final_bar;              // [2]
+  uint32_t stat_full, stat_empty;  // [2] (dk|dv)
+  uint32_t s_empty;                // [2] (dq)
   uint32_t full, empty;            // the ring
 };
 __device__ __forceinline__ BwdBars bwd_bars(uint32_t b, int stages) {
   BwdBars r;
-  r.fix_full[0] = b;
-  r.fix_full[1] = b + 8;
-  r.fix_empty[0] = b + 16;
-  r.fix_empty[1] = b + 24;
-  r.s_full[0] = b + 32;
-  r.s_full[1] = b + 40;
+  r.fix_full = b;
+  r.fix_empty = b + 16;
+  r.s_full = b + 32;
   r.dp_full = b + 48;
   r.p_full = b + 56;
   r.ds_full = b + 64;
   r.acc_full = b + 72;
   r.tail = b + 80;
   r.final_bar = b + 88;
-  r.stat_full = b + 96;
-  r.stat_empty = b + 112;
-  r.full = b + 128;
+  r.stat_full = r.s_empty = b + 104;
+  r.stat_empty = b + 120;
+  r.full = b + 136;
   r.empty = r.full + 8 * stages;
   return r;
 }
@@ -153,21 +155,24 @@ __global__ void __launch_bounds__(384, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::SLOT_OFF + 4);
   const BwdBars B = bwd_bars(base + C::BAR_OFF, C::STAGES);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(B.fix_full[i], 1);
-      mbar_init(B.fix_empty[i], 1);
-      mbar_init(B.s_full[i], 1);
+      mbar_init(B.fix_full + 8 * i, 1);
+      mbar_init(B.fix_empty + 8 * i, 1);
+      mbar_init(B.s_full + 8 * i, 1);
     }
     mbar_init(B.dp_full, 1);
     mbar_init(B.ds_full, 8);  // the computing warps
     mbar_init(B.acc_full, 1);
     mbar_init(B.tail, 1);
     mbar_init(B.final_bar, 1);
+    mbar_init(B.final_bar + 8, 1);
+    mbar_init(B.s_empty, 8);
+    mbar_init(B.s_empty + 8, 8);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(B.full + 8 * s, 1);
-      mbar_init(B.empty + 8 * s, 1);
+      mbar_init(B.empty + 8 * s, 2);  // the issuers
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -211,12 +216,12 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t uses = 0;
       bool ok = true;
       auto load_fix = [&](int i, const CUtensorMap* tm) {
-        if (!mbar_wait(B.fix_empty[i], (uses & 1u) ^ 1u, kAttnWaitNs, abort_flag)) return false;
+        if (!mbar_wait(B.fix_empty + 8 * i, (uses & 1u) ^ 1u, kAttnWaitNs, abort_flag)) return false;
         if (lane == 0) {
-          mbar_expect_tx(B.fix_full[i], (uint32_t)(p.tpt * p.gp) * 128 * C::BOXES);
+          mbar_expect_tx(B.fix_full + 8 * i, (uint32_t)(p.tpt * p.gp) * 128 * C::BOXES);
 #pragma unroll
           for (int b = 0; b < C::BOXES; ++b)
-            tma_load_3d(base + i * C::TILE + b * kBox, tm, b * 64, h0, s.q0 + tok0, B.fix_full[i]);
+            tma_load_3d(base + i * C::TILE + b * kBox, tm, b * 64, h0, s.q0 + tok0, B.fix_full + 8 * i);
         }
         __syncwarp();
         return true;
@@ -245,105 +250,92 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) {
         if (lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_TMA);
         ring.drain();
-        for (uint32_t i = 0; i < fixed; ++i) mbar_wait(B.fix_full[i], uses & 1u, 10000000ull, nullptr);
+        for (uint32_t i = 0; i < fixed; ++i) mbar_wait(B.fix_full + 8 * i, uses & 1u, 10000000ull, nullptr);
       }
-    } else if (warp == 9) {
+    } else if (warp < 11) {
       // ------------------------------------------------------------ MMAs
-      int stage = 0;  // of K of the current tile; V follows it
-      uint32_t phase = 0, uses = 0, tiles = 0;
+      const int issuer = warp - 9;
+      RingPos at;  // of K of the current tile; V follows it
+      uint32_t uses = 0, tiles = 0;
       bool ok = true;
       const uint32_t idesc_s = attn_idesc(128, false), idesc_d = attn_idesc(p.D, true);
       const int ksteps = p.D / 16;
-      auto ahead = [&](int& st, uint32_t& ph, int by) {
-        st += by;
-        if (st >= C::STAGES) {
-          st -= C::STAGES;
-          ph ^= 1u;
-        }
+      const bool lead = elected();
+      const uint64_t dfix = desc_k(base + issuer * C::TILE);
+      const uint64_t dk0 = desc_k(base + C::RING_OFF), dn0 = desc_n(base + C::RING_OFF);
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        return mbar_wait(bar, par, kAttnWaitNs, abort_flag);
       };
-      auto wait_tile = [&](int st, uint32_t ph) {
-        return mbar_wait(B.full + 8 * st, ph, kAttnWaitNs, abort_flag);
-      };
-      // 128 x 128 product of a fixed tile and a ring tile over the head's columns
-      auto mma_rows = [&](uint32_t d, int fix, int st) {
-        const uint64_t da = desc_k(base + fix * C::TILE);
-        const uint64_t db = desc_k(base + C::RING_OFF + st * C::TILE);
-        for (int k = 0; k < ksteps; ++k)
-          mma_bf16(tmem + d, step_k(da, k), step_k(db, k), idesc_s, k > 0);
+      // 128 x 128 product of this issuer's fixed tile and a ring tile over the head's columns
+      auto mma_rows = [&](uint32_t d, int st) {
+        const uint64_t db = dk0 + (uint64_t)(st * (C::TILE >> 4));
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+          if (k < ksteps) mma_bf16(tmem + d, step_k(dfix, k), step_k(db, k), idesc_s, k > 0);
       };
       for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
         if (nk == 0) continue;
-        ok = mbar_wait(B.fix_full[0], uses & 1u, kAttnWaitNs, abort_flag) && wait_tile(stage, phase);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          mma_rows((tiles & 1u) * 128, 0, stage);
-          mma_commit(B.s_full[tiles & 1u]);
-          if (nk == 1) mma_commit(B.fix_empty[0]);
-        }
-        __syncwarp();
-        int vst = stage;
-        uint32_t vph = phase;
-        ahead(vst, vph, 1);
-        ok = mbar_wait(B.fix_full[1], uses & 1u, kAttnWaitNs, abort_flag) && wait_tile(vst, vph);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          mma_rows(256, 1, vst);
-          mma_commit(B.dp_full);
-          mma_commit(B.empty + 8 * vst);
-          if (nk == 1) mma_commit(B.fix_empty[1]);
-        }
-        __syncwarp();
-        for (int j = 0; j < nk; ++j, ++tiles) {
-          const bool more = j + 1 < nk;
-          int kst = stage, nvst;
-          uint32_t kph = phase, nvph;
-          ahead(kst, kph, 2);
-          nvst = kst;
-          nvph = kph;
-          ahead(nvst, nvph, 1);
-          if (more) {
-            if (!(ok = wait_tile(kst, kph))) break;
-            tc_fence_after();
-            if (lane == 0) {
-              mma_rows(((tiles + 1) & 1u) * 128, 0, kst);
-              mma_commit(B.s_full[(tiles + 1) & 1u]);
-              if (j + 2 == nk) mma_commit(B.fix_empty[0]);
-            }
-            __syncwarp();
-          }
-          if (!(ok = mbar_wait(B.ds_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t d = desc_n(base + C::RING_OFF + stage * C::TILE);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_ta(tmem + 384, tmem + 256 + half_step(k), step_n(d, k), idesc_d,
-                          (j > 0 || k > 0) ? 1u : 0u);
-            mma_commit(B.empty + 8 * stage);
-            if (!more) mma_commit(B.acc_full);
-          }
-          __syncwarp();
-          if (more) {
-            if (!(ok = wait_tile(nvst, nvph))) break;
-            tc_fence_after();
-            if (lane == 0) {
-              mma_rows(256, 1, nvst);
-              mma_commit(B.dp_full);
-              mma_commit(B.empty + 8 * nvst);
-              if (j + 2 == nk) mma_commit(B.fix_empty[1]);
-            }
-            __syncwarp();
-          }
-          ahead(stage, phase, 2);
-        }
+        if (!(ok = wait(B.fix_full + 8 * issuer, uses & 1u))) break;
         ++uses;
+        if (issuer == 0) {
+          for (int j = 0; j < nk; ++j, ++tiles) {
+            const uint32_t buf = tiles & 1u;
+            if (!(ok = wait(B.full + 8 * at.stage, at.phase) &&
+                       wait(B.s_empty + 8 * buf, ((tiles >> 1) & 1u) ^ 1u)))
+              break;
+            tc_fence_after();
+            if (lead) {
+              mma_rows(buf * 128, at.stage);
+              mma_commit(B.s_full + 8 * buf);
+              mma_commit(B.empty + 8 * at.stage);
+              if (j + 1 == nk) mma_commit(B.fix_empty);
+            }
+            __syncwarp();
+            at.advance(C::STAGES, 2);
+          }
+        } else {
+          for (int j = 0; j <= nk; ++j) {
+            // dq of tile j - 1, dP of tile j
+            RingPos v = at;
+            v.advance(C::STAGES);
+            if (j > 0) {
+              RingPos k = at;  // two places back, which is a turn of the parity further on
+              k.advance(C::STAGES, C::STAGES - 2);
+              if (!(ok = wait(B.full + 8 * k.stage, k.phase ^ 1u) && wait(B.ds_full, tiles & 1u)))
+                break;
+              ++tiles;
+              tc_fence_after();
+              if (lead) {
+                const uint64_t d = dn0 + (uint64_t)(k.stage * (C::TILE >> 4));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  mma_bf16_ta(tmem + 384, tmem + 256 + half_step(i), step_n(d, i), idesc_d,
+                              (j > 1 || i > 0) ? 1u : 0u);
+                mma_commit(B.empty + 8 * k.stage);
+                if (j == nk) mma_commit(B.acc_full);
+              }
+              __syncwarp();
+            }
+            if (j < nk) {
+              if (!(ok = wait(B.full + 8 * v.stage, v.phase))) break;
+              tc_fence_after();
+              if (lead) {
+                mma_rows(256, v.stage);
+                mma_commit(B.dp_full);
+                mma_commit(B.empty + 8 * v.stage);  // for both issuers: the other has no use of V
+                mma_commit(B.empty + 8 * v.stage);
+                if (j + 1 == nk) mma_commit(B.fix_empty + 8);
+              }
+              __syncwarp();
+              at.advance(C::STAGES, 2);
+            }
+          }
+        }
       }
-      if (lane == 0) {
+      if (lead) {
         if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
-        mma_commit(B.final_bar);
-        mbar_wait(B.final_bar, 0, kAttnWaitNs, nullptr);
+        mma_commit(B.final_bar + 8 * issuer);
+        mbar_wait(B.final_bar + 8 * issuer, 0, kAttnWaitNs, nullptr);
       }
       __syncwarp();
     }
@@ -368,7 +360,7 @@ __global__ void __launch_bounds__(384, 1)
         delta = p.delta[at];
       }
       for (int j = 0; j < nk; ++j, ++tiles) {
-        if (!(ok = mbar_wait(B.s_full[tiles & 1u], (tiles >> 1) & 1u, kAttnWaitNs, abort_flag))) break;
+        if (!(ok = mbar_wait(B.s_full + 8 * (tiles & 1u), (tiles >> 1) & 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
         uint32_t v[64];
         const uint32_t ts = tl + (tiles & 1u) * 128 + half * 64;
@@ -376,6 +368,9 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld32(ts + 32, v + 32);
         tmem_ld_wait32(v);
         tmem_ld_wait32(v + 32);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.s_empty + 8 * (tiles & 1u));
         float pr[64];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -464,24 +459,24 @@ __global__ void __launch_bounds__(384, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::SLOT_OFF + 4);
   const BwdBars B = bwd_bars(base + C::BAR_OFF, C::STAGES);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(B.fix_full[0], 1);
-    mbar_init(B.fix_empty[0], 1);
-    mbar_init(B.s_full[0], 1);
+    mbar_init(B.fix_full, 1);
+    mbar_init(B.fix_empty, 2);  // the issuers
+    mbar_init(B.s_full, 1);
     mbar_init(B.dp_full, 1);
     mbar_init(B.p_full, 8);  // the computing warps
     mbar_init(B.ds_full, 8);
-    mbar_init(B.acc_full, 1);
+    mbar_init(B.acc_full, 2);
     mbar_init(B.tail, 1);
-    mbar_init(B.final_bar, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(B.final_bar + 8 * i, 1);
       mbar_init(B.stat_full + 8 * i, 1);
       mbar_init(B.stat_empty + 8 * i, 8);
     }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(B.full + 8 * s, 1);
-      mbar_init(B.empty + 8 * s, 1);
+      mbar_init(B.empty + 8 * s, 2);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -537,13 +532,13 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true, fixed = false;
       for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
         if (n == 0) continue;
-        if (!(ok = mbar_wait(B.fix_empty[0], (uses & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
+        if (!(ok = mbar_wait(B.fix_empty, (uses & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
         if (lane == 0) {
-          mbar_expect_tx(B.fix_full[0], 2 * C::TILE);
+          mbar_expect_tx(B.fix_full, 2 * C::TILE);
 #pragma unroll
           for (int b = 0; b < C::BOXES; ++b) {
-            tma_load_3d(base + b * kBox, &tmK, b * 64, kvh, s.k0 + key0, B.fix_full[0]);
-            tma_load_3d(base + C::TILE + b * kBox, &tmV, b * 64, kvh, s.k0 + key0, B.fix_full[0]);
+            tma_load_3d(base + b * kBox, &tmK, b * 64, kvh, s.k0 + key0, B.fix_full);
+            tma_load_3d(base + C::TILE + b * kBox, &tmV, b * 64, kvh, s.k0 + key0, B.fix_full);
           }
         }
         __syncwarp();
@@ -563,116 +558,74 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) {
         if (lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_TMA);
         ring.drain();
-        if (fixed) mbar_wait(B.fix_full[0], uses & 1u, 10000000ull, nullptr);
+        if (fixed) mbar_wait(B.fix_full, uses & 1u, 10000000ull, nullptr);
       }
-    } else if (warp == 9) {
+    } else if (warp < 11) {
       // ------------------------------------------------------------ MMAs
-      int stage = 0;  // of Q of the current tile; dO follows it
-      uint32_t phase = 0, uses = 0, tiles = 0;
+      // issuer 0: S^T = k q^T and dv += P^T do;  issuer 1: dP^T = v do^T and dk += dS^T q
+      const int issuer = warp - 9;
+      RingPos at;  // of Q of the current tile; dO follows it
+      uint32_t uses = 0, tiles = 0;
       bool ok = true;
       const uint32_t idesc_s = attn_idesc(128, false), idesc_d = attn_idesc(p.D, true);
       const int ksteps = p.D / 16;
-      auto ahead = [&](int& st, uint32_t& ph, int by) {
-        st += by;
-        if (st >= C::STAGES) {
-          st -= C::STAGES;
-          ph ^= 1u;
-        }
-      };
-      auto wait_tile = [&](int st, uint32_t ph) {
-        return mbar_wait(B.full + 8 * st, ph, kAttnWaitNs, abort_flag);
-      };
-      auto mma_rows = [&](uint32_t d, int fix, int st) {
-        const uint64_t da = desc_k(base + fix * C::TILE);
-        const uint64_t db = desc_k(base + C::RING_OFF + st * C::TILE);
-        for (int k = 0; k < ksteps; ++k)
-          mma_bf16(tmem + d, step_k(da, k), step_k(db, k), idesc_s, k > 0);
-      };
-      // sum += (P or dS at column `a`)^T times a ring tile's rows
-      auto mma_sum = [&](uint32_t d, uint32_t a, int st, bool first) {
-        const uint64_t db = desc_n(base + C::RING_OFF + st * C::TILE);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ta(tmem + d, tmem + a + half_step(k), step_n(db, k), idesc_d,
-                      (!first || k > 0) ? 1u : 0u);
+      const bool lead = elected();
+      const uint64_t dfix = desc_k(base + issuer * C::TILE);
+      const uint64_t dk0 = desc_k(base + C::RING_OFF), dn0 = desc_n(base + C::RING_OFF);
+      const uint32_t sum = tmem + 256 + issuer * 128, prod = tmem + issuer * 128;
+      const uint32_t in_full = issuer ? B.ds_full : B.p_full;
+      const uint32_t out_full = issuer ? B.dp_full : B.s_full;
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        return mbar_wait(bar, par, kAttnWaitNs, abort_flag);
       };
       for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
         if (n == 0) continue;
-        int ost = stage;
-        uint32_t oph = phase;
-        ahead(ost, oph, 1);
-        ok = mbar_wait(B.fix_full[0], uses & 1u, kAttnWaitNs, abort_flag) && wait_tile(stage, phase);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          mma_rows(0, 0, stage);
-          mma_commit(B.s_full[0]);
-        }
-        __syncwarp();
-        if (!(ok = wait_tile(ost, oph))) break;
-        tc_fence_after();
-        if (lane == 0) {
-          mma_rows(128, 1, ost);
-          mma_commit(B.dp_full);
-          if (n == 1) mma_commit(B.fix_empty[0]);
-        }
-        __syncwarp();
-        for (int i = 0; i < n; ++i, ++tiles) {
-          const bool more = i + 1 < n;
-          int nq = stage, no;
-          uint32_t nqp = phase, nop;
-          ost = stage;
-          oph = phase;
-          ahead(ost, oph, 1);
-          ahead(nq, nqp, 2);
-          no = nq;
-          nop = nqp;
-          ahead(no, nop, 1);
-          if (!(ok = mbar_wait(B.p_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
-          tc_fence_after();
-          if (lane == 0) {
-            mma_sum(256, 0, ost, i == 0);
-            mma_commit(B.empty + 8 * ost);
-          }
-          __syncwarp();
-          if (more) {
-            if (!(ok = wait_tile(nq, nqp))) break;
-            tc_fence_after();
-            if (lane == 0) {
-              mma_rows(0, 0, nq);
-              mma_commit(B.s_full[0]);
-            }
-            __syncwarp();
-          }
-          if (!(ok = mbar_wait(B.ds_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
-          tc_fence_after();
-          if (lane == 0) {
-            mma_sum(384, 128, stage, i == 0);
-            mma_commit(B.empty + 8 * stage);
-            if (!more) mma_commit(B.acc_full);
-          }
-          __syncwarp();
-          if (more) {
-            if (!(ok = wait_tile(no, nop))) break;
-            tc_fence_after();
-            if (lane == 0) {
-              mma_rows(128, 1, no);
-              mma_commit(B.dp_full);
-              if (i + 2 == n) mma_commit(B.fix_empty[0]);
-            }
-            __syncwarp();
-          }
-          ahead(stage, phase, 2);
-        }
+        if (!(ok = wait(B.fix_full, uses & 1u))) break;
         ++uses;
+        for (int i = 0; i <= n; ++i) {
+          if (i > 0) {  // the sum of tile i - 1, over dO (issuer 0) or Q (1)
+            RingPos r = at;  // one or two places back, which is a turn of the parity further on
+            r.advance(C::STAGES, C::STAGES - 2 + (issuer ? 0 : 1));
+            if (!(ok = wait(B.full + 8 * r.stage, r.phase ^ 1u) && wait(in_full, tiles & 1u))) break;
+            ++tiles;
+            tc_fence_after();
+            if (lead) {
+              const uint64_t d = dn0 + (uint64_t)(r.stage * (C::TILE >> 4));
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_bf16_ta(sum, prod + half_step(k), step_n(d, k), idesc_d,
+                            (i > 1 || k > 0) ? 1u : 0u);
+              mma_commit(B.empty + 8 * r.stage);
+              if (i == n) mma_commit(B.acc_full);
+            }
+            __syncwarp();
+          }
+          if (i < n) {  // the product of tile i, over Q (issuer 0) or dO (1)
+            RingPos r = at;
+            if (issuer) r.advance(C::STAGES);
+            if (!(ok = wait(B.full + 8 * r.stage, r.phase))) break;
+            tc_fence_after();
+            if (lead) {
+              const uint64_t d = dk0 + (uint64_t)(r.stage * (C::TILE >> 4));
+#pragma unroll
+              for (int k = 0; k < DP / 16; ++k)
+                if (k < ksteps) mma_bf16(prod, step_k(dfix, k), step_k(d, k), idesc_s, k > 0);
+              mma_commit(out_full);
+              mma_commit(B.empty + 8 * r.stage);
+              if (i + 1 == n) mma_commit(B.fix_empty);
+            }
+            __syncwarp();
+            at.advance(C::STAGES, 2);
+          }
+        }
       }
-      if (lane == 0) {
+      if (lead) {
         if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
-        mma_commit(B.final_bar);
-        mbar_wait(B.final_bar, 0, kAttnWaitNs, nullptr);
+        mma_commit(B.final_bar + 8 * issuer);
+        mbar_wait(B.final_bar + 8 * issuer, 0, kAttnWaitNs, nullptr);
       }
       __syncwarp();
-    } else if (warp == 10) {
+    } else {
       // ------------------------------------------------------------ -lse and delta of the columns
       uint32_t tiles = 0;
       bool ok = true;
@@ -725,7 +678,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t buf = tiles & 1u;
         const float* st = reinterpret_cast<const float*>(smem + C::STAT_OFF + buf * 1024) + half * 64;
         if (!(ok = mbar_wait(B.stat_full + 8 * buf, (tiles >> 1) & 1u, kAttnWaitNs, abort_flag) &&
-                   mbar_wait(B.s_full[0], tiles & 1u, kAttnWaitNs, abort_flag)))
+                   mbar_wait(B.s_full, tiles & 1u, kAttnWaitNs, abort_flag)))
           break;
         tc_fence_after();
         uint32_t v[64];

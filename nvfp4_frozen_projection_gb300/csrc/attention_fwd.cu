@@ -7,9 +7,9 @@
 // tiles of 128 query rows (attention.cuh) against tiles of 128 keys, and a warpgroup for each,
 // a row a thread; while one softmax runs, the tensor cores work for the other tile:
 //   S_i  128 TMEM columns, P_i (BF16) over the first half of them, O_i behind both S.
-// One thread issues P_0 V, S_0 of the next keys, P_1 V, S_1 of the next keys, in turn;
-// MMAs of one thread run in order, so S_i may be issued behind the P_i V that reads P_i out
-// of the same columns.  Keys and values pass through one ring of shared memory.
+// A thread for each tile issues P_i V, then S_i of the next keys; MMAs of one thread run in
+// order, so S_i may be issued behind the P_i V that reads P_i out of the same columns.  Keys
+// and values pass through one ring of shared memory.
 //
 // The running maximum m of a row moves only when a new one is above it by more than 2^8 in
 // the exponentials' scale: the sums stay far from FP32's range, and the rescaling of O in
@@ -27,8 +27,8 @@ struct FwdCfg {
   static constexpr uint32_t Q_OFF = 0, KV_OFF = 2 * TILE;
   static constexpr uint32_t BAR_OFF = KV_OFF + STAGES * TILE;
   static constexpr uint32_t SMEM = BAR_OFF + 512 + 1024;
-  // q_full[2] q_empty[2] s_full[2] p_full[2] o_done[2] tail final kv_full[ST] kv_empty[ST]
-  static constexpr int NBARS = 12 + 2 * STAGES;
+  // q_full[2] q_empty[2] s_full[2] p_full[2][2] o_done[2] final[2] tail - kv_full[ST] kv_empty[ST]
+  static constexpr int NBARS = 16 + 2 * STAGES;
   static_assert(SMEM <= 232448 && NBARS * 8 <= 504, "shared memory");
 };
 
@@ -43,25 +43,26 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* smem = smem_raw + (base - raw);
   const uint32_t bars = base + C::BAR_OFF;
   const uint32_t q_full = bars, q_empty = bars + 16, s_full = bars + 32, p_full = bars + 48,
-                 o_done = bars + 64, tail_bar = bars + 80, final_bar = bars + 88,
-                 kv_full = bars + 96, kv_empty = kv_full + 8 * C::STAGES;
+                 o_done = bars + 80, final_bar = bars + 96, tail_bar = bars + 112,
+                 kv_full = bars + 128, kv_empty = kv_full + 8 * C::STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 504);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 508);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 4);  // the warps of a tile
+      mbar_init(p_full + 16 * i, 4);  // the warps of a tile, for each half of its keys
+      mbar_init(p_full + 16 * i + 8, 4);
       mbar_init(o_done + 8 * i, 1);
+      mbar_init(final_bar + 8 * i, 1);
     }
     mbar_init(tail_bar, 1);
-    mbar_init(final_bar, 1);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(kv_full + 8 * s, 1);
-      mbar_init(kv_empty + 8 * s, 1);
+      mbar_init(kv_empty + 8 * s, 2);  // the issuers
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -175,87 +176,81 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 2; ++i)
           if (q_uses[i]) mbar_wait(q_full + 8 * i, (q_uses[i] & 1u) ^ 1u, 10000000ull, nullptr);
       }
-    } else if (warp == 9) {
-      // ------------------------------------------------------------ MMAs
-      int stage = 0;
-      uint32_t phase = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+    } else if (warp < 11) {
+      // ------------------------------------------------------------ MMAs of tile i
+      const int i = warp - 9;
+      RingPos at;
+      uint32_t q_uses = 0, p_uses = 0;
       bool ok = true;
       const uint32_t idesc_s = attn_idesc(128, false), idesc_o = attn_idesc(p.D, true);
+      const uint32_t ts = tmem + i * 128, to = tmem + 256 + i * 128;
       const int ksteps = p.D / 16;
+      const uint64_t dq = desc_k(base + C::Q_OFF + i * C::TILE);
+      const uint64_t dk0 = desc_k(base + C::KV_OFF), dv0 = desc_n(base + C::KV_OFF);
+      const bool lead = elected();
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        return mbar_wait(bar, par, kAttnWaitNs, abort_flag);
+      };
       for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
         const int n = max(nk[0], nk[1]);
-        // step j: the values of tile j - 1 (the stage that is being used), the keys of j
-        int v_stage = 0;
-        for (int j = 0; j <= n && ok; ++j) {
-          if (n == 0) break;
-          bool v_seen = false, k_seen = false;
-          uint32_t v_phase = phase;
-          int k_stage = stage;
-          uint32_t k_phase = phase;
+        // step j: the values of tile j - 1, the keys of tile j
+        for (int j = 0; j <= n && n > 0; ++j) {
           if (j > 0) {
-            v_stage = stage;
-            v_phase = phase;
-            k_stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-            k_phase = stage + 1 == C::STAGES ? phase ^ 1u : phase;
-          }
+            if (!(ok = wait(kv_full + 8 * at.stage, at.phase))) break;
+            if (j - 1 < nk[i]) {
+              const uint64_t d = dv0 + (uint64_t)(at.stage * (C::TILE >> 4));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (j > 0 && j - 1 < nk[i]) {
-              if (!v_seen) ok = ok && mbar_wait(kv_full + 8 * v_stage, v_phase, kAttnWaitNs, abort_flag);
-              v_seen = true;
-              ok = ok && mbar_wait(p_full + 8 * i, p_uses[i] & 1u, kAttnWaitNs, abort_flag);
-              ++p_uses[i];
+              for (int h = 0; h < 2; ++h) {
+                if (!(ok = wait(p_full + 16 * i + 8 * h, p_uses & 1u))) break;
+                tc_fence_after();
+                if (lead) {
+#pragma unroll
+                  for (int k = 4 * h; k < 4 * h + 4; ++k)
+                    mma_bf16_ta(to, ts + k * 8, step_n(d, k), idesc_o, (j > 1 || k > 0) ? 1u : 0u);
+                }
+                __syncwarp();
+              }
               if (!ok) break;
-              tc_fence_after();
-              if (lane == 0) {
-                const uint64_t d = desc_n(base + C::KV_OFF + v_stage * C::TILE);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  mma_bf16_ta(tmem + 256 + i * 128, tmem + i * 128 + k * 8, step_n(d, k), idesc_o,
-                              (j > 1 || k > 0) ? 1u : 0u);
+              ++p_uses;
+              if (lead) {
+                mma_commit(kv_empty + 8 * at.stage);
                 mma_commit(o_done + 8 * i);
               }
-              __syncwarp();
+            } else if (lead) {
+              mbar_arrive(kv_empty + 8 * at.stage);
             }
+            __syncwarp();
+            at.advance(C::STAGES);
+          }
+          if (j < n) {
+            if (!(ok = wait(kv_full + 8 * at.stage, at.phase))) break;
             if (j < nk[i]) {
-              if (!k_seen) ok = ok && mbar_wait(kv_full + 8 * k_stage, k_phase, kAttnWaitNs, abort_flag);
-              k_seen = true;
               if (j == 0) {
-                ok = ok && mbar_wait(q_full + 8 * i, q_uses[i] & 1u, kAttnWaitNs, abort_flag);
-                ++q_uses[i];
+                if (!(ok = wait(q_full + 8 * i, q_uses & 1u))) break;
+                ++q_uses;
               }
-              if (!ok) break;
               tc_fence_after();
-              if (lane == 0) {
-                const uint64_t da = desc_k(base + C::Q_OFF + i * C::TILE);
-                const uint64_t db = desc_k(base + C::KV_OFF + k_stage * C::TILE);
-                for (int k = 0; k < ksteps; ++k)
-                  mma_bf16(tmem + i * 128, step_k(da, k), step_k(db, k), idesc_s, k > 0);
+              if (lead) {
+                const uint64_t d = dk0 + (uint64_t)(at.stage * (C::TILE >> 4));
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                  if (k < ksteps) mma_bf16(ts, step_k(dq, k), step_k(d, k), idesc_s, k > 0);
                 mma_commit(s_full + 8 * i);
+                mma_commit(kv_empty + 8 * at.stage);
                 if (j == nk[i] - 1) mma_commit(q_empty + 8 * i);
               }
-              __syncwarp();
+            } else if (lead) {
+              mbar_arrive(kv_empty + 8 * at.stage);
             }
-          }
-          if (!ok) break;
-          if (lane == 0) {
-            if (j > 0) mma_commit(kv_empty + 8 * v_stage);
-            if (j < n) mma_commit(kv_empty + 8 * k_stage);
-          }
-          __syncwarp();
-          // the stage after the last one used: V of tile j follows K of tile j
-          stage = j < n ? k_stage : v_stage;
-          phase = j < n ? k_phase : v_phase;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            __syncwarp();
+            at.advance(C::STAGES);
           }
         }
       }
-      if (lane == 0) {
+      if (lead) {
         if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
-        mma_commit(final_bar);  // every MMA and commit of this thread has completed then
-        mbar_wait(final_bar, 0, kAttnWaitNs, nullptr);
+        mma_commit(final_bar + 8 * i);  // every MMA and commit of this thread has completed then
+        mbar_wait(final_bar + 8 * i, 0, kAttnWaitNs, nullptr);
       }
       __syncwarp();
     }
@@ -335,11 +330,12 @@ __global__ void __launch_bounds__(384, 1)
             w[e] = pack_bf16x2(x.x, x.y);
           }
           tmem_st32(ts + 32 * b, w);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          // the first half's product runs while the second half is computed
+          if (lane == 0) mbar_arrive(p_full + 16 * i + 8 * b);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * i);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;

@@ -32,40 +32,57 @@ static int rope_chunks(int64_t T, int heads, int seg, int num_sms) {
   return (int)(c < heads ? c : heads);
 }
 
-// The rotation of one lane's 8 columns: y = own c + other s.
-template <bool PAIRS>
+// The rotation of one lane's 8 columns, two at a time: y = own c + other s.  The other half
+// of a pair comes from the lane `other`, or (PAIRS) is the neighbouring column.
 struct Turn {
-  float c[PAIRS ? 4 : 8], s[PAIRS ? 4 : 8];
+  float2 c[4], s[4];
   int other;    // lane offset of the other half
   bool turned;  // the lane's columns lie in the first rot
 };
 
 template <bool PAIRS>
-__device__ __forceinline__ Turn<PAIRS> make_turn(int col, int rot, int pos, const int64_t* turns,
-                                                 bool back) {
-  Turn<PAIRS> t;
+__device__ __forceinline__ Turn make_turn(int col, int rot, int pos, const int64_t* turns,
+                                          bool back) {
+  Turn t;
   t.turned = col < rot;
   t.other = 0;
   if (!t.turned) {
 #pragma unroll
-    for (int e = 0; e < (PAIRS ? 4 : 8); ++e) t.c[e] = 1.0f, t.s[e] = 0.0f;
+    for (int e = 0; e < 4; ++e) t.c[e] = make_float2(1.0f, 1.0f), t.s[e] = make_float2(0.0f, 0.0f);
     return t;
   }
   const int half = rot >> 1;
   const bool first = PAIRS || col < half;
   if (!PAIRS) t.other = first ? (half >> 3) : -(half >> 3);
   const int i0 = PAIRS ? col >> 1 : (first ? col : col - half);
+  float c[8], s[8];
 #pragma unroll
   for (int e = 0; e < (PAIRS ? 4 : 8); ++e) {
     const uint64_t phase = (uint64_t)(int64_t)pos * (uint64_t)turns[i0 + e];
-    float s, c;
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    t.c[e] = c;
+    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s[e], &c[e]);
     // of a pair (a, b): a' = a c - b s, b' = b c + a s; backward the other way round
-    t.s[e] = (first != back) ? -s : s;
+    if (first != back) s[e] = -s[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    t.c[e] = PAIRS ? make_float2(c[e], c[e]) : make_float2(c[2 * e], c[2 * e + 1]);
+    t.s[e] = PAIRS ? make_float2(s[e], -s[e]) : make_float2(s[2 * e], s[2 * e + 1]);
   }
   return t;
 }
+
+__device__ __forceinline__ void unpack8(const uint4& v, float2* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack8(const float2* f) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                    pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 swapped(float2 v) { return make_float2(v.y, v.x); }
 
 template <int SEG>
 __device__ __forceinline__ float seg_sum(float v) {
@@ -80,9 +97,51 @@ __device__ __forceinline__ uint4 shfl_v4(const uint4& v, int lane) {
                     __shfl_sync(0xFFFFFFFFu, v.z, lane), __shfl_sync(0xFFFFFFFFu, v.w, lane));
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+// 1 / sqrt(mean + eps); rsqrtf is within 2 units in the last place.
+__device__ __forceinline__ float rstd_of(float ss, float inv_d, float eps) {
+  return rsqrtf(__fmaf_rn(ss, inv_d, eps));
+}
+
+// The first `heads` heads of a token from x on (x, out: at this lane's columns).  NORM: the gammas
+// are in the coefficients, y = rstd (own (gamma c) + other (gamma' s)).
+template <int SEG, bool NORM, bool PAIRS>
+__device__ __forceinline__ void rope_heads(const uint16_t* x, uint16_t* out, int rounds, int heads,
+                                           int D, float inv_d, float eps, bool live, const float2* c,
+                                           const float2* s, int other) {
+  for (int hb = 0; hb < rounds; hb += kRopeUnroll) {
+    uint4 v[kRopeUnroll];
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (live && hb + u < heads)
+        v[u] = *reinterpret_cast<const uint4*>(x + (int64_t)(hb + u) * D);
+    }
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      float2 f[4], o[4];
+      unpack8(v[u], f);
+      if constexpr (PAIRS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = swapped(f[e]);
+      } else {
+        unpack8(shfl_v4(v[u], other), o);
+      }
+      float2 r = both(1.0f);
+      if constexpr (NORM) {
+        float2 q = both(0.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q = __ffma2_rn(f[e], f[e], q);
+        r = both(rstd_of(seg_sum<SEG>(q.x + q.y), inv_d, eps));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = __ffma2_rn(f[e], c[e], __fmul2_rn(o[e], s[e]));
+        if constexpr (NORM) f[e] = __fmul2_rn(f[e], r);
+      }
+      if (live && hb + u < heads)
+        *reinterpret_cast<uint4*>(out + (int64_t)(hb + u) * D) = pack8(f);
+    }
+  }
 }
 
 template <int SEG, bool NORM, bool PAIRS>
@@ -90,79 +149,97 @@ __global__ void __launch_bounds__(kRopeThreads)
     k_qk_norm_rope(const RopeParams p, int64_t segs, int chunks, int per) {
   const int lane = threadIdx.x & 31, sl = lane & (SEG - 1);
   const int64_t seg = (int64_t)blockIdx.x * (kRopeThreads / SEG) + threadIdx.x / SEG;
-  if (seg - (lane / SEG) >= segs) return;  // a whole warp
-  const bool live = seg < segs && sl * 8 < p.D;
+  // a dead group stays for the shuffles of its warp, with no heads
   const int64_t t = seg < segs ? seg / chunks : 0;
-  const int h0 = seg < segs ? (int)(seg - t * chunks) * per : 0;
-  const int col = sl * 8, H = p.hq + p.hk;
-  const Turn<PAIRS> tn = make_turn<PAIRS>(live ? col : p.rot, p.rot, p.positions[t], p.turns, false);
+  const int h0 = seg < segs ? (int)(seg - t * chunks) * per : 0, H = p.hq + p.hk;
+  const int h1 = seg < segs ? min(h0 + per, H) : 0;
+  const bool live = seg < segs && sl * 8 < p.D && PACT_IN(t < p.T);
+  const int col = sl * 8;
+  const Turn tn = make_turn<PAIRS>(live ? col : p.rot, p.rot, p.positions[t], p.turns, false);
   const int other = lane + tn.other;
-  // gammas of the lane's columns and, for halves, of the pair's other half
-  uint4 gq = make_uint4(0, 0, 0, 0), gk = gq, oq = gq, ok = gq;
-  if (NORM && live) {
-    gq = *reinterpret_cast<const uint4*>(p.gamma_q + col);
-    gk = *reinterpret_cast<const uint4*>(p.gamma_k + col);
-    if (!PAIRS) {
-      oq = *reinterpret_cast<const uint4*>(p.gamma_q + col + 8 * tn.other);
-      ok = *reinterpret_cast<const uint4*>(p.gamma_k + col + 8 * tn.other);
-    }
-  }
-  for (int hb = 0; hb < per; hb += kRopeUnroll) {
-    uint4 v[kRopeUnroll];
+  const float inv_d = 1.0f / (float)p.D;
+  // every group of a warp runs as many rounds as the longest, or shuffles would miss lanes
+  auto run = [&](const uint16_t* x, uint16_t* out, const uint16_t* gamma, int a, int b) {
+    float2 c[4], s[4];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + hb + u;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (live && hb + u < per && h < H)
-        v[u] = *reinterpret_cast<const uint4*>(
-            h < p.hq ? p.q + t * p.ldq + (int64_t)h * p.D + col
-                     : p.k + t * p.ldk + (int64_t)(h - p.hq) * p.D + col);
-    }
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + hb + u;
-      float f[8], o[8];
-      bf16x8_to_f32(v[u], f);
-      float rstd = 1.0f;
-      if constexpr (NORM) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = __fmaf_rn(f[e], f[e], ss);
-        ss = seg_sum<SEG>(ss);
-        rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)p.D), p.eps)));
-        float g[8];
-        bf16x8_to_f32(h < p.hq ? gq : gk, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
-      }
+    for (int e = 0; e < 4; ++e) c[e] = tn.c[e], s[e] = tn.s[e];
+    if (NORM && live) {
+      float2 g[4], o[4];
+      unpack8(*reinterpret_cast<const uint4*>(gamma + col), g);
       if constexpr (PAIRS) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[2 * e] = f[2 * e] * tn.c[e] + f[2 * e + 1] * tn.s[e];
-          o[2 * e + 1] = f[2 * e + 1] * tn.c[e] - f[2 * e] * tn.s[e];
-        }
+        for (int e = 0; e < 4; ++e) o[e] = swapped(g[e]);
       } else {
-        const uint4 w = shfl_v4(v[u], other);
-        bf16x8_to_f32(w, o);
-        if constexpr (NORM) {
-          float g[8];
-          bf16x8_to_f32(h < p.hq ? oq : ok, g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = o[e] * rstd * g[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = f[e] * tn.c[e] + o[e] * tn.s[e];
+        unpack8(*reinterpret_cast<const uint4*>(gamma + col + 8 * tn.other), o);
       }
-      if (live && hb + u < per && h < H && PACT_IN(t < p.T && col + 8 <= p.D))
-        *reinterpret_cast<uint4*>(h < p.hq ? p.q_out + t * p.ldqo + (int64_t)h * p.D + col
-                                           : p.k_out + t * p.ldko + (int64_t)(h - p.hq) * p.D +
-                                                 col) = pack8(o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = __fmul2_rn(c[e], g[e]), s[e] = __fmul2_rn(s[e], o[e]);
     }
-  }
+    const int n = __reduce_max_sync(0xFFFFFFFFu, max(b - a, 0));
+    rope_heads<SEG, NORM, PAIRS>(x + (int64_t)a * p.D, out + (int64_t)a * p.D, n, b - a, p.D,
+                                 inv_d, p.eps, live, c, s, other);
+  };
+  run(p.q + t * p.ldq + col, p.q_out + t * p.ldqo + col, p.gamma_q, h0, min(h1, p.hq));
+  run(p.k + t * p.ldk + col, p.k_out + t * p.ldko + col, p.gamma_k, max(h0 - p.hq, 0), h1 - p.hq);
 }
 
 // Backward; q, k are dy, xq and xk the forward's inputs (NORM).  DG: the sums for dgamma_q
 // and dgamma_k of this block's groups go to part[block][2][D], group by group in order.
+template <int SEG, bool NORM, bool PAIRS, bool DG>
+__device__ __forceinline__ void rope_heads_bwd(const uint16_t* dy, const uint16_t* x,
+                                               uint16_t* out, int rounds, int heads, int D,
+                                               float inv_d, float eps, bool live, const Turn& tn,
+                                               int other, const float2* gm, float2* acc) {
+  constexpr int U = NORM ? 2 : kRopeUnroll;
+  for (int hb = 0; hb < rounds; hb += U) {
+    uint4 v[U], w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[u] = w[u] = make_uint4(0, 0, 0, 0);
+      if (live && hb + u < heads) {
+        v[u] = *reinterpret_cast<const uint4*>(dy + (int64_t)(hb + u) * D);
+        if constexpr (NORM) w[u] = *reinterpret_cast<const uint4*>(x + (int64_t)(hb + u) * D);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float2 g[4], o[4];
+      unpack8(v[u], g);
+      if constexpr (PAIRS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = swapped(g[e]);
+      } else {
+        unpack8(shfl_v4(v[u], other), o);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = __ffma2_rn(g[e], tn.c[e], __fmul2_rn(o[e], tn.s[e]));
+      if constexpr (NORM) {
+        float2 n[4];
+        unpack8(w[u], n);
+        float2 ss = both(0.0f), dot = both(0.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ss = __ffma2_rn(n[e], n[e], ss);
+          o[e] = __fmul2_rn(g[e], gm[e]);
+          dot = __ffma2_rn(o[e], n[e], dot);
+        }
+        const float rstd = rstd_of(seg_sum<SEG>(ss.x + ss.y), inv_d, eps);
+        const float c = seg_sum<SEG>(dot.x + dot.y) * rstd * inv_d;  // mean(dn n)
+        const float2 r = both(rstd), mc = both(-c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          n[e] = __fmul2_rn(n[e], r);
+          // zero in lanes and heads that hold nothing
+          if constexpr (DG) acc[e] = __ffma2_rn(g[e], n[e], acc[e]);
+          g[e] = __fmul2_rn(r, __ffma2_rn(n[e], mc, o[e]));
+        }
+      }
+      if (live && hb + u < heads)
+        *reinterpret_cast<uint4*>(out + (int64_t)(hb + u) * D) = pack8(g);
+    }
+  }
+}
+
 template <int SEG, bool NORM, bool PAIRS, bool DG>
 __global__ void __launch_bounds__(kRopeThreads)
     k_qk_norm_rope_bwd(const RopeParams p, int64_t segs, int chunks, int per, float* part) {
@@ -172,94 +249,38 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int group = threadIdx.x / SEG;
   const int col = sl * 8, H = p.hq + p.hk;
   const bool inside = col < p.D;
-  uint4 gq = make_uint4(0, 0, 0, 0), gk = gq;
-  if (NORM && inside) {
-    gq = *reinterpret_cast<const uint4*>(p.gamma_q + col);
-    gk = *reinterpret_cast<const uint4*>(p.gamma_k + col);
-  }
-  float aq[DG ? 8 : 1] = {}, ak[DG ? 8 : 1] = {};
+  const float inv_d = 1.0f / (float)p.D;
+  float2 acc[2][DG ? 4 : 1] = {};
   for (int64_t first = (int64_t)blockIdx.x * GROUPS; first < segs;
        first += (int64_t)gridDim.x * GROUPS) {
     const int64_t seg = first + group;
-    const bool live = seg < segs && inside;
     const int64_t t = seg < segs ? seg / chunks : 0;
+    const bool live = seg < segs && inside && PACT_IN(t < p.T);
     const int h0 = seg < segs ? (int)(seg - t * chunks) * per : 0;
-    const Turn<PAIRS> tn = make_turn<PAIRS>(live ? col : p.rot, p.rot, p.positions[t], p.turns, true);
+    const int h1 = seg < segs ? min(h0 + per, H) : 0;
+    const Turn tn = make_turn<PAIRS>(live ? col : p.rot, p.rot, p.positions[t], p.turns, true);
     const int other = lane + tn.other;
-    constexpr int U = NORM ? 2 : kRopeUnroll;
-    for (int hb = 0; hb < per; hb += U) {
-      uint4 v[U], x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + hb + u;
-        v[u] = x[u] = make_uint4(0, 0, 0, 0);
-        if (live && hb + u < per && h < H) {
-          const bool isq = h < p.hq;
-          const int hh = isq ? h : h - p.hq;
-          v[u] = *reinterpret_cast<const uint4*>((isq ? p.q + t * p.ldq : p.k + t * p.ldk) +
-                                                 (int64_t)hh * p.D + col);
-          if constexpr (NORM)
-            x[u] = *reinterpret_cast<const uint4*>((isq ? p.xq + t * p.ldxq : p.xk + t * p.ldxk) +
-                                                   (int64_t)hh * p.D + col);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + hb + u;
-        float f[8], g[8];
-        bf16x8_to_f32(v[u], f);
-        if constexpr (PAIRS) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g[2 * e] = f[2 * e] * tn.c[e] + f[2 * e + 1] * tn.s[e];
-            g[2 * e + 1] = f[2 * e + 1] * tn.c[e] - f[2 * e] * tn.s[e];
-          }
-        } else {
-          bf16x8_to_f32(shfl_v4(v[u], other), g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = f[e] * tn.c[e] + g[e] * tn.s[e];
-        }
-        if constexpr (NORM) {
-          float n[8], gm[8];
-          bf16x8_to_f32(x[u], n);
-          bf16x8_to_f32(h < p.hq ? gq : gk, gm);
-          float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = __fmaf_rn(n[e], n[e], ss);
-            dot = __fmaf_rn(g[e] * gm[e], n[e], dot);
-          }
-          ss = seg_sum<SEG>(ss);
-          dot = seg_sum<SEG>(dot);
-          const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)p.D), p.eps)));
-          const float c = __fdiv_rn(dot * rstd, (float)p.D);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            n[e] *= rstd;
-            if constexpr (DG) {
-              const float w = g[e] * n[e];  // zero in lanes and heads that hold nothing
-              if (h < p.hq)
-                aq[e] += w;
-              else
-                ak[e] += w;
-            }
-            g[e] = rstd * (g[e] * gm[e] - n[e] * c);
-          }
-        }
-        if (live && hb + u < per && h < H && PACT_IN(t < p.T && col + 8 <= p.D))
-          *reinterpret_cast<uint4*>(h < p.hq ? p.q_out + t * p.ldqo + (int64_t)h * p.D + col
-                                             : p.k_out + t * p.ldko + (int64_t)(h - p.hq) * p.D +
-                                                   col) = pack8(g);
-      }
+    for (int w = 0; w < 2; ++w) {  // queries, keys
+      const int a = w ? max(h0 - p.hq, 0) : h0, b = w ? h1 - p.hq : min(h1, p.hq);
+      const int64_t at = (int64_t)a * p.D + col;
+      float2 gm[4] = {};
+      if (NORM && live) unpack8(*reinterpret_cast<const uint4*>((w ? p.gamma_k : p.gamma_q) + col), gm);
+      const int rounds = __reduce_max_sync(0xFFFFFFFFu, max(b - a, 0));
+      rope_heads_bwd<SEG, NORM, PAIRS, DG>(
+          (w ? p.k + t * p.ldk : p.q + t * p.ldq) + at,
+          NORM ? (w ? p.xk + t * p.ldxk : p.xq + t * p.ldxq) + at : nullptr,
+          (w ? p.k_out + t * p.ldko : p.q_out + t * p.ldqo) + at, rounds, b - a, p.D, inv_d, p.eps,
+          live, tn, other, gm, acc[w]);
     }
   }
   if constexpr (DG) {
     if (inside) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sums[(group * 2 + 0) * (8 * SEG) + col + e] = aq[e];
-        sums[(group * 2 + 1) * (8 * SEG) + col + e] = ak[e];
-      }
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<float2*>(sums + (group * 2 + w) * (8 * SEG) + col + 2 * e) = acc[w][e];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * p.D; i += kRopeThreads) {

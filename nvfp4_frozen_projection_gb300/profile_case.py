@@ -27,6 +27,13 @@ Cases (M = tokens; the other sizes are the Llama-3B layer's):
   fp8-quant           FP8 quantisation of a BF16 [M, 8192] tensor
   fp8-norm            RMSNorm with the residual's addition -> FP8, [M, 4096]
   fp8-norm-bwd        its backward, with a residual gradient and dgamma
+  attention           causal attention of one sequence of M tokens, 16/4 heads of 128
+  attention-64        the same of sequences of 1024 tokens, 32/8 heads of 64
+  attention-bwd       its backward, sequences of 1024 tokens, 32/8 heads of 128
+  attention-bwd-64    the same with heads of 64
+  qk-norm-rope        norms and rotation of 32 + 8 heads of 128
+  qk-norm-rope-bwd    its backward, 32 + 8 heads of 64, with both dgammas
+  clip                the norm of 64 tensors of M x 128 values, and clipping
 
 The default M (4096) keeps the inputs of the SiLU, GEMM and weight-pack cases above
 the 129 MB L2 and every case's device memory under 1 GB, the size a full ncu capture
@@ -40,7 +47,8 @@ import argparse
 
 import torch
 
-from . import (pact_add_rmsnorm_bwd, pact_add_rmsnorm_quant_fp8, pact_check_status,
+from . import (GradList, pact_add_rmsnorm_bwd, pact_attention_bwd, pact_attention_fwd,
+               pact_clip_grad_norm, pact_qk_norm_rope, pact_qk_norm_rope_bwd, pact_rope_turns, pact_add_rmsnorm_quant_fp8, pact_check_status,
                pact_linear_fp8_fwd, pact_pack_weight_fp8_fwd, pact_quant_fp8, pact_lora_adapter_grad, pact_lora_linear_dgrad,
                pact_lora_linear_dgrad_q, pact_lora_linear_fwd_gate_up,
                pact_pack_weight_fwd_gate_up,
@@ -178,6 +186,32 @@ def run(case: str, m: int, reps: int) -> None:
         for _ in range(reps):
             pact_pack_weight_fwd(W, out=wf)
             pact_pack_weight_bwd(W, out=wb)
+    elif case.startswith("attention"):
+        d = 64 if case.endswith("64") else 128
+        hq, hk, n = (16, 4, m) if case == "attention" else (32, 8, min(m, 1024))
+        q, do, k, v = (torch.randn(m, h, d, device=dev, generator=gen).bfloat16() for h in (hq, hq, hk, hk))
+        cu = torch.arange(0, m + 1, n, device=dev, dtype=torch.int32)
+        o, lse = pact_attention_fwd(q, k, v, cu, cu)
+        for _ in range(reps):
+            if "bwd" in case:
+                pact_attention_bwd(do, q, k, v, o, lse, cu, cu)
+            else:
+                pact_attention_fwd(q, k, v, cu, cu, o=o, lse=lse)
+    elif case in ("qk-norm-rope", "qk-norm-rope-bwd"):
+        d = 64 if case.endswith("bwd") else 128
+        q, k = (torch.randn(m, h, d, device=dev, generator=gen).bfloat16() for h in (32, 8))
+        gamma = torch.ones(d, dtype=torch.bfloat16, device=dev)
+        pos = torch.arange(m, device=dev, dtype=torch.int32)
+        turns = pact_rope_turns(500000.0 ** (-torch.arange(0, d, 2, device=dev).double() / d))
+        for _ in range(reps):
+            if d == 64:
+                pact_qk_norm_rope_bwd(q, k, pos, turns, q, k, gamma, gamma, dgamma_q=True, dgamma_k=True)
+            else:
+                pact_qk_norm_rope(q, k, pos, turns, gamma, gamma)
+    elif case == "clip":
+        grads = GradList([torch.randn(m, 128, device=dev, generator=gen) for _ in range(64)])
+        for _ in range(reps):
+            pact_clip_grad_norm(grads, 1.0)
     else:
         raise SystemExit(f"unknown case {case!r}")
     torch.cuda.synchronize()
