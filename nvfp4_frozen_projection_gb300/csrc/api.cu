@@ -930,17 +930,15 @@ static int check_rope(const pact_heads* q, const char* qname, const pact_heads* 
     return fail(PACT_ERR_ALIGN,
                 "positions must be 4-byte, turns 8-byte and the gammas 16-byte aligned");
   std::memset(p, 0, sizeof(*p));
-  p->q = q->p;
-  p->k = k->p;
-  p->ldq = q->ld;
-  p->ldk = k->ld;
-  p->gamma_q = gq;
-  p->gamma_k = gk;
+  for (int w = 0; w < 2; ++w) {
+    p->side[w].x = w ? k->p : q->p;
+    p->side[w].ld = w ? k->ld : q->ld;
+    p->side[w].heads = (int)(w ? k->heads : q->heads);
+    p->side[w].gamma = w ? gk : gq;
+  }
   p->positions = positions;
   p->turns = turns;
   p->T = q->rows;
-  p->hq = (int)q->heads;
-  p->hk = (int)k->heads;
   p->D = (int)D;
   p->rot = (int)rot;
   p->eps = eps;
@@ -960,10 +958,10 @@ int pact_qk_norm_rope(const pact_heads* q, const pact_heads* k, int64_t D, int64
     return rc;
   if (heads_clash(q_out, q, D) || heads_clash(k_out, k, D))
     return fail(PACT_ERR_INVALID_ARG, "q_out overlaps q, or k_out k, in part");
-  p.q_out = q_out->p;
-  p.k_out = k_out->p;
-  p.ldqo = q_out->ld;
-  p.ldko = k_out->ld;
+  for (int w = 0; w < 2; ++w) {
+    p.side[w].out = w ? k_out->p : q_out->p;
+    p.side[w].ldo = w ? k_out->ld : q_out->ld;
+  }
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   cudaError_t e = launch_qk_norm_rope(p, interleaved != 0, d->sms, (cudaStream_t)stream);
@@ -975,7 +973,7 @@ size_t pact_qk_norm_rope_bwd_workspace_size(int64_t T, int64_t heads_q, int64_t 
   if (T < 1 || T > kFp8MaxRows || heads_q < 1 || heads_q > 65536 || heads_k < 1 ||
       heads_k > 65536 || D < 16 || D > 256 || D % 16)
     return 0;
-  return align256((size_t)rope_bwd_blocks(T, (int)(heads_q + heads_k), (int)D, kRopeSms) * 8 *
+  return align256((size_t)rope_bwd_blocks(T, (int)heads_q, (int)heads_k, (int)D, kRopeSms) * 4 *
                   (size_t)D);
 }
 
@@ -1000,10 +998,10 @@ int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pa
       return rc;
     if (heads_clash(dq, q_opt, D) || heads_clash(dk, k_opt, D))
       return fail(PACT_ERR_INVALID_ARG, "dq overlaps q, or dk k, in part");
-    p.xq = q_opt->p;
-    p.xk = k_opt->p;
-    p.ldxq = q_opt->ld;
-    p.ldxk = k_opt->ld;
+    for (int w = 0; w < 2; ++w) {
+      p.side[w].xf = w ? k_opt->p : q_opt->p;
+      p.side[w].ldxf = w ? k_opt->ld : q_opt->ld;
+    }
   }
   if (!dgamma_q_opt != !dgamma_k_opt)
     return fail(PACT_ERR_INVALID_ARG, "dgamma_q and dgamma_k go together: both or neither");
@@ -1012,14 +1010,14 @@ int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pa
   if (!aligned(dgamma_q_opt, 4) || !aligned(dgamma_k_opt, 4))
     return fail(PACT_ERR_ALIGN, "dgamma_q and dgamma_k must be 4-byte aligned");
   if (dgamma_q_opt) {
-    const size_t need = pact_qk_norm_rope_bwd_workspace_size(p.T, p.hq, p.hk, D);
+    const size_t need = pact_qk_norm_rope_bwd_workspace_size(p.T, dyq->heads, dyk->heads, D);
     if (!ws || ws_bytes < need || !aligned(ws, 256))
       return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
   }
-  p.q_out = dq->p;
-  p.k_out = dk->p;
-  p.ldqo = dq->ld;
-  p.ldko = dk->ld;
+  for (int w = 0; w < 2; ++w) {
+    p.side[w].out = w ? dk->p : dq->p;
+    p.side[w].ldo = w ? dk->ld : dq->ld;
+  }
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   cudaError_t e = launch_qk_norm_rope_bwd(p, interleaved != 0, dgamma_q_opt, dgamma_k_opt,

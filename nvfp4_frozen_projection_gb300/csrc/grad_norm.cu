@@ -6,7 +6,7 @@
 // clipped.  The tensors of a list are cut into chunks of 4096 values; a grid of blocks takes
 // the chunks in turn and writes one FP64 sum a block.  The second launch, which every block
 // opens by adding those sums in the same order, takes the chunks from the last to the first:
-// what the norm read last is still in L2.
+// what the norm read last is still in L2, and what is read and written there need not stay.
 //
 // Squares are added in FP32 over the 16 values of a thread, and those sums in FP64.  A thread
 // whose largest value lies outside [2^-50, 2^60], where an FP32 square could overflow or
@@ -42,14 +42,17 @@ __device__ __forceinline__ GradSpan grad_span(const GradTable& t, int64_t c) {
   return s;
 }
 
+// The block's sum, in thread 0.
 __device__ __forceinline__ double block_sum(double v, double* slots) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
   __syncthreads();
   double s = 0.0;
+  if (threadIdx.x == 0) {
 #pragma unroll
-  for (int i = 0; i < kGradThreads / 32; ++i) s += slots[i];
+    for (int i = 0; i < kGradThreads / 32; ++i) s += slots[i];
+  }
   return s;
 }
 
@@ -105,11 +108,19 @@ __global__ void __launch_bounds__(kGradThreads)
   __shared__ double slots[kGradThreads / 32];
   double sum = 0.0;
   for (int i = threadIdx.x; i < parts; i += kGradThreads) sum += part[i];
-  const double norm = sqrt(block_sum(sum, slots));
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  sum = block_sum(sum, slots);
+  __shared__ float shared_coef;
+  if (threadIdx.x == 0) {  // alone: FP64 is slow, and a warp takes as long as a thread
+    const double norm = sqrt(sum);
+    if (blockIdx.x == 0) *norm_out = (float)norm;
+    if constexpr (APPLY) {
+      const double q = max_norm / (norm + 1e-6);
+      shared_coef = q > 1.0 ? 1.0f : (float)q;  // a NaN stays one
+    }
+  }
   if constexpr (APPLY) {
-    const double q = max_norm / (norm + 1e-6);
-    const float coef = q > 1.0 ? 1.0f : (float)q;  // a NaN stays one
+    __syncthreads();
+    const float coef = shared_coef;
     for (int64_t i = blockIdx.x; i < t.chunks; i += gridDim.x) {
       const GradSpan sp = grad_span(t, t.chunks - 1 - i);
       const float* g = t.data[sp.tensor] + sp.at;
@@ -120,14 +131,14 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = (j * kGradThreads + (int)threadIdx.x) * 4;
-          if (e + 4 <= sp.len) v[j] = *reinterpret_cast<const float4*>(g + e);
+          if (e + 4 <= sp.len) v[j] = __ldcs(reinterpret_cast<const float4*>(g + e));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = (j * kGradThreads + (int)threadIdx.x) * 4;
           if (e + 4 <= sp.len) {
-            *reinterpret_cast<float4*>(o + e) =
-                make_float4(v[j].x * coef, v[j].y * coef, v[j].z * coef, v[j].w * coef);
+            __stcs(reinterpret_cast<float4*>(o + e),
+                   make_float4(v[j].x * coef, v[j].y * coef, v[j].z * coef, v[j].w * coef));
           } else {
             for (int k = e; k < sp.len; ++k) o[k] = g[k] * coef;
           }

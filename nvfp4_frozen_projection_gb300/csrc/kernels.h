@@ -183,25 +183,33 @@ cudaError_t launch_fp8_few(const uint8_t* x, const float* sx, const uint8_t* w, 
 
 // Norms of queries and keys with the rotary embedding (rope.cu).  Token t's heads of a
 // tensor begin ld values behind those of token t - 1.
+struct RopeSide {
+  const uint16_t* x;   // input; backward: the gradient of the output
+  const uint16_t* xf;  // backward with norms: the forward's input
+  uint16_t* out;       // output; backward: the input's gradient
+  int64_t ld, ldxf, ldo;
+  const uint16_t* gamma;  // [D], or null: no norms
+  int heads;
+  int per, chunks;  // heads of a group, groups of a token
+  int64_t segs;     // groups in all
+  int blocks;
+};
 struct RopeParams {
-  const uint16_t *q, *k;    // inputs; backward: the gradients of the outputs
-  const uint16_t *xq, *xk;  // backward with norms: the forward's inputs
-  uint16_t *q_out, *k_out;  // outputs; backward: dq and dk
-  int64_t ldq, ldk, ldxq, ldxk, ldqo, ldko;
-  const uint16_t *gamma_q, *gamma_k;  // [D], or null: no norms
-  const int32_t* positions;           // [T]
-  const int64_t* turns;               // [rot / 2]
+  RopeSide side[2];          // queries, keys
+  const int32_t* positions;  // [T]
+  const int64_t* turns;      // [rot / 2]
   int64_t T;
-  int hq, hk, D, rot;
+  int D, rot;
   float eps;
 };
 cudaError_t launch_rope_turns(const double* inv_freq, int n, int64_t* turns, cudaStream_t stream);
-cudaError_t launch_qk_norm_rope(const RopeParams& p, int pairs, int num_sms, cudaStream_t stream);
-// dgamma null: not computed and part unused; else part holds rope_bwd_blocks rows of 2 D FP32.
+// These fill in the sides' groups and blocks.
+cudaError_t launch_qk_norm_rope(RopeParams& p, int pairs, int num_sms, cudaStream_t stream);
+// dgamma null: not computed and part unused; else part holds rope_bwd_blocks rows of D FP32.
 constexpr int kRopeSms = 152;  // blocks are sized for these, whatever the device has
-int64_t rope_bwd_blocks(int64_t T, int heads, int D, int num_sms);
-cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, int pairs, float* dgq, float* dgk,
-                                    float* part, int num_sms, cudaStream_t stream);
+int64_t rope_bwd_blocks(int64_t T, int hq, int hk, int D, int num_sms);
+cudaError_t launch_qk_norm_rope_bwd(RopeParams& p, int pairs, float* dgq, float* dgk, float* part,
+                                    int num_sms, cudaStream_t stream);
 
 // Gradient norm and clipping (grad_norm.cu): tensor i has numel[i] values at data[i], its
 // first chunk of kGradChunk values is first[i] of `chunks`.  All on the device.
