@@ -1060,6 +1060,12 @@ static int check_attention(const pact_heads* q, const pact_heads* k, const pact_
   p->gp_mul = (uint32_t)((65536 + p->gp - 1) / p->gp);
   p->subs = p->group / p->gp;
   p->units_h = p->hk * p->subs;
+  p->units_div = FastDiv::make((uint32_t)p->units_h);
+  p->hk_div = FastDiv::make((uint32_t)p->hk);
+  const int64_t most = ((int64_t)1 << 31) - 1;
+  if (attn_units(p->tq, p->tpt, nseq, p->units_h) >= most ||
+      attn_units(p->tk, 128, nseq, p->hk) >= most)
+    return fail(PACT_ERR_SHAPE, "too many tiles: tokens times heads must stay below 2^31");
   p->scale = scale;
   p->c = scale * 1.4426950408889634f;
   p->causal = causal != 0;
@@ -1141,9 +1147,9 @@ int64_t pact_grad_chunks(int64_t numel) {
   return numel < 1 ? 0 : (numel + kGradChunk - 1) / kGradChunk;
 }
 
-// the blocks' sums: 4 an SM of the GPU that the library is for, whatever the device has
+// the blocks' sums: for the SMs of the GPU that the library is for, whatever the device has
 constexpr int kGradSms = 152;
-size_t pact_grad_norm_workspace_size(void) { return align256(4 * kGradSms * sizeof(double)); }
+size_t pact_grad_norm_workspace_size(void) { return align256(kGradBlocks * kGradSms * sizeof(double)); }
 
 static int grad_norm(const pact_tensor_list* g, float* const* out, bool clip, double max_norm,
                      float* norm, void* ws, size_t ws_bytes, pact_stream_t stream) {

@@ -101,71 +101,146 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int from, in
 // them leads outside.
 struct Seq {
   int q0, lq, k0, lk;
-  int tile;   // of this sequence
-  int tiles;  // of this sequence
+  int tile;  // of this sequence
 };
 
-// Units are numbered by sequence, then by tile.  A role's units ascend, so its search goes
-// on where the last one ended; 32 sequences a step, one a lane.
+// The order of units.  Up to 32 sequences: by the tiles that a unit goes over, in at most 32
+// levels from the most to the fewest, so that no heavy unit comes last; a CTA takes unit k of
+// the first row of gridDim.x units, the last but k of the second, and so on in turn (unit_of).
+// More sequences: by sequence, then by tile.  Units of a role ascend, so its search goes on
+// where the last one ended; 32 sequences a step, one a lane.
+//
+// OVER_K: units are tiles of keys that go over tiles of tpt tokens; else units are `per`
+// tokens that go over tiles of 128 keys.  With causal the first key tiles, or the last
+// tokens, go over the most: rank 0 is the heaviest tile of a sequence.
+template <bool OVER_K>
 struct SeqFinder {
   const int* cu_q;
   const int* cu_k;
   int nseq, tq, tk;
-  int per;        // tokens a unit
-  bool over_k;    // units are tiles of keys
-  int b0 = 0;
-  int64_t base = 0;
+  int per, tpt;
+  bool causal;
+  int b0 = -32, level = 0, step = 0;
+  uint32_t base = 0;
+  int q0 = 0, lq = 0, k0 = 0, lk = 0, n = 0;  // of this lane's sequence; n: its tiles
+  int above = 0, here = 0;  // its tiles above this level, and with those in it
+  uint32_t incl = 0;        // the level's tiles of the lanes up to this one
 
   __device__ __forceinline__ static int clampi(int v, int lo, int hi) {
     return v < lo ? lo : (v > hi ? hi : v);
   }
 
-  // Every lane of the warp calls this; false behind the last unit.
-  __device__ __forceinline__ bool find(int64_t t, Seq& s) {
-    const int lane = threadIdx.x & 31;
-    while (b0 < nseq) {
-      const int b = b0 + lane;
-      int q0 = 0, lq = 0, k0 = 0, lk = 0, n = 0;
-      if (b < nseq) {
-        q0 = clampi(__ldg(cu_q + b), 0, tq);
-        lq = clampi(__ldg(cu_q + b + 1), q0, tq) - q0;
-        k0 = clampi(__ldg(cu_k + b), 0, tk);
-        lk = clampi(__ldg(cu_k + b + 1), k0, tk) - k0;
-        n = ((over_k ? lk : lq) + per - 1) / per;
-      }
-      int64_t incl = n;
+  __device__ __forceinline__ void load() {
+    const int b = b0 + (int)(threadIdx.x & 31);
+    q0 = lq = k0 = lk = n = 0;
+    if (b < nseq) {
+      q0 = clampi(__ldg(cu_q + b), 0, tq);
+      lq = clampi(__ldg(cu_q + b + 1), q0, tq) - q0;
+      k0 = clampi(__ldg(cu_k + b), 0, tk);
+      lk = clampi(__ldg(cu_k + b + 1), k0, tk) - k0;
+      n = ((OVER_K ? lk : lq) + per - 1) / per;
+    }
+  }
+
+  // How many of the sequence's tiles go over `work` tiles or more (work > 0).
+  __device__ __forceinline__ int count(int work) const {
+    const int64_t off = (int64_t)lk - lq;
+    if (OVER_K) {
+      const int m = (lq + tpt - 1) / tpt - work;  // the last tile of tokens to begin with
+      if (m < 0) return 0;
+      const int64_t end = (int64_t)(m + 1) * tpt;
+      if (!causal || end > lq) return n;
+      const int64_t c = (end + off + 127) >> 7;
+      return c < 0 ? 0 : (c > n ? n : (int)c);
+    }
+    const int64_t x = (int64_t)(work - 1) * 128 + 1;  // keys seen at least
+    if (x > lk) return 0;
+    if (!causal) return n;
+    const int64_t y = x - off;  // tokens up to the tile's end at least
+    if (y > lq) return 0;
+    return y <= per ? n : n - (int)((y + per - 1) / per) + 1;
+  }
+
+  __device__ __forceinline__ void at_level() {
+    above = here;
+    here = level > 0 ? count(level) : n;
+    incl = (uint32_t)(here - above);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += up;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if ((int)(threadIdx.x & 31) >= o) incl += up;
+    }
+  }
+
+  __device__ __forceinline__ void take(Seq& s, int lane, int tile) {
+    s.q0 = __shfl_sync(0xFFFFFFFFu, q0, lane);
+    s.lq = __shfl_sync(0xFFFFFFFFu, lq, lane);
+    s.k0 = __shfl_sync(0xFFFFFFFFu, k0, lane);
+    s.lk = __shfl_sync(0xFFFFFFFFu, lk, lane);
+    const int tiles = __shfl_sync(0xFFFFFFFFu, n, lane);
+    s.tile = causal && !OVER_K ? tiles - 1 - tile : tile;
+  }
+
+  // Every lane of the warp calls this; false behind the last unit.
+  __device__ __forceinline__ bool find(uint32_t t, Seq& s) {
+    const bool levels = nseq <= 32;
+    if (t >= 0x7FFFFFFFu) return false;  // offsets that make no sense; see FastDiv
+    if (b0 < 0) {
+      b0 = 0;
+      load();
+      level = 0;
+      if (levels) {
+        const int most = __reduce_max_sync(0xFFFFFFFFu, OVER_K ? (lq + tpt - 1) / tpt : (lk + 127) / 128);
+        step = (most + 31) / 32;
+        if (step < 1) step = 1;
+        level = most;
       }
+      at_level();
+    }
+    for (;;) {
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, t < base + incl);
       if (hit) {
         const int l = __ffs(hit) - 1;
-        s.q0 = __shfl_sync(0xFFFFFFFFu, q0, l);
-        s.lq = __shfl_sync(0xFFFFFFFFu, lq, l);
-        s.k0 = __shfl_sync(0xFFFFFFFFu, k0, l);
-        s.lk = __shfl_sync(0xFFFFFFFFu, lk, l);
-        s.tiles = __shfl_sync(0xFFFFFFFFu, n, l);
-        s.tile = (int)(t - base - (__shfl_sync(0xFFFFFFFFu, incl, l) - s.tiles));
+        // the rank within the sequence: those of higher levels, and of this one before it
+        take(s, l, __shfl_sync(0xFFFFFFFFu, above, l) +
+                       (int)(t - base - __shfl_sync(0xFFFFFFFFu, incl - (uint32_t)(here - above), l)));
         return true;
       }
       base += __shfl_sync(0xFFFFFFFFu, incl, 31);
-      b0 += 32;
+      if (levels) {
+        if (level <= 0) return false;
+        level -= step;
+      } else {
+        b0 += 32;
+        if (b0 >= nseq) return false;
+        load();
+        here = 0;
+      }
+      at_level();
     }
-    return false;
   }
 };
 
-__device__ __forceinline__ SeqFinder seq_finder(const AttnParams& p, int per, bool over_k) {
-  SeqFinder f;
+__device__ __forceinline__ int clampi(int v, int lo, int hi) {
+  return v < lo ? lo : (v > hi ? hi : v);
+}
+
+// Unit i of this CTA's.
+__device__ __forceinline__ uint32_t unit_of(uint32_t i) {
+  return i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+template <bool OVER_K>
+__device__ __forceinline__ SeqFinder<OVER_K> seq_finder(const AttnParams& p, int per) {
+  SeqFinder<OVER_K> f;
   f.cu_q = p.cu_q;
   f.cu_k = p.cu_k;
   f.nseq = p.nseq;
   f.tq = p.tq;
   f.tk = p.tk;
   f.per = per;
-  f.over_k = over_k;
+  f.tpt = p.tpt;
+  f.causal = p.causal != 0;
   return f;
 }
 
@@ -177,10 +252,12 @@ __device__ __forceinline__ int row_token(const AttnParams& p, int row) {
 // Rows of 64 BF16 columns held one a lane (w: 8 pieces of 16 bytes) go out as whole rows of
 // 128 bytes, four an instruction: the lanes of each group of 8 exchange pieces, so that lane
 // l of a group ends up with piece l of each of the group's rows.  Stored as they are held, a
-// piece a lane, an instruction would touch 32 rows.  addr(r): where row r's columns begin,
-// null for a row that is not stored; cols: how many of the 64 columns there are.
-template <typename Addr>
-__device__ __forceinline__ void store_rows64(uint32_t (&w)[32], int lane, int cols, Addr addr) {
+// piece a lane, an instruction would touch 32 rows.  Row r of a tile is at
+// out + (r / gp) ld + (r % gp) D; from: the warp's first row; rows: the tile's rows that are
+// stored; cols: how many of the 64 columns there are.
+__device__ __forceinline__ void store_rows64(uint32_t (&w)[32], int lane, int from, int rows,
+                                             int cols, uint16_t* out, int64_t ld, int D, int gp,
+                                             uint32_t gp_mul) {
 #pragma unroll
   for (int s = 1; s < 8; s <<= 1) {
     const bool up = (lane & s) != 0;
@@ -196,13 +273,32 @@ __device__ __forceinline__ void store_rows64(uint32_t (&w)[32], int lane, int co
       }
     }
   }
-  const int piece = lane & 7;
+  const int piece = lane & 7, r0 = from + (lane & ~7);
+  const int t = (int)(((uint32_t)r0 * gp_mul) >> 16);
+  int g = r0 - t * gp;
+  uint16_t* a = out + (int64_t)t * ld + (int64_t)g * D + piece * 8;
+  const int64_t wrap = ld - (int64_t)(gp - 1) * D;
+  const int live = piece * 8 < cols ? rows - r0 : 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint16_t* a = addr((lane & ~7) + i);
-    if (a != nullptr && piece * 8 < cols)
-      *reinterpret_cast<uint4*>(a + piece * 8) =
-          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    if (i < live)
+      *reinterpret_cast<uint4*>(a) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    const bool last = ++g == gp;
+    a += last ? wrap : (int64_t)D;
+    g = last ? 0 : g;
+  }
+}
+
+// Minus infinity in the columns from x on of 128 scores, by the bits of a word: eight of them
+// become predicates in one instruction, where comparisons take one each.
+__device__ __forceinline__ void mask_from(uint32_t* v, int x) {
+#pragma unroll
+  for (int c = 0; c < 128; c += 32) {
+    // bits of the columns seen
+    const int n = x - c;
+    const uint32_t bits = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[c + e] = (bits >> e & 1u) ? v[c + e] : 0xFF800000u;
   }
 }
 

@@ -186,18 +186,18 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  SeqFinder finder = seq_finder(p, p.tpt, false);
+  SeqFinder<false> finder = seq_finder<false>(p, p.tpt);
   Seq s;
   int tok0, nk, kvh, h0;
-  auto next_unit = [&](int64_t u) {
-    const int64_t t = u / p.units_h;
+  auto next_unit = [&](uint32_t u) {
+    const uint32_t t = p.units_div.div(u);
     const int hu = (int)(u - t * p.units_h);
     if (!finder.find(t, s)) return false;
-    kvh = hu / p.subs;
+    kvh = p.subs == 1 ? hu : hu / p.subs;
     h0 = kvh * p.group + (hu - kvh * p.subs) * p.gp;
-    tok0 = (p.causal ? s.tiles - 1 - s.tile : s.tile) * p.tpt;  // the longest first
+    tok0 = s.tile * p.tpt;
     int kend = s.lk;
-    if (p.causal) kend = SeqFinder::clampi(min(tok0 + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
+    if (p.causal) kend = clampi(min(tok0 + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
     nk = (kend + 127) / 128;
     return true;
   };
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(384, 1)
         return true;
       };
       uint32_t fixed = 0;
-      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
         if (nk == 0) continue;
         for (int j = 0; j < nk && ok; ++j) {
           const int row = s.k0 + j * 128, valid = s.lk - j * 128;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int k = 0; k < DP / 16; ++k)
           if (k < ksteps) mma_bf16(tmem + d, step_k(dfix, k), step_k(db, k), idesc_s, k > 0);
       };
-      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
         if (nk == 0) continue;
         if (!(ok = wait(B.fix_full + 8 * issuer, uses & 1u))) break;
         ++uses;
@@ -296,11 +296,11 @@ __global__ void __launch_bounds__(384, 1)
         } else {
           for (int j = 0; j <= nk; ++j) {
             // dq of tile j - 1, dP of tile j
-            RingPos v = at;
+            RingPos v = at, k = at;
             v.advance(C::STAGES);
+            // two places back, which is a turn of the parity further on
+            k.advance(C::STAGES, C::STAGES - 2);
             if (j > 0) {
-              RingPos k = at;  // two places back, which is a turn of the parity further on
-              k.advance(C::STAGES, C::STAGES - 2);
               if (!(ok = wait(B.full + 8 * k.stage, k.phase ^ 1u) && wait(B.ds_full, tiles & 1u)))
                 break;
               ++tiles;
@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(384, 1)
                 if (j + 1 == nk) mma_commit(B.fix_empty + 8);
               }
               __syncwarp();
-              at.advance(C::STAGES, 2);
             }
+            if (j < nk) at.advance(C::STAGES, 2);
           }
         }
       }
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(384, 1)
     const float c = p.c;
     uint32_t tiles = 0, uses = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+    for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
       const int rt = row_token(p, row), tok = tok0 + rt;
       const bool live = tok < s.lq && row < p.tpt * p.gp;
       const int lim = p.causal ? min(s.lk, tok + 1 + s.lk - s.lq) : s.lk;
@@ -426,12 +426,10 @@ __global__ void __launch_bounds__(384, 1)
                                                        __uint_as_float(o[2 * e + 1]) * p.scale)
                                          : 0u;
       }
-      store_rows64(w, lane, min(cols, 64), [&](int r) -> uint16_t* {
-        const int rr = quarter * 32 + r;
-        const int t = row_token(p, rr), tt = tok0 + t;
-        if (tt >= s.lq || rr >= p.tpt * p.gp || !PACT_IN(s.q0 + tt < p.tq)) return nullptr;
-        return p.dq + (int64_t)(s.q0 + tt) * p.lddq + (int64_t)(h0 + rr - t * p.gp) * p.D + b;
-      });
+      if (PACT_IN(s.q0 + tok0 < p.tq))
+        store_rows64(w, lane, quarter * 32, min(p.tpt, s.lq - tok0) * p.gp, min(cols, 64),
+                     p.dq + (int64_t)(s.q0 + tok0) * p.lddq + (int64_t)h0 * p.D + b, p.lddq, p.D,
+                     p.gp, p.gp_mul);
     }
     if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
   }
@@ -496,16 +494,16 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  SeqFinder finder = seq_finder(p, 128, true);
+  SeqFinder<true> finder = seq_finder<true>(p, 128);
   Seq s;
   int key0, kvh, qt0, nqt, n;  // first key; first query tile and how many; times the subgroups
-  auto next_unit = [&](int64_t u) {
-    const int64_t t = u / p.hk;
+  auto next_unit = [&](uint32_t u) {
+    const uint32_t t = p.hk_div.div(u);
     kvh = (int)(u - t * p.hk);
     if (!finder.find(t, s)) return false;
     key0 = s.tile * 128;
     qt0 = 0;
-    if (p.causal) qt0 = SeqFinder::clampi(key0 - (s.lk - s.lq), 0, s.lq) / p.tpt;
+    if (p.causal) qt0 = clampi(key0 - (s.lk - s.lq), 0, s.lq) / p.tpt;
     nqt = (s.lq + p.tpt - 1) / p.tpt - qt0;
     n = nqt * p.subs;
     return true;
@@ -530,7 +528,7 @@ __global__ void __launch_bounds__(384, 1)
       ring.abort_flag = abort_flag;
       uint32_t uses = 0;
       bool ok = true, fixed = false;
-      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
         if (n == 0) continue;
         if (!(ok = mbar_wait(B.fix_empty, (uses & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
         if (lane == 0) {
@@ -578,14 +576,18 @@ __global__ void __launch_bounds__(384, 1)
       auto wait = [&](uint32_t bar, uint32_t par) {
         return mbar_wait(bar, par, kAttnWaitNs, abort_flag);
       };
-      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
         if (n == 0) continue;
         if (!(ok = wait(B.fix_full, uses & 1u))) break;
         ++uses;
         for (int i = 0; i <= n; ++i) {
-          if (i > 0) {  // the sum of tile i - 1, over dO (issuer 0) or Q (1)
-            RingPos r = at;  // one or two places back, which is a turn of the parity further on
-            r.advance(C::STAGES, C::STAGES - 2 + (issuer ? 0 : 1));
+          // the sum of tile i - 1, over dO (issuer 0) or Q (1), and the product of tile i, over
+          // Q (issuer 0) or dO (1)
+          RingPos r = at, x = at;
+          x.advance(C::STAGES, issuer);
+          // one or two places back, which is a turn of the parity further on
+          r.advance(C::STAGES, C::STAGES - 2 + (issuer ? 0 : 1));
+          if (i > 0) {
             if (!(ok = wait(B.full + 8 * r.stage, r.phase ^ 1u) && wait(in_full, tiles & 1u))) break;
             ++tiles;
             tc_fence_after();
@@ -600,23 +602,21 @@ __global__ void __launch_bounds__(384, 1)
             }
             __syncwarp();
           }
-          if (i < n) {  // the product of tile i, over Q (issuer 0) or dO (1)
-            RingPos r = at;
-            if (issuer) r.advance(C::STAGES);
-            if (!(ok = wait(B.full + 8 * r.stage, r.phase))) break;
+          if (i < n) {
+            if (!(ok = wait(B.full + 8 * x.stage, x.phase))) break;
             tc_fence_after();
             if (lead) {
-              const uint64_t d = dk0 + (uint64_t)(r.stage * (C::TILE >> 4));
+              const uint64_t d = dk0 + (uint64_t)(x.stage * (C::TILE >> 4));
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k)
                 if (k < ksteps) mma_bf16(prod, step_k(dfix, k), step_k(d, k), idesc_s, k > 0);
               mma_commit(out_full);
-              mma_commit(B.empty + 8 * r.stage);
+              mma_commit(B.empty + 8 * x.stage);
               if (i + 1 == n) mma_commit(B.fix_empty);
             }
             __syncwarp();
-            at.advance(C::STAGES, 2);
           }
+          if (i < n) at.advance(C::STAGES, 2);
         }
       }
       if (lead) {
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------------------------ -lse and delta of the columns
       uint32_t tiles = 0;
       bool ok = true;
-      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
         for (int i = 0; i < n; ++i, ++tiles) {
           int h0, tok0;
           tile_of(i, h0, tok0);
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(384, 1)
     const float c = p.c;
     uint32_t tiles = 0, uses = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+    for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
       const int key = key0 + row;
       for (int i = 0; i < n; ++i, ++tiles) {
         int h0, tok0;
@@ -768,11 +768,9 @@ __global__ void __launch_bounds__(384, 1)
                                               __uint_as_float(o[2 * e + 1]) * f)
                                 : 0u;
         }
-        store_rows64(w, lane, cols, [&](int r) -> uint16_t* {
-          const int k = key0 + quarter * 32 + r;
-          if (k >= s.lk || !PACT_IN(s.k0 + k < p.tk)) return nullptr;
-          return out + (int64_t)(s.k0 + k) * ld + (int64_t)kvh * p.D + b;
-        });
+        if (PACT_IN(s.k0 + key0 < p.tk))
+          store_rows64(w, lane, quarter * 32, s.lk - key0, cols,
+                       out + (int64_t)(s.k0 + key0) * ld + (int64_t)kvh * p.D + b, ld, p.D, 1, 65536u);
       }
     }
     if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
@@ -810,9 +808,8 @@ cudaError_t launch_attn_bwd(const AttnBwdLaunch& L, cudaStream_t st) {
     k_attn_delta<16><<<(unsigned)((rows + 15) / 16), 256, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // at most: whole tiles of all rows, and a ragged one for each sequence
-  const int64_t uq = ((int64_t)p.tq / p.tpt + p.nseq) * p.units_h;
-  const int64_t uk = ((int64_t)p.tk / 128 + p.nseq) * p.hk;
+  const int64_t uq = attn_units(p.tq, p.tpt, p.nseq, p.units_h);
+  const int64_t uk = attn_units(p.tk, 128, p.nseq, p.hk);
   const unsigned gq = (unsigned)(uq < L.num_sms ? uq : L.num_sms);
   const unsigned gk = (unsigned)(uk < L.num_sms ? uk : L.num_sms);
   return p.D <= 64 ? launch_bwd<64>(L, gq, gk, st) : launch_bwd<128>(L, gq, gk, st);

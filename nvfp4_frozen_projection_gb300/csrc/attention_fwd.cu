@@ -5,11 +5,15 @@
 //
 // One pass over the keys with the running maximum and sum of the softmax.  A CTA has two
 // tiles of 128 query rows (attention.cuh) against tiles of 128 keys, and a warpgroup for each,
-// a row a thread; while one softmax runs, the tensor cores work for the other tile:
-//   S_i  128 TMEM columns, P_i (BF16) over the first half of them, O_i behind both S.
-// A thread for each tile issues P_i V, then S_i of the next keys; MMAs of one thread run in
-// order, so S_i may be issued behind the P_i V that reads P_i out of the same columns.  Keys
-// and values pass through one ring of shared memory.
+// a row a thread; while one softmax runs, the tensor cores work for the other tile.  TMEM
+// columns of tile i: S_i at 128 i;
+//   D > 64:   P_i (BF16) over the first half of S_i, O_i at 256 + 128 i.  The next S_i has to
+//             wait for P_i V.
+//   D <= 64:  O_i at 256 + 64 i, P_i at 384 + 64 i: the next S_i is computed as soon as the
+//             softmax has read this one.
+// A thread for each tile issues its products; MMAs of one thread run in order, so (D > 64)
+// S_i may be issued behind the P_i V that reads P_i out of the same columns.  Keys and values
+// pass through one ring of shared memory.
 //
 // The running maximum m of a row moves only when a new one is above it by more than 2^8 in
 // the exponentials' scale: the sums stay far from FP32's range, and the rescaling of O in
@@ -21,6 +25,9 @@ namespace pact {
 
 template <int DP>
 struct FwdCfg {
+  static constexpr bool OWN_P = DP == 64;  // P has TMEM columns of its own
+  static constexpr int O_COL = 256, O_STEP = OWN_P ? 64 : 128;
+  static constexpr int P_COL = OWN_P ? 384 : 0, P_STEP = OWN_P ? 64 : 128;
   static constexpr int BOXES = DP / 64;
   static constexpr uint32_t TILE = BOXES * kBox;
   static constexpr int STAGES = DP == 64 ? 8 : 5;
@@ -28,7 +35,8 @@ struct FwdCfg {
   static constexpr uint32_t BAR_OFF = KV_OFF + STAGES * TILE;
   static constexpr uint32_t SMEM = BAR_OFF + 512 + 1024;
   // q_full[2] q_empty[2] s_full[2] p_full[2][2] o_done[2] final[2] tail - kv_full[ST] kv_empty[ST]
-  static constexpr int NBARS = 16 + 2 * STAGES;
+  // s_read[2] lag before the ring's
+  static constexpr int NBARS = 19 + 2 * STAGES;
   static_assert(SMEM <= 232448 && NBARS * 8 <= 504, "shared memory");
 };
 
@@ -44,7 +52,8 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t bars = base + C::BAR_OFF;
   const uint32_t q_full = bars, q_empty = bars + 16, s_full = bars + 32, p_full = bars + 48,
                  o_done = bars + 80, final_bar = bars + 96, tail_bar = bars + 112,
-                 kv_full = bars + 128, kv_empty = kv_full + 8 * C::STAGES;
+                 s_read = bars + 128, lag_bar = bars + 144, kv_full = bars + 152,
+                 kv_empty = kv_full + 8 * C::STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 504);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 508);
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -57,9 +66,11 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(p_full + 16 * i, 4);  // the warps of a tile, for each half of its keys
       mbar_init(p_full + 16 * i + 8, 4);
       mbar_init(o_done + 8 * i, 1);
+      mbar_init(s_read + 8 * i, 4);
       mbar_init(final_bar + 8 * i, 1);
     }
     mbar_init(tail_bar, 1);
+    mbar_init(lag_bar, 1);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(kv_full + 8 * s, 1);
       mbar_init(kv_empty + 8 * s, 2);  // the issuers
@@ -77,27 +88,25 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem = *tmem_slot;
 
   const int tpu = 2 * p.tpt;  // tokens of a unit
-  SeqFinder finder = seq_finder(p, tpu, false);
+  SeqFinder<false> finder = seq_finder<false>(p, tpu);
   Seq s;
-  // the unit's tiles: first token, and tiles of keys that they see
-  int tok0[2], nk[2], kvh, h0;
-  auto next_unit = [&](int64_t u) {
-    const int64_t t = u / p.units_h;
+  // the unit's tiles: first token, and the keys and tiles of keys that they see
+  int tok0[2], kend[2], nk[2], kvh, h0;
+  auto next_unit = [&](uint32_t u) {
+    const uint32_t t = p.units_div.div(u);
     const int hu = (int)(u - t * p.units_h);
     if (!finder.find(t, s)) return false;
-    kvh = hu / p.subs;
+    kvh = p.subs == 1 ? hu : hu / p.subs;
     h0 = kvh * p.group + (hu - kvh * p.subs) * p.gp;
-    const int tile = p.causal ? s.tiles - 1 - s.tile : s.tile;  // the longest first
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      tok0[i] = tile * tpu + i * p.tpt;
-      int kend = 0;
+      tok0[i] = s.tile * tpu + i * p.tpt;
+      kend[i] = 0;
       if (tok0[i] < s.lq) {
-        kend = s.lk;
-        if (p.causal)
-          kend = SeqFinder::clampi(min(tok0[i] + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
+        kend[i] = s.lk;
+        if (p.causal) kend[i] = clampi(min(tok0[i] + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
       }
-      nk[i] = (kend + 127) / 128;
+      nk[i] = (kend[i] + 127) / 128;
     }
     return true;
   };
@@ -158,13 +167,15 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         return true;
       };
-      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
         const int n = max(nk[0], nk[1]);
-        for (int j = 0; j < n && ok; ++j) {
-          if (j == 0 && nk[0] > 0) ok = load_q(0);
-          ok = ok && load_kv(&tmK, s.k0 + j * 128, 128);
-          if (j == 0 && nk[1] > 0) ok = ok && load_q(1);
-          ok = ok && load_kv(&tmV, s.k0 + j * 128, s.lk - j * 128);
+        // in the order of their use: K 0, then (OWN_P) K j + 1 and V j, or V j and K j + 1
+        for (int j = -1; j < n && n > 0 && ok; ++j) {
+          if (j < 0 && nk[0] > 0) ok = load_q(0);
+          if (!C::OWN_P && j >= 0) ok = ok && load_kv(&tmV, s.k0 + j * 128, s.lk - j * 128);
+          if (j + 1 < n) ok = ok && load_kv(&tmK, s.k0 + (j + 1) * 128, 128);
+          if (C::OWN_P && j >= 0) ok = ok && load_kv(&tmV, s.k0 + j * 128, s.lk - j * 128);
+          if (j < 0 && nk[1] > 0) ok = ok && load_q(1);
         }
       }
       if (!ok) {
@@ -180,10 +191,11 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------------------------ MMAs of tile i
       const int i = warp - 9;
       RingPos at;
-      uint32_t q_uses = 0, p_uses = 0;
-      bool ok = true;
+      uint32_t q_uses = 0, p_uses = 0, s_uses = 0;
+      bool ok = true, lagged = false;
       const uint32_t idesc_s = attn_idesc(128, false), idesc_o = attn_idesc(p.D, true);
-      const uint32_t ts = tmem + i * 128, to = tmem + 256 + i * 128;
+      const uint32_t ts = tmem + i * 128, to = tmem + C::O_COL + i * C::O_STEP;
+      const uint32_t tp = tmem + C::P_COL + i * C::P_STEP;
       const int ksteps = p.D / 16;
       const uint64_t dq = desc_k(base + C::Q_OFF + i * C::TILE);
       const uint64_t dk0 = desc_k(base + C::KV_OFF), dv0 = desc_n(base + C::KV_OFF);
@@ -191,60 +203,81 @@ __global__ void __launch_bounds__(384, 1)
       auto wait = [&](uint32_t bar, uint32_t par) {
         return mbar_wait(bar, par, kAttnWaitNs, abort_flag);
       };
-      for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
         const int n = max(nk[0], nk[1]);
-        // step j: the values of tile j - 1, the keys of tile j
+        if (i == 0 && !lagged && nk[0] == 0) {  // tile 1 has nobody to wait for
+          if (lead) mbar_arrive(lag_bar);
+          lagged = true;
+        }
+        // step j: the values of tile j - 1 and the keys of tile j, which come first in the
+        // ring with OWN_P.  A wait or a commit costs the thread about 100 cycles: what lies
+        // between P and the next S is as short as can be.
         for (int j = 0; j <= n && n > 0; ++j) {
-          if (j > 0) {
-            if (!(ok = wait(kv_full + 8 * at.stage, at.phase))) break;
-            if (j - 1 < nk[i]) {
-              const uint64_t d = dv0 + (uint64_t)(at.stage * (C::TILE >> 4));
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (!(ok = wait(p_full + 16 * i + 8 * h, p_uses & 1u))) break;
-                tc_fence_after();
-                if (lead) {
-#pragma unroll
-                  for (int k = 4 * h; k < 4 * h + 4; ++k)
-                    mma_bf16_ta(to, ts + k * 8, step_n(d, k), idesc_o, (j > 1 || k > 0) ? 1u : 0u);
-                }
-                __syncwarp();
-              }
-              if (!ok) break;
-              ++p_uses;
-              if (lead) {
-                mma_commit(kv_empty + 8 * at.stage);
-                mma_commit(o_done + 8 * i);
-              }
-            } else if (lead) {
-              mbar_arrive(kv_empty + 8 * at.stage);
+          const bool pv = j > 0 && j - 1 < nk[i], qk = j < nk[i];
+          RingPos v = at, k = at;
+          if (C::OWN_P ? j > 0 && j < n : false) v.advance(C::STAGES);
+          if (!C::OWN_P && j > 0) k.advance(C::STAGES);
+          if (j < n && !(ok = wait(kv_full + 8 * k.stage, k.phase))) break;
+          if (j > 0 && !(ok = wait(kv_full + 8 * v.stage, v.phase))) break;
+          if (qk && j == 0) {
+            if (!(ok = wait(q_full + 8 * i, q_uses & 1u))) break;
+            ++q_uses;
+            // Once, tile 1 starts half a step behind tile 0, and stays there: with both at
+            // the same point, both softmax warpgroups wait for the tensor cores, and then
+            // both work while those idle.
+            if (i == 1 && !lagged) {
+              if (!(ok = wait(lag_bar, 0))) break;
+              lagged = true;
             }
-            __syncwarp();
-            at.advance(C::STAGES);
           }
-          if (j < n) {
-            if (!(ok = wait(kv_full + 8 * at.stage, at.phase))) break;
-            if (j < nk[i]) {
-              if (j == 0) {
-                if (!(ok = wait(q_full + 8 * i, q_uses & 1u))) break;
-                ++q_uses;
-              }
-              tc_fence_after();
-              if (lead) {
-                const uint64_t d = dk0 + (uint64_t)(at.stage * (C::TILE >> 4));
+          auto issue_qk = [&]() {
+            const uint64_t d = dk0 + (uint64_t)(k.stage * (C::TILE >> 4));
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                  if (k < ksteps) mma_bf16(ts, step_k(dq, k), step_k(d, k), idesc_s, k > 0);
-                mma_commit(s_full + 8 * i);
-                mma_commit(kv_empty + 8 * at.stage);
-                if (j == nk[i] - 1) mma_commit(q_empty + 8 * i);
-              }
-            } else if (lead) {
-              mbar_arrive(kv_empty + 8 * at.stage);
-            }
+            for (int e = 0; e < DP / 16; ++e)
+              if (e < ksteps) mma_bf16(ts, step_k(dq, e), step_k(d, e), idesc_s, e > 0);
+            mma_commit(s_full + 8 * i);
+            mma_commit(kv_empty + 8 * k.stage);
+            if (j == nk[i] - 1) mma_commit(q_empty + 8 * i);
+          };
+          if (C::OWN_P && qk) {  // once the softmax has read the S before it
+            if (!(ok = wait(s_read + 8 * i, (s_uses & 1u) ^ 1u))) break;
+            ++s_uses;
+            tc_fence_after();
+            if (lead) issue_qk();
             __syncwarp();
-            at.advance(C::STAGES);
           }
+          const uint64_t d = dv0 + (uint64_t)(v.stage * (C::TILE >> 4));
+          if (pv) {
+            if (!(ok = wait(p_full + 16 * i, p_uses & 1u))) break;
+            tc_fence_after();
+            if (lead) {
+              if (i == 0 && !lagged) mbar_arrive(lag_bar);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                mma_bf16_ta(to, tp + e * 8, step_n(d, e), idesc_o, (j > 1 || e > 0) ? 1u : 0u);
+            }
+            lagged = lagged || i == 0;
+            __syncwarp();
+            if (!(ok = wait(p_full + 16 * i + 8, p_uses & 1u))) break;
+            ++p_uses;
+            tc_fence_after();
+          }
+          if (lead) {
+            if (pv && kend[i] - (j - 1) * 128 > 64) {
+#pragma unroll
+              for (int e = 4; e < 8; ++e) mma_bf16_ta(to, tp + e * 8, step_n(d, e), idesc_o, 1u);
+            }
+            // a stage that this tile has no use of is released all the same
+            if (pv)
+              mma_commit(kv_empty + 8 * v.stage);
+            else if (j > 0)
+              mbar_arrive(kv_empty + 8 * v.stage);
+            if (!C::OWN_P && qk) issue_qk();
+            if (pv) mma_commit(o_done + 8 * i);
+            if (!qk && j < n) mbar_arrive(kv_empty + 8 * k.stage);
+          }
+          __syncwarp();
+          at.advance(C::STAGES, j == 0 || j == n ? 1 : 2);
         }
       }
       if (lead) {
@@ -260,11 +293,13 @@ __global__ void __launch_bounds__(384, 1)
     const int i = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * 128;
+    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + C::O_COL + i * C::O_STEP;
+    const uint32_t tp = tmem + lanes + C::P_COL + i * C::P_STEP;
     const float c = p.c;
     uint32_t uses = 0;  // S tiles so far
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && next_unit(u); u += gridDim.x) {
+    uint32_t turn = 0;
+    for (bool more = next_unit(unit_of(0)); more;) {
       const int n = nk[i];
       const int tok = tok0[i] + row_token(p, row);
       // keys that this row sees, and that every row of the tile sees
@@ -279,29 +314,63 @@ __global__ void __launch_bounds__(384, 1)
         for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, v + 32 * b);
 #pragma unroll
         for (int b = 0; b < 4; ++b) tmem_ld_wait32(v + 32 * b);
-        if ((j + 1) * 128 > lim_all) {
-          const int x = lim - j * 128;
-#pragma unroll
-          for (int e = 0; e < 128; ++e) v[e] = e < x ? v[e] : 0xFF800000u;
+        if (C::OWN_P) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read + 8 * i);
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if ((j + 1) * 128 > lim_all) mask_from(v, lim - j * 128);
+        // the exponentials of half b: their sums, and P's packed columns
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t w[32];
+        auto exps = [&](int b, float mc) {
 #pragma unroll
-        for (int e = 0; e < 128; e += 8)
+          for (int e = 0; e < 32; ++e) {
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(v[64 * b + 2 * e]),
+                                              __uint_as_float(v[64 * b + 2 * e + 1])),
+                                  make_float2(c, c), make_float2(mc, mc));
+            x.x = ex2_ftz(x.x);
+            x.y = ex2_ftz(x.y);
+            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+            w[e] = pack_bf16x2(x.x, x.y);
+          }
+        };
+        auto row_max = [&]() {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1])));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (j == 0) {
-          m = top;
-        } else {
+          for (int e = 0; e < 128; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1])));
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        // P of this tile takes the place of the last one's, whose product must be done
+        auto wait_pv = [&]() {
+          return j == 0 || mbar_wait(o_done + 8 * i, (uses - 1u) & 1u, kAttnWaitNs, abort_flag);
+        };
+        // From the second tile on the exponentials begin with the old maximum, beside the
+        // search for the new one (the one needs the MUFU, the other the ALU), and are taken
+        // again in the rare case that it moves.
+        bool again = j == 0;
+        float mc = m == -INFINITY ? 0.0f : -m * c;
+        if (!again) {
+          exps(0, mc);
+          again = __any_sync(0xFFFFFFFFu, (row_max() - m) * c > 8.0f);
+        }
+        bool waited = false;
+        if (again) {
+          const float top = row_max();
           const bool move = (top - m) * c > 8.0f;
-          if (__any_sync(0xFFFFFFFFu, move)) {
+          if (j == 0) {
+            m = top;
+          } else if (__any_sync(0xFFFFFFFFu, move)) {
             const float m2 = move ? top : m;
             const float f = move ? ex2_ftz((m - m2) * c) : 1.0f;
             l *= f;
             m = m2;
             // O holds the products so far once the last P V has completed
-            if (!(ok = mbar_wait(o_done + 8 * i, (uses - 1u) & 1u, kAttnWaitNs, abort_flag))) break;
+            if (!(ok = wait_pv())) break;
+            waited = true;
             tc_fence_after();
             for (int b = 0; b < p.D; b += 16) {
               uint32_t o[16];
@@ -313,25 +382,22 @@ __global__ void __launch_bounds__(384, 1)
             }
             tmem_st_wait();
           }
+          mc = m == -INFINITY ? 0.0f : -m * c;
+          sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+          exps(0, mc);
         }
-        const float mc = m == -INFINITY ? 0.0f : -m * c;
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        if (C::OWN_P && !waited) {
+          if (!(ok = wait_pv())) break;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 x = __ffma2_rn(make_float2(__uint_as_float(v[64 * b + 2 * e]),
-                                              __uint_as_float(v[64 * b + 2 * e + 1])),
-                                  make_float2(c, c), make_float2(mc, mc));
-            x.x = ex2_ftz(x.x);
-            x.y = ex2_ftz(x.y);
-            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-            w[e] = pack_bf16x2(x.x, x.y);
+          if (b == 0 || kend[i] - j * 128 > 64) {  // else no key of the second half is seen
+            if (b == 1) exps(1, mc);
+            tmem_st32(tp + 32 * b, w);
+            tmem_st_wait();
+            tc_fence_before();
           }
-          tmem_st32(ts + 32 * b, w);
-          tmem_st_wait();
-          tc_fence_before();
           __syncwarp();
           // the first half's product runs while the second half is computed
           if (lane == 0) mbar_arrive(p_full + 16 * i + 8 * b);
@@ -340,8 +406,10 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- o and lse
-      if (tok0[i] >= s.lq) continue;
-      const bool live = tok < s.lq && row < p.tpt * p.gp;
+      // the search for the next unit runs while the last product does
+      const int t0 = tok0[i], rows = min(p.tpt, s.lq - t0) * p.gp, q0 = s.q0, head = h0;
+      more = next_unit(unit_of(++turn));
+      if (rows <= 0) continue;
       float inv = 0.0f;
       if (n > 0) {
         if (!(ok = mbar_wait(o_done + 8 * i, (uses - 1u) & 1u, kAttnWaitNs, abort_flag))) break;
@@ -351,32 +419,26 @@ __global__ void __launch_bounds__(384, 1)
       const bool empty = n == 0 || lim <= 0;
       for (int b = 0; b < p.D; b += 64) {
         uint32_t w[32];
-        const int cols = min(64, p.D - b);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint32_t o[16];
-          if (n > 0 && h * 16 < cols) {
+          if (n > 0) {  // columns past D hold nothing of use
             tmem_ld16(to + b + 16 * h, o);
             tmem_ld_wait16(o);
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            w[8 * h + e] = (empty || h * 16 >= cols)
-                               ? 0u
-                               : pack_bf16x2(__uint_as_float(o[2 * e]) * inv,
-                                             __uint_as_float(o[2 * e + 1]) * inv);
+            w[8 * h + e] = empty ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * inv,
+                                                    __uint_as_float(o[2 * e + 1]) * inv);
         }
-        store_rows64(w, lane, cols, [&](int r) -> uint16_t* {
-          const int rr = quarter * 32 + r;
-          const int t = row_token(p, rr), tt = tok0[i] + t;
-          if (tt >= s.lq || rr >= p.tpt * p.gp || !PACT_IN(s.q0 + tt < p.tq)) return nullptr;
-          return p.o + (int64_t)(s.q0 + tt) * p.ldo + (int64_t)(h0 + rr - t * p.gp) * p.D + b;
-        });
+        if (PACT_IN(q0 + t0 < p.tq))
+          store_rows64(w, lane, quarter * 32, rows, min(64, p.D - b),
+                       p.o + (int64_t)(q0 + t0) * p.ldo + (int64_t)head * p.D + b, p.ldo, p.D, p.gp,
+                       p.gp_mul);
       }
-      if (live && PACT_IN(s.q0 + tok < p.tq)) {
-        const int h = h0 + row - row_token(p, row) * p.gp;
-        p.lse[(int64_t)h * p.tq + s.q0 + tok] =
-            empty ? -INFINITY : (m * c + log2f(l)) * kLn2;
+      if (row < rows && PACT_IN(q0 + tok < p.tq)) {
+        const int h = head + row - row_token(p, row) * p.gp;
+        p.lse[(int64_t)h * p.tq + q0 + tok] = empty ? -INFINITY : (m * c + log2f(l)) * kLn2;
       }
     }
     if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
@@ -391,9 +453,8 @@ __global__ void __launch_bounds__(384, 1)
 
 cudaError_t launch_attn_fwd(const AttnFwdLaunch& L, cudaStream_t st) {
   const AttnParams& p = L.p;
-  const int64_t tpu = 2 * p.tpt;
-  // at most: whole tiles of all tokens, and a ragged one for each sequence
-  const int64_t units = ((int64_t)p.tq / tpu + p.nseq) * p.units_h;
+  const int tpu = 2 * p.tpt;
+  const int64_t units = attn_units(p.tq, tpu, p.nseq, p.units_h);
   const unsigned grid = (unsigned)(units < L.num_sms ? units : L.num_sms);
   cudaError_t e;
   note_launch();

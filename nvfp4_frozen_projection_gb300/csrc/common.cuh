@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fastdiv.h"
 #include "status.h"
 
 #if defined(__CUDA_ARCH__) && !defined(__CUDA_ARCH_FEAT_SM103_ALL)
@@ -24,25 +25,6 @@ namespace pact {
 __host__ __device__ __forceinline__ int64_t pad_to(int64_t x, int64_t m) {
   return (x + m - 1) / m * m;
 }
-
-// n / d for n < 2^31 by a multiply-high and a shift (Granlund and Montgomery's
-// division by invariant integers): p = 31 + ceil(log2 d), m = ceil(2^p / d).
-struct FastDiv {
-  uint32_t d, m, s;
-  __host__ static FastDiv make(uint32_t d) {
-    uint32_t l = 0;
-    while ((1ull << l) < d) ++l;
-    const uint64_t p2 = 1ull << (31 + l);
-    FastDiv f;
-    f.d = d;
-    f.m = (uint32_t)((p2 + d - 1) / d);
-    f.s = l - 1;  // (n * m) >> (31 + l) == umulhi(n, m) >> (l - 1) for l >= 1
-    return f;
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const {
-    return d == 1 ? n : (__umulhi(n, m) >> s);
-  }
-};
 
 // Byte offset of the E4M3 scale of (row r, block c) in the 128x4-atom layout read
 // by the block-scaled tensor-core MMA (c16p = pad4(cols/16)).

@@ -17,6 +17,8 @@
 namespace pact {
 
 constexpr int kGradThreads = 256;
+// Chunks at the end of the list that the first pass leaves in L2 for the second: 64 MB.
+constexpr int64_t kGradKept = 4096;
 static_assert(kGradChunk == kGradThreads * 16, "a thread has four vectors of a chunk");
 
 struct GradSpan {
@@ -56,7 +58,7 @@ __device__ __forceinline__ double block_sum(double v, double* slots) {
   return s;
 }
 
-__global__ void __launch_bounds__(kGradThreads) k_grad_sums(const GradTable t, double* part) {
+__global__ void __launch_bounds__(kGradThreads, kGradBlocks) k_grad_sums(const GradTable t, double* part) {
   __shared__ double slots[kGradThreads / 32];
   double sum = 0.0;
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
@@ -69,7 +71,8 @@ __global__ void __launch_bounds__(kGradThreads) k_grad_sums(const GradTable t, d
       const int e = (i * kGradThreads + (int)threadIdx.x) * 4;
       v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (vec && e + 4 <= sp.len) {
-        v[i] = *reinterpret_cast<const float4*>(g + e);
+        const float4* at = reinterpret_cast<const float4*>(g + e);
+        v[i] = t.chunks - c > kGradKept ? __ldcs(at) : *at;
       } else {
         if (e < sp.len) v[i].x = g[e];
         if (e + 1 < sp.len) v[i].y = g[e + 1];
@@ -150,9 +153,8 @@ __global__ void __launch_bounds__(kGradThreads)
   }
 }
 
-// Blocks of the sums: 4 an SM.
 int64_t grad_norm_blocks(int64_t chunks, int num_sms) {
-  const int64_t most = 4ll * num_sms;
+  const int64_t most = (int64_t)kGradBlocks * num_sms;
   return chunks < 1 ? 1 : (chunks < most ? chunks : most);
 }
 

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fastdiv.h"
 #include "status.h"
 
 namespace pact {
@@ -214,6 +215,7 @@ cudaError_t launch_qk_norm_rope_bwd(RopeParams& p, int pairs, float* dgq, float*
 // Gradient norm and clipping (grad_norm.cu): tensor i has numel[i] values at data[i], its
 // first chunk of kGradChunk values is first[i] of `chunks`.  All on the device.
 constexpr int kGradChunk = 4096;
+constexpr int kGradBlocks = 6;  // an SM
 struct GradTable {
   float* const* data;
   const int64_t* numel;
@@ -233,6 +235,7 @@ struct AttnParams {
   uint32_t gp_mul;       // ceil(2^16 / gp)
   int subs;              // query tiles of a key head's group: group / gp
   int units_h;           // units of one token range
+  FastDiv units_div, hk_div;  // by units_h and hk
   float scale, c;        // c = scale log2 e
   int causal;
   const float* lse_in;
@@ -248,6 +251,10 @@ struct AttnParams {
   int64_t lddq, lddk, lddv;
   unsigned* status;
 };
+// Units at most: whole tiles of all rows, and a ragged one for each sequence, for `heads`.
+inline int64_t attn_units(int64_t rows, int per, int64_t nseq, int64_t heads) {
+  return (rows / per + nseq) * heads;
+}
 struct AttnFwdLaunch {
   // BF16 [T, heads, D], boxes of 64 columns, 128-byte swizzle: Q gp heads x tpt tokens, K and
   // V one head x 128 tokens

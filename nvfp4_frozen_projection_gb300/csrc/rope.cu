@@ -25,6 +25,7 @@ namespace pact {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeBlocks = 4;     // an SM: 64 registers a thread
 constexpr int kRopeBwdBlocks = 3;  // 80
+constexpr int kRopeBwdMost = 16;   // an SM, in all
 
 // The rotation of one lane's 8 columns, two at a time: y = own c + other s.  The other half
 // of a pair comes from the lane `other`, or (PAIRS) is the neighbouring column.
@@ -253,18 +254,28 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
   }
 }
 
-// dgamma_q, dgamma_k [D] from the blocks' sums, those of the queries first: a warp a column,
-// its lanes' sums over every 32nd block joined by a butterfly.
-__global__ void __launch_bounds__(256)
+// dgamma_q, dgamma_k [D] from the blocks' sums, those of the queries first.  16 columns a
+// block (D is a multiple of 16), 64 threads each, which take every 64th row and are joined in
+// order.
+__global__ void __launch_bounds__(1024)
     k_qk_dgamma(const float* part, int bq, int bk, int D, float* dgq, float* dgk) {
-  const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (c >= 2 * D) return;
-  const bool isk = c >= D;
-  const float* from = part + (isk ? (int64_t)bq * D + (c - D) : c);
+  __shared__ float sums[64][17];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+  const bool isk = (int)blockIdx.x * 16 >= D;
+  const int c = (int)blockIdx.x * 16 + x - (isk ? D : 0);
+  const float* from = part + (isk ? (int64_t)bq * D : 0) + c;
+  const int rows = isk ? bk : bq;
   float s = 0.0f;
-  for (int b = lane; b < (isk ? bk : bq); b += 32) s += from[(int64_t)b * D];
-  s = seg_sum<32>(s);
-  if (lane == 0 && PACT_IN(c < 2 * D)) (isk ? dgk[c - D] : dgq[c]) = s;
+#pragma unroll 8
+  for (int b = y; b < rows; b += 64) s += from[(int64_t)b * D];
+  sums[y][x] = s;
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    s = 0.0f;
+#pragma unroll 16
+    for (int b = 0; b < 64; ++b) s += sums[b][threadIdx.x];
+    if (PACT_IN(c < D)) (isk ? dgk : dgq)[c] = s;
+  }
 }
 
 __global__ void k_rope_turns(const double* inv_freq, int n, int64_t* turns) {
@@ -334,14 +345,15 @@ cudaError_t launch_qk_norm_rope(RopeParams& p, int pairs, int num_sms, cudaStrea
   return cudaGetLastError();
 }
 
-// Blocks of the backward: one wave, so that the sums for dgamma are few.
+// Blocks of the backward: a few waves, which leave less of the last one empty than one of
+// blocks that go on would, and not so many that the sums for dgamma weigh.
 int64_t rope_bwd_blocks(int64_t T, int hq, int hk, int D, int num_sms) {
   RopeParams p = {};
   p.T = T;
   p.D = D;
   p.side[0].heads = hq;
   p.side[1].heads = hk;
-  rope_plan(p, num_sms, kRopeBwdBlocks * num_sms);
+  rope_plan(p, num_sms, kRopeBwdMost * num_sms);
   return (int64_t)p.side[0].blocks + p.side[1].blocks;
 }
 
@@ -368,7 +380,7 @@ static void launch_bwd(const RopeParams& p, bool norm, bool pairs, bool dg, floa
 cudaError_t launch_qk_norm_rope_bwd(RopeParams& p, int pairs, float* dgq, float* dgk, float* part,
                                     int num_sms, cudaStream_t st) {
   const int seg = seg_lanes(p.D);
-  rope_plan(p, num_sms, kRopeBwdBlocks * num_sms);
+  rope_plan(p, num_sms, kRopeBwdMost * num_sms);
   const bool norm = p.side[0].gamma != nullptr, dg = dgq != nullptr;
   note_launch();
   if (seg == 8)
@@ -380,7 +392,7 @@ cudaError_t launch_qk_norm_rope_bwd(RopeParams& p, int pairs, float* dgq, float*
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !dg) return e;
   note_launch();
-  k_qk_dgamma<<<(2 * p.D + 7) / 8, 256, 0, st>>>(part, p.side[0].blocks, p.side[1].blocks, p.D, dgq,
+  k_qk_dgamma<<<2 * p.D / 16, 1024, 0, st>>>(part, p.side[0].blocks, p.side[1].blocks, p.D, dgq,
                                                  dgk);
   return cudaGetLastError();
 }
