@@ -10,23 +10,30 @@
 // tiles, in an order that changes from run to run.  A CTA has one tile of 128 rows; two
 // threads issue the products, two warpgroups hold a row a thread and half its columns each.
 //
-//   dq:     rows are queries.  TMEM: S twice (0, 128), dP (256, dS over it), dq (384).
-//           One thread issues S as its buffers are read, the other, once dS is there,
-//           dq += dS k and dP of the next keys.
-//   dk|dv:  rows are keys, columns the (token, head) rows of a query tile.  TMEM: S^T (0, P^T
-//           over it), dP^T (128, dS^T over it), dv (256), dk (384).
-//           One thread issues, once P is there, dv += P^T do and S^T of the next queries,
-//           the other, once dS is there, dk += dS^T q and dP^T of the next queries.
-// So the tensor cores have work while exponentials are taken, and MMAs of one thread run in
-// order, which is what lets the next S or dP overwrite the P or dS before it.  P and dS are
-// rounded to BF16 for their products; everything else is FP32.
+//   dq:     rows are queries.  TMEM: S (0), dP (128), dS (256, BF16), dq (320).  One thread
+//           issues S of the next keys as soon as this one has been read, the other dP of the
+//           next keys and, once dS is there, dq += dS k.
+//   dk|dv:  rows are keys, columns the (token, head) rows of a query tile; one thread issues
+//           S^T and dv += P^T do, the other dP^T and dk += dS^T q.
+//           D <= 64: S^T (0), dP^T (128), P^T (256), dS^T (320), dv (384), dk (448); the next
+//           S^T or dP^T comes as soon as this one has been read.
+//           D > 64: there is no room for that.  P^T lies over S^T, dS^T over dP^T, dv at 256,
+//           dk at 384, and the next S^T comes behind dv += P^T do, the next dP^T behind
+//           dk += dS^T q: MMAs of one thread run in order.
+// So the tensor cores have work while exponentials are taken.  P and dS are rounded to BF16
+// for their products; everything else is FP32.
 #include "attention.cuh"
 
 namespace pact {
 
-// A warpgroup's half of the columns of a 128-column tile, 64 of them, becomes 32 columns of
-// BF16 pairs at its own first column (0 or 64): neither half lies over what the other reads.
-__device__ __forceinline__ uint32_t half_step(int k) { return (k >> 2) * 64 + (k & 3) * 8; }
+// TMEM column of step k (16 of 128 columns) of a BF16 operand.  OWN: it has 64 columns of its
+// own.  Else it lies over the FP32 tile that it was made from: each warpgroup's half of that,
+// 64 columns, becomes 32 at its own first column, so that neither half lies over what the
+// other still reads.
+template <bool OWN>
+__device__ __forceinline__ uint32_t half_step(int k) {
+  return OWN ? k * 8 : (k >> 2) * 64 + (k & 3) * 8;
+}
 
 // ------------------------------------------------------------------ delta
 template <int SEG>
@@ -98,27 +105,61 @@ struct TileRing {
   }
 };
 
+// -lse log2 e and delta of a query tile's rows, four a lane; `none` for the -lse of rows that
+// hold no query.  And their way through shared memory.
+__device__ __forceinline__ void load_stats(const AttnParams& p, const Seq& s, int h0, int tok0,
+                                           float none, int lane, float (&nl)[4], float (&de)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int x = k * 32 + lane, rt = row_token(p, x), tok = tok0 + rt;
+    nl[k] = none;
+    de[k] = 0.0f;
+    if (x < p.tpt * p.gp && tok < s.lq) {
+      const int64_t at = (int64_t)(h0 + x - rt * p.gp) * p.tq + s.q0 + tok;
+      nl[k] = -p.lse_in[at] * kLog2e;
+      de[k] = p.delta[at];
+    }
+  }
+}
+__device__ __forceinline__ void store_stats(float* st, int lane, const float (&nl)[4],
+                                            const float (&de)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    st[k * 32 + lane] = nl[k];
+    st[128 + k * 32 + lane] = de[k];
+  }
+  __syncwarp();
+}
+
 template <int DP>
 struct BwdCfg {
   static constexpr int BOXES = DP / 64;
   static constexpr uint32_t TILE = BOXES * kBox;
   static constexpr int STAGES = DP == 64 ? 8 : 5;
-  // two tiles that stay for a unit, the ring, and (dk|dv) two buffers of 128 -lse and delta
+  // dq: rings of K, which a tile holds from S to dq, and of V
+  static constexpr int NK = DP == 64 ? 4 : 3, NV = STAGES - NK;
+  static constexpr bool OWN_P = DP == 64;  // dk|dv: P and dS have TMEM columns of their own
+  static constexpr int SUM_COL = OWN_P ? 384 : 256, SUM_STEP = OWN_P ? 64 : 128;
+  // two tiles that stay for a unit, the ring, and two buffers of 128 -lse and delta
   static constexpr uint32_t RING_OFF = 2 * TILE, STAT_OFF = RING_OFF + STAGES * TILE;
   static constexpr uint32_t BAR_OFF = STAT_OFF + 2048;
-  // 17 barriers and the ring's; behind them the TMEM slot and the abort flag
-  static constexpr uint32_t SLOT_OFF = BAR_OFF + 136 + 16 * STAGES, SMEM = SLOT_OFF + 16;
+  // 23 barriers and the ring's; behind them the TMEM slot and the abort flag
+  static constexpr uint32_t SLOT_OFF = BAR_OFF + 184 + 16 * STAGES, SMEM = SLOT_OFF + 16;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
 // Shared addresses of the barriers; those with a number in brackets lie 8 bytes apart.
 struct BwdBars {
   uint32_t fix_full, fix_empty;  // [2] the two tiles of a unit
-  uint32_t s_full;               // [2]
-  uint32_t dp_full, p_full, ds_full, acc_full, tail;
+  uint32_t s_full, dp_full;      // S and dP are there
+  uint32_t s_read, dp_read;      // and have been read
+  uint32_t p_full;               // [2] P is there: the first and the second half of each half
+  uint32_t ds_full;              // dS is there
+  uint32_t p_empty, ds_empty;    // and their products are done
+  uint32_t acc_full;
+  uint32_t tail;                   // [2]
   uint32_t final_bar;              // [2]
-  uint32_t stat_full, stat_empty;  // [2] (dk|dv)
-  uint32_t s_empty;                // [2] (dq)
+  uint32_t stat_full, stat_empty;  // [2] -lse and delta
   uint32_t full, empty;            // the ring
 };
 __device__ __forceinline__ BwdBars bwd_bars(uint32_t b, int stages) {
@@ -126,15 +167,19 @@ __device__ __forceinline__ BwdBars bwd_bars(uint32_t b, int stages) {
   r.fix_full = b;
   r.fix_empty = b + 16;
   r.s_full = b + 32;
-  r.dp_full = b + 48;
-  r.p_full = b + 56;
-  r.ds_full = b + 64;
-  r.acc_full = b + 72;
-  r.tail = b + 80;
-  r.final_bar = b + 88;
-  r.stat_full = r.s_empty = b + 104;
-  r.stat_empty = b + 120;
-  r.full = b + 136;
+  r.dp_full = b + 40;
+  r.s_read = b + 48;
+  r.dp_read = b + 56;
+  r.p_full = b + 64;
+  r.ds_full = b + 80;
+  r.p_empty = b + 88;
+  r.ds_empty = b + 96;
+  r.acc_full = b + 104;
+  r.tail = b + 112;
+  r.final_bar = b + 128;
+  r.stat_full = b + 144;
+  r.stat_empty = b + 160;
+  r.full = b + 184;
   r.empty = r.full + 8 * stages;
   return r;
 }
@@ -160,16 +205,20 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(B.fix_full + 8 * i, 1);
       mbar_init(B.fix_empty + 8 * i, 1);
-      mbar_init(B.s_full + 8 * i, 1);
     }
+    mbar_init(B.s_full, 1);
     mbar_init(B.dp_full, 1);
-    mbar_init(B.ds_full, 8);  // the computing warps
+    mbar_init(B.s_read, 8);  // the computing warps
+    mbar_init(B.dp_read, 8);
+    mbar_init(B.ds_full, 8);
+    mbar_init(B.ds_empty, 1);
     mbar_init(B.acc_full, 1);
-    mbar_init(B.tail, 1);
-    mbar_init(B.final_bar, 1);
-    mbar_init(B.final_bar + 8, 1);
-    mbar_init(B.s_empty, 8);
-    mbar_init(B.s_empty + 8, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B.tail + 8 * i, 1);
+      mbar_init(B.final_bar + 8 * i, 1);
+      mbar_init(B.stat_full + 8 * i, 1);
+      mbar_init(B.stat_empty + 8 * i, 8);
+    }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(B.full + 8 * s, 1);
       mbar_init(B.empty + 8 * s, 2);  // the issuers
@@ -206,13 +255,19 @@ __global__ void __launch_bounds__(384, 1)
     setmaxnreg_dec<72>();
     if (warp == 8) {
       // ------------------------------------------------------------ copies
-      TileRing<C::BOXES, C::STAGES> ring;
-      ring.tiles = base + C::RING_OFF;
-      ring.mem = smem + C::RING_OFF;
-      ring.full = B.full;
-      ring.empty = B.empty;
-      ring.tail = B.tail;
-      ring.abort_flag = abort_flag;
+      TileRing<C::BOXES, C::NK> kring;
+      TileRing<C::BOXES, C::NV> vring;
+      kring.tiles = base + C::RING_OFF;
+      kring.mem = smem + C::RING_OFF;
+      kring.full = B.full;
+      kring.empty = B.empty;
+      kring.tail = B.tail;
+      vring.tiles = kring.tiles + C::NK * C::TILE;
+      vring.mem = kring.mem + C::NK * C::TILE;
+      vring.full = B.full + 8 * C::NK;
+      vring.empty = B.empty + 8 * C::NK;
+      vring.tail = B.tail + 8;
+      kring.abort_flag = vring.abort_flag = abort_flag;
       uint32_t uses = 0;
       bool ok = true;
       auto load_fix = [&](int i, const CUtensorMap* tm) {
@@ -235,12 +290,12 @@ __global__ void __launch_bounds__(384, 1)
             ok = load_fix(0, &tmQ);
             if (ok) fixed = 1;
           }
-          ok = ok && ring.load(&tmK, kvh, row, 128, valid, lane);
+          ok = ok && kring.load(&tmK, kvh, row, 128, valid, lane);
           if (j == 0) {
             ok = ok && load_fix(1, &tmdO);
             if (ok) fixed = 2;
           }
-          ok = ok && ring.load(&tmV, kvh, row, 128, valid, lane);
+          ok = ok && vring.load(&tmV, kvh, row, 128, valid, lane);
         }
         if (ok) {
           ++uses;
@@ -249,13 +304,14 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) {
         if (lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_TMA);
-        ring.drain();
+        kring.drain();
+        vring.drain();
         for (uint32_t i = 0; i < fixed; ++i) mbar_wait(B.fix_full + 8 * i, uses & 1u, 10000000ull, nullptr);
       }
     } else if (warp < 11) {
       // ------------------------------------------------------------ MMAs
       const int issuer = warp - 9;
-      RingPos at;  // of K of the current tile; V follows it
+      RingPos k, v;
       uint32_t uses = 0, tiles = 0;
       bool ok = true;
       const uint32_t idesc_s = attn_idesc(128, false), idesc_d = attn_idesc(p.D, true);
@@ -279,57 +335,57 @@ __global__ void __launch_bounds__(384, 1)
         ++uses;
         if (issuer == 0) {
           for (int j = 0; j < nk; ++j, ++tiles) {
-            const uint32_t buf = tiles & 1u;
-            if (!(ok = wait(B.full + 8 * at.stage, at.phase) &&
-                       wait(B.s_empty + 8 * buf, ((tiles >> 1) & 1u) ^ 1u)))
+            if (!(ok = wait(B.full + 8 * k.stage, k.phase) && wait(B.s_read, (tiles & 1u) ^ 1u)))
               break;
             tc_fence_after();
             if (lead) {
-              mma_rows(buf * 128, at.stage);
-              mma_commit(B.s_full + 8 * buf);
-              mma_commit(B.empty + 8 * at.stage);
+              mma_rows(0, k.stage);
+              mma_commit(B.s_full);
+              mma_commit(B.empty + 8 * k.stage);
               if (j + 1 == nk) mma_commit(B.fix_empty);
             }
             __syncwarp();
-            at.advance(C::STAGES, 2);
+            k.advance(C::NK);
           }
         } else {
           for (int j = 0; j <= nk; ++j) {
-            // dq of tile j - 1, dP of tile j
-            RingPos v = at, k = at;
-            v.advance(C::STAGES);
-            // two places back, which is a turn of the parity further on
-            k.advance(C::STAGES, C::STAGES - 2);
-            if (j > 0) {
-              if (!(ok = wait(B.full + 8 * k.stage, k.phase ^ 1u) && wait(B.ds_full, tiles & 1u)))
+            // dP of tile j, dq of tile j - 1
+            if (j < nk) {
+              const int st = C::NK + v.stage;
+              if (!(ok = wait(B.full + 8 * st, v.phase) &&
+                         wait(B.dp_read, ((tiles + j) & 1u) ^ 1u)))
                 break;
-              ++tiles;
+              tc_fence_after();
+              if (lead) {
+                mma_rows(128, st);
+                mma_commit(B.dp_full);
+                mma_commit(B.empty + 8 * st);  // for both issuers: the other has no use of V
+                mma_commit(B.empty + 8 * st);
+                if (j + 1 == nk) mma_commit(B.fix_empty + 8);
+              }
+              __syncwarp();
+              v.advance(C::NV);
+            }
+            if (j > 0) {
+              if (!(ok = wait(B.full + 8 * k.stage, k.phase) &&
+                         wait(B.ds_full, (tiles + j - 1) & 1u)))
+                break;
               tc_fence_after();
               if (lead) {
                 const uint64_t d = dn0 + (uint64_t)(k.stage * (C::TILE >> 4));
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  mma_bf16_ta(tmem + 384, tmem + 256 + half_step(i), step_n(d, i), idesc_d,
+                  mma_bf16_ta(tmem + 320, tmem + 256 + half_step<true>(i), step_n(d, i), idesc_d,
                               (j > 1 || i > 0) ? 1u : 0u);
+                mma_commit(B.ds_empty);
                 mma_commit(B.empty + 8 * k.stage);
                 if (j == nk) mma_commit(B.acc_full);
               }
               __syncwarp();
+              k.advance(C::NK);
             }
-            if (j < nk) {
-              if (!(ok = wait(B.full + 8 * v.stage, v.phase))) break;
-              tc_fence_after();
-              if (lead) {
-                mma_rows(256, v.stage);
-                mma_commit(B.dp_full);
-                mma_commit(B.empty + 8 * v.stage);  // for both issuers: the other has no use of V
-                mma_commit(B.empty + 8 * v.stage);
-                if (j + 1 == nk) mma_commit(B.fix_empty + 8);
-              }
-              __syncwarp();
-            }
-            if (j < nk) at.advance(C::STAGES, 2);
           }
+          tiles += nk;
         }
       }
       if (lead) {
@@ -338,6 +394,22 @@ __global__ void __launch_bounds__(384, 1)
         mbar_wait(B.final_bar + 8 * issuer, 0, kAttnWaitNs, nullptr);
       }
       __syncwarp();
+    } else {
+      // ------------------------------------------------------------ -lse and delta of the rows
+      uint32_t units = 0;
+      bool ok = true;
+      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
+        if (nk == 0) continue;
+        const uint32_t buf = units & 1u;
+        float nl[4], de[4];
+        load_stats(p, s, h0, tok0, 0.0f, lane, nl, de);
+        if (!(ok = mbar_wait(B.stat_empty + 8 * buf, ((units >> 1) & 1u) ^ 1u, kAttnWaitNs, abort_flag)))
+          break;
+        store_stats(reinterpret_cast<float*>(smem + C::STAT_OFF + buf * 1024), lane, nl, de);
+        if (lane == 0) mbar_arrive(B.stat_full + 8 * buf);
+        ++units;
+      }
+      if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_SF);
     }
   } else {
     // -------------------------------------------------------------- a row and 64 columns a thread
@@ -346,31 +418,34 @@ __global__ void __launch_bounds__(384, 1)
     const int row = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const float c = p.c;
-    uint32_t tiles = 0, uses = 0;
+    uint32_t tiles = 0, uses = 0, turn = 0;
     bool ok = true;
-    for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
-      const int rt = row_token(p, row), tok = tok0 + rt;
-      const bool live = tok < s.lq && row < p.tpt * p.gp;
+    for (bool more = next_unit(unit_of(0)); more;) {
+      const int tok = tok0 + row_token(p, row), n = nk;
       const int lim = p.causal ? min(s.lk, tok + 1 + s.lk - s.lq) : s.lk;
       const int lim_all = p.causal ? min(s.lk, tok0 + 1 + s.lk - s.lq) : s.lk;
       float nlse = 0.0f, delta = 0.0f;
-      if (live && nk > 0) {
-        const int64_t at = (int64_t)(h0 + row - rt * p.gp) * p.tq + s.q0 + tok;
-        nlse = -p.lse_in[at] * kLog2e;
-        delta = p.delta[at];
+      if (n > 0) {
+        const uint32_t buf = uses & 1u;
+        if (!(ok = mbar_wait(B.stat_full + 8 * buf, (uses >> 1) & 1u, kAttnWaitNs, abort_flag))) break;
+        const float* st = reinterpret_cast<const float*>(smem + C::STAT_OFF + buf * 1024);
+        nlse = st[row];
+        delta = st[128 + row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.stat_empty + 8 * buf);
       }
-      for (int j = 0; j < nk; ++j, ++tiles) {
-        if (!(ok = mbar_wait(B.s_full + 8 * (tiles & 1u), (tiles >> 1) & 1u, kAttnWaitNs, abort_flag))) break;
+      for (int j = 0; j < n; ++j, ++tiles) {
+        if (!(ok = mbar_wait(B.s_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
         uint32_t v[64];
-        const uint32_t ts = tl + (tiles & 1u) * 128 + half * 64;
+        const uint32_t ts = tl + half * 64;
         tmem_ld32(ts, v);
         tmem_ld32(ts + 32, v + 32);
         tmem_ld_wait32(v);
         tmem_ld_wait32(v + 32);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(B.s_empty + 8 * (tiles & 1u));
+        if (lane == 0) mbar_arrive(B.s_read);
         float pr[64];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -381,30 +456,42 @@ __global__ void __launch_bounds__(384, 1)
           pr[2 * e + 1] = ex2_ftz(x.y);
         }
         if ((j + 1) * 128 > lim_all) {
-          const int x = lim - j * 128 - half * 64;
 #pragma unroll
-          for (int e = 0; e < 64; ++e) pr[e] = e < x ? pr[e] : 0.0f;
+          for (int q = 0; q < 64; q += 32) {
+            const int x = lim - j * 128 - half * 64 - q;  // columns that are seen
+            const uint32_t bits = x >= 32 ? 0xFFFFFFFFu : (x <= 0 ? 0u : (1u << x) - 1u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pr[q + e] = (bits >> e & 1u) ? pr[q + e] : 0.0f;
+          }
         }
         if (!(ok = mbar_wait(B.dp_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
-        const uint32_t td = tl + 256 + half * 64;
+        const uint32_t td = tl + 128 + half * 64;
         tmem_ld32(td, v);
         tmem_ld32(td + 32, v + 32);
         tmem_ld_wait32(v);
         tmem_ld_wait32(v + 32);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.dp_read);
         uint32_t w[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           w[e] = pack_bf16x2(pr[2 * e] * (__uint_as_float(v[2 * e]) - delta),
                              pr[2 * e + 1] * (__uint_as_float(v[2 * e + 1]) - delta));
-        tmem_st32(td, w);
+        if (!(ok = mbar_wait(B.ds_empty, (tiles & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
+        tc_fence_after();
+        tmem_st32(tl + 256 + half * 32, w);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(B.ds_full);
       }
       if (!ok) break;
-      if (nk > 0) {
+      // the search for the next unit runs while the last product does
+      const int rows = min(p.tpt, s.lq - tok0) * p.gp, t0 = s.q0 + tok0, head = h0;
+      more = next_unit(unit_of(++turn));
+      if (n > 0) {
         if (!(ok = mbar_wait(B.acc_full, uses & 1u, kAttnWaitNs, abort_flag))) break;
         ++uses;
         tc_fence_after();
@@ -415,9 +502,9 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         uint32_t o[16];
-        const bool have = nk > 0 && h * 16 < cols;
+        const bool have = n > 0 && h * 16 < cols;
         if (have) {
-          tmem_ld16(tl + 384 + b + 16 * h, o);
+          tmem_ld16(tl + 320 + b + 16 * h, o);
           tmem_ld_wait16(o);
         }
 #pragma unroll
@@ -426,10 +513,10 @@ __global__ void __launch_bounds__(384, 1)
                                                        __uint_as_float(o[2 * e + 1]) * p.scale)
                                          : 0u;
       }
-      if (PACT_IN(s.q0 + tok0 < p.tq))
-        store_rows64(w, lane, quarter * 32, min(p.tpt, s.lq - tok0) * p.gp, min(cols, 64),
-                     p.dq + (int64_t)(s.q0 + tok0) * p.lddq + (int64_t)h0 * p.D + b, p.lddq, p.D,
-                     p.gp, p.gp_mul);
+      if (PACT_IN(t0 < p.tq))
+        store_rows64(w, lane, quarter * 32, rows, min(cols, 64),
+                     p.dq + (int64_t)t0 * p.lddq + (int64_t)head * p.D + b, p.lddq, p.D, p.gp,
+                     p.gp_mul);
     }
     if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
   }
@@ -463,8 +550,13 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(B.fix_empty, 2);  // the issuers
     mbar_init(B.s_full, 1);
     mbar_init(B.dp_full, 1);
-    mbar_init(B.p_full, 8);  // the computing warps
+    mbar_init(B.s_read, 8);  // the computing warps
+    mbar_init(B.dp_read, 8);
+    mbar_init(B.p_full, 8);
+    mbar_init(B.p_full + 8, 8);
     mbar_init(B.ds_full, 8);
+    mbar_init(B.p_empty, 1);
+    mbar_init(B.ds_empty, 1);
     mbar_init(B.acc_full, 2);
     mbar_init(B.tail, 1);
     for (int i = 0; i < 2; ++i) {
@@ -570,8 +662,11 @@ __global__ void __launch_bounds__(384, 1)
       const bool lead = elected();
       const uint64_t dfix = desc_k(base + issuer * C::TILE);
       const uint64_t dk0 = desc_k(base + C::RING_OFF), dn0 = desc_n(base + C::RING_OFF);
-      const uint32_t sum = tmem + 256 + issuer * 128, prod = tmem + issuer * 128;
-      const uint32_t in_full = issuer ? B.ds_full : B.p_full;
+      constexpr bool OWN = C::OWN_P;
+      const uint32_t sum = tmem + C::SUM_COL + issuer * C::SUM_STEP, prod = tmem + issuer * 128;
+      const uint32_t in_col = OWN ? tmem + 256 + issuer * 64 : prod;
+      const uint32_t read = issuer ? B.dp_read : B.s_read;
+      const uint32_t in_empty = issuer ? B.ds_empty : B.p_empty;
       const uint32_t out_full = issuer ? B.dp_full : B.s_full;
       auto wait = [&](uint32_t bar, uint32_t par) {
         return mbar_wait(bar, par, kAttnWaitNs, abort_flag);
@@ -587,23 +682,44 @@ __global__ void __launch_bounds__(384, 1)
           x.advance(C::STAGES, issuer);
           // one or two places back, which is a turn of the parity further on
           r.advance(C::STAGES, C::STAGES - 2 + (issuer ? 0 : 1));
-          if (i > 0) {
-            if (!(ok = wait(B.full + 8 * r.stage, r.phase ^ 1u) && wait(in_full, tiles & 1u))) break;
-            ++tiles;
-            tc_fence_after();
-            if (lead) {
-              const uint64_t d = dn0 + (uint64_t)(r.stage * (C::TILE >> 4));
+          // P comes in two parts, steps 0 1 4 5 and 2 3 6 7: the first one's product runs
+          // while the second is computed.  dS, which has time, comes whole.
+          auto issue_sum = [&]() {
+            if (!(ok = wait(B.full + 8 * r.stage, r.phase ^ 1u))) return;
+            // with P it is the next S that the computing warps wait for: what it needs first
+            if (!OWN && !issuer && i < n && !(ok = wait(B.full + 8 * x.stage, x.phase))) return;
+            const uint64_t d = dn0 + (uint64_t)(r.stage * (C::TILE >> 4));
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_bf16_ta(sum, prod + half_step(k), step_n(d, k), idesc_d,
-                            (i > 1 || k > 0) ? 1u : 0u);
+            for (int part = 0; part < 2; ++part) {
+              if (part == 0 || !issuer) {
+                if (!(ok = wait(issuer ? B.ds_full : B.p_full + 8 * part, (tiles + i - 1) & 1u))) return;
+                tc_fence_after();
+              }
+              if (lead) {
+#pragma unroll
+                for (int k = 2 * part; k < 2 * part + 6; k += (k & 1) ? 3 : 1)
+                  mma_bf16_ta(sum, in_col + half_step<OWN>(k), step_n(d, k), idesc_d,
+                              (i > 1 || k > 0) ? 1u : 0u);
+              }
+              __syncwarp();
+            }
+          };
+          auto sum_issued = [&]() {
+            if (lead) {
+              if (OWN) mma_commit(in_empty);
               mma_commit(B.empty + 8 * r.stage);
               if (i == n) mma_commit(B.acc_full);
             }
             __syncwarp();
+          };
+          if (!OWN && i > 0) {
+            issue_sum();
+            if (!ok) break;
+            if (issuer || i == n) sum_issued();
           }
           if (i < n) {
-            if (!(ok = wait(B.full + 8 * x.stage, x.phase))) break;
+            if ((OWN || issuer || i == 0) && !(ok = wait(B.full + 8 * x.stage, x.phase))) break;
+            if (OWN && !(ok = wait(read, ((tiles + i) & 1u) ^ 1u))) break;
             tc_fence_after();
             if (lead) {
               const uint64_t d = dk0 + (uint64_t)(x.stage * (C::TILE >> 4));
@@ -615,9 +731,16 @@ __global__ void __launch_bounds__(384, 1)
               if (i + 1 == n) mma_commit(B.fix_empty);
             }
             __syncwarp();
+            if (!OWN && !issuer && i > 0) sum_issued();
+          }
+          if (OWN && i > 0) {
+            issue_sum();
+            if (!ok) break;
+            sum_issued();
           }
           if (i < n) at.advance(C::STAGES, 2);
         }
+        tiles += n;
       }
       if (lead) {
         if (!ok) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_MMA);
@@ -635,27 +758,11 @@ __global__ void __launch_bounds__(384, 1)
           tile_of(i, h0, tok0);
           const uint32_t buf = tiles & 1u;
           float nl[4], de[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int x = k * 32 + lane, rt = row_token(p, x), tok = tok0 + rt;
-            nl[k] = -INFINITY;  // rows of no query: P = 0
-            de[k] = 0.0f;
-            if (x < p.tpt * p.gp && tok < s.lq) {
-              const int64_t at = (int64_t)(h0 + x - rt * p.gp) * p.tq + s.q0 + tok;
-              nl[k] = -p.lse_in[at] * kLog2e;
-              de[k] = p.delta[at];
-            }
-          }
+          load_stats(p, s, h0, tok0, -INFINITY, lane, nl, de);  // rows of no query: P = 0
           if (!(ok = mbar_wait(B.stat_empty + 8 * buf, ((tiles >> 1) & 1u) ^ 1u, kAttnWaitNs,
                                abort_flag)))
             break;
-          float* st = reinterpret_cast<float*>(smem + C::STAT_OFF + buf * 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            st[k * 32 + lane] = nl[k];
-            st[128 + k * 32 + lane] = de[k];
-          }
-          __syncwarp();
+          store_stats(reinterpret_cast<float*>(smem + C::STAT_OFF + buf * 1024), lane, nl, de);
           if (lane == 0) mbar_arrive(B.stat_full + 8 * buf);
         }
       }
@@ -666,7 +773,8 @@ __global__ void __launch_bounds__(384, 1)
     setmaxnreg_inc<216>();
     const int half = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tl = tmem + lanes + half * 64, tp = tmem + lanes + 256 + half * 32;
     const float c = p.c;
     uint32_t tiles = 0, uses = 0;
     bool ok = true;
@@ -686,36 +794,56 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld32(tl + 32, v + 32);
         tmem_ld_wait32(v);
         tmem_ld_wait32(v + 32);
-        float pr[64];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 nl = *reinterpret_cast<const float4*>(st + 4 * e);
-          const float2 a = __ffma2_rn(
-              make_float2(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])),
-              make_float2(c, c), make_float2(nl.x, nl.y));
-          const float2 b = __ffma2_rn(
-              make_float2(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])),
-              make_float2(c, c), make_float2(nl.z, nl.w));
-          pr[4 * e] = ex2_ftz(a.x);
-          pr[4 * e + 1] = ex2_ftz(a.y);
-          pr[4 * e + 2] = ex2_ftz(b.x);
-          pr[4 * e + 3] = ex2_ftz(b.y);
+        if (C::OWN_P) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(B.s_read);
         }
+        // the first column whose token sees this key
+        int x = 0;
         if (p.causal && key0 + 127 - (s.lk - s.lq) > tok0) {
-          // the first column whose token sees this key
           const int64_t x0 = (int64_t)(key - (s.lk - s.lq) - tok0) * p.gp - half * 64;
-          const int x = (int)(x0 > 64 ? 64 : (x0 < 0 ? 0 : x0));
-#pragma unroll
-          for (int e = 0; e < 64; ++e) pr[e] = e >= x ? pr[e] : 0.0f;
+          x = (int)(x0 > 64 ? 64 : (x0 < 0 ? 0 : x0));
         }
+        const bool masked = __any_sync(0xFFFFFFFFu, x > 0);
+        if (C::OWN_P) {
+          if (!(ok = mbar_wait(B.p_empty, (tiles & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
+          tc_fence_after();
+        }
+        float pr[64];
         uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
-        tmem_st32(tl, w);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(B.p_full);
+        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+          for (int e = 8 * part; e < 8 * part + 8; ++e) {
+            const float4 nl = *reinterpret_cast<const float4*>(st + 4 * e);
+            const float2 a = __ffma2_rn(
+                make_float2(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])),
+                make_float2(c, c), make_float2(nl.x, nl.y));
+            const float2 b = __ffma2_rn(
+                make_float2(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])),
+                make_float2(c, c), make_float2(nl.z, nl.w));
+            pr[4 * e] = ex2_ftz(a.x);
+            pr[4 * e + 1] = ex2_ftz(a.y);
+            pr[4 * e + 2] = ex2_ftz(b.x);
+            pr[4 * e + 3] = ex2_ftz(b.y);
+          }
+          if (masked) {
+            const int n0 = x - 32 * part;  // columns that do not see this key
+            const uint32_t bits = n0 >= 32 ? 0u : (n0 <= 0 ? 0xFFFFFFFFu : 0xFFFFFFFFu << n0);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              pr[32 * part + e] = (bits >> e & 1u) ? pr[32 * part + e] : 0.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(pr[32 * part + 2 * e], pr[32 * part + 2 * e + 1]);
+          tmem_st16((C::OWN_P ? tp : tl) + 16 * part, w);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(B.p_full + 8 * part);
+        }
 
         if (!(ok = mbar_wait(B.dp_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
@@ -723,6 +851,11 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld32(tl + 160, v + 32);
         tmem_ld_wait32(v);
         tmem_ld_wait32(v + 32);
+        if (C::OWN_P) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(B.dp_read);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float4 de = *reinterpret_cast<const float4*>(st + 128 + 4 * e);
@@ -731,7 +864,11 @@ __global__ void __launch_bounds__(384, 1)
           w[2 * e + 1] = pack_bf16x2(pr[4 * e + 2] * (__uint_as_float(v[4 * e + 2]) - de.z),
                                      pr[4 * e + 3] * (__uint_as_float(v[4 * e + 3]) - de.w));
         }
-        tmem_st32(tl + 128, w);
+        if (C::OWN_P) {
+          if (!(ok = mbar_wait(B.ds_empty, (tiles & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
+          tc_fence_after();
+        }
+        tmem_st32(C::OWN_P ? tp + 64 : tl + 128, w);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -747,7 +884,7 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
       }
       // one warpgroup stores dv, the other dk
-      const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (half ? 384 : 256);
+      const uint32_t ta = tmem + lanes + C::SUM_COL + half * C::SUM_STEP;
       uint16_t* out = half ? p.dk : p.dv;
       const int64_t ld = half ? p.lddk : p.lddv;
       const float f = half ? p.scale : 1.0f;
