@@ -434,18 +434,28 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(B.stat_empty + 8 * buf);
       }
-      for (int j = 0; j < n; ++j, ++tiles) {
-        if (!(ok = mbar_wait(B.s_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
+      // S of the next tile is loaded while dS is stored
+      uint32_t v[64];
+      const uint32_t ts = tl + half * 64, td = tl + 128 + half * 64;
+      auto load_s = [&](uint32_t tile) {
+        if (!mbar_wait(B.s_full, tile & 1u, kAttnWaitNs, abort_flag)) return false;
         tc_fence_after();
-        uint32_t v[64];
-        const uint32_t ts = tl + half * 64;
         tmem_ld32(ts, v);
         tmem_ld32(ts + 32, v + 32);
+        return true;
+      };
+      auto s_loaded = [&]() {
         tmem_ld_wait32(v);
         tmem_ld_wait32(v + 32);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(B.s_read);
+      };
+      if (n > 0) {
+        if (!(ok = load_s(tiles))) break;
+        s_loaded();
+      }
+      for (int j = 0; j < n; ++j, ++tiles) {
         float pr[64];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -466,7 +476,6 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (!(ok = mbar_wait(B.dp_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
-        const uint32_t td = tl + 128 + half * 64;
         tmem_ld32(td, v);
         tmem_ld32(td + 32, v + 32);
         tmem_ld_wait32(v);
@@ -482,10 +491,12 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = mbar_wait(B.ds_empty, (tiles & 1u) ^ 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
         tmem_st32(tl + 256 + half * 32, w);
+        if (j + 1 < n && !(ok = load_s(tiles + 1))) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(B.ds_full);
+        if (j + 1 < n) s_loaded();
       }
       if (!ok) break;
       // the search for the next unit runs while the last product does
@@ -780,24 +791,38 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
       const int key = key0 + row;
-      for (int i = 0; i < n; ++i, ++tiles) {
-        int h0, tok0;
-        tile_of(i, h0, tok0);
-        const uint32_t buf = tiles & 1u;
-        const float* st = reinterpret_cast<const float*>(smem + C::STAT_OFF + buf * 1024) + half * 64;
-        if (!(ok = mbar_wait(B.stat_full + 8 * buf, (tiles >> 1) & 1u, kAttnWaitNs, abort_flag) &&
-                   mbar_wait(B.s_full, tiles & 1u, kAttnWaitNs, abort_flag)))
-          break;
+      // OWN_P: S of the next tile is there early, and is loaded while dS is stored
+      uint32_t v[64];
+      auto load_s = [&](uint32_t tile) {
+        if (!mbar_wait(B.stat_full + 8 * (tile & 1u), (tile >> 1) & 1u, kAttnWaitNs, abort_flag) ||
+            !mbar_wait(B.s_full, tile & 1u, kAttnWaitNs, abort_flag))
+          return false;
         tc_fence_after();
-        uint32_t v[64];
         tmem_ld32(tl, v);
         tmem_ld32(tl + 32, v + 32);
+        return true;
+      };
+      auto s_loaded = [&]() {
         tmem_ld_wait32(v);
         tmem_ld_wait32(v + 32);
         if (C::OWN_P) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(B.s_read);
+        }
+      };
+      if (C::OWN_P && n > 0) {
+        if (!(ok = load_s(tiles))) break;
+        s_loaded();
+      }
+      for (int i = 0; i < n; ++i, ++tiles) {
+        int h0, tok0;
+        tile_of(i, h0, tok0);
+        const uint32_t buf = tiles & 1u;
+        const float* st = reinterpret_cast<const float*>(smem + C::STAT_OFF + buf * 1024) + half * 64;
+        if (!C::OWN_P) {
+          if (!(ok = load_s(tiles))) break;
+          s_loaded();
         }
         // the first column whose token sees this key
         int x = 0;
@@ -839,10 +864,14 @@ __global__ void __launch_bounds__(384, 1)
           for (int e = 0; e < 16; ++e)
             w[e] = pack_bf16x2(pr[32 * part + 2 * e], pr[32 * part + 2 * e + 1]);
           tmem_st16((C::OWN_P ? tp : tl) + 16 * part, w);
+          if (C::OWN_P && part == 0) continue;  // nobody waits for the first part alone
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(B.p_full + 8 * part);
+          if (lane == 0) {
+            if (C::OWN_P) mbar_arrive(B.p_full);
+            mbar_arrive(B.p_full + 8 * part);
+          }
         }
 
         if (!(ok = mbar_wait(B.dp_full, tiles & 1u, kAttnWaitNs, abort_flag))) break;
@@ -869,6 +898,7 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_after();
         }
         tmem_st32(C::OWN_P ? tp + 64 : tl + 128, w);
+        if (C::OWN_P && i + 1 < n && !(ok = load_s(tiles + 1))) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -876,6 +906,7 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive(B.ds_full);
           mbar_arrive(B.stat_empty + 8 * buf);
         }
+        if (C::OWN_P && i + 1 < n) s_loaded();
       }
       if (!ok) break;
       if (n > 0) {
