@@ -4,8 +4,10 @@
 flow) and Table 7 (precision allocation): RMSNorm -> NVFP4 feeds the q/k/v
 projections, the attention output feeds o, a residual add, RMSNorm -> NVFP4 feeds
 the fused gate/up projection, SiLU-multiply -> NVFP4 feeds down, and a second
-residual add.  Attention and its backward are out of scope: the attention output
-and the gradients flowing back into q/k/v are given tensors.
+residual add.  In DecoderProjectionStack the attention output and the gradients
+flowing back into q/k/v are given tensors; DecoderLayer has the attention between them:
+norms of queries and keys with the rotary embedding, attention over packed sequences, and
+their backward passes.
 
 Every operation here is a libpact call; this module only owns buffers and the
 order of calls.  Buffers are allocated once, so one step can be captured in a
@@ -16,7 +18,9 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (FP8, NVFP4, pact_linear_fp8_dgrad, pact_linear_fp8_fwd, pact_lora_linear_dgrad,
+from . import (FP8, NVFP4, GradList, pact_attention_bwd, pact_attention_fwd, pact_clip_grad_norm,
+               pact_linear_fp8_dgrad, pact_linear_fp8_fwd, pact_lora_linear_dgrad,
+               pact_qk_norm_rope, pact_qk_norm_rope_bwd, pact_rope_turns,
                pact_lora_linear_dgrad_q, pact_lora_linear_fwd,
                pact_lora_linear_fwd_gate_up, pact_pack_weight_bwd, pact_pack_weight_fwd_gate_up,
                pact_lora_adapter_grad, pact_pack_weight_fp8_bwd, pact_pack_weight_fp8_fwd,
@@ -157,7 +161,7 @@ class DecoderProjectionStack:
         if side is not None:
             side.wait_stream(main)
             with torch.cuda.stream(side):
-                # attention core (out of scope): its output is the given tensor attn
+                # the attention core's output is the given tensor attn
                 pact_quant_nvfp4(attn, out=self.attnq)
                 p["o"].forward(self.attnq, self.h1, residual=x)
         pact_rmsnorm_quant(x, self.gamma1, self.eps, out=self.xq1, rstd=self.rstd1)
@@ -178,6 +182,10 @@ class DecoderProjectionStack:
             p["o"].forward(self.attnq, self.h1, residual=x)
         else:
             main.wait_stream(side)
+        return self._mlp_forward()
+
+    def _mlp_forward(self) -> torch.Tensor:
+        p = self.p
         pact_rmsnorm_quant(self.h1, self.gamma2, self.eps, out=self.xq2, rstd=self.rstd2)
         # the gate|up GEMM's epilogue yields the three amaxes: one pass of SiLU-multiply
         p["gate_up"].forward_gate_up(self.xq2, self.gu, self.gu_amax3)
@@ -198,8 +206,7 @@ class DecoderProjectionStack:
 
     def backward(self, dy, dq, dk, dv) -> torch.Tensor:
         """dy: gradient of the layer output; dq, dk, dv: the gradients flowing back
-        from the (out of scope) attention core into the q, k, v outputs."""
-        p = self.p
+        from the attention core into the q, k, v outputs."""
         main, side = torch.cuda.current_stream(), self._side()
         # every input gradient quantises its dY in the same pass that forms the
         # LoRA down-projection (pact_lora_linear_dgrad_q).  The q, k and v input
@@ -210,18 +217,23 @@ class DecoderProjectionStack:
             side.wait_stream(main)
             with torch.cuda.stream(side):
                 self._qkv_dgrad(dq, dk, dv)
-        p["down"].dgrad_q(dy, self.dyq, self.dh)
-        pact_silu_mul_bwd(self.gq, self.uq, self.dh, dgateup=self.dgu, out_amax=self.dgu_amax)
-        p["gate_up"].dgrad_q(self.dgu, self.dguq, self.dxn2, amax=self.dgu_amax)
-        pact_rmsnorm_bwd(self.xq2, self.gamma2, self.rstd2, self.dxn2, dres=dy, dx=self.dh1,
-                         out_amax=self.dh1_amax)
-        p["o"].dgrad_q(self.dh1, self.dh1q, self.dattn, amax=self.dh1_amax)  # into attention
+        self._mlp_backward(dy)
         if side is None:
             self._qkv_dgrad(dq, dk, dv)
         else:
             main.wait_stream(side)
         pact_rmsnorm_bwd(self.xq1, self.gamma1, self.rstd1, self.dxn1, dres=self.dh1, dx=self.dx)
         return self.dx
+
+    def _mlp_backward(self, dy):
+        """From the layer output's gradient back into the attention output (dattn)."""
+        p = self.p
+        p["down"].dgrad_q(dy, self.dyq, self.dh)
+        pact_silu_mul_bwd(self.gq, self.uq, self.dh, dgateup=self.dgu, out_amax=self.dgu_amax)
+        p["gate_up"].dgrad_q(self.dgu, self.dguq, self.dxn2, amax=self.dgu_amax)
+        pact_rmsnorm_bwd(self.xq2, self.gamma2, self.rstd2, self.dxn2, dres=dy, dx=self.dh1,
+                         out_amax=self.dh1_amax)
+        p["o"].dgrad_q(self.dh1, self.dh1q, self.dattn, amax=self.dh1_amax)  # into attention
 
     def _qkv_dgrad(self, dq, dk, dv):
         p = self.p
@@ -249,3 +261,112 @@ class DecoderProjectionStack:
         """2*M*N*K over the 12 frozen-projection GEMMs of one forward + dgrad pass (six
         projections, q, k, v, o, gate|up and down, each forward and input gradient)."""
         return 2.0 * sum(l.gemm_flops(self.m) for l in self.p.values())
+
+
+class DecoderLayer(DecoderProjectionStack):
+    """A whole decoder layer over packed sequences: the projection stack with the attention
+    between q, k, v and o, forward, backward and adapter gradients.
+
+    heads and kv_heads of q.d_out / heads columns; inv_freq: the rotary embedding's
+    frequencies (float64, radians per position); gamma_q, gamma_k: norms of the queries'
+    and keys' heads (BF16, both or neither).  The sequences are given at each call: cu
+    (int32 offsets of the packed rows) and positions (int32, of each row)."""
+
+    def __init__(self, m: int, proj: dict, gamma1, gamma2, heads: int, kv_heads: int,
+                 inv_freq: torch.Tensor, eps: float = 1e-5, gamma_q=None, gamma_k=None,
+                 concurrent: bool = True):
+        super().__init__(m, proj, gamma1, gamma2, eps, concurrent)
+        if proj["q"].d_out % heads or proj["k"].d_out * heads != proj["q"].d_out * kv_heads:
+            raise ValueError("q and k must hold whole heads of the same width")
+        d = proj["q"].d_out // heads
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, d
+        self.turns = pact_rope_turns(inv_freq)
+        self.gamma_q, self.gamma_k = gamma_q, gamma_k
+        dev = gamma1.device
+        bf = dict(dtype=torch.bfloat16, device=dev)
+
+        def split(t, n):
+            return t.view(m, n, d)
+
+        # heads of the projections' outputs, and of what lies between them
+        self.qh, self.kh, self.vh = split(self.q, heads), split(self.k, kv_heads), split(self.v, kv_heads)
+        self.qr, self.kr = torch.empty(m, heads, d, **bf), torch.empty(m, kv_heads, d, **bf)
+        self.attn = torch.empty(m, heads, d, **bf)
+        self.lse = torch.empty(heads, m, dtype=torch.float32, device=dev)
+        # the gradients of the rotated heads, turned back in place
+        self.dq, self.dk, self.dv = (torch.empty_like(t) for t in (self.q, self.k, self.v))
+        self.dgamma_q = self.dgamma_k = None
+        if gamma_q is not None:
+            self.dgamma_q, self.dgamma_k = (torch.empty(d, dtype=torch.float32, device=dev)
+                                            for _ in range(2))
+        # the adapters' gradients, and the list that their norm is taken over
+        self.grads = {n: tuple(torch.empty(t.shape, dtype=torch.float32, device=dev)
+                               for t in (l.A, l.B)) for n, l in proj.items()}
+        listed = [t for t in (self.dgamma_q, self.dgamma_k) if t is not None]
+        for n, (dA, dB) in self.grads.items():
+            listed.append(dA)
+            if proj[n].gate_up:  # of the fused B the diagonal blocks alone are parameters
+                r, w = dB.shape
+                listed += [dB[i, :w // 2] if i < r // 2 else dB[i, w // 2:] for i in range(r)]
+            else:
+                listed.append(dB)
+        self.grad_list = GradList(listed)
+
+    def forward(self, x: torch.Tensor, cu: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
+        p = self.p
+        main, side = torch.cuda.current_stream(), self._side()
+        pact_rmsnorm_quant(x, self.gamma1, self.eps, out=self.xq1, rstd=self.rstd1)
+        if side is not None:  # q, k and v all read xq1 only: run them side by side
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                p["k"].forward(self.xq1, self.k)
+                p["v"].forward(self.xq1, self.v)
+        p["q"].forward(self.xq1, self.q)
+        if side is None:
+            p["k"].forward(self.xq1, self.k)
+            p["v"].forward(self.xq1, self.v)
+        else:
+            main.wait_stream(side)
+        pact_qk_norm_rope(self.qh, self.kh, positions, self.turns, self.gamma_q, self.gamma_k,
+                          self.eps, q_out=self.qr, k_out=self.kr)
+        pact_attention_fwd(self.qr, self.kr, self.vh, cu, cu, o=self.attn, lse=self.lse)
+        pact_quant_nvfp4(self.attn.view(self.m, -1), out=self.attnq)
+        p["o"].forward(self.attnq, self.h1, residual=x)
+        return self._mlp_forward()
+
+    def backward(self, dy: torch.Tensor, cu: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
+        """The gradient of x; dq, dk, dv (of the projections' outputs) and the gradients of
+        gamma_q and gamma_k are left in their buffers."""
+        self._mlp_backward(dy)
+        dq, dk, dv = (self.dq.view_as(self.qh), self.dk.view_as(self.kh), self.dv.view_as(self.vh))
+        pact_attention_bwd(self.dattn.view_as(self.attn), self.qr, self.kr, self.vh, self.attn, self.lse,
+                           cu, cu, dq=dq, dk=dk, dv=dv)
+        own = self.gamma_q is not None
+        pact_qk_norm_rope_bwd(dq, dk, positions, self.turns, self.qh if own else None,
+                              self.kh if own else None, self.gamma_q, self.gamma_k, self.eps, dq=dq,
+                              dk=dk, dgamma_q=self.dgamma_q, dgamma_k=self.dgamma_k)
+        self._qkv_dgrad(self.dq, self.dk, self.dv)
+        pact_rmsnorm_bwd(self.xq1, self.gamma1, self.rstd1, self.dxn1, dres=self.dh1, dx=self.dx)
+        return self.dx
+
+    def adapter_grads(self, dy) -> dict:
+        """dA, dB of all adapters into the layer's own buffers (call after backward)."""
+        pairs = {"q": (self.xq1, self.dq), "k": (self.xq1, self.dk), "v": (self.xq1, self.dv),
+                 "o": (self.attnq, self.dh1),
+                 "gate_up": (self.xq2, self.dgu), "down": (self.hq, dy)}
+        for name, (xq, g) in pairs.items():
+            self.p[name].adapter_grad(xq, g, *self.grads[name])
+        return self.grads
+
+    def clip_grads(self, max_norm: float, norm: torch.Tensor = None) -> torch.Tensor:
+        """Clip the adapters' gradients (and those of gamma_q and gamma_k) by their norm
+        together; returns it."""
+        return pact_clip_grad_norm(self.grad_list, max_norm, norm=norm)
+
+    @classmethod
+    def from_workload(cls, d: dict, device, heads: int, kv_heads: int, inv_freq, gamma_q=None,
+                      gamma_k=None) -> "DecoderLayer":
+        """As DecoderProjectionStack.from_workload, with the attention's parameters."""
+        base = DecoderProjectionStack.from_workload(d, device)
+        return cls(base.m, base.p, base.gamma1, base.gamma2, heads, kv_heads, inv_freq.to(device),
+                   base.eps, gamma_q, gamma_k)
