@@ -712,23 +712,47 @@ def pact_add_rmsnorm_bwd(h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tenso
 
 
 # ------------------------------------------------------------------ heads and attention
-def _need_heads(t, name, dev, like=None) -> _HeadsStruct:
-    """t is a BF16 tensor of heads [T, heads, D] on the current device, of this shape when
-    given, whose tokens lie ld values apart and whose heads are contiguous; its struct."""
+def _heads(t, name, dev, like=None) -> tuple:
+    """The fields of pact_heads for t: a BF16 tensor of heads [T, heads, D] on the current
+    device, of this shape when given, whose tokens lie ld values apart and whose heads are
+    contiguous."""
+    try:
+        rows, heads, d = shape = t.shape
+        ld, sh, sd = t.stride()
+        if (t.dtype is torch.bfloat16 and t.get_device() == dev and sd == 1 and sh == d
+                and (like is None or shape == like)):
+            # the stride of a single row says nothing: torch may report any number there
+            return t.data_ptr(), rows, heads, ld if rows > 1 else heads * d
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a 3-D CUDA tensor [tokens, heads, D]")
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    rows, heads, d = shape = t.shape
     if like is not None and shape != like:
         raise ValueError(f"{name} must have shape {list(like)}, got {list(shape)}")
-    ld, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and heads > 1):
         raise ValueError(f"the heads of {name} must be contiguous")
-    # the stride of a single row says nothing: torch may report any number there
-    return _HeadsStruct(t.data_ptr(), rows, heads, ld if rows > 1 else heads * d)
+    return t.data_ptr(), rows, heads, ld if rows > 1 else heads * d
+
+
+# Several pact_heads at once: one array of their fields, whose addresses are passed.  A
+# structure for each costs twice as much, which a call on one token would notice.
+_HEADS = {n: _i64 * (4 * n) for n in (4, 6, 8)}
+_FAST = {}
+
+
+def _heads_call(lib, name):
+    """The library's function with plain addresses for its pact_heads."""
+    fn = _FAST.get(name)
+    if fn is None:
+        fn = lib[name]  # an object of its own, beside the attribute of that name
+        res, args = _SIGNATURES[name]
+        fn.restype, fn.argtypes = res, [_vp if a is _SPH else a for a in args]
+        _FAST[name] = fn
+    return fn
 
 
 def pact_rope_turns(inv_freq: torch.Tensor, turns: torch.Tensor | None = None) -> torch.Tensor:
@@ -766,7 +790,7 @@ def pact_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     input.  Returns (q_out, k_out)."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
-    sq, sk = _need_heads(q, "q", dev), _need_heads(k, "k", dev)
+    hq, hk = _heads(q, "q", dev), _heads(k, "k", dev)
     T, _, D = q.shape
     if k.shape[2] != D:
         raise ValueError(f"q has heads of {D}, k of {k.shape[2]}")
@@ -775,10 +799,11 @@ def pact_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
         q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-    so, sp = _need_heads(q_out, "q_out", dev, q.shape), _need_heads(k_out, "k_out", dev, k.shape)
-    _check(lib.pact_qk_norm_rope(sq, sk, D, rot, _addr(positions), _addr(turns),
-                                 int(bool(interleaved)), _addr(gamma_q), _addr(gamma_k), float(eps),
-                                 so, sp, _raw_stream(dev)))
+    h = _HEADS[4](*hq, *hk, *_heads(q_out, "q_out", dev, q.shape), *_heads(k_out, "k_out", dev, k.shape))
+    at = ctypes.addressof(h)
+    _check(_heads_call(lib, "pact_qk_norm_rope")(
+        at, at + 32, D, rot, positions.data_ptr(), turns.data_ptr(), 1 if interleaved else 0,
+        _addr(gamma_q), _addr(gamma_k), float(eps), at + 64, at + 96, _raw_stream(dev)))
     return q_out, k_out
 
 
@@ -795,18 +820,20 @@ def pact_qk_norm_rope_bwd(dyq: torch.Tensor, dyk: torch.Tensor, positions: torch
     new ones, None to leave both out.  Returns (dq, dk, dgamma_q, dgamma_k)."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
-    sq, sk = _need_heads(dyq, "dyq", dev), _need_heads(dyk, "dyk", dev)
+    sq, sk = _heads(dyq, "dyq", dev), _heads(dyk, "dyk", dev)
     T, hq, D = dyq.shape
     if dyk.shape[2] != D:
         raise ValueError(f"dyq has heads of {D}, dyk of {dyk.shape[2]}")
     rot = _need_rope(positions, turns, gamma_q, gamma_k, T, D, dev)
-    xq = _need_heads(q, "q", dev, dyq.shape) if q is not None else None
-    xk = _need_heads(k, "k", dev, dyk.shape) if k is not None else None
+    none = (0, 0, 0, 0)
+    xq = _heads(q, "q", dev, dyq.shape) if q is not None else none
+    xk = _heads(k, "k", dev, dyk.shape) if k is not None else none
     if dq is None:
         dq = torch.empty(dyq.shape, dtype=torch.bfloat16, device=dyq.device)
     if dk is None:
         dk = torch.empty(dyk.shape, dtype=torch.bfloat16, device=dyq.device)
-    so, sp = _need_heads(dq, "dq", dev, dyq.shape), _need_heads(dk, "dk", dev, dyk.shape)
+    h = _HEADS[6](*sq, *sk, *xq, *xk, *_heads(dq, "dq", dev, dyq.shape), *_heads(dk, "dk", dev, dyk.shape))
+    at = ctypes.addressof(h)
     grads = []
     for g, name in ((dgamma_q, "dgamma_q"), (dgamma_k, "dgamma_k")):
         if g is True:
@@ -821,16 +848,17 @@ def pact_qk_norm_rope_bwd(dyq: torch.Tensor, dyk: torch.Tensor, positions: torch
         # its own scratch in every call: a captured graph then keeps one of its own
         ws = torch.empty((lib.pact_qk_norm_rope_bwd_workspace_size(T, hq, dyk.shape[1], D),),
                          dtype=torch.uint8, device=dyq.device)
-    _check(lib.pact_qk_norm_rope_bwd(sq, sk, xq, xk, D, rot, _addr(positions), _addr(turns),
-                                     int(bool(interleaved)), _addr(gamma_q), _addr(gamma_k),
-                                     float(eps), so, sp, _addr(grads[0]), _addr(grads[1]), _addr(ws),
-                                     0 if ws is None else ws.numel(), _raw_stream(dev)))
+    _check(_heads_call(lib, "pact_qk_norm_rope_bwd")(
+        at, at + 32, at + 64 if q is not None else None, at + 96 if k is not None else None, D, rot,
+        positions.data_ptr(), turns.data_ptr(), 1 if interleaved else 0, _addr(gamma_q),
+        _addr(gamma_k), float(eps), at + 128, at + 160, _addr(grads[0]), _addr(grads[1]), _addr(ws),
+        0 if ws is None else ws.numel(), _raw_stream(dev)))
     return dq, dk, grads[0], grads[1]
 
 
 def _need_attention(q, k, v, cu_q, cu_k, scale, dev):
-    sq, sk = _need_heads(q, "q", dev), _need_heads(k, "k", dev)
-    sv = _need_heads(v, "v", dev, k.shape)
+    """The fields of q, k and v, the heads' width, the number of sequences and the scale."""
+    fields = _heads(q, "q", dev) + _heads(k, "k", dev) + _heads(v, "v", dev, k.shape)
     D = q.shape[2]
     if k.shape[2] != D:
         raise ValueError(f"q has heads of {D}, k of {k.shape[2]}")
@@ -838,7 +866,7 @@ def _need_attention(q, k, v, cu_q, cu_k, scale, dev):
         raise ValueError("cu_q must be a 1-D tensor of at least two offsets")
     _need(cu_q, torch.int32, cu_q.shape, "cu_q", dev)
     _need(cu_k, torch.int32, cu_q.shape, "cu_k", dev)
-    return sq, sk, sv, D, cu_q.shape[0] - 1, float(D ** -0.5 if scale is None else scale)
+    return fields, D, cu_q.shape[0] - 1, float(D ** -0.5 if scale is None else scale)
 
 
 def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -850,15 +878,18 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: 
     sequence are left as they were."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
-    sq, sk, sv, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
+    fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
     if o is None:
         o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    so = _need_heads(o, "o", dev, q.shape)
+    h = _HEADS[4](*fields, *_heads(o, "o", dev, q.shape))
+    at = ctypes.addressof(h)
+    shape = (q.shape[1], q.shape[0])
     if lse is None:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    _need(lse, torch.float32, (q.shape[1], q.shape[0]), "lse", dev)
-    _check(lib.pact_attention_fwd(sq, sk, sv, D, _addr(cu_q), _addr(cu_k), n, int(bool(causal)),
-                                  scale, so, _addr(lse), _raw_stream(dev)))
+        lse = torch.empty(shape, dtype=torch.float32, device=q.device)
+    _need(lse, torch.float32, shape, "lse", dev)
+    _check(_heads_call(lib, "pact_attention_fwd")(
+        at, at + 32, at + 64, D, cu_q.data_ptr(), cu_k.data_ptr(), n, 1 if causal else 0, scale,
+        at + 96, lse.data_ptr(), _raw_stream(dev)))
     return o, lse
 
 
@@ -871,19 +902,21 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     o.  Returns (dq, dk, dv); rows of no sequence are left as they were."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
-    sq, sk, sv, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
-    sdo, so = _need_heads(do, "do", dev, q.shape), _need_heads(o, "o", dev, q.shape)
+    fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
+    fields += _heads(do, "do", dev, q.shape) + _heads(o, "o", dev, q.shape)
     _need(lse, torch.float32, (q.shape[1], q.shape[0]), "lse", dev)
     dq, dk, dv = (torch.empty(x.shape, dtype=torch.bfloat16, device=q.device) if g is None else g
                   for g, x in ((dq, q), (dk, k), (dv, v)))
-    outs = [_need_heads(g, name, dev, x.shape)
-            for g, x, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"))]
+    h = _HEADS[8](*fields, *_heads(dq, "dq", dev, q.shape), *_heads(dk, "dk", dev, k.shape),
+                  *_heads(dv, "dv", dev, v.shape))
+    at = ctypes.addressof(h)
     # its own scratch in every call: a captured graph then keeps one of its own
     ws = torch.empty((lib.pact_attention_bwd_workspace_size(q.shape[0], q.shape[1]),),
                      dtype=torch.uint8, device=q.device)
-    _check(lib.pact_attention_bwd(sdo, sq, sk, sv, so, _addr(lse), D, _addr(cu_q), _addr(cu_k), n,
-                                  int(bool(causal)), scale, *outs, _addr(ws), ws.numel(),
-                                  _raw_stream(dev)))
+    _check(_heads_call(lib, "pact_attention_bwd")(
+        at + 96, at, at + 32, at + 64, at + 128, lse.data_ptr(), D, cu_q.data_ptr(), cu_k.data_ptr(),
+        n, 1 if causal else 0, scale, at + 160, at + 192, at + 224, ws.data_ptr(), ws.numel(),
+        _raw_stream(dev)))
     return dq, dk, dv
 
 

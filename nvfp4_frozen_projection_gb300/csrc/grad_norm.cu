@@ -8,9 +8,9 @@
 // opens by adding those sums in the same order, takes the chunks from the last to the first:
 // what the norm read last is still in L2, and what is read and written there need not stay.
 //
-// Squares are added in FP32 over the 16 values of a thread, and those sums in FP64.  A thread
-// whose largest value lies outside [2^-50, 2^60], where an FP32 square could overflow or
-// vanish, adds its values in FP64 instead.
+// Squares are added in FP32 over 16 values of a thread, four such sums again in FP32, and
+// those in FP64.  A thread whose largest value of the 16 lies outside [2^-50, 2^60], where an
+// FP32 square could overflow or vanish, adds them in FP64 instead.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -26,9 +26,10 @@ struct GradSpan {
   int len;
 };
 
-// The tensor and the values of chunk c: the last tensor whose first chunk is not behind it.
-__device__ __forceinline__ GradSpan grad_span(const GradTable& t, int64_t c) {
-  int64_t lo = 0, hi = t.count - 1;
+// The tensor and the values of chunk c: the last tensor whose first chunk is not behind it,
+// looked for from tensor `lo` on.
+__device__ __forceinline__ GradSpan grad_span(const GradTable& t, int64_t c, int64_t lo) {
+  int64_t hi = t.count - 1;
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) >> 1;
     if (t.first[mid] <= c)
@@ -58,21 +59,26 @@ __device__ __forceinline__ double block_sum(double v, double* slots) {
   return s;
 }
 
-__global__ void __launch_bounds__(kGradThreads, kGradBlocks) k_grad_sums(const GradTable t, double* part) {
+__global__ void __launch_bounds__(kGradThreads, kGradBlocks)
+    k_grad_sums(const GradTable t, double* part) {
   __shared__ double slots[kGradThreads / 32];
   double sum = 0.0;
-  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const GradSpan sp = grad_span(t, c);
+  float few = 0.0f;  // of up to four chunks
+  int held = 0;
+  int64_t c = blockIdx.x;
+  GradSpan sp = {};
+  if (c < t.chunks) sp = grad_span(t, c, 0);
+  while (c < t.chunks) {
     const float* g = t.data[sp.tensor] + sp.at;
     float4 v[4];
-    const bool vec = ((uintptr_t)g & 15u) == 0;
+    const bool vec = ((uintptr_t)g & 15u) == 0, keep = t.chunks - c <= kGradKept;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = (i * kGradThreads + (int)threadIdx.x) * 4;
       v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (vec && e + 4 <= sp.len) {
         const float4* at = reinterpret_cast<const float4*>(g + e);
-        v[i] = t.chunks - c > kGradKept ? __ldcs(at) : *at;
+        v[i] = keep ? *at : __ldcs(at);
       } else {
         if (e < sp.len) v[i].x = g[e];
         if (e + 1 < sp.len) v[i].y = g[e + 1];
@@ -80,6 +86,9 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks) k_grad_sums(const G
         if (e + 3 < sp.len) v[i].w = g[e + 3];
       }
     }
+    // the next chunk is looked up while these values are on their way
+    c += gridDim.x;
+    if (c < t.chunks) sp = grad_span(t, c, sp.tensor);
     float s = 0.0f, top = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -88,7 +97,12 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks) k_grad_sums(const G
                   fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
     }
     if (top <= 0x1p60f && !(top < 0x1p-50f && top > 0.0f)) {
-      sum += (double)s;
+      few += s;
+      if (++held == 4) {
+        sum += (double)few;
+        few = 0.0f;
+        held = 0;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -99,13 +113,13 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks) k_grad_sums(const G
       }
     }
   }
-  sum = block_sum(sum, slots);
+  sum = block_sum(sum + (double)few, slots);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 // APPLY: clip into out (which may be the list itself); else the norm alone, by one block.
 template <bool APPLY>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(kGradThreads, kGradBlocks)
     k_grad_clip(const GradTable t, float* const* out, const double* part, int parts,
                 double max_norm, float* norm_out) {
   __shared__ double slots[kGradThreads / 32];
@@ -125,7 +139,7 @@ __global__ void __launch_bounds__(kGradThreads)
     __syncthreads();
     const float coef = shared_coef;
     for (int64_t i = blockIdx.x; i < t.chunks; i += gridDim.x) {
-      const GradSpan sp = grad_span(t, t.chunks - 1 - i);
+      const GradSpan sp = grad_span(t, t.chunks - 1 - i, 0);
       const float* g = t.data[sp.tensor] + sp.at;
       float* o = out[sp.tensor] + sp.at;
       if (o == g && coef == 1.0f) continue;  // nothing to clip

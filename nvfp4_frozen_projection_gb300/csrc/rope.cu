@@ -13,10 +13,10 @@
 //
 // Both directions are bound by HBM: 4 bytes a value forward, 6 backward (4 without norms).
 // A block works for the queries or for the keys.  A group of 8, 16 or 32 of its lanes holds a
-// head, 8 values (16 bytes) a lane, and takes heads of one token in turn, so that a lane
-// computes the sines of its columns once for all of them; a pair's other half comes from the
-// lane that holds it as packed BF16.  With few tokens the heads of a token are shared out
-// over more groups.
+// head and takes heads of one token in turn, so that a lane computes the sines of its columns
+// once for all of them.  A lane has both halves of four pairs, 8 columns: four angles, and
+// nothing to exchange but the sums over a head.  With few tokens the heads of a token are
+// shared out over more groups.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -24,72 +24,100 @@ namespace pact {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeBlocks = 4;     // an SM: 64 registers a thread
-constexpr int kRopeBwdBlocks = 3;  // 80
 constexpr int kRopeBwdMost = 16;   // an SM, in all
 
-// The rotation of one lane's 8 columns, two at a time: y = own c + other s.  The other half
-// of a pair comes from the lane `other`, or (PAIRS) is the neighbouring column.
-struct Turn {
-  float2 c[4], s[4];
-  int other;    // lane offset of the other half
-  bool turned;  // the lane's columns lie in the first rot
+// A lane's 8 columns as two vectors of four, u and v: the halves of four pairs, or (behind the
+// turned columns) neighbours that stay.  Pairs of halves: u from column a on, v from column b
+// on; neighbouring pairs (PAIRS): the even and the odd ones of 8 columns from a on.
+struct Cols {
+  int a, b;
+  bool turned;
 };
-
 template <bool PAIRS>
-__device__ __forceinline__ Turn make_turn(int col, int rot, int pos, const int64_t* turns,
-                                          bool back) {
+__device__ __forceinline__ Cols lane_cols(int sl, int rot) {
+  Cols c;
+  c.turned = sl * 8 < rot;
+  c.a = PAIRS || !c.turned ? sl * 8 : sl * 4;
+  c.b = PAIRS || !c.turned ? c.a + 4 : (rot >> 1) + c.a;
+  return c;
+}
+
+struct Vec {
+  float2 u[2], v[2];
+};
+template <bool PAIRS>
+__device__ __forceinline__ uint4 load_cols(const uint16_t* row, const Cols& c) {
+  if constexpr (PAIRS) return *reinterpret_cast<const uint4*>(row + c.a);
+  const uint2 lo = *reinterpret_cast<const uint2*>(row + c.a);
+  const uint2 hi = *reinterpret_cast<const uint2*>(row + c.b);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ float2 bf16x2_f2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <bool PAIRS>
+__device__ __forceinline__ Vec unpack(const uint4& w) {
+  const float2 a = bf16x2_f2(w.x), b = bf16x2_f2(w.y), c = bf16x2_f2(w.z), d = bf16x2_f2(w.w);
+  Vec r;
+  if constexpr (PAIRS) {
+    r.u[0] = make_float2(a.x, b.x);
+    r.u[1] = make_float2(c.x, d.x);
+    r.v[0] = make_float2(a.y, b.y);
+    r.v[1] = make_float2(c.y, d.y);
+  } else {
+    r.u[0] = a;
+    r.u[1] = b;
+    r.v[0] = c;
+    r.v[1] = d;
+  }
+  return r;
+}
+template <bool PAIRS>
+__device__ __forceinline__ void store_cols(uint16_t* row, const Cols& c, const Vec& r) {
+  if constexpr (PAIRS) {
+    *reinterpret_cast<uint4*>(row + c.a) =
+        make_uint4(pack_bf16x2(r.u[0].x, r.v[0].x), pack_bf16x2(r.u[0].y, r.v[0].y),
+                   pack_bf16x2(r.u[1].x, r.v[1].x), pack_bf16x2(r.u[1].y, r.v[1].y));
+  } else {
+    *reinterpret_cast<uint2*>(row + c.a) =
+        make_uint2(pack_bf16x2(r.u[0].x, r.u[0].y), pack_bf16x2(r.u[1].x, r.u[1].y));
+    *reinterpret_cast<uint2*>(row + c.b) =
+        make_uint2(pack_bf16x2(r.v[0].x, r.v[0].y), pack_bf16x2(r.v[1].x, r.v[1].y));
+  }
+}
+
+// Cosines and sines of the lane's four pairs.
+struct Turn {
+  float2 c[2], s[2];
+};
+template <bool PAIRS>
+__device__ __forceinline__ Turn make_turn(const Cols& cols, bool live, int pos,
+                                          const int64_t* turns) {
+  float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {};
+  if (live && cols.turned) {
+    const int i0 = PAIRS ? cols.a >> 1 : cols.a;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t phase = (uint64_t)(int64_t)pos * (uint64_t)turns[i0 + e];
+      sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s[e], &c[e]);
+    }
+  }
   Turn t;
-  t.turned = col < rot;
-  t.other = 0;
-  if (!t.turned) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) t.c[e] = make_float2(1.0f, 1.0f), t.s[e] = make_float2(0.0f, 0.0f);
-    return t;
-  }
-  const int half = rot >> 1;
-  const bool first = PAIRS || col < half;
-  if (!PAIRS) t.other = first ? (half >> 3) : -(half >> 3);
-  const int i0 = PAIRS ? col >> 1 : (first ? col : col - half);
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < (PAIRS ? 4 : 8); ++e) {
-    const uint64_t phase = (uint64_t)(int64_t)pos * (uint64_t)turns[i0 + e];
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s[e], &c[e]);
-    // of a pair (a, b): a' = a c - b s, b' = b c + a s; backward the other way round
-    if (first != back) s[e] = -s[e];
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    t.c[e] = PAIRS ? make_float2(c[e], c[e]) : make_float2(c[2 * e], c[2 * e + 1]);
-    t.s[e] = PAIRS ? make_float2(s[e], -s[e]) : make_float2(s[2 * e], s[2 * e + 1]);
-  }
+  t.c[0] = make_float2(c[0], c[1]);
+  t.c[1] = make_float2(c[2], c[3]);
+  t.s[0] = make_float2(s[0], s[1]);
+  t.s[1] = make_float2(s[2], s[3]);
   return t;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float2* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint4 pack8(const float2* f) {
-  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
-                    pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
-}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 swapped(float2 v) { return make_float2(v.y, v.x); }
+__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
 
 template <int SEG>
 __device__ __forceinline__ float seg_sum(float v) {
 #pragma unroll
   for (int o = SEG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
-}
-
-// The lanes' other halves of a pair, as packed BF16.
-__device__ __forceinline__ uint4 shfl_v4(const uint4& v, int lane) {
-  return make_uint4(__shfl_sync(0xFFFFFFFFu, v.x, lane), __shfl_sync(0xFFFFFFFFu, v.y, lane),
-                    __shfl_sync(0xFFFFFFFFu, v.z, lane), __shfl_sync(0xFFFFFFFFu, v.w, lane));
 }
 
 // 1 / sqrt(mean + eps); rsqrtf is within 2 units in the last place.
@@ -102,65 +130,57 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) k_qk_norm_rope(cons
   constexpr int U = 4;  // heads in flight
   const bool isk = (int)blockIdx.x >= p.side[0].blocks;
   const RopeSide& sd = p.side[isk];
-  const int lane = threadIdx.x & 31, col = (lane & (SEG - 1)) * 8;
+  const int sl = threadIdx.x & (SEG - 1);
   const int64_t seg = (int64_t)(blockIdx.x - (isk ? p.side[0].blocks : 0)) * (kRopeThreads / SEG) +
                       threadIdx.x / SEG;
   // a dead group stays for the shuffles of its warp, with no heads
   const bool alive = seg < sd.segs;
   const int64_t t = alive ? seg / sd.chunks : 0;
   const int h0 = alive ? (int)(seg - t * sd.chunks) * sd.per : 0;
-  const int heads = alive && col < p.D && PACT_IN(t < p.T) ? min(sd.per, sd.heads - h0) : 0;
-  const Turn tn = make_turn<PAIRS>(heads ? col : p.rot, p.rot, p.positions[t], p.turns, false);
-  const int other = lane + tn.other;
+  const int heads = alive && sl * 8 < p.D && PACT_IN(t < p.T) ? min(sd.per, sd.heads - h0) : 0;
+  const Cols cols = lane_cols<PAIRS>(sl, p.rot);
+  const Turn tn = make_turn<PAIRS>(cols, heads > 0, p.positions[t], p.turns);
   const float inv_d = 1.0f / (float)p.D;
-  // the gammas go into the coefficients: y = rstd (own (gamma c) + other (gamma' s))
-  float2 c[4], s[4];
+  // u' = u uc - v vs, v' = v vc + u us: the gammas go into the coefficients
+  float2 uc[2], us[2], vc[2], vs[2];
+  Vec g;
+  g.u[0] = g.u[1] = g.v[0] = g.v[1] = both(1.0f);
+  if (NORM && heads > 0) g = unpack<PAIRS>(load_cols<PAIRS>(sd.gamma, cols));
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = tn.c[e], s[e] = tn.s[e];
-  if (NORM && heads) {
-    float2 g[4], o[4];
-    unpack8(*reinterpret_cast<const uint4*>(sd.gamma + col), g);
-    if constexpr (PAIRS) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = swapped(g[e]);
-    } else {
-      unpack8(*reinterpret_cast<const uint4*>(sd.gamma + col + 8 * tn.other), o);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = __fmul2_rn(c[e], g[e]), s[e] = __fmul2_rn(s[e], o[e]);
+  for (int e = 0; e < 2; ++e) {
+    uc[e] = __fmul2_rn(tn.c[e], g.u[e]);
+    us[e] = __fmul2_rn(tn.s[e], g.u[e]);
+    vc[e] = __fmul2_rn(tn.c[e], g.v[e]);
+    vs[e] = __fmul2_rn(neg(tn.s[e]), g.v[e]);
   }
-  const uint16_t* x = sd.x + t * sd.ld + (int64_t)h0 * p.D + col;
-  uint16_t* out = sd.out + t * sd.ldo + (int64_t)h0 * p.D + col;
+  const uint16_t* x = sd.x + t * sd.ld + (int64_t)h0 * p.D;
+  uint16_t* out = sd.out + t * sd.ldo + (int64_t)h0 * p.D;
   for (int hb = 0; hb < sd.per; hb += U) {
-    uint4 v[U];
+    uint4 w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (hb + u < heads) v[u] = *reinterpret_cast<const uint4*>(x + (hb + u) * p.D);
+    for (int i = 0; i < U; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (hb + i < heads) w[i] = load_cols<PAIRS>(x + (hb + i) * p.D, cols);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 f[4], o[4];
-      unpack8(v[u], f);
-      if constexpr (PAIRS) {
+    for (int i = 0; i < U; ++i) {
+      const Vec f = unpack<PAIRS>(w[i]);
+      Vec o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = swapped(f[e]);
-      } else {
-        unpack8(shfl_v4(v[u], other), o);
+      for (int e = 0; e < 2; ++e) {
+        o.u[e] = __ffma2_rn(f.u[e], uc[e], __fmul2_rn(f.v[e], vs[e]));
+        o.v[e] = __ffma2_rn(f.v[e], vc[e], __fmul2_rn(f.u[e], us[e]));
       }
-      float2 r = both(1.0f);
       if constexpr (NORM) {
-        float2 q = both(0.0f);
+        float2 q = __fmul2_rn(f.u[0], f.u[0]);
+        q = __ffma2_rn(f.u[1], f.u[1], q);
+        q = __ffma2_rn(f.v[0], f.v[0], q);
+        q = __ffma2_rn(f.v[1], f.v[1], q);
+        const float2 r = both(rstd_of(seg_sum<SEG>(q.x + q.y), inv_d, p.eps));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q = __ffma2_rn(f[e], f[e], q);
-        r = both(rstd_of(seg_sum<SEG>(q.x + q.y), inv_d, p.eps));
+        for (int e = 0; e < 2; ++e) o.u[e] = __fmul2_rn(o.u[e], r), o.v[e] = __fmul2_rn(o.v[e], r);
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[e] = __ffma2_rn(f[e], c[e], __fmul2_rn(o[e], s[e]));
-        if constexpr (NORM) f[e] = __fmul2_rn(f[e], r);
-      }
-      if (hb + u < heads) *reinterpret_cast<uint4*>(out + (hb + u) * p.D) = pack8(f);
+      if (hb + i < heads) store_cols<PAIRS>(out + (hb + i) * p.D, cols, o);
     }
   }
 }
@@ -168,7 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) k_qk_norm_rope(cons
 // Backward; a side's x is dy, xf the forward's input (NORM).  DG: the sum for dgamma of this
 // block's groups goes to part[block][D], group by group in order.
 template <int SEG, bool NORM, bool PAIRS, bool DG>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     k_qk_norm_rope_bwd(const RopeParams p, float* part) {
   constexpr int U = NORM ? 2 : 4;  // heads in flight
   constexpr int GROUPS = kRopeThreads / SEG;
@@ -176,74 +196,84 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
   const bool isk = (int)blockIdx.x >= p.side[0].blocks;
   const RopeSide& sd = p.side[isk];
   const int block = (int)blockIdx.x - (isk ? p.side[0].blocks : 0);
-  const int lane = threadIdx.x & 31, col = (lane & (SEG - 1)) * 8, group = threadIdx.x / SEG;
+  const int sl = threadIdx.x & (SEG - 1), group = threadIdx.x / SEG;
   const float inv_d = 1.0f / (float)p.D;
-  float2 acc[DG ? 4 : 1] = {}, gm[4] = {};
-  if (NORM && col < p.D) unpack8(*reinterpret_cast<const uint4*>(sd.gamma + col), gm);
+  const Cols cols = lane_cols<PAIRS>(sl, p.rot);
+  Vec gm, acc;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) gm.u[e] = gm.v[e] = acc.u[e] = acc.v[e] = both(0.0f);
+  if (NORM && sl * 8 < p.D) gm = unpack<PAIRS>(load_cols<PAIRS>(sd.gamma, cols));
   for (int64_t first = (int64_t)block * GROUPS; first < sd.segs;
        first += (int64_t)sd.blocks * GROUPS) {
     const int64_t seg = first + group;
     const bool alive = seg < sd.segs;
     const int64_t t = alive ? seg / sd.chunks : 0;
     const int h0 = alive ? (int)(seg - t * sd.chunks) * sd.per : 0;
-    const int heads = alive && col < p.D && PACT_IN(t < p.T) ? min(sd.per, sd.heads - h0) : 0;
-    const Turn tn = make_turn<PAIRS>(heads ? col : p.rot, p.rot, p.positions[t], p.turns, true);
-    const int other = lane + tn.other;
-    const uint16_t* dy = sd.x + t * sd.ld + (int64_t)h0 * p.D + col;
-    const uint16_t* x = NORM ? sd.xf + t * sd.ldxf + (int64_t)h0 * p.D + col : nullptr;
-    uint16_t* out = sd.out + t * sd.ldo + (int64_t)h0 * p.D + col;
+    const int heads = alive && sl * 8 < p.D && PACT_IN(t < p.T) ? min(sd.per, sd.heads - h0) : 0;
+    const Turn tn = make_turn<PAIRS>(cols, heads > 0, p.positions[t], p.turns);
+    const uint16_t* dy = sd.x + t * sd.ld + (int64_t)h0 * p.D;
+    const uint16_t* x = NORM ? sd.xf + t * sd.ldxf + (int64_t)h0 * p.D : nullptr;
+    uint16_t* out = sd.out + t * sd.ldo + (int64_t)h0 * p.D;
     for (int hb = 0; hb < sd.per; hb += U) {
-      uint4 v[U], w[U];
+      uint4 wy[U], wx[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        v[u] = w[u] = make_uint4(0, 0, 0, 0);
-        if (hb + u < heads) {
-          v[u] = *reinterpret_cast<const uint4*>(dy + (hb + u) * p.D);
-          if constexpr (NORM) w[u] = *reinterpret_cast<const uint4*>(x + (hb + u) * p.D);
+      for (int i = 0; i < U; ++i) {
+        wy[i] = wx[i] = make_uint4(0, 0, 0, 0);
+        if (hb + i < heads) {
+          wy[i] = load_cols<PAIRS>(dy + (hb + i) * p.D, cols);
+          if constexpr (NORM) wx[i] = load_cols<PAIRS>(x + (hb + i) * p.D, cols);
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float2 g[4], o[4];
-        unpack8(v[u], g);
-        if constexpr (PAIRS) {
+      for (int i = 0; i < U; ++i) {
+        const Vec f = unpack<PAIRS>(wy[i]);
+        Vec g;  // turned back
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = swapped(g[e]);
-        } else {
-          unpack8(shfl_v4(v[u], other), o);
+        for (int e = 0; e < 2; ++e) {
+          g.u[e] = __ffma2_rn(f.u[e], tn.c[e], __fmul2_rn(f.v[e], tn.s[e]));
+          g.v[e] = __ffma2_rn(f.v[e], tn.c[e], __fmul2_rn(neg(f.u[e]), tn.s[e]));
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = __ffma2_rn(g[e], tn.c[e], __fmul2_rn(o[e], tn.s[e]));
         if constexpr (NORM) {
-          float2 n[4];
-          unpack8(w[u], n);
+          Vec n = unpack<PAIRS>(wx[i]), d;
           float2 ss = both(0.0f), dot = both(0.0f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ss = __ffma2_rn(n[e], n[e], ss);
-            o[e] = __fmul2_rn(g[e], gm[e]);
-            dot = __ffma2_rn(o[e], n[e], dot);
+          for (int e = 0; e < 2; ++e) {
+            ss = __ffma2_rn(n.u[e], n.u[e], ss);
+            ss = __ffma2_rn(n.v[e], n.v[e], ss);
+            d.u[e] = __fmul2_rn(g.u[e], gm.u[e]);
+            d.v[e] = __fmul2_rn(g.v[e], gm.v[e]);
+            dot = __ffma2_rn(d.u[e], n.u[e], dot);
+            dot = __ffma2_rn(d.v[e], n.v[e], dot);
           }
           const float rstd = rstd_of(seg_sum<SEG>(ss.x + ss.y), inv_d, p.eps);
           const float c = seg_sum<SEG>(dot.x + dot.y) * rstd * inv_d;  // mean(dn n)
           const float2 r = both(rstd), mc = both(-c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            n[e] = __fmul2_rn(n[e], r);
-            // zero in lanes and heads that hold nothing
-            if constexpr (DG) acc[e] = __ffma2_rn(g[e], n[e], acc[e]);
-            g[e] = __fmul2_rn(r, __ffma2_rn(n[e], mc, o[e]));
+          for (int e = 0; e < 2; ++e) {
+            n.u[e] = __fmul2_rn(n.u[e], r);
+            n.v[e] = __fmul2_rn(n.v[e], r);
+            if constexpr (DG) {  // zero in lanes and heads that hold nothing
+              acc.u[e] = __ffma2_rn(g.u[e], n.u[e], acc.u[e]);
+              acc.v[e] = __ffma2_rn(g.v[e], n.v[e], acc.v[e]);
+            }
+            g.u[e] = __fmul2_rn(r, __ffma2_rn(n.u[e], mc, d.u[e]));
+            g.v[e] = __fmul2_rn(r, __ffma2_rn(n.v[e], mc, d.v[e]));
           }
         }
-        if (hb + u < heads) *reinterpret_cast<uint4*>(out + (hb + u) * p.D) = pack8(g);
+        if (hb + i < heads) store_cols<PAIRS>(out + (hb + i) * p.D, cols, g);
       }
     }
   }
   if constexpr (DG) {
-    if (col < p.D) {
+    if (sl * 8 < p.D) {
+      const float u[4] = {acc.u[0].x, acc.u[0].y, acc.u[1].x, acc.u[1].y};
+      const float v[4] = {acc.v[0].x, acc.v[0].y, acc.v[1].x, acc.v[1].y};
+      float* row = sums + group * (8 * SEG);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float2*>(sums + group * (8 * SEG) + col + 2 * e) = acc[e];
+      for (int e = 0; e < 4; ++e) {
+        row[PAIRS ? cols.a + 2 * e : cols.a + e] = u[e];
+        row[PAIRS ? cols.a + 2 * e + 1 : cols.b + e] = v[e];
+      }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < p.D; c += kRopeThreads) {
@@ -255,8 +285,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
 }
 
 // dgamma_q, dgamma_k [D] from the blocks' sums, those of the queries first.  16 columns a
-// block (D is a multiple of 16), 64 threads each, which take every 64th row and are joined in
-// order.
+// block (D is a multiple of 16), 64 threads each, which take every 64th row and are joined
+// eight by eight.
 __global__ void __launch_bounds__(1024)
     k_qk_dgamma(const float* part, int bq, int bk, int D, float* dgq, float* dgk) {
   __shared__ float sums[64][17];
@@ -266,14 +296,20 @@ __global__ void __launch_bounds__(1024)
   const float* from = part + (isk ? (int64_t)bq * D : 0) + c;
   const int rows = isk ? bk : bq;
   float s = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
   for (int b = y; b < rows; b += 64) s += from[(int64_t)b * D];
   sums[y][x] = s;
   __syncthreads();
-  if (threadIdx.x < 16) {
+  if (y < 8) {
     s = 0.0f;
-#pragma unroll 16
-    for (int b = 0; b < 64; ++b) s += sums[b][threadIdx.x];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) s += sums[y + 8 * b][x];
+    sums[y][x] = s;
+  }
+  __syncthreads();
+  if (y == 0) {
+#pragma unroll
+    for (int b = 1; b < 8; ++b) s += sums[b][x];
     if (PACT_IN(c < D)) (isk ? dgk : dgq)[c] = s;
   }
 }
