@@ -33,11 +33,12 @@ struct FwdCfg {
   static constexpr int STAGES = DP == 64 ? 8 : 5;
   static constexpr uint32_t Q_OFF = 0, KV_OFF = 2 * TILE;
   static constexpr uint32_t BAR_OFF = KV_OFF + STAGES * TILE;
-  static constexpr uint32_t SMEM = BAR_OFF + 512 + 1024;
+  static constexpr uint32_t SMEM = BAR_OFF + 512;
   // q_full[2] q_empty[2] s_full[2] p_full[2][2] o_done[2] final[2] tail - kv_full[ST] kv_empty[ST]
-  // s_read[2] lag before the ring's
-  static constexpr int NBARS = 19 + 2 * STAGES;
-  static_assert(SMEM <= 232448 && NBARS * 8 <= 504, "shared memory");
+  // s_read[2] lag unit_full[3] unit_empty[3] before the ring's
+  static constexpr int NBARS = 25 + 2 * STAGES;
+  static constexpr uint32_t UNIT_OFF = BAR_OFF + 384;  // three descriptions of a unit
+  static_assert(SMEM <= 232448 && NBARS * 8 <= 384, "shared memory");
 };
 
 template <int DP>
@@ -45,14 +46,17 @@ __global__ void __launch_bounds__(384, 1)
     k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using C = FwdCfg<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_addr(smem);
+  if (base & 1023u) {  // the swizzle needs it, and the budget leaves no room to round up
+    if (threadIdx.x == 0) atomicOr(p.status, (unsigned)PACT_DEV_BOUNDS);
+    return;
+  }
   const uint32_t bars = base + C::BAR_OFF;
   const uint32_t q_full = bars, q_empty = bars + 16, s_full = bars + 32, p_full = bars + 48,
                  o_done = bars + 80, final_bar = bars + 96, tail_bar = bars + 112,
-                 s_read = bars + 128, lag_bar = bars + 144, kv_full = bars + 152,
+                 s_read = bars + 128, lag_bar = bars + 144, unit_full = bars + 152, unit_empty = bars + 176,
+                 kv_full = bars + 200,
                  kv_empty = kv_full + 8 * C::STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 504);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::BAR_OFF + 508);
@@ -71,6 +75,10 @@ __global__ void __launch_bounds__(384, 1)
     }
     mbar_init(tail_bar, 1);
     mbar_init(lag_bar, 1);
+    for (int u = 0; u < 3; ++u) {
+      mbar_init(unit_full + 8 * u, 1);
+      mbar_init(unit_empty + 8 * u, 10);  // the warps of the softmax and the issuers
+    }
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(kv_full + 8 * s, 1);
       mbar_init(kv_empty + 8 * s, 2);  // the issuers
@@ -87,38 +95,47 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int tpu = 2 * p.tpt;  // tokens of a unit
-  SeqFinder<false> finder = seq_finder<false>(p, tpu);
-  Seq s;
-  // the unit's tiles: first token, and the keys and tiles of keys that they see
-  int tok0[2], kend[2], nk[2], kvh, h0;
-  auto next_unit = [&](uint32_t u) {
-    const uint32_t t = p.units_div.div(u);
-    const int hu = (int)(u - t * p.units_h);
-    if (!finder.find(t, s)) return false;
-    kvh = p.subs == 1 ? hu : hu / p.subs;
-    h0 = kvh * p.group + (hu - kvh * p.subs) * p.gp;
+  // A unit: tok0[i], the first tokens of its tiles; kend[i], the keys that they see, and nk[i]
+  // tiles of them; h0, its first query head.  The copying warp looks the units up and hands
+  // them to the other warps.
+  int q0, lq, lk, tok0[2], kend[2], nk[2], h0;
+  auto set_unit = [&](int4 d, int head) {
+    q0 = d.x;
+    lq = d.y;
+    lk = d.z;
+    h0 = head;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      tok0[i] = s.tile * tpu + i * p.tpt;
+      tok0[i] = d.w + i * p.tpt;
       kend[i] = 0;
-      if (tok0[i] < s.lq) {
-        kend[i] = s.lk;
-        if (p.causal) kend[i] = clampi(min(tok0[i] + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
+      if (tok0[i] < lq) {
+        kend[i] = lk;
+        if (p.causal) kend[i] = clampi(min(tok0[i] + p.tpt, lq) + lk - lq, 0, lk);
       }
       nk[i] = (kend[i] + 127) / 128;
     }
-    return true;
+  };
+  RingPos slot;
+  bool ok = true;
+  auto next_unit = [&]() {  // false behind the last one, and (ok false) when it took too long
+    if (!(ok = mbar_wait(unit_full + 8 * slot.stage, slot.phase, kAttnWaitNs, abort_flag))) return false;
+    const int4* d = reinterpret_cast<const int4*>(smem + C::UNIT_OFF + 32 * slot.stage);
+    const int4 a = d[0], b = d[1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(unit_empty + 8 * slot.stage);
+    slot.advance(3);
+    set_unit(a, b.x);
+    return b.y != 0;
   };
 
   if (warp >= 8) {
-    setmaxnreg_dec<72>();
+    setmaxnreg_dec<56>();
     if (warp == 8) {
       // ------------------------------------------------------------ copies
       int stage = 0;
       uint32_t phase = 0, q_uses[2] = {0, 0}, tails = 0;
       uint32_t pend = 0, pend_par = 0;
-      bool ok = true;
+      int kvh = 0;
       auto load_kv = [&](const CUtensorMap* tm, int row, int valid) {
         if (!mbar_wait(kv_empty + 8 * stage, phase ^ 1u, kAttnWaitNs, abort_flag)) return false;
         const uint32_t dst = base + C::KV_OFF + stage * C::TILE, full = kv_full + 8 * stage;
@@ -161,13 +178,32 @@ __global__ void __launch_bounds__(384, 1)
           mbar_expect_tx(full, rows * 128 * C::BOXES);
 #pragma unroll
           for (int b = 0; b < C::BOXES; ++b)
-            tma_load_3d(base + C::Q_OFF + i * C::TILE + b * kBox, &tmQ, b * 64, h0, s.q0 + tok0[i],
+            tma_load_3d(base + C::Q_OFF + i * C::TILE + b * kBox, &tmQ, b * 64, h0, q0 + tok0[i],
                         full);
         }
         __syncwarp();
         return true;
       };
-      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
+      SeqFinder<false> finder = seq_finder<false>(p, 2 * p.tpt);
+      Seq s;
+      for (uint32_t turn = 0;; ++turn) {
+        const uint32_t u = unit_of(turn), t = p.units_div.div(u);
+        const int hu = (int)(u - t * p.units_h);
+        const bool there = finder.find(t, s);
+        kvh = p.subs == 1 ? hu : hu / p.subs;
+        set_unit(make_int4(s.q0, s.lq, s.lk, s.tile * 2 * p.tpt),
+                 kvh * p.group + (hu - kvh * p.subs) * p.gp);
+        if (!(ok = mbar_wait(unit_empty + 8 * slot.stage, slot.phase ^ 1u, kAttnWaitNs, abort_flag)))
+          break;
+        if (lane == 0) {
+          int4* d = reinterpret_cast<int4*>(smem + C::UNIT_OFF + 32 * slot.stage);
+          d[0] = make_int4(q0, lq, lk, tok0[0]);
+          d[1] = make_int4(h0, there, 0, 0);
+          mbar_arrive(unit_full + 8 * slot.stage);
+        }
+        __syncwarp();
+        slot.advance(3);
+        if (!there) break;
         const int n = max(nk[0], nk[1]);
         // in the order of their use: K 0, then (OWN_P) K j + 1 and V j, or V j and K j + 1
         for (int j = -1; j < n && n > 0 && ok; ++j) {
@@ -177,6 +213,7 @@ __global__ void __launch_bounds__(384, 1)
           if (C::OWN_P && j >= 0) ok = ok && load_kv(&tmV, s.k0 + j * 128, s.lk - j * 128);
           if (j < 0 && nk[1] > 0) ok = ok && load_q(1);
         }
+        if (!ok) break;
       }
       if (!ok) {
         if (lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_TMA);
@@ -192,7 +229,7 @@ __global__ void __launch_bounds__(384, 1)
       const int i = warp - 9;
       RingPos at;
       uint32_t q_uses = 0, p_uses = 0, s_uses = 0;
-      bool ok = true, lagged = false;
+      bool lagged = false;
       const uint32_t idesc_s = attn_idesc(128, false), idesc_o = attn_idesc(p.D, true);
       const uint32_t ts = tmem + i * 128, to = tmem + C::O_COL + i * C::O_STEP;
       const uint32_t tp = tmem + C::P_COL + i * C::P_STEP;
@@ -203,8 +240,8 @@ __global__ void __launch_bounds__(384, 1)
       auto wait = [&](uint32_t bar, uint32_t par) {
         return mbar_wait(bar, par, kAttnWaitNs, abort_flag);
       };
-      for (uint32_t turn = 0; ok && next_unit(unit_of(turn)); ++turn) {
-        const int n = max(nk[0], nk[1]);
+      while (ok && next_unit()) {
+        const int n = max(nk[0], nk[1]), my_nk = i ? nk[1] : nk[0], my_kend = i ? kend[1] : kend[0];
         if (i == 0 && !lagged && nk[0] == 0) {  // tile 1 has nobody to wait for
           if (lead) mbar_arrive(lag_bar);
           lagged = true;
@@ -213,7 +250,7 @@ __global__ void __launch_bounds__(384, 1)
         // ring with OWN_P.  A wait or a commit costs the thread about 100 cycles: what lies
         // between P and the next S is as short as can be.
         for (int j = 0; j <= n && n > 0; ++j) {
-          const bool pv = j > 0 && j - 1 < nk[i], qk = j < nk[i];
+          const bool pv = j > 0 && j - 1 < my_nk, qk = j < my_nk;
           RingPos v = at, k = at;
           if (C::OWN_P ? j > 0 && j < n : false) v.advance(C::STAGES);
           if (!C::OWN_P && j > 0) k.advance(C::STAGES);
@@ -237,7 +274,7 @@ __global__ void __launch_bounds__(384, 1)
               if (e < ksteps) mma_bf16(ts, step_k(dq, e), step_k(d, e), idesc_s, e > 0);
             mma_commit(s_full + 8 * i);
             mma_commit(kv_empty + 8 * k.stage);
-            if (j == nk[i] - 1) mma_commit(q_empty + 8 * i);
+            if (j == my_nk - 1) mma_commit(q_empty + 8 * i);
           };
           if (C::OWN_P && qk) {  // once the softmax has read the S before it
             if (!(ok = wait(s_read + 8 * i, (s_uses & 1u) ^ 1u))) break;
@@ -263,7 +300,7 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
           }
           if (lead) {
-            if (pv && kend[i] - (j - 1) * 128 > 64) {
+            if (pv && my_kend - (j - 1) * 128 > 64) {
 #pragma unroll
               for (int e = 4; e < 8; ++e) mma_bf16_ta(to, tp + e * 8, step_n(d, e), idesc_o, 1u);
             }
@@ -289,7 +326,7 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else {
     // -------------------------------------------------------------- softmax, a row a thread
-    setmaxnreg_inc<216>();
+    setmaxnreg_inc<224>();
     const int i = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -297,14 +334,12 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tp = tmem + lanes + C::P_COL + i * C::P_STEP;
     const float c = p.c;
     uint32_t uses = 0;  // S tiles so far
-    bool ok = true;
-    uint32_t turn = 0;
-    for (bool more = next_unit(unit_of(0)); more;) {
-      const int n = nk[i];
-      const int tok = tok0[i] + row_token(p, row);
+    while (ok && next_unit()) {
+      const int n = i ? nk[1] : nk[0], my_kend = i ? kend[1] : kend[0], my_tok = i ? tok0[1] : tok0[0];
+      const int tok = my_tok + row_token(p, row);
       // keys that this row sees, and that every row of the tile sees
-      const int lim = p.causal ? min(s.lk, tok + 1 + s.lk - s.lq) : s.lk;
-      const int lim_all = p.causal ? min(s.lk, tok0[i] + 1 + s.lk - s.lq) : s.lk;
+      const int lim = p.causal ? min(lk, tok + 1 + lk - lq) : lk;
+      const int lim_all = p.causal ? min(lk, my_tok + 1 + lk - lq) : lk;
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j, ++uses) {
         if (!(ok = mbar_wait(s_full + 8 * i, uses & 1u, kAttnWaitNs, abort_flag))) break;
@@ -392,7 +427,7 @@ __global__ void __launch_bounds__(384, 1)
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          if (b == 0 || kend[i] - j * 128 > 64) {  // else no key of the second half is seen
+          if (b == 0 || my_kend - j * 128 > 64) {  // else no key of the second half is seen
             if (b == 1) exps(1, mc);
             tmem_st32(tp + 32 * b, w);
             tmem_st_wait();
@@ -406,17 +441,18 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- o and lse
-      // the search for the next unit runs while the last product does
-      const int t0 = tok0[i], rows = min(p.tpt, s.lq - t0) * p.gp, q0 = s.q0, head = h0;
-      more = next_unit(unit_of(++turn));
+      const int rows = min(p.tpt, lq - my_tok) * p.gp;
       if (rows <= 0) continue;
-      float inv = 0.0f;
+      const bool empty = n == 0 || lim <= 0;
+      if (row < rows && PACT_IN(q0 + tok < p.tq)) {
+        const int h = h0 + row - row_token(p, row) * p.gp;
+        p.lse[(int64_t)h * p.tq + q0 + tok] = empty ? -INFINITY : (m * c + log2f(l)) * kLn2;
+      }
+      const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : l;  // a NaN stays one
       if (n > 0) {
         if (!(ok = mbar_wait(o_done + 8 * i, (uses - 1u) & 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
-        inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // a NaN stays one
       }
-      const bool empty = n == 0 || lim <= 0;
       for (int b = 0; b < p.D; b += 64) {
         uint32_t w[32];
 #pragma unroll
@@ -431,14 +467,10 @@ __global__ void __launch_bounds__(384, 1)
             w[8 * h + e] = empty ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * inv,
                                                     __uint_as_float(o[2 * e + 1]) * inv);
         }
-        if (PACT_IN(q0 + t0 < p.tq))
+        if (PACT_IN(q0 + my_tok < p.tq))
           store_rows64(w, lane, quarter * 32, rows, min(64, p.D - b),
-                       p.o + (int64_t)(q0 + t0) * p.ldo + (int64_t)head * p.D + b, p.ldo, p.D, p.gp,
+                       p.o + (int64_t)(q0 + my_tok) * p.ldo + (int64_t)h0 * p.D + b, p.ldo, p.D, p.gp,
                        p.gp_mul);
-      }
-      if (row < rows && PACT_IN(q0 + tok < p.tq)) {
-        const int h = head + row - row_token(p, row) * p.gp;
-        p.lse[(int64_t)h * p.tq + q0 + tok] = empty ? -INFINITY : (m * c + log2f(l)) * kLn2;
       }
     }
     if (!ok && lane == 0) raise_error(abort_flag, p.status, PACT_DEV_TIMEOUT | PACT_DEV_ROLE_EPI);
