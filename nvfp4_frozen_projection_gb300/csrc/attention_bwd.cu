@@ -23,6 +23,7 @@
 // So the tensor cores have work while exponentials are taken.  P and dS are rounded to BF16
 // for their products; everything else is FP32.
 #include "attention.cuh"
+#include "dependent.cuh"
 
 namespace pact {
 
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(384, 1)
   }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::SLOT_OFF + 4);
+  let_dependents_start();  // dk|dv needs nothing of dq: it takes the SMs that this one leaves
   const BwdBars B = bwd_bars(base + C::BAR_OFF, C::STAGES);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -949,6 +951,7 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  wait_for_prerequisites();  // done means done with dq, too
 }
 
 template <int DP>
@@ -962,8 +965,7 @@ static cudaError_t launch_bwd(const AttnBwdLaunch& L, unsigned gq, unsigned gk, 
   k_attn_dq<DP><<<gq, 384, sm, st>>>(L.tmQ, L.tmdO, L.tmK, L.tmV, L.p);
   if ((e = cudaGetLastError())) return e;
   note_launch();
-  k_attn_dkdv<DP><<<gk, 384, sm, st>>>(L.tmQ, L.tmdO, L.tmK, L.tmV, L.p);
-  return cudaGetLastError();
+  return launch_dependent(k_attn_dkdv<DP>, gk, 384, sm, st, L.tmQ, L.tmdO, L.tmK, L.tmV, L.p);
 }
 
 cudaError_t launch_attn_bwd(const AttnBwdLaunch& L, cudaStream_t st) {
