@@ -72,6 +72,42 @@ def test_backward(lq, lk, hq, hk, d, causal):
         ref.check(g, w, b, name)
 
 
+# several units for every SM: units of all lengths in one CTA, tiles 0 or 1 without keys, rows
+# that see nothing, keys that end in either half of a tile
+MANY = [
+    ([700, 1, 1300, 257, 64], [700, 1, 1300, 257, 64], 32, 32, 128),
+    ([900, 300], [1000, 333], 60, 20, 80),
+    ([640, 129, 513], [640, 129, 513], 64, 16, 96),
+    ([300, 500, 40, 0, 7], [200, 577, 0, 5, 1200], 48, 48, 112),
+    ([1100] * 3, [1100] * 3, 48, 12, 128),
+    ([1030] * 6, [1030] * 6, 32, 8, 64),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,hq,hk,d", MANY, ids=[f"h{c[2]}-{c[3]}d{c[4]}" for c in MANY])
+def test_many_units(lq, lk, hq, hk, d, causal):
+    q, k, v, _, cq, ck = make(lq, lk, hq, hk, d, 50)
+    o, lse = pk.pact_attention_fwd(q, k, v, dev(cq), dev(ck), causal)
+    pk.pact_check_status()
+    wo, wl, bo, bl = ref.attention(q, k, v, cq, ck, causal, d ** -0.5)
+    ref.check(o, wo, bo, "o")
+    ref.check(lse, wl, bl, "lse")
+
+
+def test_many_units_keep_a_nan_in_its_sequence():
+    lens = [700, 77, 900]
+    q, k, v, _, cq, ck = make(lens, lens, 32, 32, 128)
+    args = dev(cq), dev(ck)
+    o, lse = pk.pact_attention_fwd(q, k, v, *args)
+    for t in (q, k, v):
+        t[700:777] = math.nan
+    o2, lse2 = pk.pact_attention_fwd(q, k, v, *args)
+    pk.pact_check_status()
+    for a, b in ((o, o2), (lse.t(), lse2.t())):
+        assert torch.equal(a[:700], b[:700]) and torch.equal(a[777:], b[777:])
+
+
 def test_a_large_group():
     """Groups above 128 heads are cut at their largest divisor."""
     for hq, hk in ((130, 1), (160, 1), (254, 2)):
