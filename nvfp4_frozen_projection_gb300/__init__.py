@@ -9,7 +9,9 @@ library is missing or the device is not sm_103, calls raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import itertools
 import os
 import threading
 from dataclasses import dataclass
@@ -932,24 +934,25 @@ class GradList:
         if not self.tensors:
             raise ValueError("a gradient list needs at least one tensor")
         self.device = dev = torch.cuda.current_device()
+        f32 = torch.float32
         for i, t in enumerate(self.tensors):
-            _need(t, torch.float32, tuple(t.shape) if isinstance(t, torch.Tensor) else (),
-                  f"tensor {i}", dev)
+            if not (isinstance(t, torch.Tensor) and t.dtype is f32 and t.get_device() == dev
+                    and t.is_contiguous()):
+                _need(t, f32, tuple(t.shape) if isinstance(t, torch.Tensor) else (), f"tensor {i}", dev)
+        ptrs = [t.data_ptr() for t in self.tensors]
         self.numels = tuple(t.numel() for t in self.tensors)
-        spans = sorted((t.data_ptr(), t.numel()) for t in self.tensors if t.numel())
+        spans = sorted((a, n) for a, n in zip(ptrs, self.numels) if n)
         if any(a + 4 * n > b for (a, n), (b, _) in zip(spans, spans[1:])):
             raise ValueError("the tensors of a gradient list must not share memory")
-        first, at = [], 0
-        for n in self.numels:
-            first.append(at)
-            at += lib.pact_grad_chunks(n)
-        self.chunks = at
-        self._table = torch.tensor([[t.data_ptr() for t in self.tensors], list(self.numels), first],
-                                   dtype=torch.int64).to(f"cuda:{dev}")
+        chunks = {n: lib.pact_grad_chunks(n) for n in set(self.numels)}
+        first = [0, *itertools.accumulate(chunks[n] for n in self.numels)]
+        self.chunks = first.pop()
+        table = array.array("q", itertools.chain(ptrs, self.numels, first))
+        self._table = torch.frombuffer(table, dtype=torch.int64).to(f"cuda:{dev}")
         step = 8 * len(self.tensors)
         self.data = self._table.data_ptr()
         self._struct = _ListStruct(self.data, self.data + step, self.data + 2 * step,
-                                   len(self.tensors), at)
+                                   len(self.tensors), self.chunks)
 
 
 def _need_list(g, name, dev):
@@ -980,8 +983,9 @@ def pact_grad_norm(grads: GradList, norm: torch.Tensor | None = None) -> torch.T
 
 def pact_clip_grad_norm(grads: GradList, max_norm: float, norm: torch.Tensor | None = None,
                         out: GradList | None = None) -> torch.Tensor:
-    """Scale every value by min(1, max_norm / (norm + 1e-6)), in place or into `out` (a list
-    of the same sizes).  Returns the norm before clipping, FP32 [1]."""
+    """Scale every value by min(1, max_norm / (norm + 1e-6)), in place or into `out`: a list
+    of the same sizes, whose tensors share no memory with those of grads but, each, with its
+    own.  Returns the norm before clipping, FP32 [1]."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
     _need_list(grads, "grads", dev)

@@ -184,7 +184,6 @@ struct SeqFinder {
   // Every lane of the warp calls this; false behind the last unit.
   __device__ __forceinline__ bool find(uint32_t t, Seq& s) {
     const bool levels = nseq <= 32;
-    if (t >= 0x7FFFFFFFu) return false;  // offsets that make no sense; see FastDiv
     if (b0 < 0) {
       b0 = 0;
       load();
@@ -224,6 +223,9 @@ struct SeqFinder {
 __device__ __forceinline__ int clampi(int v, int lo, int hi) {
   return v < lo ? lo : (v > hi ? hi : v);
 }
+
+// Units end here whatever the offsets say; the host refuses sizes that need more (FastDiv).
+constexpr uint32_t kMaxUnit = 0x7FFFFFFFu;
 
 // Unit i of this CTA's.
 __device__ __forceinline__ uint32_t unit_of(uint32_t i) {

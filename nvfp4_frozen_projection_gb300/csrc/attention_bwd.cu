@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(384, 1)
   Seq s;
   int tok0, nk, kvh, h0;
   auto next_unit = [&](uint32_t u) {
+    if (u >= kMaxUnit) return false;
     const uint32_t t = p.units_div.div(u);
     const int hu = (int)(u - t * p.units_h);
     if (!finder.find(t, s)) return false;
@@ -603,6 +604,7 @@ __global__ void __launch_bounds__(384, 1)
   Seq s;
   int key0, kvh, qt0, nqt, n;  // first key; first query tile and how many; times the subgroups
   auto next_unit = [&](uint32_t u) {
+    if (u >= kMaxUnit) return false;
     const uint32_t t = p.hk_div.div(u);
     kvh = (int)(u - t * p.hk);
     if (!finder.find(t, s)) return false;

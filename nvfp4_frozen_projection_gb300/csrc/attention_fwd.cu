@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(384, 1)
       for (uint32_t turn = 0;; ++turn) {
         const uint32_t u = unit_of(turn), t = p.units_div.div(u);
         const int hu = (int)(u - t * p.units_h);
-        const bool there = finder.find(t, s);
+        const bool there = u < kMaxUnit && finder.find(t, s);
         kvh = p.subs == 1 ? hu : hu / p.subs;
         set_unit(make_int4(s.q0, s.lq, s.lk, s.tile * 2 * p.tpt),
                  kvh * p.group + (hu - kvh * p.subs) * p.gp);

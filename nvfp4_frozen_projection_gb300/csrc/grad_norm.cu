@@ -72,14 +72,15 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks)
     const float* g = t.data[sp.tensor] + sp.at;
     float4 v[4];
     const bool vec = ((uintptr_t)g & 15u) == 0, keep = t.chunks - c <= kGradKept;
+    if (vec && sp.len == kGradChunk) {
+      const float4* at = reinterpret_cast<const float4*>(g) + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = (i * kGradThreads + (int)threadIdx.x) * 4;
-      v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (vec && e + 4 <= sp.len) {
-        const float4* at = reinterpret_cast<const float4*>(g + e);
-        v[i] = keep ? *at : __ldcs(at);
-      } else {
+      for (int i = 0; i < 4; ++i) v[i] = keep ? at[i * kGradThreads] : __ldcs(at + i * kGradThreads);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = (i * kGradThreads + (int)threadIdx.x) * 4;
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (e < sp.len) v[i].x = g[e];
         if (e + 1 < sp.len) v[i].y = g[e + 1];
         if (e + 2 < sp.len) v[i].z = g[e + 2];

@@ -289,34 +289,35 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
   }
 }
 
-// dgamma_q, dgamma_k [D] from the blocks' sums, those of the queries first.  16 columns a
-// block (D is a multiple of 16), 64 threads each, which take every 64th row and are joined
-// eight by eight.
+// dgamma_q, dgamma_k [D] from the blocks' sums, those of the queries first.  Four columns a
+// block (D is a multiple of 16), 256 threads each, so that a thread's few rows are all on
+// their way at once; joined by butterflies and in order.
 __global__ void __launch_bounds__(1024)
     k_qk_dgamma(const float* part, int bq, int bk, int D, float* dgq, float* dgk) {
-  __shared__ float sums[64][17];
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const bool isk = (int)blockIdx.x * 16 >= D;
-  const int c = (int)blockIdx.x * 16 + x - (isk ? D : 0);
+  __shared__ float sums[32][4];
+  const int x = threadIdx.x & 3, y = threadIdx.x >> 2;
+  const bool isk = (int)blockIdx.x * 4 >= D;
+  const int c = (int)blockIdx.x * 4 + x - (isk ? D : 0);
   const float* from = part + (isk ? (int64_t)bq * D : 0) + c;
   const int rows = isk ? bk : bq;
   float s = 0.0f;
-#pragma unroll 16
-  for (int b = y; b < rows; b += 64) s += from[(int64_t)b * D];
-  sums[y][x] = s;
-  __syncthreads();
-  if (y < 8) {
-    s = 0.0f;
+#pragma unroll 8
+  for (int b = y; b < rows; b += 256) s += from[(int64_t)b * D];
+  auto eight = [](float v) {  // over the eight rows of a warp
 #pragma unroll
-    for (int b = 0; b < 8; ++b) s += sums[y + 8 * b][x];
-    sums[y][x] = s;
+    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  };
+  s = eight(s);
+  if ((threadIdx.x & 31) < 4) sums[threadIdx.x >> 5][x] = s;
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    s = eight(sums[y][x]);
+    if ((threadIdx.x & 31) < 4) sums[threadIdx.x >> 5][x] = s;  // its own warp's rows alone
   }
   __syncthreads();
-  if (y == 0) {
-#pragma unroll
-    for (int b = 1; b < 8; ++b) s += sums[b][x];
-    if (PACT_IN(c < D)) (isk ? dgk : dgq)[c] = s;
-  }
+  if (threadIdx.x < 4 && PACT_IN(c < D))
+    (isk ? dgk : dgq)[c] = (sums[0][x] + sums[1][x]) + (sums[2][x] + sums[3][x]);
 }
 
 __global__ void k_rope_turns(const double* inv_freq, int n, int64_t* turns) {
@@ -433,7 +434,7 @@ cudaError_t launch_qk_norm_rope_bwd(RopeParams& p, int pairs, float* dgq, float*
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !dg) return e;
   note_launch();
-  k_qk_dgamma<<<2 * p.D / 16, 1024, 0, st>>>(part, p.side[0].blocks, p.side[1].blocks, p.D, dgq,
+  k_qk_dgamma<<<2 * p.D / 4, 1024, 0, st>>>(part, p.side[0].blocks, p.side[1].blocks, p.D, dgq,
                                                  dgk);
   return cudaGetLastError();
 }

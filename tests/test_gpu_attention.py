@@ -270,6 +270,27 @@ def test_repeats_itself_on_streams_and_in_graphs():
             assert torch.equal(a, b)
 
 
+def test_past_32_bits():
+    """A sequence whose rows lie more than 2^32 bytes, and 2^31 values, into every tensor:
+    the same bits as from tensors of its own."""
+    t, n, h, d = 140000, 300, 128, 128
+    full = [torch.zeros(t, h, d, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    lse = torch.zeros(h, t, device="cuda")
+    own = [normal((n, h, d), 70 + i) for i in range(4)]
+    for a, b in zip(full, own):
+        a[t - n:] = b
+    q, k, v, do, o, dq, dk, dv = full
+    c, c0 = dev([t - n, t]), dev([0, n])
+    pk.pact_attention_fwd(q, k, v, c, c, o=o, lse=lse)
+    pk.pact_attention_bwd(do, q, k, v, o, lse, c, c, dq=dq, dk=dk, dv=dv)
+    pk.pact_check_status()
+    wo, wl = pk.pact_attention_fwd(*own[:3], c0, c0)
+    want = (wo, *pk.pact_attention_bwd(own[3], *own[:3], wo, wl, c0, c0))
+    for a, b in zip(full[4:], want):
+        assert torch.equal(a[t - n:], b) and not a[:t - n].any()
+    assert torch.equal(lse[:, t - n:], wl) and not lse[:, :t - n].any()
+
+
 def test_gradients_against_differences():
     """The kernels' gradients against differences of the 64-bit forward: a step along a
     random direction changes <o, do> by the gradient's product with it."""

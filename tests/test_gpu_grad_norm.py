@@ -122,6 +122,16 @@ def test_repeats_itself_and_replays():
     assert torch.equal(n1, n2) and all(torch.equal(a, b) for a, b in zip(first, outs))
 
 
+def test_past_32_bits():
+    """A tensor of more than 2^31 values; what its end holds counts and is clipped."""
+    t = torch.zeros(2**31 + 5000, device="cuda")
+    t[-3], t[7] = 3.0, 4.0
+    grads = pk.GradList([t])
+    assert pk.pact_clip_grad_norm(grads, 1.0).item() == 5.0
+    assert abs(t[-3].item() - 0.6) < 1e-6 and abs(t[7].item() - 0.8) < 1e-6
+    assert int((t != 0).sum()) == 2
+
+
 def test_refusals():
     a, b = tensors([100, 100])
     for bad in (lambda: pk.GradList([]), lambda: pk.GradList([a.double()]), lambda: pk.GradList([a.cpu()]),

@@ -21,6 +21,7 @@ def test_suite_under_the_debug_build(name):
     pact_build.build_debug()
     env = dict(os.environ, PACT_DEBUG="1")
     env["PYTHONPATH"] = os.pathsep.join(p for p in (ROOT, env.get("PYTHONPATH")) if p)
-    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", os.path.join(HERE, name)],
-                       env=env, cwd=ROOT, capture_output=True, text=True, timeout=900)
+    # cases of tens of gigabytes are left to the release build
+    r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", "-k", "not past_32_bits",
+                        os.path.join(HERE, name)], env=env, cwd=ROOT, capture_output=True, text=True, timeout=900)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]

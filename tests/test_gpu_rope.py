@@ -146,6 +146,23 @@ def test_backward_repeats_itself_and_replays():
         assert torch.equal(a, b)
 
 
+def test_past_32_bits():
+    """The last tokens of tensors of more than 2^31 values: the same bits as from their own."""
+    t, n = 140000, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, dy = (torch.randn(t, 128, 128, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    k, dk = q[:, :1].contiguous(), dy[:, :1].contiguous()
+    gam = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(t, dtype=torch.int32, device="cuda")
+    turns = pk.pact_rope_turns(freqs(128))
+    a = pk.pact_qk_norm_rope(q, k, pos, turns, gam, gam)
+    b = pk.pact_qk_norm_rope(q[-n:], k[-n:], pos[-n:], turns, gam, gam)
+    assert torch.equal(a[0][-n:], b[0]) and torch.equal(a[1][-n:], b[1])
+    a = pk.pact_qk_norm_rope_bwd(dy, dk, pos, turns, q, k, gam, gam)
+    b = pk.pact_qk_norm_rope_bwd(dy[-n:], dk[-n:], pos[-n:], turns, q[-n:], k[-n:], gam, gam)
+    assert torch.equal(a[0][-n:], b[0]) and torch.equal(a[1][-n:], b[1])
+
+
 def test_zero_rows_and_a_zero_eps():
     """A head of zeros under eps > 0 stays zero; its gradient is finite."""
     q, k, pos, (gq, gk), (dyq, dyk) = make(4, 2, 1, 64, True)

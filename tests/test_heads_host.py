@@ -107,6 +107,8 @@ def test_attention_refusals(lib):
         assert attn(lib, n=n) == SHAPE
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert attn(lib, scale=s) == INVALID
+    wide = heads(rows=2**30, n=65536, d=16)
+    assert attn(lib, q=wide, k=wide, v=wide, o=wide, D=16) == SHAPE  # too many tiles
 
 
 def test_attention_backward_refusals(lib):
