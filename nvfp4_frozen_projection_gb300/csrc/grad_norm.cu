@@ -27,15 +27,15 @@ struct GradSpan {
 };
 
 // The tensor and the values of chunk c: the last tensor whose first chunk is not behind it,
-// looked for from tensor `lo` on.
+// looked for from tensor `lo` on, 32 places at a time.  Every lane of the warp calls this.
 __device__ __forceinline__ GradSpan grad_span(const GradTable& t, int64_t c, int64_t lo) {
-  int64_t hi = t.count - 1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (t.first[mid] <= c)
-      lo = mid;
-    else
-      hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  for (int64_t n = t.count - lo; n > 1;) {
+    const int64_t step = (n + 31) >> 5, at = lane * step;
+    const unsigned not_behind = __ballot_sync(0xFFFFFFFFu, at < n && t.first[at < n ? lo + at : lo] <= c);
+    const int64_t by = (31 - __clz(not_behind)) * step;  // lane 0 is always among them
+    lo += by;
+    n = n - by < step ? n - by : step;
   }
   GradSpan s;
   s.tensor = lo;
@@ -129,10 +129,14 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks)
   sum = block_sum(sum, slots);
   __shared__ float shared_coef;
   if (threadIdx.x == 0) {  // alone: FP64 is slow, and a warp takes as long as a thread
-    const double norm = sqrt(sum);
+    // In FP32 where the sum, the norm and the limit are far from its ends: an FP64 root and
+    // quotient are 2 us of latency, and either is rounded to FP32 in the end.
+    const bool usual = sum > 1e-30 && sum < 1e30 && max_norm < 1e30;
+    const double norm = usual ? (double)__fsqrt_rn((float)sum) : sqrt(sum);
     if (blockIdx.x == 0) *norm_out = (float)norm;
     if constexpr (APPLY) {
-      const double q = max_norm / (norm + 1e-6);
+      const double q = usual ? (double)__fdiv_rn((float)max_norm, (float)norm + 1e-6f)
+                             : max_norm / (norm + 1e-6);
       shared_coef = q > 1.0 ? 1.0f : (float)q;  // a NaN stays one
     }
   }

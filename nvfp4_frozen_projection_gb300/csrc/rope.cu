@@ -142,6 +142,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) k_qk_norm_rope(cons
   const int h0 = alive ? (int)(seg - t * sd.chunks) * sd.per : 0;
   const int heads = alive && sl * 8 < p.D && PACT_IN(t < p.T) ? min(sd.per, sd.heads - h0) : 0;
   const Cols cols = lane_cols<PAIRS>(sl, p.rot);
+  const uint16_t* x = sd.x + t * sd.ld + (int64_t)h0 * p.D;
+  uint16_t* out = sd.out + t * sd.ldo + (int64_t)h0 * p.D;
+  uint4 w[U];
+  auto load = [&](int hb) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (hb + i < heads) w[i] = load_cols<PAIRS>(x + (hb + i) * p.D, cols);
+    }
+  };
+  load(0);  // on their way while the angles are computed
   const Turn tn = make_turn<PAIRS>(cols, heads > 0, p.positions[t], p.turns);
   const float inv_d = 1.0f / (float)p.D;
   // u' = u uc - v vs, v' = v vc + u us: the gammas go into the coefficients
@@ -156,15 +167,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) k_qk_norm_rope(cons
     vc[e] = __fmul2_rn(tn.c[e], g.v[e]);
     vs[e] = __fmul2_rn(neg(tn.s[e]), g.v[e]);
   }
-  const uint16_t* x = sd.x + t * sd.ld + (int64_t)h0 * p.D;
-  uint16_t* out = sd.out + t * sd.ldo + (int64_t)h0 * p.D;
   for (int hb = 0; hb < sd.per; hb += U) {
-    uint4 w[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (hb + i < heads) w[i] = load_cols<PAIRS>(x + (hb + i) * p.D, cols);
-    }
+    if (hb > 0) load(hb);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (hb + i >= sd.per) break;  // for the whole block
@@ -214,12 +218,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
     const int64_t t = alive ? seg / sd.chunks : 0;
     const int h0 = alive ? (int)(seg - t * sd.chunks) * sd.per : 0;
     const int heads = alive && sl * 8 < p.D && PACT_IN(t < p.T) ? min(sd.per, sd.heads - h0) : 0;
-    const Turn tn = make_turn<PAIRS>(cols, heads > 0, p.positions[t], p.turns);
     const uint16_t* dy = sd.x + t * sd.ld + (int64_t)h0 * p.D;
     const uint16_t* x = NORM ? sd.xf + t * sd.ldxf + (int64_t)h0 * p.D : nullptr;
     uint16_t* out = sd.out + t * sd.ldo + (int64_t)h0 * p.D;
-    for (int hb = 0; hb < sd.per; hb += U) {
-      uint4 wy[U], wx[U];
+    uint4 wy[U], wx[U];
+    auto load = [&](int hb) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         wy[i] = wx[i] = make_uint4(0, 0, 0, 0);
@@ -228,6 +231,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
           if constexpr (NORM) wx[i] = load_cols<PAIRS>(x + (hb + i) * p.D, cols);
         }
       }
+    };
+    load(0);  // on their way while the angles are computed
+    const Turn tn = make_turn<PAIRS>(cols, heads > 0, p.positions[t], p.turns);
+    for (int hb = 0; hb < sd.per; hb += U) {
+      if (hb > 0) load(hb);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         if (hb + i >= sd.per) break;  // for the whole block
