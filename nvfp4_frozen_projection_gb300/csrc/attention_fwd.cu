@@ -15,6 +15,16 @@
 // S_i may be issued behind the P_i V that reads P_i out of the same columns.  Keys and values
 // pass through one ring of shared memory.
 //
+// What bounds it.  Heads of 128: a pair of tiles against 128 keys has 2048 cycles of products
+// (16 MMAs of 64 cycles for each tile) and takes about 3000 to 3700: the softmax of a tile,
+// 1370 cycles, the signals to and from the issuers, 300, and P V and the next S, 768, follow
+// one another, and the other tile fills the gaps in part.  16384 causal, 16/4 heads of 128: 765
+// us, 1.44 PFLOP/s.  Heads of 64: the softmax alone, 2250 cycles a pair of tiles (its 32768
+// exponentials are 1024); 26 x 1024 causal, 32/8 heads of 64: 164 us.  CTA pairs, which halve
+// what shared memory has to deliver, were slower (16384: 816 us): a tile then waits for the
+// softmax of two CTAs.  A third warpgroup for the end of a unit was slower, too (8 x 1024, 32/8
+// heads of 128: 107 us, 78 without): four warps store two tiles one after the other.
+//
 // The running maximum m of a row moves only when a new one is above it by more than 2^8 in
 // the exponentials' scale: the sums stay far from FP32's range, and the rescaling of O in
 // TMEM that a moved m needs is rare.  P is rounded to BF16 for its product (its sum is of
