@@ -504,11 +504,17 @@ int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pa
  *   nearest of these, a length below zero as zero: no value leads outside the tensors, and
  *   sequences that overlap give unspecified values in their shared rows.
  *   A NaN or an infinity stays within its sequence and its key head.
+ * ws_opt: pact_attention_fwd_workspace_size() bytes, 256-byte aligned, or NULL.  With it, where
+ * there are few tokens for the GPU, the keys of a token are shared out over several CTAs and
+ * their results joined in a fixed order; the size is 0 where that does not pay.
  * Rules: D <= 128; hq % hk == 0; 1 <= nseq <= 2^20; scale finite and > 0.
  */
+size_t pact_attention_fwd_workspace_size(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k,
+                                         int64_t D, int64_t nseq);
 int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_heads* v, int64_t D,
                        const int32_t* cu_q, const int32_t* cu_k, int64_t nseq, int causal,
-                       float scale, pact_heads* o, float* lse, pact_stream_t stream);
+                       float scale, pact_heads* o, float* lse, void* ws_opt, size_t ws_bytes,
+                       pact_stream_t stream);
 
 /*
  * Its backward, which recomputes the probabilities P = exp(scale q k^T - lse):

@@ -123,7 +123,9 @@ _SIGNATURES = {
     "pact_qk_norm_rope_bwd_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
     "pact_qk_norm_rope_bwd": (_int, [_SPH, _SPH, _SPH, _SPH, _i64, _i64, _vp, _vp, _int, _vp, _vp,
                                      _f32, _SPH, _SPH, _vp, _vp, _vp, _sz, _vp]),
-    "pact_attention_fwd": (_int, [_SPH, _SPH, _SPH, _i64, _vp, _vp, _i64, _int, _f32, _SPH, _vp, _vp]),
+    "pact_attention_fwd": (_int, [_SPH, _SPH, _SPH, _i64, _vp, _vp, _i64, _int, _f32, _SPH, _vp, _vp, _sz,
+                                  _vp]),
+    "pact_attention_fwd_workspace_size": (_sz, [_i64] * 6),
     "pact_attention_bwd_workspace_size": (_sz, [_i64, _i64]),
     "pact_attention_bwd": (_int, [_SPH, _SPH, _SPH, _SPH, _SPH, _vp, _i64, _vp, _vp, _i64, _int, _f32,
                                   _SPH, _SPH, _SPH, _vp, _sz, _vp]),
@@ -889,9 +891,11 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: 
     if lse is None:
         lse = torch.empty(shape, dtype=torch.float32, device=q.device)
     _need(lse, torch.float32, shape, "lse", dev)
+    size = lib.pact_attention_fwd_workspace_size(shape[1], shape[0], k.shape[0], k.shape[1], D, n)
+    ws = torch.empty((size,), dtype=torch.uint8, device=q.device) if size else None
     _check(_heads_call(lib, "pact_attention_fwd")(
         at, at + 32, at + 64, D, cu_q.data_ptr(), cu_k.data_ptr(), n, 1 if causal else 0, scale,
-        at + 96, lse.data_ptr(), _raw_stream(dev)))
+        at + 96, lse.data_ptr(), _addr(ws), size, _raw_stream(dev)))
     return o, lse
 
 

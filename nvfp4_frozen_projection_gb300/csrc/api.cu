@@ -1054,8 +1054,7 @@ static int check_attention(const pact_heads* q, const pact_heads* k, const pact_
   p->hk = (int)k->heads;
   p->group = p->hq / p->hk;
   p->D = (int)D;
-  for (p->gp = p->group < 128 ? p->group : 128; p->group % p->gp; --p->gp) {
-  }
+  p->gp = attn_tile_heads(p->group);
   p->tpt = 128 / p->gp;
   p->gp_mul = (uint32_t)((65536 + p->gp - 1) / p->gp);
   p->subs = p->group / p->gp;
@@ -1072,9 +1071,27 @@ static int check_attention(const pact_heads* q, const pact_heads* k, const pact_
   return PACT_OK;
 }
 
+// The parts' lse, and their rows behind it.
+static size_t parts_lse_bytes(int parts, int64_t tq, int64_t hq) {
+  return align256((size_t)parts * tq * hq * 4);
+}
+
+size_t pact_attention_fwd_workspace_size(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k,
+                                         int64_t D, int64_t nseq) {
+  const auto in = [](int64_t x, int64_t most) { return x >= 1 && x <= most; };
+  if (!in(Tq, kFp8MaxRows) || !in(Tk, kFp8MaxRows) || !in(heads_k, 65536) ||
+      !in(heads_q, 65536) || heads_q % heads_k || !in(D, 128) || D % 16 ||
+      !in(nseq, (int64_t)1 << 20))
+    return 0;
+  const int parts = attn_parts(Tq, Tk, nseq, (int)heads_q, (int)heads_k);
+  if (parts == 1) return 0;
+  return parts_lse_bytes(parts, Tq, heads_q) + (size_t)parts * Tq * heads_q * D * 4;
+}
+
 int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_heads* v, int64_t D,
                        const int32_t* cu_q, const int32_t* cu_k, int64_t nseq, int causal,
-                       float scale, pact_heads* o, float* lse, pact_stream_t stream) {
+                       float scale, pact_heads* o, float* lse, void* ws_opt, size_t ws_bytes,
+                       pact_stream_t stream) {
   AttnFwdLaunch L;
   int rc;
   if ((rc = check_attention(q, k, v, D, cu_q, cu_k, nseq, causal, scale, &L.p)) ||
@@ -1082,6 +1099,18 @@ int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_head
     return rc;
   if (!lse) return fail(PACT_ERR_INVALID_ARG, "lse is required");
   if (!aligned(lse, 4)) return fail(PACT_ERR_ALIGN, "lse must be 4-byte aligned");
+  L.p.parts = 1;
+  const size_t need =
+      pact_attention_fwd_workspace_size(q->rows, q->heads, k->rows, k->heads, D, nseq);
+  if (ws_opt) {
+    if (ws_bytes < need || !aligned(ws_opt, 256))
+      return fail(PACT_ERR_INVALID_ARG, "workspace too small or not 256-byte aligned");
+    if (need) {
+      L.p.parts = attn_parts(q->rows, k->rows, nseq, L.p.hq, L.p.hk);
+      L.p.part_lse = (float*)ws_opt;
+      L.p.part_o = (float*)((char*)ws_opt + parts_lse_bytes(L.p.parts, q->rows, q->heads));
+    }
+  }
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   if ((rc = make_heads_map(&L.tmQ, q, D, L.p.gp, L.p.tpt)) ||

@@ -30,6 +30,7 @@
 // TMEM that a moved m needs is rare.  P is rounded to BF16 for its product (its sum is of
 // the FP32 values); sums, maxima and O are FP32.
 #include "attention.cuh"
+#include "dependent.cuh"
 
 namespace pact {
 
@@ -51,7 +52,8 @@ struct FwdCfg {
   static_assert(SMEM <= 232448 && NBARS * 8 <= 384, "shared memory");
 };
 
-template <int DP>
+// PARTS: the key tiles of a unit are cut into p.parts runs, each a unit of its own.
+template <int DP, bool PARTS>
 __global__ void __launch_bounds__(384, 1)
     k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
@@ -104,12 +106,14 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (PARTS) let_dependents_start();
 
   // A unit: tok0[i], the first tokens of its tiles; kend[i], the keys that they see, and nk[i]
   // tiles of them; h0, its first query head.  The copying warp looks the units up and hands
-  // them to the other warps.
-  int q0, lq, lk, tok0[2], kend[2], nk[2], h0;
-  auto set_unit = [&](int4 d, int head) {
+  // them to the other warps.  With PARTS keys are counted from tile `first` on, and there are
+  // `run` tiles of them.
+  int q0, lq, lk, tok0[2], kend[2], nk[2], h0, part = 0;
+  auto set_unit = [&](int4 d, int head, int first, int run) {
     q0 = d.x;
     lq = d.y;
     lk = d.z;
@@ -121,9 +125,11 @@ __global__ void __launch_bounds__(384, 1)
       if (tok0[i] < lq) {
         kend[i] = lk;
         if (p.causal) kend[i] = clampi(min(tok0[i] + p.tpt, lq) + lk - lq, 0, lk);
+        if (PARTS) kend[i] = clampi(kend[i] - first * 128, 0, run * 128);
       }
       nk[i] = (kend[i] + 127) / 128;
     }
+    if (PARTS) lk -= first * 128;
   };
   RingPos slot;
   bool ok = true;
@@ -134,7 +140,8 @@ __global__ void __launch_bounds__(384, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(unit_empty + 8 * slot.stage);
     slot.advance(3);
-    set_unit(a, b.x);
+    set_unit(a, b.x, b.z, b.w);
+    part = b.y >> 1;
     return b.y != 0;
   };
 
@@ -197,30 +204,41 @@ __global__ void __launch_bounds__(384, 1)
       SeqFinder<false> finder = seq_finder<false>(p, 2 * p.tpt);
       Seq s;
       for (uint32_t turn = 0;; ++turn) {
-        const uint32_t u = unit_of(turn), t = p.units_div.div(u);
+        const uint32_t turned = unit_of(turn);
+        const uint32_t u = PARTS ? turned / (uint32_t)p.parts : turned, t = p.units_div.div(u);
         const int hu = (int)(u - t * p.units_h);
         const bool there = u < kMaxUnit && finder.find(t, s);
         kvh = p.subs == 1 ? hu : hu / p.subs;
-        set_unit(make_int4(s.q0, s.lq, s.lk, s.tile * 2 * p.tpt),
-                 kvh * p.group + (hu - kvh * p.subs) * p.gp);
+        const int4 where = make_int4(s.q0, s.lq, s.lk, s.tile * 2 * p.tpt);
+        const int head = kvh * p.group + (hu - kvh * p.subs) * p.gp;
+        int first = 0, run = 0;
+        if (PARTS) {
+          set_unit(where, head, 0, (1 << 24) - 1);
+          const int all = max(nk[0], nk[1]);
+          part = (int)(turned - u * (uint32_t)p.parts);
+          first = (int)((int64_t)all * part / p.parts);
+          run = (int)((int64_t)all * (part + 1) / p.parts) - first;
+        }
+        set_unit(where, head, first, run);
         if (!(ok = mbar_wait(unit_empty + 8 * slot.stage, slot.phase ^ 1u, kAttnWaitNs, abort_flag)))
           break;
         if (lane == 0) {
           int4* d = reinterpret_cast<int4*>(smem + C::UNIT_OFF + 32 * slot.stage);
-          d[0] = make_int4(q0, lq, lk, tok0[0]);
-          d[1] = make_int4(h0, there, 0, 0);
+          d[0] = where;
+          d[1] = make_int4(head, there ? 2 * part + 1 : 0, first, run);
           mbar_arrive(unit_full + 8 * slot.stage);
         }
         __syncwarp();
         slot.advance(3);
         if (!there) break;
+        if (PARTS) s.k0 += first * 128;
         const int n = max(nk[0], nk[1]);
         // in the order of their use: K 0, then (OWN_P) K j + 1 and V j, or V j and K j + 1
         for (int j = -1; j < n && n > 0 && ok; ++j) {
           if (j < 0 && nk[0] > 0) ok = load_q(0);
-          if (!C::OWN_P && j >= 0) ok = ok && load_kv(&tmV, s.k0 + j * 128, s.lk - j * 128);
+          if (!C::OWN_P && j >= 0) ok = ok && load_kv(&tmV, s.k0 + j * 128, lk - j * 128);
           if (j + 1 < n) ok = ok && load_kv(&tmK, s.k0 + (j + 1) * 128, 128);
-          if (C::OWN_P && j >= 0) ok = ok && load_kv(&tmV, s.k0 + j * 128, s.lk - j * 128);
+          if (C::OWN_P && j >= 0) ok = ok && load_kv(&tmV, s.k0 + j * 128, lk - j * 128);
           if (j < 0 && nk[1] > 0) ok = ok && load_q(1);
         }
         if (!ok) break;
@@ -456,12 +474,32 @@ __global__ void __launch_bounds__(384, 1)
       const bool empty = n == 0 || lim <= 0;
       if (row < rows && PACT_IN(q0 + tok < p.tq)) {
         const int h = h0 + row - row_token(p, row) * p.gp;
-        p.lse[(int64_t)h * p.tq + q0 + tok] = empty ? -INFINITY : (m * c + log2f(l)) * kLn2;
+        (PARTS ? p.part_lse + (int64_t)part * p.hq * p.tq : p.lse)[(int64_t)h * p.tq + q0 + tok] =
+            empty ? -INFINITY : (m * c + log2f(l)) * kLn2;
       }
       const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : l;  // a NaN stays one
       if (n > 0) {
         if (!(ok = mbar_wait(o_done + 8 * i, (uses - 1u) & 1u, kAttnWaitNs, abort_flag))) break;
         tc_fence_after();
+      }
+      if (PARTS) {
+        if (n > 0) {
+          const int h = h0 + row - row_token(p, row) * p.gp;
+          float* at = p.part_o + (((int64_t)part * p.tq + q0 + tok) * p.hq + h) * p.D;
+          for (int b = 0; b < p.D; b += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + b, o);
+            tmem_ld_wait16(o);
+            if (row < rows && PACT_IN(q0 + tok < p.tq)) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4*>(at + b + e) =
+                    make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            }
+          }
+        }
+        continue;
       }
       for (int b = 0; b < p.D; b += 64) {
         uint32_t w[32];
@@ -493,25 +531,101 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
+// ------------------------------------------------------------------ the parts together
+//   lse = log sum exp lse_s;  o = sum exp(lse_s - lse) o_s.
+// 2^seg lanes have a row; a warp's rows are heads of one token.  Starts while the forward
+// still runs, and finds out meanwhile whether its token is of a sequence.
+__global__ void __launch_bounds__(256) k_attn_join(const AttnParams p, int seg, int groups) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t t64 = w / groups;
+  const int t = (int)t64, sl = lane & ((1 << seg) - 1);
+  const int h = (int)(w - t64 * groups) * (32 >> seg) + (lane >> seg);
+  // tokens of no sequence stay as they were
+  bool in = false;
+  if (t64 < p.tq)
+    for (int b = lane; b < p.nseq; b += 32) {
+      const int q0 = clampi(__ldg(p.cu_q + b), 0, p.tq);
+      in = in || (t >= q0 && t < clampi(__ldg(p.cu_q + b + 1), q0, p.tq));
+    }
+  in = __any_sync(0xFFFFFFFFu, in);
+  wait_for_prerequisites();
+  if (!in || h >= p.hq || sl * 8 >= p.D) return;
+  const float* ls = p.part_lse + (int64_t)h * p.tq + t;
+  const int64_t step = (int64_t)p.hq * p.tq;
+  float top = -INFINITY;
+  for (int s = 0; s < p.parts; ++s) top = fmaxf(top, ls[s * step]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  const float* at = p.part_o + ((int64_t)t * p.hq + h) * p.D + sl * 8;
+  float sum = 0.0f, acc[8] = {};
+  for (int s = 0; s < p.parts; ++s) {
+    const float l = ls[s * step];
+    if (l == -INFINITY) continue;  // this part saw no key; its row may not be there
+    const float f = ex2_ftz((l - base) * kLog2e);
+    const float4 a = *reinterpret_cast<const float4*>(at + s * step * p.D);
+    const float4 b = *reinterpret_cast<const float4*>(at + s * step * p.D + 4);
+    sum += f;
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = __fmaf_rn(f, x[e], acc[e]);
+  }
+  const bool empty = sum == 0.0f;
+  const float inv = empty ? 0.0f : __fdiv_rn(1.0f, sum);
+  if (!PACT_IN(t < p.tq && h < p.hq)) return;
+  if (sl == 0) p.lse[(int64_t)h * p.tq + t] = empty ? -INFINITY : base + log2f(sum) * kLn2;
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  *reinterpret_cast<uint4*>(p.o + (int64_t)t * p.ldo + (int64_t)h * p.D + sl * 8) =
+      make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Few units leave SMs without work while each goes through all of its keys.  In parts they
+// pay for more ends of units and the join, 3 us and more, so there are no more parts than
+// SMs for them, none of fewer than two tiles, and none at all below 16 tiles of keys a
+// sequence (on average: the lengths are on the device).  In us, one part and with this rule:
+// 8192 causal, one head of 128, 118 and 52; 4096, 2 heads of 64, 49 and 29; 2048, 8/2 heads of
+// 128, 36 and 34; a token over 2048 keys, 8/1 heads, 26 and 13, over 16384, 162 and 27, over
+// 131072, 32/8 heads, 1203 and 100.  More parts than that: 8 x 1 over 2048, 32/8 heads, 26, with
+// two 20, with three 27; 1024 keys (8 tiles): 21, with four 20.
+int attn_parts(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk) {
+  constexpr int64_t kSms = 152, kMost = 32;  // whatever the device has
+  const int gp = attn_tile_heads(hq / hk);
+  const int64_t units = attn_units(tq, 2 * (128 / gp), nseq, (int64_t)(hq / gp));
+  const int64_t tiles = tk / nseq / 128;
+  if (tiles < 16 || units * 2 > kSms) return 1;
+  int64_t parts = kSms / units;
+  if (parts > tiles / 2) parts = tiles / 2;
+  return (int)(parts < kMost ? parts : kMost);
+}
+
+template <int DP, bool PARTS>
+static cudaError_t launch_fwd(const AttnFwdLaunch& L, unsigned grid, cudaStream_t st) {
+  constexpr uint32_t sm = FwdCfg<DP>::SMEM;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(k_attn_fwd<DP, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                sm)))
+    return e;
+  note_launch();
+  k_attn_fwd<DP, PARTS><<<grid, 384, sm, st>>>(L.tmQ, L.tmK, L.tmV, L.p);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_attn_fwd(const AttnFwdLaunch& L, cudaStream_t st) {
   const AttnParams& p = L.p;
-  const int tpu = 2 * p.tpt;
-  const int64_t units = attn_units(p.tq, tpu, p.nseq, p.units_h);
+  const int64_t units = attn_units(p.tq, 2 * p.tpt, p.nseq, p.units_h) * p.parts;
   const unsigned grid = (unsigned)(units < L.num_sms ? units : L.num_sms);
-  cudaError_t e;
+  if (p.parts == 1)
+    return p.D <= 64 ? launch_fwd<64, false>(L, grid, st) : launch_fwd<128, false>(L, grid, st);
+  const cudaError_t e =
+      p.D <= 64 ? launch_fwd<64, true>(L, grid, st) : launch_fwd<128, true>(L, grid, st);
+  if (e) return e;
+  int seg = 1;
+  while (8 << seg < p.D) ++seg;
+  const int groups = (p.hq + (32 >> seg) - 1) / (32 >> seg);
   note_launch();
-  if (p.D <= 64) {
-    constexpr uint32_t sm = FwdCfg<64>::SMEM;
-    if ((e = cudaFuncSetAttribute(k_attn_fwd<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)))
-      return e;
-    k_attn_fwd<64><<<grid, 384, sm, st>>>(L.tmQ, L.tmK, L.tmV, p);
-  } else {
-    constexpr uint32_t sm = FwdCfg<128>::SMEM;
-    if ((e = cudaFuncSetAttribute(k_attn_fwd<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)))
-      return e;
-    k_attn_fwd<128><<<grid, 384, sm, st>>>(L.tmQ, L.tmK, L.tmV, p);
-  }
-  return cudaGetLastError();
+  return launch_dependent(k_attn_join, (unsigned)(((int64_t)p.tq * groups + 7) / 8), 256, 0, st, p,
+                          seg, groups);
 }
 
 }  // namespace pact

@@ -242,6 +242,10 @@ struct AttnParams {
   float* lse;  // [hq, tq]
   uint16_t* o;
   int64_t ldo;
+  // forward with the keys in several parts: what the parts say, FP32
+  int parts;
+  float* part_o;    // [parts, tq, hq, D]
+  float* part_lse;  // [parts, hq, tq]
   // backward
   const uint16_t* o_in;
   const uint16_t* dout;
@@ -251,10 +255,18 @@ struct AttnParams {
   int64_t lddq, lddk, lddv;
   unsigned* status;
 };
+// The query heads of one key head that share a tile: the largest divisor of the group up to 128.
+inline int attn_tile_heads(int group) {
+  int gp = group < 128 ? group : 128;
+  while (group % gp) --gp;
+  return gp;
+}
 // Units at most: whole tiles of all rows, and a ragged one for each sequence, for `heads`.
 inline int64_t attn_units(int64_t rows, int per, int64_t nseq, int64_t heads) {
   return (rows / per + nseq) * heads;
 }
+// Parts that the keys of every unit of the forward are cut into.
+int attn_parts(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
 struct AttnFwdLaunch {
   // BF16 [T, heads, D], boxes of 64 columns, 128-byte swizzle: Q gp heads x tpt tokens, K and
   // V one head x 128 tokens

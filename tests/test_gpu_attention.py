@@ -341,3 +341,83 @@ def test_refusals():
             bad()
     with pytest.raises(pk.PactError):
         pk.pact_attention_fwd(*(torch.zeros(4, 1, 144, device="cuda").bfloat16() for _ in range(3)), a, b)
+
+
+# few tokens over many keys: the keys of a token are shared out over CTAs
+PARTS = [
+    ([1], [2100], 8, 1, 128),
+    ([1], [70001], 4, 2, 16),
+    ([2048], [2048], 1, 1, 128),
+    ([2500], [2500], 2, 1, 64),
+    ([1, 1, 3, 1], [4000, 77, 5000, 1], 6, 2, 96),     # parts without a key
+    ([3, 0, 5], [9000, 500, 0], 4, 4, 112),
+    ([2200], [2048], 1, 1, 48),                        # rows that see nothing
+    ([9], [4096], 5, 1, 80),
+    ([2, 2], [2300, 2300], 130, 1, 32),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,hq,hk,d", PARTS, ids=[f"{max(a)}x{max(b)}h{h}-{g}d{d}" for a, b, h, g, d in PARTS])
+def test_parts_of_the_keys(lq, lk, hq, hk, d, causal):
+    q, k, v, _, cq, ck = make(lq, lk, hq, hk, d, 40)
+    assert pk.load_library().pact_attention_fwd_workspace_size(q.shape[0], hq, k.shape[0], hk, d, len(lq)) > 0
+    o, lse = pk.pact_attention_fwd(q, k, v, dev(cq), dev(ck), causal)
+    pk.pact_check_status()
+    wo, wl, bo, bl = ref.attention(q, k, v, cq, ck, causal, d ** -0.5)
+    ref.check(o, wo, bo, "o")
+    ref.check(lse, wl, bl, "lse")
+    o2, lse2 = pk.pact_attention_fwd(q, k, v, dev(cq), dev(ck), causal)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_parts_leave_other_rows():
+    q, k, v, _, _, _ = make([20], [6000], 4, 2, 64, 50)
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((4, 20), 7.0, device="cuda")
+    args = dev([2, 3, 9]), dev([100, 3000, 5990])
+    pk.pact_attention_fwd(q, k, v, *args, o=o, lse=lse)
+    pk.pact_check_status()
+    wo, wl, bo, bl = ref.attention(q, k, v, [2, 3, 9], [100, 3000, 5990], True, 0.125)
+    ref.check(o, wo, bo, "o")
+    ref.check(lse, wl, bl, "lse")
+    for rows in (slice(0, 2), slice(9, 20)):
+        assert (o[rows] == 7.0).all() and (lse[:, rows] == 7.0).all()
+
+
+def test_parts_keep_a_nan_to_its_head_and_sequence():
+    lq, lk = [1, 4], [5000, 4700]
+    q, k, v, _, cq, ck = make(lq, lk, 4, 2, 64, 60)
+    args = dev(cq), dev(ck)
+    o, lse = pk.pact_attention_fwd(q, k, v, *args)
+    v2, k2 = v.clone(), k.clone()
+    v2[4321, 1] = math.nan      # sequence 0, its second key head
+    k2[9000, 0, 3] = math.nan   # sequence 1, its first
+    o2, lse2 = pk.pact_attention_fwd(q, k2, v2, *args)
+    assert torch.isnan(o2[0, 2:]).all() and torch.isnan(o2[1:, :2]).all() and torch.isnan(lse2[:2, 1:]).all()
+    assert torch.equal(o2[0, :2], o[0, :2]) and torch.equal(o2[1:, 2:], o[1:, 2:])
+    assert torch.equal(lse2[:2, 0], lse[:2, 0]) and torch.equal(lse2[2:], lse[2:])
+
+
+def test_parts_in_graphs_on_two_streams():
+    cases = [make([1], [4000 + 700 * i], 8, 2, 128, 70 + 10 * i) for i in range(2)]
+    want, got, graphs, streams = [], [], [], [torch.cuda.Stream() for _ in cases]
+    for (q, k, v, _, cq, ck), st in zip(cases, streams):
+        a, b = dev(cq), dev(ck)
+        want.append(pk.pact_attention_fwd(q, k, v, a, b))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            out = pk.pact_attention_fwd(q, k, v, a, b)
+            for _ in range(5):
+                out = pk.pact_attention_fwd(q, k, v, a, b, o=out[0], lse=out[1])
+        got.append(out)
+        graphs.append((g, a, b))
+    for _ in range(3):
+        for (g, _, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    pk.pact_check_status()
+    for (o, lse), (wo, wl) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(lse, wl)

@@ -85,10 +85,11 @@ def test_rope_backward_refusals(lib):
         assert lib.pact_qk_norm_rope_bwd_workspace_size(*args) == 0
 
 
-def attn(lib, q=None, k=None, v=None, D=64, cq=P, ck=P, n=2, scale=0.125, o=None, lse=P):
+def attn(lib, q=None, k=None, v=None, D=64, cq=P, ck=P, n=2, scale=0.125, o=None, lse=P, ws=None,
+         size=0):
     return lib.pact_attention_fwd(heads() if q is None else q, heads(n=2) if k is None else k,
                                   heads(n=2) if v is None else v, D, cq, ck, n, 1, scale,
-                                  heads() if o is None else o, lse, None)
+                                  heads() if o is None else o, lse, ws, size, None)
 
 
 def test_attention_refusals(lib):
@@ -109,6 +110,22 @@ def test_attention_refusals(lib):
         assert attn(lib, scale=s) == INVALID
     wide = heads(rows=2**30, n=65536, d=16)
     assert attn(lib, q=wide, k=wide, v=wide, o=wide, D=16) == SHAPE  # too many tiles
+
+
+def test_attention_parts_refusals(lib):
+    def size(tq=4, hq=8, tk=4096, hk=2, d=64, n=1):
+        return lib.pact_attention_fwd_workspace_size(tq, hq, tk, hk, d, n)
+    assert size() > 0 and size() % 4 == 0
+    assert size(tk=2047) == size(tq=8192, hk=8) == size(n=3) == 0  # few keys, enough units
+    for bad in (dict(tq=0), dict(hq=0), dict(tk=0), dict(hk=0), dict(hk=3), dict(d=24), dict(d=144), dict(n=0),
+                dict(tq=2**30 + 1), dict(tk=2**30 + 1), dict(n=2**20 + 1), dict(hq=65552, hk=1), dict(tq=-4)):
+        assert size(**bad) == 0
+
+    def f(ws, n):
+        k = heads(rows=4096, n=2, p=P + 2**21)
+        return attn(lib, q=heads(rows=4, n=8), k=k, v=k, n=1, o=heads(rows=4, n=8, p=P + 2**20), ws=ws, size=n)
+    assert f(P + 64, 1 << 30) == INVALID
+    assert f(P, size() - 1) == INVALID
 
 
 def test_attention_backward_refusals(lib):
