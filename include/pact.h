@@ -523,9 +523,12 @@ int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_head
  * P and dS are rounded to BF16 for their products.  Deterministic: no atomics.
  *   d_o (the gradient of o), o, dq  as q;  dk, dv  as k;  lse  the forward's.
  * Rows of dq, dk and dv that belong to no sequence are left as they were; a key that no
- * query sees gets zeros.  ws: pact_attention_bwd_workspace_size() bytes, 256-byte aligned.
+ * query sees gets zeros.  ws: pact_attention_bwd_workspace_size() bytes, 256-byte aligned;
+ * it also holds what CTAs that share a tile's work add up to (in a fixed order), where there
+ * are few tiles for the GPU.
  */
-size_t pact_attention_bwd_workspace_size(int64_t Tq, int64_t heads_q);
+size_t pact_attention_bwd_workspace_size(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k,
+                                         int64_t D, int64_t nseq);
 int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_heads* k,
                        const pact_heads* v, const pact_heads* o, const float* lse, int64_t D,
                        const int32_t* cu_q, const int32_t* cu_k, int64_t nseq, int causal,

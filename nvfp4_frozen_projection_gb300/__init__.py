@@ -126,7 +126,7 @@ _SIGNATURES = {
     "pact_attention_fwd": (_int, [_SPH, _SPH, _SPH, _i64, _vp, _vp, _i64, _int, _f32, _SPH, _vp, _vp, _sz,
                                   _vp]),
     "pact_attention_fwd_workspace_size": (_sz, [_i64] * 6),
-    "pact_attention_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "pact_attention_bwd_workspace_size": (_sz, [_i64] * 6),
     "pact_attention_bwd": (_int, [_SPH, _SPH, _SPH, _SPH, _SPH, _vp, _i64, _vp, _vp, _i64, _int, _f32,
                                   _SPH, _SPH, _SPH, _vp, _sz, _vp]),
     "pact_grad_chunks": (_i64, [_i64]),
@@ -917,11 +917,11 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                   *_heads(dv, "dv", dev, v.shape))
     at = ctypes.addressof(h)
     # its own scratch in every call: a captured graph then keeps one of its own
-    ws = torch.empty((lib.pact_attention_bwd_workspace_size(q.shape[0], q.shape[1]),),
-                     dtype=torch.uint8, device=q.device)
+    size = lib.pact_attention_bwd_workspace_size(q.shape[0], q.shape[1], k.shape[0], k.shape[1], D, n)
+    ws = torch.empty((size,), dtype=torch.uint8, device=q.device)
     _check(_heads_call(lib, "pact_attention_bwd")(
         at + 96, at, at + 32, at + 64, at + 128, lse.data_ptr(), D, cu_q.data_ptr(), cu_k.data_ptr(),
-        n, 1 if causal else 0, scale, at + 160, at + 192, at + 224, ws.data_ptr(), ws.numel(),
+        n, 1 if causal else 0, scale, at + 160, at + 192, at + 224, ws.data_ptr(), size,
         _raw_stream(dev)))
     return dq, dk, dv
 

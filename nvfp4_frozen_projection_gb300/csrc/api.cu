@@ -1076,13 +1076,16 @@ static size_t parts_lse_bytes(int parts, int64_t tq, int64_t hq) {
   return align256((size_t)parts * tq * hq * 4);
 }
 
+static bool attention_sizes(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k, int64_t D,
+                            int64_t nseq) {
+  const auto in = [](int64_t x, int64_t most) { return x >= 1 && x <= most; };
+  return in(Tq, kFp8MaxRows) && in(Tk, kFp8MaxRows) && in(heads_k, 65536) && in(heads_q, 65536) &&
+         heads_q % heads_k == 0 && in(D, 128) && D % 16 == 0 && in(nseq, (int64_t)1 << 20);
+}
+
 size_t pact_attention_fwd_workspace_size(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k,
                                          int64_t D, int64_t nseq) {
-  const auto in = [](int64_t x, int64_t most) { return x >= 1 && x <= most; };
-  if (!in(Tq, kFp8MaxRows) || !in(Tk, kFp8MaxRows) || !in(heads_k, 65536) ||
-      !in(heads_q, 65536) || heads_q % heads_k || !in(D, 128) || D % 16 ||
-      !in(nseq, (int64_t)1 << 20))
-    return 0;
+  if (!attention_sizes(Tq, heads_q, Tk, heads_k, D, nseq)) return 0;
   const int parts = attn_parts(Tq, Tk, nseq, (int)heads_q, (int)heads_k);
   if (parts == 1) return 0;
   return parts_lse_bytes(parts, Tq, heads_q) + (size_t)parts * Tq * heads_q * D * 4;
@@ -1125,9 +1128,26 @@ int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_head
   return e == cudaSuccess ? PACT_OK : cuda_fail(e, "attention launch");
 }
 
-size_t pact_attention_bwd_workspace_size(int64_t Tq, int64_t heads_q) {
-  if (Tq < 1 || Tq > kFp8MaxRows || heads_q < 1 || heads_q > 65536) return 0;
-  return align256((size_t)Tq * (size_t)heads_q * 4);
+// The backward's workspace: delta, the parts of dq, those of dv and dk.
+struct AttnBwdPlan {
+  int parts, parts_q;
+  size_t part_o, part_kv, bytes;
+};
+static AttnBwdPlan attention_bwd_plan(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k,
+                                      int64_t D, int64_t nseq) {
+  AttnBwdPlan w;
+  w.parts = attn_parts_dq(Tq, Tk, nseq, (int)heads_q, (int)heads_k);
+  w.parts_q = attn_parts_dkdv(Tq, Tk, nseq, (int)heads_q, (int)heads_k);
+  w.part_o = align256((size_t)Tq * heads_q * 4);
+  w.part_kv = w.part_o + (w.parts > 1 ? align256((size_t)w.parts * Tq * heads_q * D * 4) : 0);
+  w.bytes = w.part_kv + (w.parts_q > 1 ? align256((size_t)2 * w.parts_q * Tk * heads_k * D * 4) : 0);
+  return w;
+}
+
+size_t pact_attention_bwd_workspace_size(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k,
+                                         int64_t D, int64_t nseq) {
+  if (!attention_sizes(Tq, heads_q, Tk, heads_k, D, nseq)) return 0;
+  return attention_bwd_plan(Tq, heads_q, Tk, heads_k, D, nseq).bytes;
 }
 
 int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_heads* k,
@@ -1146,7 +1166,9 @@ int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_he
     return rc;
   if (!lse) return fail(PACT_ERR_INVALID_ARG, "lse is required");
   if (!aligned(lse, 4)) return fail(PACT_ERR_ALIGN, "lse must be 4-byte aligned");
-  if (!ws || ws_bytes < pact_attention_bwd_workspace_size(q->rows, q->heads) || !aligned(ws, 256))
+  const AttnBwdPlan plan =
+      attention_bwd_plan(q->rows, q->heads, k->rows, k->heads, D, nseq);
+  if (!ws || ws_bytes < plan.bytes || !aligned(ws, 256))
     return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
@@ -1160,6 +1182,10 @@ int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_he
   L.p.dout = d_o->p;
   L.p.lddo = d_o->ld;
   L.p.delta = (float*)ws;
+  L.p.parts = plan.parts;
+  L.p.parts_q = plan.parts_q;
+  L.p.part_o = (float*)((char*)ws + plan.part_o);
+  L.p.part_kv = (float*)((char*)ws + plan.part_kv);
   L.p.dq = dq->p;
   L.p.dk = dk->p;
   L.p.dv = dv->p;

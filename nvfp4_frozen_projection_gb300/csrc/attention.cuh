@@ -232,6 +232,17 @@ __device__ __forceinline__ uint32_t unit_of(uint32_t i) {
   return i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+// Whether token t is of a sequence.  Every lane of the warp calls this.
+__device__ __forceinline__ bool in_sequence(const int* cu, int nseq, int rows, int64_t t) {
+  bool in = false;
+  if (t < rows)
+    for (int b = threadIdx.x & 31; b < nseq; b += 32) {
+      const int from = clampi(__ldg(cu + b), 0, rows);
+      in = in || (t >= from && t < clampi(__ldg(cu + b + 1), from, rows));
+    }
+  return __any_sync(0xFFFFFFFFu, in);
+}
+
 template <bool OVER_K>
 __device__ __forceinline__ SeqFinder<OVER_K> seq_finder(const AttnParams& p, int per) {
   SeqFinder<OVER_K> f;

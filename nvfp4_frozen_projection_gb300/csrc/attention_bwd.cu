@@ -9,6 +9,8 @@
 // place of the five of one kernel, whose dq would have to be added up in memory over all key
 // tiles, in an order that changes from run to run.  A CTA has one tile of 128 rows; two
 // threads issue the products, two warpgroups hold a row a thread and half its columns each.
+// Where there are few units, those of one of the two are cut up and a fourth launch adds what
+// their parts make, in FP32.
 //
 //   dq:     rows are queries.  TMEM: S (0), dP (128), dS (256, BF16), dq (320).  One thread
 //           issues S of the next keys as soon as this one has been read, the other dP of the
@@ -64,6 +66,28 @@ __global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
 #pragma unroll
   for (int o = SEG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (live && sl == 0 && PACT_IN(t < p.tq && h < p.hq)) p.delta[(int64_t)h * p.tq + t] = sum;
+}
+
+// A row of sums times f, FP32: `cols` columns out of TMEM (zeros, when there is none).
+__device__ __forceinline__ void store_part(float* out, uint32_t ta, int cols, bool store, bool have,
+                                           float f) {
+  for (int b = 0; b < cols; b += 16) {
+    uint32_t o[16];
+    if (have) {
+      tmem_ld16(ta + b, o);
+      tmem_ld_wait16(o);
+    }
+    if (store) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (have && f != 0.0f)
+          x = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                          __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+        *reinterpret_cast<float4*>(out + b + e) = x;
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------ a ring of tiles
@@ -194,7 +218,8 @@ __device__ __forceinline__ BwdBars bwd_bars(uint32_t b, int stages) {
 }
 
 // ------------------------------------------------------------------ dq
-template <int DP>
+// PARTS: the key tiles of a unit are cut into p.parts runs, each a unit of its own.
+template <int DP, bool PARTS>
 __global__ void __launch_bounds__(384, 1)
     k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -247,9 +272,14 @@ __global__ void __launch_bounds__(384, 1)
 
   SeqFinder<false> finder = seq_finder<false>(p, p.tpt);
   Seq s;
-  int tok0, nk, kvh, h0;
+  int tok0, nk, kvh, h0, part = 0;
   auto next_unit = [&](uint32_t u) {
     if (u >= kMaxUnit) return false;
+    if (PARTS) {
+      const uint32_t whole = u / (uint32_t)p.parts;
+      part = (int)(u - whole * (uint32_t)p.parts);
+      u = whole;
+    }
     const uint32_t t = p.units_div.div(u);
     const int hu = (int)(u - t * p.units_h);
     if (!finder.find(t, s)) return false;
@@ -259,6 +289,12 @@ __global__ void __launch_bounds__(384, 1)
     int kend = s.lk;
     if (p.causal) kend = clampi(min(tok0 + p.tpt, s.lq) + s.lk - s.lq, 0, s.lk);
     nk = (kend + 127) / 128;
+    if (PARTS) {  // keys are counted from the first one of this part on
+      const int first = (int)((int64_t)nk * part / p.parts);
+      nk = (int)((int64_t)nk * (part + 1) / p.parts) - first;
+      s.k0 += first * 128;
+      s.lk -= first * 128;
+    }
     return true;
   };
 
@@ -512,6 +548,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       // the search for the next unit runs while the last product does
       const int rows = min(p.tpt, s.lq - tok0) * p.gp, t0 = s.q0 + tok0, head = h0;
+      float* const own = PARTS ? p.part_o + (int64_t)part * p.tq * p.hq * p.D : nullptr;
       more = next_unit(unit_of(++turn));
       if (n > 0) {
         if (!(ok = mbar_wait(B.acc_full, uses & 1u, kAttnWaitNs, abort_flag))) break;
@@ -520,6 +557,13 @@ __global__ void __launch_bounds__(384, 1)
       }
       const int b = half * 64, cols = p.D - b;
       if (cols <= 0) continue;
+      if (PARTS) {
+        const int t = row_token(p, row);
+        const bool store = row < rows && PACT_IN(t0 + t < p.tq);
+        store_part(own + ((int64_t)(t0 + t) * p.hq + head + row - t * p.gp) * p.D + b, tl + 320 + b,
+                   min(cols, 64), store, n > 0, lim > 0 ? p.scale : 0.0f);
+        continue;
+      }
       uint32_t w[32];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -551,7 +595,8 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // ------------------------------------------------------------------ dk and dv
-template <int DP>
+// PARTS: the query tiles of a unit are cut into p.parts_q runs, each a unit of its own.
+template <int DP, bool PARTS>
 __global__ void __launch_bounds__(384, 1)
     k_attn_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -607,12 +652,19 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (PARTS) let_dependents_start();
 
   SeqFinder<true> finder = seq_finder<true>(p, 128);
   Seq s;
-  int key0, kvh, qt0, nqt, n;  // first key; first query tile and how many; times the subgroups
+  // first key; first query tile and how many; iterations, from i0 on, over them and the subgroups
+  int key0, kvh, qt0, nqt, n, i0 = 0, part = 0;
   auto next_unit = [&](uint32_t u) {
     if (u >= kMaxUnit) return false;
+    if (PARTS) {
+      const uint32_t whole = u / (uint32_t)p.parts_q;
+      part = (int)(u - whole * (uint32_t)p.parts_q);
+      u = whole;
+    }
     const uint32_t t = p.hk_div.div(u);
     kvh = (int)(u - t * p.hk);
     if (!finder.find(t, s)) return false;
@@ -621,10 +673,15 @@ __global__ void __launch_bounds__(384, 1)
     if (p.causal) qt0 = clampi(key0 - (s.lk - s.lq), 0, s.lq) / p.tpt;
     nqt = (s.lq + p.tpt - 1) / p.tpt - qt0;
     n = nqt * p.subs;
+    if (PARTS) {
+      i0 = (int)((int64_t)n * part / p.parts_q);
+      n = (int)((int64_t)n * (part + 1) / p.parts_q) - i0;
+    }
     return true;
   };
   // iteration i of a unit: its first query head, and its tile's first token
   auto tile_of = [&](int i, int& h0, int& tok0) {
+    if (PARTS) i += i0;
     const int sub = p.subs == 1 ? 0 : i / nqt;
     h0 = kvh * p.group + sub * p.gp;
     tok0 = (qt0 + i - sub * nqt) * p.tpt;
@@ -931,6 +988,14 @@ __global__ void __launch_bounds__(384, 1)
       uint16_t* out = half ? p.dk : p.dv;
       const int64_t ld = half ? p.lddk : p.lddv;
       const float f = half ? p.scale : 1.0f;
+      if (PARTS) {
+        const int64_t at = (int64_t)s.k0 + key;
+        const bool store = key < s.lk && PACT_IN(at < p.tk);
+        store_part(p.part_kv +
+                       (((half ? p.parts_q : 0) + part) * (int64_t)p.tk + at) * p.hk * p.D + kvh * p.D,
+                   ta, p.D, store, n > 0, f);
+        continue;
+      }
       for (int b = 0; b < p.D; b += 64) {
         const int cols = min(64, p.D - b);
         uint32_t w[32];
@@ -964,18 +1029,110 @@ __global__ void __launch_bounds__(384, 1)
   wait_for_prerequisites();  // done means done with dq, too
 }
 
+// ------------------------------------------------------------------ the parts together
+struct AttnSum {
+  const float* parts;  // [count, rows, heads, D]
+  uint16_t* out;
+  int64_t ld, first;  // warps before these
+  const int* cu;
+  int count, rows, heads, groups;
+};
+struct AttnSums {
+  AttnSum of[3];
+  int n;
+};
+// The sums of the parts in their order.  2^seg lanes have a row; a warp's rows are heads of
+// one token.
+__global__ void __launch_bounds__(256) k_attn_sum(const AttnSums sums, int nseq, int D, int seg) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  AttnSum a = sums.of[0];
+  for (int i = 1; i < sums.n; ++i)
+    if (w >= sums.of[i].first) a = sums.of[i];
+  const int64_t t = (w - a.first) / a.groups;
+  const int h = (int)(w - a.first - t * a.groups) * (32 >> seg) + (lane >> seg);
+  const int c = (lane & ((1 << seg) - 1)) * 8;
+  const bool in = in_sequence(a.cu, nseq, a.rows, t);  // others stay as they were
+  wait_for_prerequisites();
+  if (!in || h >= a.heads || c >= D) return;
+  const int64_t step = (int64_t)a.rows * a.heads * D;
+  const float* at = a.parts + (t * a.heads + h) * D + c;
+  float acc[8] = {};
+  for (int s = 0; s < a.count; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(at + s * step);
+    const float4 y = *reinterpret_cast<const float4*>(at + s * step + 4);
+    acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
+    acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
+  }
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = pack_bf16x2(acc[2 * e], acc[2 * e + 1]);
+  if (PACT_IN(t < a.rows && h < a.heads))
+    *reinterpret_cast<uint4*>(a.out + t * a.ld + (int64_t)h * D + c) =
+        make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Few units leave SMs without work.  dq and dk|dv run beside each other then (the latter takes
+// what SMs the former has left), so that it pays to cut up the one that is by far the longer:
+// dk|dv where query heads share key heads, dq where a few queries see many keys.  There are no
+// more parts than SMs for them, none of fewer than four tiles, and none at all below 16 tiles a
+// unit (on average: the lengths are on the device).  One part and with this rule, us: 8192
+// causal, 8/1 heads of 128, 752 and 464; 2048, 8/2 heads of 128, 96 and 57; 1024, 16/2 heads of
+// 64, 93 and 43; 512, 8/1 heads of 64, 56 and 29; 256 over 2304 keys, 4 heads of 128, 32 and 25.
+// Where both are as long it does not: 4096 both ways, 2 heads of 64, 55 as it is, 80 with dk|dv
+// in two parts, 73 with both.
+static int bwd_parts(int64_t units, int64_t tiles, int64_t others) {
+  constexpr int64_t kSms = 152, kMost = 16;  // whatever the device has
+  if (tiles < 16 || tiles < 2 * others || units * 2 > kSms) return 1;
+  int64_t parts = kSms / units;
+  if (parts > tiles / 4) parts = tiles / 4;
+  return (int)(parts < kMost ? parts : kMost);
+}
+static int64_t query_tiles(int64_t tq, int64_t nseq, int hq, int hk) {
+  return tq * (hq / hk) / (128 * nseq);
+}
+int attn_parts_dq(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk) {
+  const int gp = attn_tile_heads(hq / hk);
+  return bwd_parts(attn_units(tq, 128 / gp, nseq, hq / gp), tk / nseq / 128,
+                   query_tiles(tq, nseq, hq, hk));
+}
+int attn_parts_dkdv(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk) {
+  return bwd_parts(attn_units(tk, 128, nseq, hk), query_tiles(tq, nseq, hq, hk), tk / nseq / 128);
+}
+
 template <int DP>
 static cudaError_t launch_bwd(const AttnBwdLaunch& L, unsigned gq, unsigned gk, cudaStream_t st) {
   constexpr uint32_t sm = BwdCfg<DP>::SMEM;
+  const AttnParams& p = L.p;
+  const auto dq = p.parts > 1 ? k_attn_dq<DP, true> : k_attn_dq<DP, false>;
+  const auto dkdv = p.parts_q > 1 ? k_attn_dkdv<DP, true> : k_attn_dkdv<DP, false>;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(k_attn_dq<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)) ||
-      (e = cudaFuncSetAttribute(k_attn_dkdv<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)))
+  if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)) ||
+      (e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, sm)))
     return e;
   note_launch();
-  k_attn_dq<DP><<<gq, 384, sm, st>>>(L.tmQ, L.tmdO, L.tmK, L.tmV, L.p);
+  dq<<<gq, 384, sm, st>>>(L.tmQ, L.tmdO, L.tmK, L.tmV, p);
   if ((e = cudaGetLastError())) return e;
   note_launch();
-  return launch_dependent(k_attn_dkdv<DP>, gk, 384, sm, st, L.tmQ, L.tmdO, L.tmK, L.tmV, L.p);
+  if ((e = launch_dependent(dkdv, gk, 384, sm, st, L.tmQ, L.tmdO, L.tmK, L.tmV, p))) return e;
+  if (p.parts == 1 && p.parts_q == 1) return cudaSuccess;
+  int seg = 1;
+  while (8 << seg < p.D) ++seg;
+  AttnSums sums = {};
+  int64_t warps = 0;
+  auto add = [&](const float* parts, int count, uint16_t* out, int64_t ld, const int* cu, int rows,
+                 int heads) {
+    const int groups = (heads + (32 >> seg) - 1) / (32 >> seg);
+    sums.of[sums.n++] = AttnSum{parts, out, ld, warps, cu, count, rows, heads, groups};
+    warps += (int64_t)rows * groups;
+  };
+  if (p.parts > 1) add(p.part_o, p.parts, p.dq, p.lddq, p.cu_q, p.tq, p.hq);
+  if (p.parts_q > 1) {
+    add(p.part_kv, p.parts_q, p.dv, p.lddv, p.cu_k, p.tk, p.hk);
+    add(p.part_kv + (int64_t)p.parts_q * p.tk * p.hk * p.D, p.parts_q, p.dk, p.lddk, p.cu_k, p.tk, p.hk);
+  }
+  note_launch();
+  return launch_dependent(k_attn_sum, (unsigned)((warps + 7) / 8), 256, 0, st, sums, p.nseq, p.D, seg);
 }
 
 cudaError_t launch_attn_bwd(const AttnBwdLaunch& L, cudaStream_t st) {
@@ -988,8 +1145,8 @@ cudaError_t launch_attn_bwd(const AttnBwdLaunch& L, cudaStream_t st) {
     k_attn_delta<16><<<(unsigned)((rows + 15) / 16), 256, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t uq = attn_units(p.tq, p.tpt, p.nseq, p.units_h);
-  const int64_t uk = attn_units(p.tk, 128, p.nseq, p.hk);
+  const int64_t uq = attn_units(p.tq, p.tpt, p.nseq, p.units_h) * p.parts;
+  const int64_t uk = attn_units(p.tk, 128, p.nseq, p.hk) * p.parts_q;
   const unsigned gq = (unsigned)(uq < L.num_sms ? uq : L.num_sms);
   const unsigned gk = (unsigned)(uk < L.num_sms ? uk : L.num_sms);
   return p.D <= 64 ? launch_bwd<64>(L, gq, gk, st) : launch_bwd<128>(L, gq, gk, st);

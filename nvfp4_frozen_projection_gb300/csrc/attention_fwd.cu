@@ -541,14 +541,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnParams p, int seg, 
   const int64_t t64 = w / groups;
   const int t = (int)t64, sl = lane & ((1 << seg) - 1);
   const int h = (int)(w - t64 * groups) * (32 >> seg) + (lane >> seg);
-  // tokens of no sequence stay as they were
-  bool in = false;
-  if (t64 < p.tq)
-    for (int b = lane; b < p.nseq; b += 32) {
-      const int q0 = clampi(__ldg(p.cu_q + b), 0, p.tq);
-      in = in || (t >= q0 && t < clampi(__ldg(p.cu_q + b + 1), q0, p.tq));
-    }
-  in = __any_sync(0xFFFFFFFFu, in);
+  const bool in = in_sequence(p.cu_q, p.nseq, p.tq, t64);  // others stay as they were
   wait_for_prerequisites();
   if (!in || h >= p.hq || sl * 8 >= p.D) return;
   const float* ls = p.part_lse + (int64_t)h * p.tq + t;

@@ -242,10 +242,12 @@ struct AttnParams {
   float* lse;  // [hq, tq]
   uint16_t* o;
   int64_t ldo;
-  // forward with the keys in several parts: what the parts say, FP32
-  int parts;
-  float* part_o;    // [parts, tq, hq, D]
+  // units in several parts, of which each says its own in FP32: of keys (o, or dq), and of
+  // queries (dk and dv)
+  int parts, parts_q;
+  float* part_o;    // [parts, tq, hq, D], o or dq
   float* part_lse;  // [parts, hq, tq]
+  float* part_kv;   // [dv or dk, parts_q, tk, hk, D]
   // backward
   const uint16_t* o_in;
   const uint16_t* dout;
@@ -265,8 +267,11 @@ inline int attn_tile_heads(int group) {
 inline int64_t attn_units(int64_t rows, int per, int64_t nseq, int64_t heads) {
   return (rows / per + nseq) * heads;
 }
-// Parts that the keys of every unit of the forward are cut into.
+// Parts that the keys of every unit of the forward are cut into; those of dq, and the parts of
+// the queries of dk|dv.
 int attn_parts(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
+int attn_parts_dq(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
+int attn_parts_dkdv(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
 struct AttnFwdLaunch {
   // BF16 [T, heads, D], boxes of 64 columns, 128-byte swizzle: Q gp heads x tpt tokens, K and
   // V one head x 128 tokens

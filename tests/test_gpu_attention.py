@@ -421,3 +421,47 @@ def test_parts_in_graphs_on_two_streams():
     pk.pact_check_status()
     for (o, lse), (wo, wl) in zip(got, want):
         assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+# few tiles: the work of dk and dv (shared heads), or of dq (many keys), is shared out
+BWD_PARTS = [
+    ([1024], [1024], 16, 2, 64),
+    ([700], [700], 8, 1, 128),
+    ([900, 1, 0, 1100], [900, 70, 5, 1100], 24, 1, 96),
+    ([520, 600], [400, 600], 130, 1, 32),
+    ([200], [2304], 4, 4, 128),
+    ([3, 0, 70], [9000, 500, 40], 4, 2, 48),
+    ([1], [5000], 8, 1, 80),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,hq,hk,d", BWD_PARTS,
+                         ids=[f"{max(a)}x{max(b)}h{h}-{g}d{d}" for a, b, h, g, d in BWD_PARTS])
+def test_backward_in_parts(lq, lk, hq, hk, d, causal):
+    q, k, v, do, cq, ck = make(lq, lk, hq, hk, d, 80)
+    size = pk.load_library().pact_attention_bwd_workspace_size(q.shape[0], hq, k.shape[0], hk, d, len(lq))
+    assert size > 2 * 4 * q.shape[0] * hq + 256
+    o, lse = pk.pact_attention_fwd(q, k, v, dev(cq), dev(ck), causal)
+    got = pk.pact_attention_bwd(do, q, k, v, o, lse, dev(cq), dev(ck), causal)
+    pk.pact_check_status()
+    want, bounds = ref.attention_bwd(do, q, k, v, o, lse, cq, ck, causal, d ** -0.5)
+    for g, w, b, name in zip(got, want, bounds, ("dq", "dk", "dv")):
+        ref.check(g, w, b, name)
+    again = pk.pact_attention_bwd(do, q, k, v, o, lse, dev(cq), dev(ck), causal)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("tq,tk,cq,ck,hq,hk", [(1300, 1200, [7, 500, 1200], [0, 493, 1190], 16, 1),
+                                               (100, 9000, [7, 20, 90], [3, 4000, 8990], 4, 4)])
+def test_backward_in_parts_leaves_other_rows(tq, tk, cq, ck, hq, hk):
+    q, k, v, do, _, _ = make([tq], [tk], hq, hk, 64, 90)
+    args = dev(cq), dev(ck)
+    o, lse = pk.pact_attention_fwd(q, k, v, *args)
+    outs = [torch.full_like(x, 7.0) for x in (q, k, v)]
+    pk.pact_attention_bwd(do, q, k, v, o, lse, *args, dq=outs[0], dk=outs[1], dv=outs[2])
+    pk.pact_check_status()
+    want, bounds = ref.attention_bwd(do, q, k, v, o, lse, cq, ck, True, 0.125)
+    for g, w, b, c, name in zip(outs, want, bounds, (cq, ck, ck), ("dq", "dk", "dv")):
+        ref.check(g, w, b, name)
+        assert (g[:c[0]] == 7.0).all() and (g[c[-1]:] == 7.0).all()

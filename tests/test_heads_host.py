@@ -121,6 +121,15 @@ def test_attention_parts_refusals(lib):
                 dict(tq=2**30 + 1), dict(tk=2**30 + 1), dict(n=2**20 + 1), dict(hq=65552, hk=1), dict(tq=-4)):
         assert size(**bad) == 0
 
+    def back(tq, hq, tk, hk, d=64, n=1):
+        return lib.pact_attention_bwd_workspace_size(tq, hq, tk, hk, d, n)
+    own = 2048 * 8 * 4
+    assert back(2048, 8, 2048, 8) == own                       # every head has its keys
+    assert back(2048, 8, 2048, 1) > own + 2 * 2 * 2048 * 64 * 4  # shared heads: dk and dv in parts
+    assert back(64, 8, 4096, 8) > 64 * 8 * 64 * 2 * 4            # many keys: dq in parts
+    for bad in ((0, 8, 8, 8), (8, 8, 8, 3), (8, 8, 0, 8), (8, 8, 8, 8, 24), (8, 8, 8, 8, 64, 0)):
+        assert back(*bad) == 0
+
     def f(ws, n):
         k = heads(rows=4096, n=2, p=P + 2**21)
         return attn(lib, q=heads(rows=4, n=8), k=k, v=k, n=1, o=heads(rows=4, n=8, p=P + 2**20), ws=ws, size=n)
@@ -132,9 +141,9 @@ def test_attention_backward_refusals(lib):
     def f(do=heads(), o=heads(), dq=heads(), dk=heads(n=2), lse=P, ws=P, size=1 << 30):
         return lib.pact_attention_bwd(do, heads(), heads(n=2), heads(n=2), o, lse, 64, P, P, 1, 1, 0.125, dq, dk,
                                       heads(n=2), ws, size, None)
-    need = lib.pact_attention_bwd_workspace_size(8, 4)
+    need = lib.pact_attention_bwd_workspace_size(8, 4, 8, 2, 64, 1)
     assert need >= 8 * 4 * 4
-    assert lib.pact_attention_bwd_workspace_size(0, 4) == 0
+    assert lib.pact_attention_bwd_workspace_size(0, 4, 8, 2, 64, 1) == 0
     assert f(do=heads(rows=9)) == SHAPE
     assert f(o=heads(p=0)) == INVALID
     assert f(dq=heads(n=2)) == SHAPE
