@@ -746,6 +746,7 @@ def _heads(t, name, dev, like=None) -> tuple:
 # structure for each costs twice as much, which a call on one token would notice.
 _HEADS = {n: _i64 * (4 * n) for n in (4, 6, 8)}
 _FAST = {}
+_DENSE = torch.contiguous_format  # outputs of inputs with strides have none
 
 
 def _heads_call(lib, name):
@@ -800,9 +801,9 @@ def pact_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
         raise ValueError(f"q has heads of {D}, k of {k.shape[2]}")
     rot = _need_rope(positions, turns, gamma_q, gamma_k, T, D, dev)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty_like(q, memory_format=_DENSE)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+        k_out = torch.empty_like(k, memory_format=_DENSE)
     h = _HEADS[4](*hq, *hk, *_heads(q_out, "q_out", dev, q.shape), *_heads(k_out, "k_out", dev, k.shape))
     at = ctypes.addressof(h)
     _check(_heads_call(lib, "pact_qk_norm_rope")(
@@ -833,9 +834,9 @@ def pact_qk_norm_rope_bwd(dyq: torch.Tensor, dyk: torch.Tensor, positions: torch
     xq = _heads(q, "q", dev, dyq.shape) if q is not None else none
     xk = _heads(k, "k", dev, dyk.shape) if k is not None else none
     if dq is None:
-        dq = torch.empty(dyq.shape, dtype=torch.bfloat16, device=dyq.device)
+        dq = torch.empty_like(dyq, memory_format=_DENSE)
     if dk is None:
-        dk = torch.empty(dyk.shape, dtype=torch.bfloat16, device=dyq.device)
+        dk = torch.empty_like(dyk, memory_format=_DENSE)
     h = _HEADS[6](*sq, *sk, *xq, *xk, *_heads(dq, "dq", dev, dyq.shape), *_heads(dk, "dk", dev, dyk.shape))
     at = ctypes.addressof(h)
     grads = []
@@ -884,15 +885,18 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: 
     dev = torch.cuda.current_device()
     fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
     if o is None:
-        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        o = torch.empty_like(q, memory_format=_DENSE)
     h = _HEADS[4](*fields, *_heads(o, "o", dev, q.shape))
     at = ctypes.addressof(h)
     shape = (q.shape[1], q.shape[0])
     if lse is None:
         lse = torch.empty(shape, dtype=torch.float32, device=q.device)
     _need(lse, torch.float32, shape, "lse", dev)
-    size = lib.pact_attention_fwd_workspace_size(shape[1], shape[0], k.shape[0], k.shape[1], D, n)
-    ws = torch.empty((size,), dtype=torch.uint8, device=q.device) if size else None
+    Tk, size, ws = k.shape[0], 0, None
+    if Tk >= 2048 * n:  # fewer keys never take a workspace: the question costs a small call 1 us
+        size = lib.pact_attention_fwd_workspace_size(shape[1], shape[0], Tk, k.shape[1], D, n)
+        # its own in every call, as for the backward
+        ws = torch.empty((size,), dtype=torch.uint8, device=q.device) if size else None
     _check(_heads_call(lib, "pact_attention_fwd")(
         at, at + 32, at + 64, D, cu_q.data_ptr(), cu_k.data_ptr(), n, 1 if causal else 0, scale,
         at + 96, lse.data_ptr(), _addr(ws), size, _raw_stream(dev)))
@@ -911,7 +915,7 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
     fields += _heads(do, "do", dev, q.shape) + _heads(o, "o", dev, q.shape)
     _need(lse, torch.float32, (q.shape[1], q.shape[0]), "lse", dev)
-    dq, dk, dv = (torch.empty(x.shape, dtype=torch.bfloat16, device=q.device) if g is None else g
+    dq, dk, dv = (torch.empty_like(x, memory_format=_DENSE) if g is None else g
                   for g, x in ((dq, q), (dk, k), (dv, v)))
     h = _HEADS[8](*fields, *_heads(dq, "dq", dev, q.shape), *_heads(dk, "dk", dev, k.shape),
                   *_heads(dv, "dv", dev, v.shape))
@@ -966,9 +970,9 @@ def _need_list(g, name, dev):
         raise ValueError(f"{name} is on cuda:{g.device}, the current device is cuda:{dev}")
 
 
-def _grad_scratch(norm, dev, lib):
+def _grad_scratch(grads, norm, dev, lib):
     if norm is None:
-        norm = torch.empty((1,), dtype=torch.float32, device=f"cuda:{dev}")
+        norm = torch.empty((1,), dtype=torch.float32, device=grads._table.device)
     _need(norm, torch.float32, (1,), "norm", dev)
     # its own scratch in every call: a captured graph then keeps one of its own
     return norm, torch.empty((lib.pact_grad_norm_workspace_size(),), dtype=torch.uint8,
@@ -980,7 +984,7 @@ def pact_grad_norm(grads: GradList, norm: torch.Tensor | None = None) -> torch.T
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
     _need_list(grads, "grads", dev)
-    norm, ws = _grad_scratch(norm, dev, lib)
+    norm, ws = _grad_scratch(grads, norm, dev, lib)
     _check(lib.pact_grad_norm(grads._struct, _addr(norm), _addr(ws), ws.numel(), _raw_stream(dev)))
     return norm
 
@@ -999,7 +1003,7 @@ def pact_clip_grad_norm(grads: GradList, max_norm: float, norm: torch.Tensor | N
         _need_list(out, "out", dev)
         if out.numels != grads.numels:
             raise ValueError("out must list tensors of the same sizes as grads")
-    norm, ws = _grad_scratch(norm, dev, lib)
+    norm, ws = _grad_scratch(grads, norm, dev, lib)
     _check(lib.pact_clip_grad_norm(grads._struct, out.data, float(max_norm), _addr(norm), _addr(ws),
                                    ws.numel(), _raw_stream(dev)))
     return norm
