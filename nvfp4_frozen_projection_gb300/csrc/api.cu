@@ -1086,7 +1086,7 @@ static bool attention_sizes(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t hea
 size_t pact_attention_fwd_workspace_size(int64_t Tq, int64_t heads_q, int64_t Tk, int64_t heads_k,
                                          int64_t D, int64_t nseq) {
   if (!attention_sizes(Tq, heads_q, Tk, heads_k, D, nseq)) return 0;
-  const int parts = attn_parts(Tq, Tk, nseq, (int)heads_q, (int)heads_k);
+  const int parts = attn_fwd_plan(Tq, Tk, nseq, (int)heads_q, (int)heads_k).parts;
   if (parts == 1) return 0;
   return parts_lse_bytes(parts, Tq, heads_q) + (size_t)parts * Tq * heads_q * D * 4;
 }
@@ -1102,14 +1102,16 @@ int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_head
     return rc;
   if (!lse) return fail(PACT_ERR_INVALID_ARG, "lse is required");
   if (!aligned(lse, 4)) return fail(PACT_ERR_ALIGN, "lse must be 4-byte aligned");
+  const AttnFwdPlan plan = attn_fwd_plan(q->rows, k->rows, nseq, L.p.hq, L.p.hk);
   L.p.parts = 1;
+  L.p.unit_tiles = plan.unit_tiles;
   const size_t need =
       pact_attention_fwd_workspace_size(q->rows, q->heads, k->rows, k->heads, D, nseq);
   if (ws_opt) {
     if (ws_bytes < need || !aligned(ws_opt, 256))
       return fail(PACT_ERR_INVALID_ARG, "workspace too small or not 256-byte aligned");
     if (need) {
-      L.p.parts = attn_parts(q->rows, k->rows, nseq, L.p.hq, L.p.hk);
+      L.p.parts = plan.parts;
       L.p.part_lse = (float*)ws_opt;
       L.p.part_o = (float*)((char*)ws_opt + parts_lse_bytes(L.p.parts, q->rows, q->heads));
     }

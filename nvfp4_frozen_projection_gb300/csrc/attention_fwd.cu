@@ -25,8 +25,8 @@
 // softmax of two CTAs.  A third warpgroup for the end of a unit was slower, too (8 x 1024, 32/8
 // heads of 128: 107 us, 78 without): four warps store two tiles one after the other.
 //
-// Where there are few units, their keys are cut into parts, units of their own, and a second
-// kernel joins what these say of a row (attn_parts).  A token over many keys is then bound by
+// Where there are few units, they have one tile, and their keys are cut into parts, units of
+// their own, and a second kernel joins what these say of a row (attn_fwd_plan).  A token over many keys is then bound by
 // HBM: 131072 keys, 32/8 heads of 128, 100 us, 5.4 TB/s; 16 of them over 16384 each, 165 us, 6.5.
 //
 // The running maximum m of a row moves only when a new one is above it by more than 2^8 in
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(384, 1)
     h0 = head;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      tok0[i] = d.w + i * p.tpt;
+      tok0[i] = i < p.unit_tiles ? d.w + i * p.tpt : lq;
       kend[i] = 0;
       if (tok0[i] < lq) {
         kend[i] = lk;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         return true;
       };
-      SeqFinder<false> finder = seq_finder<false>(p, 2 * p.tpt);
+      SeqFinder<false> finder = seq_finder<false>(p, p.unit_tiles * p.tpt);
       Seq s;
       for (uint32_t turn = 0;; ++turn) {
         const uint32_t turned = unit_of(turn);
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(384, 1)
         const int hu = (int)(u - t * p.units_h);
         const bool there = u < kMaxUnit && finder.find(t, s);
         kvh = p.subs == 1 ? hu : hu / p.subs;
-        const int4 where = make_int4(s.q0, s.lq, s.lk, s.tile * 2 * p.tpt);
+        const int4 where = make_int4(s.q0, s.lq, s.lk, s.tile * p.unit_tiles * p.tpt);
         const int head = kvh * p.group + (hu - kvh * p.subs) * p.gp;
         int first = 0, run = 0;
         if (PARTS) {
@@ -577,23 +577,36 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnParams p, int seg, 
       make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Few units leave SMs without work while each goes through all of its keys.  In parts they
-// pay for more ends of units and the join, 3 us and more, so there are no more parts than
-// SMs for them, none of fewer than two tiles, and none at all below 16 tiles of keys a
-// sequence (on average: the lengths are on the device).  In us, one part and with this rule:
-// 8192 causal, one head of 128, 118 and 52; 4096, 2 heads of 64, 49 and 29; 2048, 8/2 heads of
-// 128, 36 and 34; a token over 2048 keys, 8/1 heads, 26 and 13, over 16384, 162 and 27, over
-// 131072, 32/8 heads, 1203 and 100.  More parts than that: 8 x 1 over 2048, 32/8 heads, 26, with
-// two 20, with three 27; 1024 keys (8 tiles): 21, with four 20.
-int attn_parts(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk) {
-  constexpr int64_t kSms = 152, kMost = 32;  // whatever the device has
-  const int gp = attn_tile_heads(hq / hk);
-  const int64_t units = attn_units(tq, 2 * (128 / gp), nseq, (int64_t)(hq / gp));
-  const int64_t tiles = tk / nseq / 128;
+// ------------------------------------------------------------------ few units
+// They leave SMs without work while each goes through all of its keys.
+constexpr int64_t kSms = 152;  // whatever the device has
+
+// Keys in parts pay for more ends of units and the join, 3 us and more, so there are no more
+// parts than SMs for them, none of fewer than two tiles, and none at all below 16 tiles of keys
+// a sequence (on average: the lengths are on the device).  One part and with this rule, us: 8192
+// causal, one head of 128, 118 and 52; 4096, 2 heads of 64, 49 and 29; a token over 2048 keys,
+// 8/1 heads, 26 and 13, over 16384, 162 and 27, over 131072, 32/8 heads, 1203 and 100.  More
+// parts than that: 8 x 1 over 2048, 32/8 heads, 26, with two 20, with three 27; 1024 keys (8
+// tiles): 21, with four 20.
+static int parts_of(int64_t units, int64_t tiles) {
   if (tiles < 16 || units * 2 > kSms) return 1;
   int64_t parts = kSms / units;
   if (parts > tiles / 2) parts = tiles / 2;
-  return (int)(parts < kMost ? parts : kMost);
+  return (int)(parts < 32 ? parts : 32);
+}
+
+// Units of one tile, where that many do not fill the SMs, go through their keys faster than
+// units of two, which share the tensor cores: 1024, 8 heads of 128, 16.0 us for 20.8; 2048, 8/2
+// heads, 27.7 for 33.9; 512, 2 heads, 11.3 for 14.0.  Two tiles do more work in the same time,
+// which tells where more parts make up for fewer units: 8192, one head of 128, 52 us for 57.
+AttnFwdPlan attn_fwd_plan(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk) {
+  const int gp = attn_tile_heads(hq / hk), tpt = 128 / gp;
+  const int64_t tiles = tk / nseq / 128;
+  const int64_t one = attn_units(tq, tpt, nseq, hq / gp);
+  const int64_t two = attn_units(tq, 2 * tpt, nseq, hq / gp);
+  const int p1 = parts_of(one, tiles), p2 = parts_of(two, tiles);
+  if (two * 2 > kSms || (p2 >= 4 && p1 < p2)) return AttnFwdPlan{2, p2};
+  return AttnFwdPlan{1, p1};
 }
 
 template <int DP, bool PARTS>
@@ -610,7 +623,7 @@ static cudaError_t launch_fwd(const AttnFwdLaunch& L, unsigned grid, cudaStream_
 
 cudaError_t launch_attn_fwd(const AttnFwdLaunch& L, cudaStream_t st) {
   const AttnParams& p = L.p;
-  const int64_t units = attn_units(p.tq, 2 * p.tpt, p.nseq, p.units_h) * p.parts;
+  const int64_t units = attn_units(p.tq, p.unit_tiles * p.tpt, p.nseq, p.units_h) * p.parts;
   const unsigned grid = (unsigned)(units < L.num_sms ? units : L.num_sms);
   if (p.parts == 1)
     return p.D <= 64 ? launch_fwd<64, false>(L, grid, st) : launch_fwd<128, false>(L, grid, st);

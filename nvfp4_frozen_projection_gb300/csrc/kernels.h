@@ -242,6 +242,7 @@ struct AttnParams {
   float* lse;  // [hq, tq]
   uint16_t* o;
   int64_t ldo;
+  int unit_tiles;  // query tiles of a unit of the forward
   // units in several parts, of which each says its own in FP32: of keys (o, or dq), and of
   // queries (dk and dv)
   int parts, parts_q;
@@ -267,9 +268,12 @@ inline int attn_tile_heads(int group) {
 inline int64_t attn_units(int64_t rows, int per, int64_t nseq, int64_t heads) {
   return (rows / per + nseq) * heads;
 }
-// Parts that the keys of every unit of the forward are cut into; those of dq, and the parts of
-// the queries of dk|dv.
-int attn_parts(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
+// Query tiles of a unit of the forward, 1 or 2, and parts that its keys are cut into.
+struct AttnFwdPlan {
+  int unit_tiles, parts;
+};
+AttnFwdPlan attn_fwd_plan(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
+// Parts that the keys of the units of dq are cut into, and the queries of those of dk|dv.
 int attn_parts_dq(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
 int attn_parts_dkdv(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk);
 struct AttnFwdLaunch {

@@ -371,6 +371,21 @@ def test_parts_of_the_keys(lq, lk, hq, hk, d, causal):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_one_part_without_a_workspace():
+    q, k, v, _, cq, ck = make([40], [5000], 4, 2, 64, 45)
+    a, b = dev(cq), dev(ck)
+    o, lse = torch.empty_like(q), torch.empty(4, 40, device="cuda")
+    fields = [pk._HeadsStruct(t.data_ptr(), *t.shape[:2], t.stride(0)) for t in (q, k, v, o)]
+    lib = pk.load_library()
+    rc = lib.pact_attention_fwd(*fields[:3], 64, a.data_ptr(), b.data_ptr(), 1, 1, 0.125, fields[3], lse.data_ptr(),
+                                None, 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    pk.pact_check_status()
+    wo, wl, bo, bl = ref.attention(q, k, v, cq, ck, True, 0.125)
+    ref.check(o, wo, bo, "o")
+    ref.check(lse, wl, bl, "lse")
+
+
 def test_parts_leave_other_rows():
     q, k, v, _, _, _ = make([20], [6000], 4, 2, 64, 50)
     o = torch.full_like(q, 7.0)
