@@ -595,17 +595,19 @@ static int parts_of(int64_t units, int64_t tiles) {
   return (int)(parts < 32 ? parts : 32);
 }
 
-// Units of one tile, where that many do not fill the SMs, go through their keys faster than
-// units of two, which share the tensor cores: 1024, 8 heads of 128, 16.0 us for 20.8; 2048, 8/2
-// heads, 27.7 for 33.9; 512, 2 heads, 11.3 for 14.0.  Two tiles do more work in the same time,
-// which tells where more parts make up for fewer units: 8192, one head of 128, 52 us for 57.
+// Units of one tile go through their keys faster than units of two, which share the tensor
+// cores, and where there are few units it is the longest that counts: 1024, 8 heads of 128, 16.0
+// us for 20.8; 2048, 16 heads, 29.3 for 36.2; 4000, 8/4 heads, 51 for 65; 512, 2 heads, 11.3 for
+// 14.0.  Two tiles do more work in the same time, which tells where all SMs are at work: 8192,
+// 8/1 heads, 119 us for 153; 6 x 900, 8/2 heads, 20.5 for 24.2; 4 x 500, 16/4 heads of 64, 11.9
+// for 15.0; and where parts make up for fewer units: 8192, one head, 52 for 57.
 AttnFwdPlan attn_fwd_plan(int64_t tq, int64_t tk, int64_t nseq, int hq, int hk) {
   const int gp = attn_tile_heads(hq / hk), tpt = 128 / gp;
   const int64_t tiles = tk / nseq / 128;
   const int64_t one = attn_units(tq, tpt, nseq, hq / gp);
   const int64_t two = attn_units(tq, 2 * tpt, nseq, hq / gp);
   const int p1 = parts_of(one, tiles), p2 = parts_of(two, tiles);
-  if (two * 2 > kSms || (p2 >= 4 && p1 < p2)) return AttnFwdPlan{2, p2};
+  if (two > (tiles < 5 ? kSms / 2 : kSms) || (p2 >= 4 && p1 < p2)) return AttnFwdPlan{2, p2};
   return AttnFwdPlan{1, p1};
 }
 
