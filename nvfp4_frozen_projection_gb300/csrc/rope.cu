@@ -301,10 +301,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
 
 // dgamma_q, dgamma_k [D] from the blocks' sums, those of the queries first.  Four columns a
 // block (D is a multiple of 16), 256 threads each, so that a thread's few rows are all on
-// their way at once; joined by butterflies and in order.
+// their way at once; joined by butterflies and in order.  The joined sums have an
+// array of their own: a warp that is ahead must not store over rows that another has yet to
+// read.
 __global__ void __launch_bounds__(1024)
     k_qk_dgamma(const float* part, int bq, int bk, int D, float* dgq, float* dgk) {
-  __shared__ float sums[32][4];
+  __shared__ float sums[32][4], joined[4][4];
   const int x = threadIdx.x & 3, y = threadIdx.x >> 2;
   const bool isk = (int)blockIdx.x * 4 >= D;
   const int c = (int)blockIdx.x * 4 + x - (isk ? D : 0);
@@ -323,11 +325,11 @@ __global__ void __launch_bounds__(1024)
   __syncthreads();
   if (threadIdx.x < 128) {
     s = eight(sums[y][x]);
-    if ((threadIdx.x & 31) < 4) sums[threadIdx.x >> 5][x] = s;  // its own warp's rows alone
+    if ((threadIdx.x & 31) < 4) joined[threadIdx.x >> 5][x] = s;
   }
   __syncthreads();
   if (threadIdx.x < 4 && PACT_IN(c < D))
-    (isk ? dgk : dgq)[c] = (sums[0][x] + sums[1][x]) + (sums[2][x] + sums[3][x]);
+    (isk ? dgk : dgq)[c] = (joined[0][x] + joined[1][x]) + (joined[2][x] + joined[3][x]);
 }
 
 __global__ void k_rope_turns(const double* inv_freq, int n, int64_t* turns) {
