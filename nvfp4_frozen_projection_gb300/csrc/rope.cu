@@ -260,7 +260,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
             dot = __ffma2_rn(d.u[e], n.u[e], dot);
             dot = __ffma2_rn(d.v[e], n.v[e], dot);
           }
-          const float rstd = rstd_of(seg_sum<SEG>(ss.x + ss.y), inv_d, p.eps);
+          // a head that is not there has no norm: with eps 0 its rstd would be infinite
+          const float there = rstd_of(seg_sum<SEG>(ss.x + ss.y), inv_d, p.eps);
+          const float rstd = hb + i < heads ? there : 0.0f;
           const float c = seg_sum<SEG>(dot.x + dot.y) * rstd * inv_d;  // mean(dn n)
           const float2 r = both(rstd), mc = both(-c);
 #pragma unroll
