@@ -462,7 +462,8 @@ int pact_rope_turns(const double* inv_freq, int64_t n, int64_t* turns, pact_stre
  *   (a, b) = (z[i], z[i + rot/2]), or with interleaved != 0 (z[2i], z[2i + 1]);
  *   columns from rot on stay as they are.
  * FP32 arithmetic, one rounding at the end; the angle is exact before its rounding to FP32.
- *   q, k, q_out, k_out  heads [T, hq, D] and [T, hk, D]; an output may be its own input;
+ *   q, k, q_out, k_out  heads [T, hq, D] and [T, hk, D]; an output may be its own input, and
+ *   shares no memory with the other's input or output;
  *   positions  INT32 [T], any value;  turns  [rot/2] (pact_rope_turns);
  *   gamma_q_opt, gamma_k_opt  BF16 [D], both or neither, 16-byte aligned.
  * Rules: D <= 256; rot % 16 == 0, 16 <= rot <= D; eps finite and >= 0.
@@ -477,7 +478,8 @@ int pact_qk_norm_rope(const pact_heads* q, const pact_heads* k, int64_t D, int64
  *   dx = (dn - n mean(dn n)) / sqrt(mean(x^2) + eps)   (dx = g without gammas);
  *   dgamma = sum over tokens and heads g n.
  *   dyq, dyk  the gradients of q_out and k_out;  q_opt, k_opt  the forward's inputs, needed
- *   with gammas and unused without;  dq, dk  outputs, each may be dyq or dyk, or q or k;
+ *   with gammas and unused without;  dq, dk  outputs: dq may be dyq or q, dk may be dyk or k,
+ *   and neither shares memory with the other or with what belongs to the other;
  *   dgamma_q_opt, dgamma_k_opt  FP32 [D], both or neither (with gammas only), overwritten.
  * ws: pact_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned, when dgamma is asked
  * for.  Deterministic.  Other rules as for the forward.
@@ -498,7 +500,8 @@ int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pa
  *   o = softmax(scale q k^T) v over the keys seen;  lse = log(sum exp(scale q k^T)), natural.
  * A query that sees no key gets o = 0 and lse = -inf.  FP32 sums; the probabilities are
  * rounded to BF16 for their product with v.
- *   q, o  heads [Tq, hq, D];  k, v  heads [Tk, hk, D];  lse  FP32 [hq, Tq];
+ *   q, o  heads [Tq, hq, D];  k, v  heads [Tk, hk, D];  lse  FP32 [hq, Tq];  o may be q, and
+ *   o and lse share no memory with anything else;
  *   cu_q, cu_k  INT32 [nseq + 1], ascending, on the device.  Rows of o and lse that belong
  *   to no sequence are left as they were.  Values of cu outside [0, T] are taken as the
  *   nearest of these, a length below zero as zero: no value leads outside the tensors, and
@@ -521,7 +524,8 @@ int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_head
  *   delta = sum_d do o;  dv = P^T do;  dS = P (do v^T - delta);
  *   dq = scale dS k;  dk = scale dS^T q, dk and dv summed over the query heads of a key head.
  * P and dS are rounded to BF16 for their products.  Deterministic: no atomics.
- *   d_o (the gradient of o), o, dq  as q;  dk, dv  as k;  lse  the forward's.
+ *   d_o (the gradient of o), o, dq  as q;  dk, dv  as k;  lse  the forward's;  dq, dk and dv
+ *   share no memory with one another or with an input.
  * Rows of dq, dk and dv that belong to no sequence are left as they were; a key that no
  * query sees gets zeros.  ws: pact_attention_bwd_workspace_size() bytes, 256-byte aligned;
  * it also holds what CTAs that share a tile's work add up to (in a fixed order), where there

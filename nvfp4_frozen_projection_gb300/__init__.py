@@ -879,8 +879,8 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: 
                        o: torch.Tensor | None = None, lse: torch.Tensor | None = None):
     """Attention over packed sequences: q [Tq, hq, D], k and v [Tk, hk, D], sequence b at
     rows cu_q[b]:cu_q[b + 1] and cu_k[b]:cu_k[b + 1] (int32, on the device).  scale is
-    1 / sqrt(D) by default.  Returns (o [Tq, hq, D], lse FP32 [hq, Tq]); rows of no
-    sequence are left as they were."""
+    1 / sqrt(D) by default.  o may be q.  Returns (o [Tq, hq, D], lse FP32 [hq, Tq]); rows of
+    no sequence are left as they were."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
     fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
@@ -909,7 +909,8 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                        dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
                        dv: torch.Tensor | None = None):
     """Backward of pact_attention_fwd from its inputs, its o and lse and the gradient do of
-    o.  Returns (dq, dk, dv); rows of no sequence are left as they were."""
+    o.  Returns (dq, dk, dv), which share no memory with one another or an input; rows of no
+    sequence are left as they were."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
     fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)

@@ -192,18 +192,40 @@ int check_heads(const pact_heads* t, const char* name, int64_t rows, int64_t hea
   return PACT_OK;
 }
 
-// Whether two tensors of heads share memory without being the same one: columns of one
-// matrix that do not meet share none.
+// Rows of `width` bytes, `ld` bytes apart.
+struct Block {
+  uintptr_t at;
+  uint64_t rows, width, ld;
+};
+Block block_of(const pact_heads* t, int64_t D) {
+  return Block{(uintptr_t)t->p, (uint64_t)t->rows, 2 * (uint64_t)(t->heads * D), 2 * (uint64_t)t->ld};
+}
+Block block_of(const float* p, uint64_t values) { return Block{(uintptr_t)p, 1, 4 * values, 4 * values}; }
+
+// Whether two blocks share memory: columns of one matrix that do not meet share none, nor does
+// a single row that lies between the rows of the other.  Blocks within each other whose rows
+// lie at different distances are taken to meet.
+bool share(Block a, Block b) {
+  if (a.at > b.at) {
+    const Block t = a;
+    a = b;
+    b = t;
+  }
+  const uint64_t gap = b.at - a.at;
+  if (gap >= (a.rows - 1) * a.ld + a.width) return false;
+  if (a.rows == 1 || (b.rows > 1 && a.ld != b.ld)) return true;
+  // b begins in a row of a, or behind it, where another one follows
+  const uint64_t off = gap % a.ld;
+  return off < a.width || off + b.width > a.ld;
+}
+bool heads_share(const pact_heads* a, const pact_heads* b, int64_t D) {
+  return share(block_of(a, D), block_of(b, D));
+}
+
+// Whether two tensors of heads of as many rows share memory without being the same one.
 bool heads_clash(const pact_heads* a, const pact_heads* b, int64_t D) {
-  const uintptr_t x = (uintptr_t)a->p, y = (uintptr_t)b->p;
-  if (x == y) return a->ld != b->ld || a->heads != b->heads;
-  const pact_heads *lo = x < y ? a : b, *hi = x < y ? b : a;
-  const uint64_t gap = (uint64_t)((uintptr_t)hi->p - (uintptr_t)lo->p) / 2;
-  const uint64_t wl = (uint64_t)(lo->heads * D), wh = (uint64_t)(hi->heads * D);
-  if (gap >= (uint64_t)((lo->rows - 1) * lo->ld) + wl) return false;
-  if (lo->ld != hi->ld) return true;
-  const uint64_t off = gap % (uint64_t)lo->ld;
-  return off < wl || off + wh > (uint64_t)lo->ld;
+  const bool same = a->p == b->p && a->heads == b->heads && (a->ld == b->ld || a->rows == 1);
+  return !same && heads_share(a, b, D);
 }
 
 // LoRA rank padded to 16, 32 or 64; the fused GEMM's LoRA operands are twice as
@@ -958,6 +980,8 @@ int pact_qk_norm_rope(const pact_heads* q, const pact_heads* k, int64_t D, int64
     return rc;
   if (heads_clash(q_out, q, D) || heads_clash(k_out, k, D))
     return fail(PACT_ERR_INVALID_ARG, "q_out overlaps q, or k_out k, in part");
+  if (heads_share(q_out, k, D) || heads_share(k_out, q, D) || heads_share(q_out, k_out, D))
+    return fail(PACT_ERR_INVALID_ARG, "q_out and k_out share memory, or one does with the other's input");
   for (int w = 0; w < 2; ++w) {
     p.side[w].out = w ? k_out->p : q_out->p;
     p.side[w].ldo = w ? k_out->ld : q_out->ld;
@@ -992,12 +1016,16 @@ int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pa
     return rc;
   if (heads_clash(dq, dyq, D) || heads_clash(dk, dyk, D))
     return fail(PACT_ERR_INVALID_ARG, "dq overlaps dyq, or dk dyk, in part");
+  if (heads_share(dq, dyk, D) || heads_share(dk, dyq, D) || heads_share(dq, dk, D))
+    return fail(PACT_ERR_INVALID_ARG, "dq and dk share memory, or one does with the other's dy");
   if (gamma_q_opt) {
     if ((rc = check_heads(q_opt, "q", dyq->rows, dyq->heads, D)) ||
         (rc = check_heads(k_opt, "k", dyk->rows, dyk->heads, D)))
       return rc;
     if (heads_clash(dq, q_opt, D) || heads_clash(dk, k_opt, D))
       return fail(PACT_ERR_INVALID_ARG, "dq overlaps q, or dk k, in part");
+    if (heads_share(dq, k_opt, D) || heads_share(dk, q_opt, D))
+      return fail(PACT_ERR_INVALID_ARG, "dq shares memory with k, or dk with q");
     for (int w = 0; w < 2; ++w) {
       p.side[w].xf = w ? k_opt->p : q_opt->p;
       p.side[w].ldxf = w ? k_opt->ld : q_opt->ld;
@@ -1116,6 +1144,11 @@ int pact_attention_fwd(const pact_heads* q, const pact_heads* k, const pact_head
       L.p.part_o = (float*)((char*)ws_opt + parts_lse_bytes(L.p.parts, q->rows, q->heads));
     }
   }
+  // o may be q: the unit that writes a row of heads is the one that has read it
+  const Block bl = block_of(lse, (uint64_t)(q->rows * q->heads));
+  if (heads_clash(o, q, D) || heads_share(o, k, D) || heads_share(o, v, D) || share(bl, block_of(o, D)) ||
+      share(bl, block_of(q, D)) || share(bl, block_of(k, D)) || share(bl, block_of(v, D)))
+    return fail(PACT_ERR_INVALID_ARG, "o or lse shares memory with another tensor (o may be q itself)");
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   if ((rc = make_heads_map(&L.tmQ, q, D, L.p.gp, L.p.tpt)) ||
@@ -1172,6 +1205,16 @@ int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_he
       attention_bwd_plan(q->rows, q->heads, k->rows, k->heads, D, nseq);
   if (!ws || ws_bytes < plan.bytes || !aligned(ws, 256))
     return fail(PACT_ERR_INVALID_ARG, "workspace missing, too small or not 256-byte aligned");
+  // dq and dk|dv run side by side: neither may write what the other reads
+  const Block bl = block_of(lse, (uint64_t)(q->rows * q->heads));
+  const pact_heads* const outs[3] = {dq, dk, dv};
+  const pact_heads* const ins[5] = {q, k, v, o, d_o};
+  for (int i = 0; i < 3; ++i) {
+    bool meets = share(block_of(outs[i], D), bl) || heads_share(outs[i], outs[(i + 1) % 3], D);
+    for (const pact_heads* in : ins) meets = meets || heads_share(outs[i], in, D);
+    if (meets)
+      return fail(PACT_ERR_INVALID_ARG, "dq, dk or dv shares memory with another tensor");
+  }
   DeviceInfo* d;
   if ((rc = device_info(&d))) return rc;
   if ((rc = make_heads_map(&L.tmQ, q, D, L.p.gp, L.p.tpt)) ||
