@@ -14,6 +14,11 @@
 namespace pact {
 
 constexpr uint64_t kAttnWaitNs = 2000000000ull;  // 2 s per pipeline wait
+// A wait of a role that has nothing to do while others go through all the keys of a unit, at
+// most those of the tensor: 20 us a tile of keys more, of which none takes 3.
+__device__ __forceinline__ uint64_t unit_wait_ns(const AttnParams& p) {
+  return kAttnWaitNs + (uint64_t)((uint32_t)p.tk >> 7) * 20000ull;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t buf = units & 1u;
         float nl[4], de[4];
         load_stats(p, s, h0, tok0, 0.0f, lane, nl, de);
-        if (!(ok = mbar_wait(B.stat_empty + 8 * buf, ((units >> 1) & 1u) ^ 1u, kAttnWaitNs, abort_flag)))
+        // at most two units ahead: it waits while the computing warps go through one
+        if (!(ok = mbar_wait(B.stat_empty + 8 * buf, ((units >> 1) & 1u) ^ 1u, unit_wait_ns(p), abort_flag)))
           break;
         store_stats(reinterpret_cast<float*>(smem + C::STAT_OFF + buf * 1024), lane, nl, de);
         if (lane == 0) mbar_arrive(B.stat_full + 8 * buf);

@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(384, 1)
   RingPos slot;
   bool ok = true;
   auto next_unit = [&]() {  // false behind the last one, and (ok false) when it took too long
-    if (!(ok = mbar_wait(unit_full + 8 * slot.stage, slot.phase, kAttnWaitNs, abort_flag))) return false;
+    // a tile without keys waits here while the other tile goes through its own
+    if (!(ok = mbar_wait(unit_full + 8 * slot.stage, slot.phase, unit_wait_ns(p), abort_flag))) return false;
     const int4* d = reinterpret_cast<const int4*>(smem + C::UNIT_OFF + 32 * slot.stage);
     const int4 a = d[0], b = d[1];
     __syncwarp();
