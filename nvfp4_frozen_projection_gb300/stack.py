@@ -270,7 +270,9 @@ class DecoderLayer(DecoderProjectionStack):
     heads and kv_heads of q.d_out / heads columns; inv_freq: the rotary embedding's
     frequencies (float64, radians per position); gamma_q, gamma_k: norms of the queries'
     and keys' heads (BF16, both or neither).  The sequences are given at each call: cu
-    (int32 offsets of the packed rows) and positions (int32, of each row)."""
+    (int32 offsets of the packed rows) and positions (int32, of each row).  Rows of no
+    sequence (a padded batch) have an attention output of zeros, and their dq, dk and dv are
+    zeros, so that with a dy of zeros they add nothing to any gradient."""
 
     def __init__(self, m: int, proj: dict, gamma1, gamma2, heads: int, kv_heads: int,
                  inv_freq: torch.Tensor, eps: float = 1e-5, gamma_q=None, gamma_k=None,
@@ -321,10 +323,12 @@ class DecoderLayer(DecoderProjectionStack):
             with torch.cuda.stream(side):
                 p["k"].forward(self.xq1, self.k)
                 p["v"].forward(self.xq1, self.v)
+                self.attn.zero_()
         p["q"].forward(self.xq1, self.q)
         if side is None:
             p["k"].forward(self.xq1, self.k)
             p["v"].forward(self.xq1, self.v)
+            self.attn.zero_()  # the attention leaves rows of no sequence as they were
         else:
             main.wait_stream(side)
         pact_qk_norm_rope(self.qh, self.kh, positions, self.turns, self.gamma_q, self.gamma_k,
@@ -337,7 +341,15 @@ class DecoderLayer(DecoderProjectionStack):
     def backward(self, dy: torch.Tensor, cu: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
         """The gradient of x; dq, dk, dv (of the projections' outputs) and the gradients of
         gamma_q and gamma_k are left in their buffers."""
+        main, side = torch.cuda.current_stream(), self._side()
+        if side is not None:
+            side.wait_stream(main)
+        with torch.cuda.stream(side):  # no stream: the current one
+            for t in (self.dq, self.dk, self.dv):
+                t.zero_()
         self._mlp_backward(dy)
+        if side is not None:
+            main.wait_stream(side)
         dq, dk, dv = (self.dq.view_as(self.qh), self.dk.view_as(self.kh), self.dv.view_as(self.vh))
         pact_attention_bwd(self.dattn.view_as(self.attn), self.qr, self.kr, self.vh, self.attn, self.lse,
                            cu, cu, dq=dq, dk=dk, dv=dv)
