@@ -874,6 +874,11 @@ def _need_attention(q, k, v, cu_q, cu_k, scale, dev):
     return fields, D, cu_q.shape[0] - 1, float(D ** -0.5 if scale is None else scale)
 
 
+# Keys a sequence has on average below which pact_attention_fwd_workspace_size is 0 whatever
+# else it is given: asking costs a small call 1 us.
+_PARTS_KEYS = 2048
+
+
 def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
                        cu_k: torch.Tensor, causal: bool = True, scale: float | None = None,
                        o: torch.Tensor | None = None, lse: torch.Tensor | None = None):
@@ -893,7 +898,7 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: 
         lse = torch.empty(shape, dtype=torch.float32, device=q.device)
     _need(lse, torch.float32, shape, "lse", dev)
     Tk, size, ws = k.shape[0], 0, None
-    if Tk >= 2048 * n:  # fewer keys never take a workspace: the question costs a small call 1 us
+    if Tk >= _PARTS_KEYS * n:
         size = lib.pact_attention_fwd_workspace_size(shape[1], shape[0], Tk, k.shape[1], D, n)
         # its own in every call, as for the backward
         ws = torch.empty((size,), dtype=torch.uint8, device=q.device) if size else None
