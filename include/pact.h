@@ -499,7 +499,8 @@ int pact_qk_norm_rope_bwd(const pact_heads* dyq, const pact_heads* dyk, const pa
  * the last query stands at the last key.
  *   o = softmax(scale q k^T) v over the keys seen;  lse = log(sum exp(scale q k^T)), natural.
  * A query that sees no key gets o = 0 and lse = -inf.  FP32 sums; the probabilities are
- * rounded to BF16 for their product with v.
+ * rounded to BF16 for their product with v, which adds about a quarter to the error that the
+ * rounding of o makes.
  *   q, o  heads [Tq, hq, D];  k, v  heads [Tk, hk, D];  lse  FP32 [hq, Tq];  o may be q, and
  *   o and lse share no memory with anything else;
  *   cu_q, cu_k  INT32 [nseq + 1], ascending, on the device.  Rows of o and lse that belong
@@ -549,10 +550,12 @@ int pact_attention_bwd(const pact_heads* d_o, const pact_heads* q, const pact_he
  * over the tensors before it; chunks is the sum over all.  The lists are read when the call
  * runs, and no value of them may lead outside the tensors.
  * out: a list of pointers like data (may be data itself: clipping in place; a tensor that
- * needs no clipping is not written then), each a whole tensor of its own.  norm FP32 [1].
- * Squares are summed in FP32 over 16 values and in FP64 beyond, without overflow or
- * underflow for any finite values.  A NaN, or an infinity with a finite max_norm, makes the
- * norm NaN or infinite, and the coefficient NaN or zero.  Deterministic.
+ * needs no clipping is not written then): out[i] is data[i], or shares no memory with any tensor
+ * of either list.  norm FP32 [1].
+ * Squares are summed in FP32 over up to 64 values of a thread (16 at a time) and in FP64 beyond,
+ * without overflow or underflow for any finite values; coef is rounded to FP32.  A NaN, or an
+ * infinity with a finite max_norm, makes the norm NaN or infinite, and the coefficient NaN or
+ * zero.  Deterministic.
  * Rules: count 1 .. 2^20; chunks 0 .. 2^40; max_norm >= 0 (infinity: no clipping).
  * ws: pact_grad_norm_workspace_size() bytes, 256-byte aligned.
  */

@@ -885,7 +885,7 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: 
     """Attention over packed sequences: q [Tq, hq, D], k and v [Tk, hk, D], sequence b at
     rows cu_q[b]:cu_q[b + 1] and cu_k[b]:cu_k[b + 1] (int32, on the device).  scale is
     1 / sqrt(D) by default.  o may be q.  Returns (o [Tq, hq, D], lse FP32 [hq, Tq]); rows of
-    no sequence are left as they were."""
+    no sequence are left as they were (in new tensors: as the memory was)."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
     fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
@@ -915,7 +915,8 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                        dv: torch.Tensor | None = None):
     """Backward of pact_attention_fwd from its inputs, its o and lse and the gradient do of
     o.  Returns (dq, dk, dv), which share no memory with one another or an input; rows of no
-    sequence are left as they were."""
+    sequence are left as they were (in new tensors: as the memory was), so a padded batch whose
+    gradients are summed over all rows wants tensors of zeros."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
     fields, D, n, scale = _need_attention(q, k, v, cu_q, cu_k, scale, dev)
@@ -940,7 +941,11 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
 class GradList:
     """FP32 tensors whose norm is taken together, listed in device memory once; they keep
     their addresses while the list is in use.  Contiguous, all on the current device, no two
-    sharing memory."""
+    sharing memory.
+
+    Making a list takes longer than clipping with it (448 tensors 0.35 ms, 14 tensors 40 us, on
+    the host, with a copy that waits for the device): it pays for gradients that stay where they
+    are, as those that are zeroed or overwritten in place do, not for new tensors each step."""
 
     def __init__(self, tensors):
         lib = _LIB or load_library()
@@ -998,8 +1003,8 @@ def pact_grad_norm(grads: GradList, norm: torch.Tensor | None = None) -> torch.T
 def pact_clip_grad_norm(grads: GradList, max_norm: float, norm: torch.Tensor | None = None,
                         out: GradList | None = None) -> torch.Tensor:
     """Scale every value by min(1, max_norm / (norm + 1e-6)), in place or into `out`: a list
-    of the same sizes, whose tensors share no memory with those of grads but, each, with its
-    own.  Returns the norm before clipping, FP32 [1]."""
+    of the same sizes, each of whose tensors is its counterpart in grads or shares no memory
+    with any tensor of the two.  Returns the norm before clipping, FP32 [1]."""
     lib = _LIB or load_library()
     dev = torch.cuda.current_device()
     _need_list(grads, "grads", dev)

@@ -18,21 +18,27 @@
 // What bounds it.  Heads of 128: a pair of tiles against 128 keys has 2048 cycles of products
 // (16 MMAs of 64 cycles for each tile) and takes about 3000 to 3700: the softmax of a tile,
 // 1370 cycles, the signals to and from the issuers, 300, and P V and the next S, 768, follow
-// one another, and the other tile fills the gaps in part.  16384 causal, 16/4 heads of 128: 765
-// us, 1.44 PFLOP/s.  Heads of 64: the softmax alone, 2250 cycles a pair of tiles (its 32768
-// exponentials are 1024); 26 x 1024 causal, 32/8 heads of 64: 164 us.  CTA pairs, which halve
-// what shared memory has to deliver, were slower (16384: 816 us): a tile then waits for the
-// softmax of two CTAs.  A third warpgroup for the end of a unit was slower, too (8 x 1024, 32/8
-// heads of 128: 107 us, 78 without): four warps store two tiles one after the other.
+// one another, and the other tile fills the gaps in part.  16384 causal, 16/4 heads of 128: 767
+// to 810 us, 1.36 to 1.43 PFLOP/s, by the power cap.  Heads of 64: the latencies of the softmax,
+// 2250 cycles a pair of tiles (its 32768 exponentials are 1024), with two warps a scheduler to
+// cover them: exponentials' pipe and tensor pipe 30 % busy, issue slots 48 %; 26 x 1024 causal,
+// 32/8 heads of 64: 164 us.  CTA pairs, which halve what shared memory has to deliver, were
+// slower (16384: 816 us): a tile then waits for the softmax of two CTAs.  A third warpgroup for
+// the end of a unit was slower, too (8 x 1024, 32/8 heads of 128: 107 us, 78 without): four
+// warps store two tiles one after the other.
 //
 // Where there are few units, they have one tile, and their keys are cut into parts, units of
-// their own, and a second kernel joins what these say of a row (attn_fwd_plan).  A token over many keys is then bound by
-// HBM: 131072 keys, 32/8 heads of 128, 100 us, 5.4 TB/s; 16 of them over 16384 each, 165 us, 6.5.
+// their own, and a second kernel joins what these say of a row (attn_fwd_plan).  A token over
+// many keys is then bound by HBM: 131072 keys, 32/8 heads of 128, 100 us, 5.4 TB/s; 16 of them
+// over 16384 each, 165 us, 6.5.  The kernels for parts spill 36 bytes a thread (heads of 128) and
+// 16 (64), those without parts none.
 //
 // The running maximum m of a row moves only when a new one is above it by more than 2^8 in
 // the exponentials' scale: the sums stay far from FP32's range, and the rescaling of O in
-// TMEM that a moved m needs is rare.  P is rounded to BF16 for its product (its sum is of
-// the FP32 values); sums, maxima and O are FP32.
+// TMEM that a moved m needs is rare.  P is rounded to BF16 for its product, since the tensor
+// cores take it as they take V (TF32 would halve their rate, two BF16 parts double the work);
+// its sum is of the FP32 values, and sums, maxima and O are FP32.  Error of o against 64 bits,
+// relative: 0.0020, of which its own rounding to BF16 is 0.0016.
 #include "attention.cuh"
 #include "dependent.cuh"
 
@@ -584,7 +590,9 @@ constexpr int64_t kSms = 152;  // whatever the device has
 
 // Keys in parts pay for more ends of units and the join, 3 us and more, so there are no more
 // parts than SMs for them, none of fewer than two tiles, and none at all below 16 tiles of keys
-// a sequence (on average: the lengths are on the device).  One part and with this rule, us: 8192
+// a sequence (on average: the lengths are on the device, so a long sequence among many short
+// ones stays whole: 8192 causal, 2/1 heads of 128, 91 alone and 122 with 31 of 128 tokens).  One
+// part and with this rule, us: 8192
 // causal, one head of 128, 118 and 52; 4096, 2 heads of 64, 49 and 29; a token over 2048 keys,
 // 8/1 heads, 26 and 13, over 16384, 162 and 27, over 131072, 32/8 heads, 1203 and 100.  More
 // parts than that: 8 x 1 over 2048, 32/8 heads, 26, with two 20, with three 27; 1024 keys (8

@@ -17,8 +17,10 @@
 // once for all of them.  A lane has both halves of four pairs, 8 columns: four angles, and
 // nothing to exchange but the sums over a head.  With few tokens the heads of a token are
 // shared out over more groups.  8192 x 40 x 128 with norms: 31 us, 5.4 TB/s; backward 26624 x
-// 40 x 64 with both dgammas: 80 us, 5.1 TB/s.  (A tile of tokens with its angles in shared
-// memory and neighbouring groups on neighbouring heads: 45 and 107 us.)
+// 40 x 64 without norms: 45 us, 6.0 TB/s, with them 69, 5.9, with both dgammas 80, 5.1: a second
+// launch, 6 us, and the sums.  The loads in flight are those that a thread's registers hold,
+// since the values go straight to them.  (A tile of tokens with its angles in shared memory and
+// neighbouring groups on neighbouring heads: 45 us forward, 107 backward.)
 #include "common.cuh"
 #include "kernels.h"
 

@@ -371,8 +371,9 @@ class DecoderLayer(DecoderProjectionStack):
         return self.grads
 
     def clip_grads(self, max_norm: float, norm: torch.Tensor = None) -> torch.Tensor:
-        """Clip the adapters' gradients (and those of gamma_q and gamma_k) by their norm
-        together; returns it."""
+        """Clip this layer's adapters' gradients (and those of gamma_q and gamma_k) by their
+        norm together; returns it.  Several layers by one norm: pact_clip_grad_norm with one
+        GradList of all their grad_list.tensors."""
         return pact_clip_grad_norm(self.grad_list, max_norm, norm=norm)
 
     @classmethod
